@@ -1,0 +1,245 @@
+"""Python binding of the cache calls of libspecverify (``include/speccache.h``; argument marshalling only).
+
+A verify step's target model appends each chunk's keys and values to a paged cache, attends over it, and,
+once a token tree is verified, keeps the accepted path:
+
+    cache = PagedCache(k, v, page_table)             # k, v: [layers, pages, page_size, heads, head_dim]
+    chunk = Chunk(seq_offsets, cached, rows, max_gamma, parents)
+    for layer in range(layers):
+        cache.append(chunk, q, k_new, v_new, q_rot, rope=rope, layer=layer)
+        cache.attend(chunk, q_rot, out, scale=scale, layer=layer)
+    ... logits, specverify.spec_verify_tree ...
+    cache.compact(chunk, out_num_accepted, out_path, cached)
+
+Every call enqueues on the given stream (default: torch's current one) and returns the library's host status
+code. The library reads tensors by address: each object keeps references to the tensors it describes, and a
+caller using another stream than the one its tensors were made on orders the two itself.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from .specverify import SV_BF16, _ptr, lib
+
+SV_F16, SV_E4M3 = 2, 3
+
+# every exported symbol of speccache.h, in header order
+EXPORTS = ("spec_cache_append", "spec_cache_workspace_size", "spec_cache_attend", "spec_cache_compact")
+
+
+class SvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("stride_page", ctypes.c_int64),
+                ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64), ("stride_layer", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("layers", ctypes.c_int32), ("pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class SvChunk(ctypes.Structure):
+    _fields_ = [("seq_offsets", ctypes.c_void_p), ("cached", ctypes.c_void_p), ("parents", ctypes.c_void_p),
+                ("B", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_gamma", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class SvRope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+def _bind():
+    vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    lib.spec_cache_append.argtypes = [vp, i32, vp, vp, ctypes.c_int, i32, vp, i64, vp, vp, i64, vp, vp, vp]
+    lib.spec_cache_append.restype = ctypes.c_int
+    lib.spec_cache_workspace_size.argtypes = [vp]
+    lib.spec_cache_workspace_size.restype = sz
+    lib.spec_cache_attend.argtypes = [vp, i32, vp, ctypes.c_int, i32, vp, i64, ctypes.c_float, i32, vp, vp, vp, vp, sz,
+                                      vp]
+    lib.spec_cache_attend.restype = ctypes.c_int
+    lib.spec_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp]
+    lib.spec_cache_compact.restype = ctypes.c_int
+
+
+_bind()
+
+
+def _ref(s):
+    return None if s is None else ctypes.addressof(s)
+
+
+def spec_cache_append(cache, layer, chunk, rope, dtype, q_heads, q, q_stride, k, v, kv_stride, q_out, device_status,
+                      cuda_stream) -> int:
+    """Rotate and append a chunk. cache, chunk, rope: SvCache, SvChunk, SvRope or None; the rest addresses."""
+    return lib.spec_cache_append(_ref(cache), layer, _ref(chunk), _ref(rope), dtype, q_heads, q, q_stride, k, v,
+                                 kv_stride, q_out, device_status, cuda_stream)
+
+
+def spec_cache_workspace_size(cache) -> int:
+    return lib.spec_cache_workspace_size(_ref(cache))
+
+
+def spec_cache_attend(cache, layer, chunk, dtype, q_heads, q, q_stride, scale, window, out, lse, device_status,
+                      workspace, workspace_bytes, cuda_stream) -> int:
+    """Attention of a chunk over the cache. cache, chunk: SvCache, SvChunk or None; the rest addresses."""
+    return lib.spec_cache_attend(_ref(cache), layer, _ref(chunk), dtype, q_heads, q, q_stride, scale, window, out, lse,
+                                 device_status, workspace, workspace_bytes, cuda_stream)
+
+
+def spec_cache_compact(cache, chunk, out_num_accepted, out_path, out_cached, device_status, cuda_stream) -> int:
+    """Keep the accepted path of a verified chunk. cache, chunk: SvCache, SvChunk or None; the rest addresses."""
+    return lib.spec_cache_compact(_ref(cache), _ref(chunk), out_num_accepted, out_path, out_cached, device_status,
+                                  cuda_stream)
+
+
+# ------------------------------------------------------------------------------------------------
+# torch marshalling helpers
+# ------------------------------------------------------------------------------------------------
+def _codes():
+    import torch
+    return {torch.bfloat16: SV_BF16, torch.float16: SV_F16, torch.float8_e4m3fn: SV_E4M3}
+
+
+def _check(t, name, dtypes, shape=None, device=None):
+    """A tensor argument's type, shape (None: any extent) and device."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape))):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _stream(stream):
+    import torch
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+class Chunk:
+    """One batch of chunks in the verify step's layout (device int32 tensors; see sv_chunk)."""
+
+    def __init__(self, seq_offsets, cached, rows: int, max_gamma: int, parents=None):
+        import torch
+        B = cached.numel()
+        _check(cached, "cached", (torch.int32,), (B,))
+        _check(seq_offsets, "seq_offsets", (torch.int32,), (B + 1,), cached.device)
+        if parents is not None:
+            _check(parents, "parents", (torch.int32,), (None,), cached.device)
+        for t, name in ((seq_offsets, "seq_offsets"), (cached, "cached"), (parents, "parents")):
+            if t is not None and not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        self.seq_offsets, self.cached, self.parents = seq_offsets, cached, parents
+        self.B, self.rows, self.max_gamma = B, rows, max_gamma
+        self.struct = SvChunk(_ptr(seq_offsets), _ptr(cached), _ptr(parents), B, rows, max_gamma, 0)
+
+
+class Rope:
+    """Rotary positions: a float32 table [positions, dim], cosines then sines (see sv_rope)."""
+
+    def __init__(self, table, interleaved: bool = False):
+        import torch
+        _check(table, "table", (torch.float32,), (None, None))
+        if not table.is_contiguous():
+            raise ValueError("table must be contiguous")
+        self.table = table
+        self.struct = SvRope(_ptr(table), table.shape[0], table.shape[1], int(interleaved), 0)
+
+
+class PagedCache:
+    """A paged key/value cache over the caller's tensors, with the workspace and status word of its calls.
+
+    k, v: [layers, pages, page_size, heads, head_dim], bfloat16, float16 or float8_e4m3fn, of equal strides
+    (views of another order, such as head-major pages, are fine; the last dimension is contiguous).
+    page_table: int32 [B, pages per sequence]. k_scale, v_scale: float32 [layers, heads] (float8_e4m3fn only).
+    Calls of one object share its workspace and must not overlap on the GPU.
+    """
+
+    def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
+        import torch
+        codes = _codes()
+        _check(k, "k", tuple(codes), (None,) * 5)
+        _check(v, "v", (k.dtype,), k.shape, k.device)
+        if k.stride() != v.stride() or k.stride(4) != 1:
+            raise ValueError("k and v must have equal strides and contiguous heads")
+        _check(page_table, "page_table", (torch.int32,), (None, None), k.device)
+        if page_table.shape[0] > 1 and page_table.stride(0) < page_table.shape[1] or page_table.stride(1) != 1:
+            raise ValueError("page_table's rows must be contiguous")
+        layers, pages, page_size, heads, dim = k.shape
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None:
+                _check(t, name, (torch.float32,), (layers, heads), k.device)
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+        self.k, self.v, self.page_table, self.k_scale, self.v_scale = k, v, page_table, k_scale, v_scale
+        self.heads, self.head_dim = heads, dim
+        # of a dimension of extent one the stride says nothing: any valid one does
+        st = [k.stride(i) if k.shape[i] > 1 else heads * page_size * dim for i in range(4)]
+        width = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
+        if width != page_table.shape[1]:
+            raise ValueError("page_table must be contiguous")
+        self.struct = SvCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), st[1], st[2], st[3],
+                              st[0], codes[k.dtype], layers, pages, page_size, heads, dim, page_table.shape[1], 0)
+        self.ws_bytes = spec_cache_workspace_size(self.struct)
+        self.workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=k.device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._types = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}
+
+    def _heads(self, t, name, rows, heads=None):
+        """Rows of [heads, head_dim], contiguous within a row: the row stride."""
+        if t.dim() != 3 or t.shape[0] < rows or t.shape[2] != self.head_dim or (heads and t.shape[1] != heads):
+            raise ValueError(f"{name} must be [{rows}, {heads or 'heads'}, {self.head_dim}], got {tuple(t.shape)}")
+        if t.stride(2) != 1 or (t.stride(1) != self.head_dim and t.shape[1] > 1):
+            raise ValueError(f"{name}'s heads must be contiguous within a row")
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * self.head_dim
+
+    def _type(self, *ts):
+        code = self._types.get(ts[0].dtype)
+        if code is None or any(t.dtype != ts[0].dtype for t in ts):
+            raise TypeError(f"tensors must share bfloat16 or float16, got {[str(t.dtype) for t in ts]}")
+        return code
+
+    def append(self, chunk: Chunk, q, k, v, q_out, rope: Rope | None = None, layer: int = 0, stream=None) -> int:
+        """Enqueue spec_cache_append: rotated queries to q_out, rotated keys and values to the cache. q and
+        q_out may be None."""
+        code = self._type(k, v) if q is None else self._type(k, v, q, q_out)
+        ks = self._heads(k, "k", chunk.rows, self.heads)
+        if self._heads(v, "v", chunk.rows, self.heads) != ks:
+            raise ValueError("k and v must have equal row strides")
+        qh, qs = 0, 0
+        if q is not None:
+            qh, qs = q.shape[1], self._heads(q, "q", chunk.rows)
+            if self._heads(q_out, "q_out", chunk.rows, qh) != qh * self.head_dim:
+                raise ValueError("q_out must be contiguous")
+        return spec_cache_append(self.struct, layer, chunk.struct, None if rope is None else rope.struct, code, qh,
+                                 _ptr(q), qs, _ptr(k), _ptr(v), ks, _ptr(q_out), _ptr(self.status), _stream(stream))
+
+    def attend(self, chunk: Chunk, q, out, lse=None, scale: float | None = None, window: int = 0, layer: int = 0,
+               stream=None) -> int:
+        """Enqueue spec_cache_attend: attention of the chunk's rotated queries into out (and lse, float32
+        [rows, q_heads]). scale: 1 / sqrt(head_dim) by default."""
+        import torch
+        code = self._type(q, out)
+        qh, qs = q.shape[1], self._heads(q, "q", chunk.rows)
+        if self._heads(out, "out", chunk.rows, qh) != qh * self.head_dim:
+            raise ValueError("out must be contiguous")
+        if lse is not None:
+            _check(lse, "lse", (torch.float32,), (None, qh))
+            if lse.shape[0] < chunk.rows or not lse.is_contiguous():
+                raise ValueError("lse must be contiguous with a row for every chunk row")
+        if scale is None:
+            scale = self.head_dim ** -0.5
+        return spec_cache_attend(self.struct, layer, chunk.struct, code, qh, _ptr(q), qs, scale, window, _ptr(out),
+                                 _ptr(lse), _ptr(self.status), _ptr(self.workspace), self.ws_bytes, _stream(stream))
+
+    def compact(self, chunk: Chunk, out_num_accepted, out_path, out_cached, stream=None) -> int:
+        """Enqueue spec_cache_compact on a verify call's outputs. out_path None: linear drafts. out_cached may
+        be the chunk's `cached`."""
+        import torch
+        _check(out_num_accepted, "out_num_accepted", (torch.int32,), (chunk.B,))
+        _check(out_cached, "out_cached", (torch.int32,), (chunk.B,))
+        if out_path is not None:
+            _check(out_path, "out_path", (torch.int32,), (None,))
+        return spec_cache_compact(self.struct, chunk.struct, _ptr(out_num_accepted), _ptr(out_path), _ptr(out_cached),
+                                  _ptr(self.status), _stream(stream))
+
+    def status_bits(self) -> int:
+        return int(self.status.item()) & 0xFFFFFFFF
