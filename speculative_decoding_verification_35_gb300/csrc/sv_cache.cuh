@@ -69,6 +69,7 @@ struct CompactArgs {
     int32_t esize;
 };
 
+size_t attend_workspace(int dim, int cache_dtype);  // bytes
 cudaError_t launch_append(const AppendArgs& A, int dtype, int cache_dtype, bool interleaved, cudaStream_t st);
 cudaError_t launch_attend(const AttendArgs& A, int dtype, int cache_dtype, cudaStream_t st);
 cudaError_t launch_compact(const CompactArgs& A, cudaStream_t st);

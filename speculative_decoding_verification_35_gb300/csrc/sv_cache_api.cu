@@ -108,7 +108,9 @@ int spec_cache_append(const sv_cache* cache, int32_t layer, const sv_chunk* chun
     return result(launch_append(A, dtype, cache->dtype, rope && rope->interleaved, (cudaStream_t)cuda_stream));
 }
 
-size_t spec_cache_workspace_size(const sv_cache* cache) { return valid(cache) ? 256 : 0; }
+size_t spec_cache_workspace_size(const sv_cache* cache) {
+    return valid(cache) ? attend_workspace(cache->head_dim, cache->dtype) : 0;
+}
 
 int spec_cache_attend(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, sv_dtype dtype, int32_t q_heads,
                       const void* q, int64_t q_stride, float scale, int32_t window, void* out, float* lse,
