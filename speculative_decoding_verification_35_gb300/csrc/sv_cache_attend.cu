@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kThreads = 384;   // two softmax warpgroups, then warps for loads, products and value tiles
 constexpr int kTile = 128;      // slots of a tile, and rows of a query tile
-constexpr int kMaxSlots = 12;   // key or value tiles in flight
+constexpr int kMaxSlots = 6;    // key tiles in flight, and value tiles
 constexpr int kBadRing = 16;
 constexpr int kMaxCtas = 160;
 constexpr int kHalf = kTile * 128;  // bytes of 128 rows of 128 bytes, the unit of an operand in shared memory
@@ -85,7 +85,8 @@ struct Params {
     AttendArgs a;
     int32_t G, tokens;  // query heads per key head; tokens of a query tile, kTile / G
     int32_t q_tiles;    // query tiles that shared memory has room for: 1 or 2
-    int32_t slots;      // key or value tiles that fit
+    int32_t q_box;      // tokens of one copy into a query tile
+    int32_t k_slots, v_slots;  // key and value tiles that shared memory has room for
     int32_t box;        // slots of one copy, a divisor of the page size and of kTile
     float* part_o;      // [2 n][256][DP]
     float2* part_ml;    // [2 n][256]
@@ -147,6 +148,13 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, i
         "l"(map), "r"(d), "r"(token), "r"(head), "r"(page), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void copy_queries(uint32_t dst, const CUtensorMap* map, int d, int head, int row, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(map), "r"(d), "r"(head), "r"(row), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -177,46 +185,64 @@ __device__ __forceinline__ void tc_st16(uint32_t col, const uint32_t* r) {
         SV_W8(r, 0), SV_W8(r, 8)
         : "memory");
 }
-__device__ __forceinline__ void tc_st8(uint32_t col, const uint32_t* r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(col), SV_W8(r, 0)
-                 : "memory");
+// Shared-memory operand of 128-byte rows under the 128-byte swizzle, eight rows 1024 bytes apart: the low word
+// of its descriptor (address, and the bytes between column halves of an operand whose rows run along the depth),
+// and the high word, which all share.
+constexpr uint32_t kOperandHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t far) {
+    return (addr & 0x3ffffu) >> 4 | (far >> 4) << 16;
 }
-// Shared-memory operand of 128-byte rows under the 128-byte swizzle; eight rows are 1024 bytes apart. far: bytes
-// between column halves of an operand whose rows run along its depth.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t far) {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(far >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+#define SV_MMA(kind, a)                                                                                            \
+    "{\n.reg .pred p;\n.reg .b64 x, y;\nsetp.ne.u32 p, %4, 0;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %5};\n"      \
+    "tcgen05.mma.cta_group::1.kind::" kind " [%0], " a ", y, %3, p;\n}"
+template <bool k8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
+    if (k8) asm volatile(SV_MMA("f8f6f4", "x") ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(add), "n"(kOperandHigh) : "memory");
+    else asm volatile(SV_MMA("f16", "x") ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(add), "n"(kOperandHigh) : "memory");
 }
 template <bool k8>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    if (k8)
-        asm volatile(
-            "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(add)
-            : "memory");
-    else
-        asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(
-                         d),
-                     "l"(a), "l"(b), "r"(idesc), "r"(add)
-                     : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
+    if (k8) asm volatile(SV_MMA("f8f6f4", "[%1]") ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(add), "n"(kOperandHigh) : "memory");
+    else asm volatile(SV_MMA("f16", "[%1]") ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(add), "n"(kOperandHigh) : "memory");
 }
-template <bool k8>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    if (k8)
-        asm volatile(
-            "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-            "r"(a), "l"(b), "r"(idesc), "r"(add)
-            : "memory");
-    else
-        asm volatile(
-            "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-            "r"(a), "l"(b), "r"(idesc), "r"(add)
-            : "memory");
+// One thread of a converged warp, always the same.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p;
 }
+// A position in a ring of n slots and the parity of its current use.
+struct Ring {
+    uint32_t i = 0, parity = 0;
+    __device__ __forceinline__ void step(uint32_t n) {
+        if (++i == n) {
+            i = 0;
+            parity ^= 1;
+        }
+    }
+};
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// Two floats in one register pair, for the packed multiply-add and add.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
@@ -270,35 +296,38 @@ __device__ __forceinline__ Seq checked_seq(const Params& P, int32_t b) {
     return s;
 }
 
-// Tiles of a sequence over all its row blocks and key heads.
-__device__ __forceinline__ long long units_of(const Params& P, const Seq& s) {
-    if (s.err) return 0;
-    const int32_t per = 2 * P.tokens;
-    long long u = 0;
-    for (int32_t p = 0; p * per < s.T; ++p) {
+// Tiles and row blocks of a sequence, for one key head.
+__device__ __forceinline__ void size_of(const Params& P, const Seq& s, long long& tiles, long long& blocks) {
+    tiles = blocks = 0;
+    if (s.err) return;
+    for (int32_t p = 0; p * 2 * P.tokens < s.T; ++p) {
         Item it;
         int32_t first, count;
         span(P, s.T, s.past, p, it, first, count);
-        u += count;
+        tiles += count;
+        ++blocks;
     }
-    return u * P.a.pool.heads;
 }
 
-struct Start {  // where a CTA begins
-    int32_t b, p, h, j;
+// Where a CTA begins. An item is `lead` units of beginning and ending (its queries' way in, its outputs' way
+// out, and the pipeline's filling in between) and a unit a tile; x counts them.
+struct Start {
+    int32_t b, p, h, T, past, row0;
+    int32_t lead, x;
     long long left;
 };
 
 // The items of a CTA, one after the other. Every warp walks by itself.
 struct Walk {
     const Params& P;
-    int32_t b, p, h, j, T, past, row0;
+    int32_t b, p, h, x, T, past, row0;
+    const int32_t lead;
     long long left;
-    bool fresh;
-    __device__ Walk(const Params& P_, const Start& s) : P(P_), b(s.b), p(s.p), h(s.h), j(s.j), left(s.left), fresh(true) {}
+    __device__ Walk(const Params& P_, const Start& s)
+        : P(P_), b(s.b), p(s.p), h(s.h), x(s.x), T(s.T), past(s.past), row0(s.row0), lead(s.lead), left(s.left) {}
     __device__ bool next(Item& it) {
         if (left <= 0) return false;
-        if (fresh) {
+        if (T < 0) {  // past the last sequence
             for (; b < P.a.chunk.B; ++b) {
                 const Seq s = checked_seq(P, b);
                 if (!s.err) {
@@ -308,11 +337,13 @@ struct Walk {
                     break;
                 }
             }
-            if (b >= P.a.chunk.B) return false;
-            fresh = false;
+            if (T < 0) return false;
         }
+        left -= max(0, lead - x);
+        if (left <= 0) return false;
         int32_t first, count;
         span(P, T, past, p, it, first, count);
+        const int32_t j = max(0, x - lead);
         it.b = b;
         it.h = h;
         it.row0 = row0;
@@ -321,60 +352,99 @@ struct Walk {
         it.n = (int32_t)min((long long)(count - j), left);
         it.finishes = j + it.n == count;
         left -= it.n;
-        j = 0;
+        x = 0;
         if (++h == P.a.pool.heads) {
             h = 0;
             ++p;
             if (p * 2 * P.tokens >= T) {
                 p = 0;
                 ++b;
-                fresh = true;
+                T = -1;
             }
         }
         return true;
     }
 };
 
-struct Shared {
-    uint64_t full[kMaxSlots], empty[kMaxSlots], value[kMaxSlots];  // value: a value tile is in and clean
+struct Shared {  // behind the operand tiles
+    uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
+    uint64_t value[kMaxSlots];  // a value tile is in and clean
     uint64_t s_full[2], p_ready[2], pv_done[2];
-    uint64_t q_full, q_empty, meet, part, drain;
+    uint64_t q_in, q_full, q_empty, meet, part, drain;
     uint32_t tmem;
     int gave_up;
     Start start;
-    long long scan[kThreads / 32 + 1];
-    uint32_t bad[kBadRing];         // per tile: groups of 8 slots that lie on a bad page
+    long long scan[kThreads / 32], scan2[kThreads / 32];
+    int failing;  // some sequence of this CTA's share has a finding
+    uint32_t bad[2][kBadRing];      // per key and per value tile: groups of 8 slots that lie on a bad page
     uint32_t odd[kBadRing][4];      // per value tile: slots with a non-finite value that was cleared
     float2 ml[2][kTile];
+    float q_down[1];  // e4m3 caches: [2][256], what a row's scores are scaled by, for even and odd items
 };
+template <int K>
+constexpr int shared_bytes() {
+    return (int)sizeof(Shared) + (K == kE4m3 ? 2 * 2 * kTile * 4 : 0);
+}
 
 // Where the CTA begins, and the record of an item that its predecessor began. All threads.
+constexpr int32_t kLead = 3;  // measured: about three tiles' time between an item's last tile and the next one's pace
 __device__ __forceinline__ void plan(const Params& P, Shared& sh) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int32_t B = P.a.chunk.B, c = (int32_t)blockIdx.x;
-    long long mine = 0, sum = 0;
-    for (int32_t b = tid; b < B; b += kThreads) {
-        const long long u = units_of(P, checked_seq(P, b));
-        if (b == tid) mine = u;
-        sum += u;
-    }
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if (lane == 0) sh.scan[w] = sum;
+    const int32_t B = P.a.chunk.B, c = (int32_t)blockIdx.x, heads = P.a.pool.heads;
+    Seq mine{};
+    long long my_tiles = 0, my_blocks = 0, tiles = 0, blocks = 0;
     if (tid == 0) {
         sh.start.left = 0;
-        if (blockIdx.x > 0) P.records[c].parts = 0;
+        sh.failing = 0;
+        if (c > 0) P.records[c].parts = 0;
     }
-    __syncthreads();
-    long long W = 0;
-    for (int i = 0; i < kThreads / 32; ++i) W += sh.scan[i];
-    // with fewer tiles than CTAs the first W take one each, so that an item's CTAs follow one another
-    const int32_t n = (int32_t)min((long long)gridDim.x, W);
+    bool fails = false;
+    for (int32_t b = tid; b < B; b += kThreads) {
+        const Seq s = checked_seq(P, b);
+        long long t, n;
+        size_of(P, s, t, n);
+        fails |= s.err && b % gridDim.x == c;
+        tiles += t;
+        blocks += n;
+        if (b == tid) {
+            mine = s;
+            my_tiles = t;
+            my_blocks = n;
+        }
+    }
+    for (int o = 16; o; o >>= 1) {
+        tiles += __shfl_xor_sync(kAll, tiles, o);
+        blocks += __shfl_xor_sync(kAll, blocks, o);
+    }
+    if (lane == 0) {
+        sh.scan[w] = tiles;
+        sh.scan2[w] = blocks;
+    }
+    if (__syncthreads_or(fails) && tid == 0) sh.failing = 1;
+    tiles = blocks = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+        tiles += sh.scan[i];
+        blocks += sh.scan2[i];
+    }
+    tiles *= heads;
+    blocks *= heads;
+    // With few tiles there is a CTA for each, and an item's beginning is nobody's but its own.
+    const int32_t lead = tiles <= 2 * (long long)gridDim.x ? 0 : kLead;
+    const long long W = tiles + lead * blocks;
+    const int32_t n = (int32_t)min((long long)gridDim.x, tiles);
     if (c >= n) return;  // the same for the whole CTA
     const long long u0 = W * c / n, u1 = W * (c + 1) / n;
     long long base = 0;
     for (int32_t b0 = 0; b0 < B && base <= u0; b0 += kThreads) {
         const int32_t b = b0 + tid;
-        const long long u = b0 == 0 ? mine : b < B ? units_of(P, checked_seq(P, b)) : 0;
+        if (b0 > 0) {
+            my_tiles = my_blocks = 0;
+            if (b < B) {
+                mine = checked_seq(P, b);
+                size_of(P, mine, my_tiles, my_blocks);
+            }
+        }
+        const long long u = (my_tiles + lead * my_blocks) * heads;
         long long incl = u;
         for (int o = 1; o < 32; o <<= 1) {
             const long long x = __shfl_up_sync(kAll, incl, o);
@@ -390,29 +460,24 @@ __device__ __forceinline__ void plan(const Params& P, Shared& sh) {
         }
         const long long begin = before + incl - u;
         if (u > 0 && u0 >= begin && u0 < begin + u) {
-            const Seq s = checked_seq(P, b);
             long long rest = u0 - begin;
             Item it;
             int32_t first, count, p = 0;
             for (;; ++p) {
-                span(P, s.T, s.past, p, it, first, count);
-                if (rest < (long long)count * P.a.pool.heads) break;
-                rest -= (long long)count * P.a.pool.heads;
+                span(P, mine.T, mine.past, p, it, first, count);
+                const long long block = (long long)(count + lead) * heads;
+                if (rest < block) break;
+                rest -= block;
             }
-            const int32_t h = (int32_t)(rest / count), j = (int32_t)(rest - (long long)h * count);
-            sh.start.b = b;
-            sh.start.p = p;
-            sh.start.h = h;
-            sh.start.j = j;
-            sh.start.left = u1 - u0;
-            if (j > 0) {
-                // the item began at u0 - j; if the CTA before this one began it, this one records it
-                const long long from = u0 - j, to = from + count;
+            const int32_t h = (int32_t)(rest / (count + lead)), x = (int32_t)(rest - (long long)h * (count + lead));
+            sh.start = {b, p, h, mine.T, mine.past, mine.row0, lead, x, u1 - u0};
+            if (x > lead) {
+                // the item's first tile is unit `from`; if the CTA before this one had it, this one records the item
+                const long long from = u0 - x + lead;
                 if (from >= W * (c - 1) / n) {
                     Record r{};
-                    const long long last = (to * n - 1) / W;  // the CTA of its last tile
-                    r.parts = (int32_t)(last - c) + 2;
-                    r.row0 = s.row0 + it.t0;
+                    r.parts = (int32_t)(((from + count) * n - 1) / W - c) + 2;  // to the CTA of its last tile
+                    r.row0 = mine.row0 + it.t0;
                     r.tokens = it.nt;
                     r.head = h;
                     r.two = it.two;
@@ -430,19 +495,24 @@ __device__ __forceinline__ void plan(const Params& P, Shared& sh) {
 // A row of a query tile as its thread knows it.
 struct Row {
     bool real;
-    int32_t token, g;   // chunk token, head of the group
+    int32_t token;      // chunk token
     int32_t low, limit; // slots low .. limit - 1 are seen, as far as they are not a tree's
     uint32_t above;     // a tree: the chunk tokens it sees
-    float sl;           // score units to log2 of the weight
+    float sl;           // score units to log2 of the weight, not negative
 };
 
-template <int K>
-__device__ __forceinline__ void load_queries(const Params& P, const Item& it, int stream, int r, uint32_t q_smem, Row& row) {
-    using T = typename KindOf<K>::T;
+// Scores to log2 of the weights. A negative factor changes the queries' signs; one of zero is kept above it, so
+// that -inf stays -inf.
+__device__ __forceinline__ float score_unit(const AttendArgs& A, int32_t h, bool& flip) {
+    const float sl = A.scale * (A.pool.k_scale ? A.pool.k_scale[h] : 1.f) * kLog2e;
+    flip = sl < 0.f;
+    return fmaxf(fabsf(sl), 1e-30f);
+}
+
+// tl: the row's token within its tile.
+__device__ __forceinline__ Row row_of(const Params& P, const Item& it, int stream, int32_t tl) {
     const AttendArgs& A = P.a;
-    const int32_t D = A.pool.dim;
-    const int32_t tl = r / P.G;
-    row.g = r - tl * P.G;
+    Row row;
     row.token = it.t0 + tl + (it.two && stream ? P.tokens : 0);
     row.real = tl < P.tokens && row.token < it.t0 + it.nt;
     row.above = 0;
@@ -460,76 +530,9 @@ __device__ __forceinline__ void load_queries(const Params& P, const Item& it, in
     const int32_t pos = it.past + depth;
     row.low = A.window > 0 ? max(0, pos - A.window + 1) : 0;
     row.limit = it.past + (A.chunk.parents ? 0 : row.token + 1);
-    float sl = A.scale * (A.pool.k_scale ? A.pool.k_scale[it.h] : 1.f) * kLog2e;
-    const bool flip = sl < 0.f;
-    sl = fmaxf(fabsf(sl), 1e-30f);  // a scale of zero: all weights equal, and -inf stays -inf
-    row.sl = sl;
-    const T* q = (const T*)A.q + (int64_t)(it.row0 + row.token) * A.q_stride + (int64_t)(it.h * P.G + row.g) * D;
-    // a query tile shared by both streams is loaded by both, every other 16 bytes each
-    const uint32_t base = q_smem + (it.two && stream ? (K == kE4m3 ? 2 : (D > 64 ? 2 : 1)) * kHalf : 0) + r * 128;
-    const int begin = it.two ? 0 : stream, by = it.two ? 1 : 2;
-    if (K != kE4m3) {
-        const int chunks = (D + 15) / 16 * 2;
-        for (int c = begin; c < chunks; c += by) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (row.real && c * 8 < D) {
-                u = *reinterpret_cast<const uint4*>(q + c * 8);
-                if (flip) {
-                    u.x ^= 0x80008000u;
-                    u.y ^= 0x80008000u;
-                    u.z ^= 0x80008000u;
-                    u.w ^= 0x80008000u;
-                }
-            }
-            const uint32_t at = base + (c >> 3) * kHalf + (((c & 7) ^ (r & 7)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w)
-                         : "memory");
-        }
-    } else {
-        float top = 0.f;
-        if (row.real)
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 u = *reinterpret_cast<const uint4*>(q + c * 8);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = to_float2<T>(w[i]);
-                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                }
-            }
-        int e = 0;
-        if (top > 0.f && top < INFINITY) e = max(-120, min(120, 7 - ilogbf(top)));
-        const float up = exp2f((float)e) * (flip ? -1.f : 1.f);
-        row.sl = sl * exp2f((float)-e);
-        const int chunks = (D + 31) / 32 * 2;
-        for (int c = begin; c < chunks; c += by) {
-            uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-            if (row.real && c * 16 < D) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(q + c * 16 + half * 8);
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float2 f = to_float2<T>(w[i]);
-                        // an infinite query has no finite parts: its row is NaN, as its softmax is
-                        f.x = isinf(f.x) ? NAN : f.x * up;
-                        f.y = isinf(f.y) ? NAN : f.y * up;
-                        const uint32_t a = e4m3x2(f.x, f.y);
-                        const float2 g = from_e4m3x2(a);
-                        const uint32_t b = e4m3x2(f.x - g.x, f.y - g.y);
-                        hi[half * 2 + (i >> 1)] |= a << (16 * (i & 1));
-                        lo[half * 2 + (i >> 1)] |= b << (16 * (i & 1));
-                    }
-                }
-            }
-            const uint32_t at = base + (((c & 7) ^ (r & 7)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
-                         : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + kHalf), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]),
-                         "r"(lo[3])
-                         : "memory");
-        }
-    }
+    bool flip;
+    row.sl = score_unit(A, it.h, flip);
+    return row;
 }
 
 __device__ __forceinline__ uint32_t prefix32(int32_t n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
@@ -553,17 +556,26 @@ __device__ __forceinline__ void seen_of(const Row& row, const Item& it, int32_t 
     }
 }
 
-// Slots of the item that some of its rows see and others do not: only there can a value meet a weight of
-// zero, and a NaN or infinity be carried into a row that does not see it.
-__device__ __forceinline__ bool mixed_tile(const Params& P, const Item& it, int32_t k0) {
+// Scores of slots that are not seen.
+__device__ __forceinline__ void hide(uint32_t* s, uint32_t seen) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (!(seen >> i & 1u)) s[i] = 0xff800000u;
+}
+
+// Slots of the item that some of its rows see and others do not: those below lo and those from hi on. Only there
+// can a value meet a weight of zero, and a NaN or infinity be carried into a row that does not see it.
+__device__ __forceinline__ void mixed_slots(const Params& P, const Item& it, int32_t& lo, int32_t& hi) {
     const bool tree = P.a.chunk.parents != nullptr;
-    if (it.nt == 1 && !tree) return false;
-    if (k0 + kTile > it.past + (tree ? 0 : it.t0 + 1)) return true;
-    return P.a.window > 0 && k0 < it.lo + it.nt + (tree ? it.t0 : 0);
+    hi = it.past + (tree ? 0 : it.t0 + 1);
+    lo = P.a.window > 0 && (tree || it.nt > 1) ? it.lo + it.nt + (tree ? it.t0 : 0) : 0;
+}
+__device__ __forceinline__ bool mixed_tile(const Item& it, int32_t k0, int32_t lo, int32_t hi) {
+    return k0 < lo || max(k0, hi) < min(k0 + kTile, it.end);
 }
 
 template <int K, int DP>
-__device__ __forceinline__ void softmax_role(const Params& P, Shared& sh, uint32_t q_smem) {
+__device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
     using KT = KindOf<K>;
     using T = typename KT::T;
     const AttendArgs& A = P.a;
@@ -573,111 +585,125 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh, uint32
     const uint32_t o_col[2] = {sh.tmem + lanes + 256, sh.tmem + lanes + 256 + DP};
     const uint32_t s_full = smem_u32(&sh.s_full[stream]), p_ready = smem_u32(&sh.p_ready[stream]),
                    pv_done = smem_u32(&sh.pv_done[stream]);
-    const uint32_t q_full = smem_u32(&sh.q_full), q_empty = smem_u32(&sh.q_empty);
     const int32_t D = A.pool.dim;
     const bool tree = A.chunk.parents != nullptr;
     volatile int* gave_up = &sh.gave_up;
+    const int32_t tl = r / P.G, g = r - tl * P.G;
     uint32_t steps = 0;   // of this stream, over all items
     uint32_t tiles = 0;   // of the CTA, before this item
     uint32_t items = 0, merges = 0;
 
     Walk walk(P, sh.start);
-    Item it, nx;
-    Row row, nrow;
-    bool more = walk.next(it);
-    if (more) {
-        load_queries<K>(P, it, stream, r, q_smem, row);
-        fence_async();
-        __syncwarp();
-        if (lane == 0) bar_arrive(q_full);
-    }
-    while (more) {
+    Item it;
+    for (; walk.next(it); ++items) {
+        Row row = row_of(P, it, stream, tl);
         float m = -INFINITY, l = 0.f;
         const bool busy = __any_sync(kAll, row.real);
         const int32_t first = it.two ? 0 : stream, by = it.two ? 1 : 2;
         uint32_t done = 0;
+        int32_t mixed_lo, mixed_hi;
+        mixed_slots(P, it, mixed_lo, mixed_hi);
         for (int32_t j = first; j < it.n; j += by, ++done, ++steps) {
             if (!wait(s_full, steps & 1, gave_up)) return;
             tc_after();
+            if (K == kE4m3 && done == 0)
+                row.sl *= sh.q_down[(items & 1) * 2 * kTile + (it.two ? stream * kTile : 0) + r];
             const int32_t k0 = (it.tile + j) * kTile;
             const uint32_t ring = (tiles + j) % kBadRing;
-            const uint32_t bad = sh.bad[ring];
             uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
             if (busy) {
-                uint32_t s[128];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tc_ld32(s_col + 32 * i, s + 32 * i);
-                tc_wait_ld();
+                const uint32_t bad = sh.bad[0][ring];
                 const bool whole = (k0 + kTile <= row.limit && row.low <= k0 && !bad) || !row.real;
-                if (!__all_sync(kAll, whole)) {
-                    seen_of(row, it, k0, bad, tree, seen);
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (!(seen[c >> 5] >> (c & 31) & 1u)) s[c] = 0xff800000u;
-                }
+                const bool masked = !__all_sync(kAll, whole);
+                if (masked) seen_of(row, it, k0, bad, tree, seen);
+                uint32_t s[2][32];
+                // the tile's maximum
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 128; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
+                for (int q = 0; q < 4; q += 2) {
+                    tc_ld32(s_col + 32 * q, s[0]);
+                    tc_ld32(s_col + 32 * q + 32, s[1]);
+                    tc_wait_ld();
+                    if (masked) {
+                        hide(s[0], seen[q]);
+                        hide(s[1], seen[q + 1]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            top[e] = fmaxf(top[e], fmaxf(__uint_as_float(s[0][i + e]), __uint_as_float(s[1][i + e])));
+                }
+                tc_ld32(s_col, s[0]);
                 const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                const bool move = (mx - m) * row.sl > KT::kSlack || (m == -INFINITY && mx > m);
-                const unsigned movers = __ballot_sync(kAll, move);
-                if (movers) {
+                const bool move = row.real && ((mx - m) * row.sl > KT::kSlack || (m == -INFINITY && mx > m));
+                if (__any_sync(kAll, move)) {
                     const float old = m;
                     if (move) m = mx;
-                    const float f = old == -INFINITY ? 1.f : exp2_fast((old - m) * row.sl);
+                    const float f = !move || old == -INFINITY ? 1.f : exp2_fast((old - m) * row.sl);
                     l *= f;
-                    if (done > 0 && __any_sync(kAll, move && old != -INFINITY)) {
+                    if (__any_sync(kAll, move && old != -INFINITY)) {
                         if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
                         tc_after();
+                        tc_wait_ld();
                         for (int c = 0; c < DP; c += 32) {
-                            uint32_t o[32];
-                            tc_ld32(o_col[stream] + c, o);
+                            tc_ld32(o_col[stream] + c, s[1]);
                             tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * (move ? f : 1.f));
-                            tc_st32(o_col[stream] + c, o);
+                            for (int i = 0; i < 32; ++i) s[1][i] = __float_as_uint(__uint_as_float(s[1][i]) * f);
+                            tc_st32(o_col[stream] + c, s[1]);
                         }
                     }
                 }
+                // its weights, in place of the scores
                 const float off = KT::kShift - (m == -INFINITY ? 0.f : m * row.sl);
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const F2 sl2 = pack2(row.sl, row.sl), off2 = pack2(off, off);
+                F2 sum[2] = {0, 0};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t pk[16], lo[8];
+                    tc_wait_ld();
+                    uint32_t* x = s[q & 1];
+                    if (q < 3) tc_ld32(s_col + 32 * q + 32, s[(q + 1) & 1]);
+                    if (masked) hide(x, seen[q]);
+                    uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
                         float p[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            p[e] = exp2_fast(fmaf(__uint_as_float(s[32 * q + i + e]), row.sl, off));
-                            sum[e] += p[e];
+                        for (int e = 0; e < 4; e += 2) {
+                            unpack2(fma2(pack2(__uint_as_float(x[i + e]), __uint_as_float(x[i + e + 1])), sl2, off2), p[e],
+                                    p[e + 1]);
+                            p[e] = exp2_fast(p[e]);
+                            p[e + 1] = exp2_fast(p[e + 1]);
+                            sum[e >> 1] = add2(sum[e >> 1], pack2(p[e], p[e + 1]));
                         }
                         if (K != kE4m3) {
                             pk[i >> 1] = from_float2<T>(p[0], p[1]);
                             pk[(i >> 1) + 1] = from_float2<T>(p[2], p[3]);
                         } else {
                             const uint32_t a = e4m3x2(p[0], p[1]), b = e4m3x2(p[2], p[3]);
-                            const float2 x = from_e4m3x2(a), y = from_e4m3x2(b);
+                            const float2 u = from_e4m3x2(a), w = from_e4m3x2(b);
                             pk[i >> 2] = a | b << 16;
-                            lo[i >> 2] = e4m3x2(p[0] - x.x, p[1] - x.y) | e4m3x2(p[2] - y.x, p[3] - y.y) << 16;
+                            pk[8 + (i >> 2)] = e4m3x2(p[0] - u.x, p[1] - u.y) | e4m3x2(p[2] - w.x, p[3] - w.y) << 16;
                         }
                     }
-                    if (K != kE4m3) tc_st16(s_col + 16 * q, pk);
-                    else {
-                        tc_st8(s_col + 8 * q, pk);
-                        tc_st8(s_col + 32 + 8 * q, lo);
-                    }
+                    tc_st16(s_col + 16 * q, pk);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float a, b;
+                unpack2(add2(sum[0], sum[1]), a, b);
+                l += a + b;
                 tc_wait_st();
+            }
+            const bool mixed = mixed_tile(it, k0, mixed_lo, mixed_hi);
+            if (mixed) {  // before p_ready: the tile cannot be released, nor its barrier move on, until then
+                const uint32_t v = tiles + j;
+                if (!wait(smem_u32(&sh.value[v % P.v_slots]), (v / P.v_slots) & 1, gave_up)) return;
             }
             tc_before();
             __syncwarp();
             if (lane == 0) bar_arrive(p_ready);
-            if (mixed_tile(P, it, k0)) {
+            if (mixed) {
                 // rows that see a non-finite value, which the product met as zero, get it added here
-                const uint32_t v = tiles + j;
-                if (!wait(smem_u32(&sh.value[v % P.slots]), (v / P.slots) & 1, gave_up)) return;
                 uint32_t odd[4], any = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) any |= odd[i] = sh.odd[ring][i];
@@ -715,17 +741,6 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh, uint32
         }
         tiles += it.n;
 
-        // the next item's queries, as soon as the products of this one have read theirs
-        more = walk.next(nx);
-        if (more) {
-            if (!wait(q_empty, items & 1, gave_up)) return;
-            load_queries<K>(P, nx, stream, r, q_smem, nrow);
-            fence_async();
-            __syncwarp();
-            if (lane == 0) bar_arrive(q_full);
-        }
-        ++items;
-
         // the item's end
         if (done > 0) {
             if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
@@ -753,7 +768,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh, uint32
         const int32_t row_at = it.row0 + row.token;
         const float vs = A.pool.v_scale ? A.pool.v_scale[it.h] : 1.f;
         const float inv = total == 0.f ? 0.f : vs / total;
-        const int32_t head = it.h * P.G + row.g;
+        const int32_t head = it.h * P.G + g;
         // a row that carries NaN or infinity in its sum stays so: inv is then NaN or zero
         const int c_begin = it.two ? 0 : stream * (DP / 2), c_end = it.two ? DP : c_begin + DP / 2;
         const size_t prow = (size_t)(2 * blockIdx.x + (it.begins ? 1 : 0)) * 256 + (it.two && stream ? kTile : 0) + r;
@@ -810,75 +825,87 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh, uint32
             tc_after();
             ++merges;
         }
-        it = nx;
-        row = nrow;
     }
 }
 
 // ---------------------------------------------------------------------------------------------------------
 // loads, products, value tiles: one warp each (value tiles: two)
 // ---------------------------------------------------------------------------------------------------------
+// Keys (kv 0) or values (kv 1).
 template <int NH>
-__device__ __forceinline__ void load_role(const Params& P, Shared& sh, uint32_t kv_smem, const CUtensorMap* km,
-                                          const CUtensorMap* vm) {
+__device__ __forceinline__ void load_role(const Params& P, Shared& sh, uint32_t smem, const CUtensorMap* map, int kv) {
     const int lane = threadIdx.x & 31;
     const int32_t box = P.box, boxes = kTile / box, ps = P.a.pool.page_size;
+    const uint32_t full = smem_u32(kv ? sh.v_full : sh.k_full), empty = smem_u32(kv ? sh.v_empty : sh.k_empty);
+    const uint32_t slots = kv ? P.v_slots : P.k_slots;
     volatile int* gave_up = &sh.gave_up;
-    uint32_t load = 0, tile = 0;
+    uint32_t tile = 0;
+    Ring ring;
     bool ok = true;
     Walk walk(P, sh.start);
     Item it;
     while (ok && walk.next(it)) {
         const int32_t* table = P.a.pool.table + (int64_t)it.b * P.a.pool.table_stride;
-        for (int32_t j = 0; j < it.n && ok; ++j, ++tile) {
+        // where a lane's box of a tile lies; read a tile ahead
+        auto look = [&](int32_t j, bool& need, int32_t& page, int32_t& at) {
             const int32_t slot = (it.tile + j) * kTile + lane * box;
-            int32_t page = -1, at = 0;
-            bool need = lane < boxes && slot < it.end && slot + box > it.lo;
+            need = j < it.n && lane < boxes && slot < it.end && slot + box > it.lo;
+            page = -1;
+            at = 0;
             if (need) {
                 const int32_t i = slot / ps;
                 at = slot - i * ps;
                 page = table[i];
             }
-            const bool miss = need && (page < 0 || page >= P.a.pool.pages);
-            if (miss) report(P.a.status, 1u << SV_ERR_BAD_OFFSETS);
-            need = need && !miss;
-            uint32_t bad = miss ? ((1u << (box / 8)) - 1u) << (lane * (box / 8)) : 0u;
-            bad = __reduce_or_sync(kAll, bad);
-            const uint32_t bytes = __popc(__ballot_sync(kAll, need)) * box * 128 * NH;
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv, ++load) {
-                const uint32_t slot_i = load % P.slots, full = smem_u32(&sh.full[slot_i]);
-                if (load >= (uint32_t)P.slots &&
-                    !wait(smem_u32(&sh.empty[slot_i]), (load / P.slots - 1) & 1, gave_up)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    if (kv == 0) sh.bad[tile % kBadRing] = bad;
-                    bar_expect(full, bytes);
-                }
-                __syncwarp();
-                if (need) {
-                    const uint32_t dst = kv_smem + slot_i * (NH * kHalf) + lane * box * 128;
-#pragma unroll
-                    for (int h = 0; h < NH; ++h) copy_box(dst + h * kHalf, kv ? vm : km, h * 64, at, it.h, page, full);
-                }
+        };
+        bool next_need;
+        int32_t next_page, next_at;
+        look(0, next_need, next_page, next_at);
+        for (int32_t j = 0; j < it.n; ++j, ++tile, ring.step(slots)) {
+            bool need = next_need;
+            const int32_t page = next_page, at = next_at;
+            look(j + 1, next_need, next_page, next_at);
+            if (tile >= slots && !wait(empty + 8 * ring.i, ring.parity ^ 1, gave_up)) {
+                ok = false;
+                break;
             }
+            const bool miss = need && (page < 0 || page >= P.a.pool.pages);
+            need = need && !miss;
+            const uint32_t bytes = __popc(__ballot_sync(kAll, need)) * box * 128 * NH;
+            uint32_t bad = 0;
+            if (__any_sync(kAll, miss)) {
+                if (miss) {
+                    report(P.a.status, 1u << SV_ERR_BAD_OFFSETS);
+                    bad = ((1u << (box / 8)) - 1u) << (lane * (box / 8));
+                }
+                bad = __reduce_or_sync(kAll, bad);
+            }
+            const uint32_t bar = full + 8 * ring.i;
+            if (lane == 0) {
+                sh.bad[kv][tile % kBadRing] = bad;
+                bar_expect(bar, bytes);
+            }
+            __syncwarp();
+            if (need) {
+                const uint32_t dst = smem + ring.i * (NH * kHalf) + lane * box * 128;
+#pragma unroll
+                for (int h = 0; h < NH; ++h) copy_box(dst + h * kHalf, map, h * 64, at, it.h, page, bar);
+            }
+            __syncwarp();
         }
     }
     // copies still under way land before the CTA ends, also where another role gave up
-    for (uint32_t i = load > (uint32_t)P.slots ? load - P.slots : 0; i < load; ++i) {
+    for (uint32_t i = tile > slots ? tile - slots : 0; i < tile; ++i) {
         int none = 0;
-        wait(smem_u32(&sh.full[i % P.slots]), (i / P.slots) & 1, &none);
+        wait(full + 8 * (i % slots), (i / slots) & 1, &none);
     }
 }
 
 template <int K, int NH>
-__device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32_t q_smem, uint32_t kv_smem) {
+__device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem) {
     constexpr bool k8 = K == kE4m3;
-    constexpr int parts = k8 ? 2 : 1, slot_bytes = NH * kHalf;
+    constexpr int parts = k8 ? 2 : 1, slot_bytes = NH * kHalf, steps_max = k8 ? 4 : 4 * NH;
     constexpr uint32_t fmt = K == kBf16 ? 1u : 0u;
-    const int lane = threadIdx.x & 31;
     const int32_t D = P.a.pool.dim;
     const int32_t depth = (D + KindOf<K>::kStep - 1) / KindOf<K>::kStep;
     // float accumulators, 128 rows; scores are 128 columns wide, outputs D rounded up to 16 with the value
@@ -886,58 +913,68 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
     const uint32_t base = 1u << 4 | fmt << 7 | fmt << 10 | (uint32_t)(kTile >> 4) << 24;
     const uint32_t id_s = base | (uint32_t)(kTile >> 3) << 17;
     const uint32_t id_o = base | 1u << 16 | (uint32_t)((D + 15) / 16 * 2) << 17;
-    const uint32_t q_bytes = (k8 ? 2 : NH) * kHalf;
-    const uint32_t dp = NH == 1 && !k8 ? 64 : 128;
+    constexpr uint32_t q_bytes = (k8 ? 2 : NH) * kHalf;
+    constexpr uint32_t dp = NH == 1 && !k8 ? 64 : 128;
+    const uint32_t tmem = __shfl_sync(kAll, sh.tmem, 0);
+    const uint32_t k_full = smem_u32(sh.k_full), k_empty = smem_u32(sh.k_empty), v_empty = smem_u32(sh.v_empty),
+                   value = smem_u32(sh.value), s_full = smem_u32(sh.s_full), p_ready = smem_u32(sh.p_ready),
+                   pv_done = smem_u32(sh.pv_done), q_empty = smem_u32(&sh.q_empty);
+    const bool leader = elect();
     volatile int* gave_up = &sh.gave_up;
-    uint32_t tiles = 0, items = 0, steps[2] = {0, 0};
+    uint32_t items = 0, p_parity = 0;  // p_parity: bit st for stream st
+    Ring kr, vr;
     Walk walk(P, sh.start);
     Item it;
     bool ok = true;
     while (ok && walk.next(it)) {
         if (!(ok = wait(smem_u32(&sh.q_full), items & 1, gave_up))) break;
         tc_after();
-        const int32_t S = it.two ? 2 * it.n : it.n;
+        // the same in every lane; taken from one, so that the operands below live in uniform registers
+        const bool two = __shfl_sync(kAll, (int)it.two, 0);
+        const int32_t S = __shfl_sync(kAll, it.two ? 2 * it.n : it.n, 0);
         auto scores = [&](int32_t n) {
-            const int st = n & 1;
-            const int32_t t = it.two ? n >> 1 : n;
-            const uint32_t load = 2 * (tiles + t), slot = load % P.slots;
-            if (!(it.two && st) && !wait(smem_u32(&sh.full[slot]), (load / P.slots) & 1, gave_up)) return false;
-            if (lane == 0) {
-                const uint32_t q = q_smem + (it.two && st ? q_bytes : 0), k = kv_smem + slot * slot_bytes;
-                const uint32_t d = sh.tmem + st * kTile;
+            const uint32_t st = n & 1;
+            const bool last_use = !two || st;
+            if (!(two && st) && !wait(k_full + 8 * kr.i, kr.parity, gave_up)) return false;
+            const uint32_t q = operand(q_smem + (two && st ? q_bytes : 0), 16), k = operand(k_smem + kr.i * slot_bytes, 16);
+            const uint32_t d = tmem + st * kTile;
+            if (leader) {
 #pragma unroll
                 for (int part = 0; part < parts; ++part)
-                    for (int i = 0; i < depth; ++i) {
-                        const uint32_t off = (i >> 2) * kHalf + (i & 3) * 32;
-                        mma_ss<k8>(d, operand(q + part * kHalf + off, 16), operand(k + off, 16), id_s, part + i > 0);
+#pragma unroll
+                    for (int i = 0; i < steps_max; ++i) {
+                        const uint32_t off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
+                        if (i < depth) mma_ss<k8>(d, q + (part * kHalf >> 4) + off, k + off, id_s, part + i > 0);
                     }
-                tc_commit(smem_u32(&sh.s_full[st]));
-                if (!it.two || st) tc_commit(smem_u32(&sh.empty[slot]));
-                if (n == S - 1) tc_commit(smem_u32(&sh.q_empty));
+                tc_commit(s_full + 8 * st);
+                if (last_use) tc_commit(k_empty + 8 * kr.i);
+                if (n == S - 1) tc_commit(q_empty);
             }
             __syncwarp();
+            if (last_use) kr.step(P.k_slots);
             return true;
         };
         auto outputs = [&](int32_t n) {
-            const int st = n & 1;
-            const int32_t t = it.two ? n >> 1 : n;
-            const uint32_t v = tiles + t, slot = (2 * v + 1) % P.slots;
-            if (!(it.two && st) && !wait(smem_u32(&sh.value[v % P.slots]), (v / P.slots) & 1, gave_up)) return false;
-            if (!wait(smem_u32(&sh.p_ready[st]), steps[st] & 1, gave_up)) return false;
+            const uint32_t st = n & 1;
+            const bool last_use = !two || st;
+            if (!(two && st) && !wait(value + 8 * vr.i, vr.parity, gave_up)) return false;
+            if (!wait(p_ready + 8 * st, p_parity >> st & 1, gave_up)) return false;
+            p_parity ^= 1u << st;
             tc_after();
-            if (lane == 0) {
-                const uint32_t a = sh.tmem + st * kTile, b = kv_smem + slot * slot_bytes, d = sh.tmem + 256 + st * dp;
+            const uint32_t a = tmem + st * kTile, b = operand(v_smem + vr.i * slot_bytes, kHalf), d = tmem + 256 + st * dp;
+            const uint32_t add = n > 1;
+            if (leader) {
 #pragma unroll
-                for (int part = 0; part < parts; ++part)
+                for (int i = 0; i < kTile / KindOf<K>::kStep; ++i)
 #pragma unroll
-                    for (int i = 0; i < kTile / KindOf<K>::kStep; ++i)
-                        mma_ts<k8>(d, a + part * 32 + i * 8, operand(b + i * KindOf<K>::kStep * 128, kHalf), id_o,
-                                   n > 1 || part + i > 0);
-                tc_commit(smem_u32(&sh.pv_done[st]));
-                if (!it.two || st) tc_commit(smem_u32(&sh.empty[slot]));
+                    for (int part = 0; part < parts; ++part)
+                        mma_ts<k8>(d, a + (k8 ? part * 8 + i * 16 : i * 8), b + (i * KindOf<K>::kStep * 128 >> 4), id_o,
+                                   part + i > 0 ? 1u : add);
+                tc_commit(pv_done + 8 * st);
+                if (last_use) tc_commit(v_empty + 8 * vr.i);
             }
             __syncwarp();
-            ++steps[st];
+            if (last_use) vr.step(P.v_slots);
             return true;
         };
         ok = scores(0);
@@ -946,116 +983,232 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
             ok = outputs(n);
             if (ok && n + 2 < S) ok = scores(n + 2);
         }
-        tiles += it.n;
         ++items;
     }
     // products under way end before the tensor memory is given back
-    if (lane == 0) tc_commit(smem_u32(&sh.drain));
+    if (leader) tc_commit(smem_u32(&sh.drain));
     __syncwarp();
     int none = 0;
     wait(smem_u32(&sh.drain), 0, &none);
 }
 
-// Value tiles before they are multiplied: rows of slots that no row of the item sees are cleared (they may
-// hold anything, and a weight of zero times NaN is NaN), and so are single non-finite values that only some
-// rows see; those are noted for the rows that do.
+// The rows of an item's query tiles. 16-bit caches: copied, G heads of q_box tokens at once (rows past the
+// sequence's end are another sequence's, or zero: a product's row depends on its own row only). e4m3: split
+// into the parts hi and lo, each row brought to [128, 256) by a power of two.
 template <int K, int NH>
-__device__ __forceinline__ void value_role(const Params& P, Shared& sh, uint32_t kv_smem) {
-    const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) & 1;  // rows 64 half .. 64 half + 63
+__device__ __forceinline__ bool load_queries(const Params& P, Shared& sh, const Item& it, uint32_t q_smem,
+                                             const CUtensorMap* qm, uint32_t items) {
+    using T = typename KindOf<K>::T;
+    const AttendArgs& A = P.a;
+    const int lane = threadIdx.x & 31;
+    const uint32_t q_full = smem_u32(&sh.q_full);
+    bool flip;
+    score_unit(A, it.h, flip);
+    if (K != kE4m3) {
+        const uint32_t bar = flip ? smem_u32(&sh.q_in) : q_full;
+        if (lane == 0) {
+            bar_expect(bar, (it.two ? 2 : 1) * NH * P.q_box * P.G * 128);
+            for (int t = 0; t < (it.two ? 2 : 1); ++t)
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+                    copy_queries(q_smem + (t * NH + h) * kHalf, qm, h * 64, it.h * P.G, it.row0 + it.t0 + t * P.tokens, bar);
+        }
+        __syncwarp();
+        if (!flip) return true;
+        if (!wait(bar, items & 1, &sh.gave_up)) return false;
+        for (int i = lane; i < (it.two ? 2 : 1) * NH * kHalf / 16; i += 32) {
+            uint32_t u[4];
+            const uint32_t at = q_smem + i * 16;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(at));
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(u[0] ^ 0x80008000u), "r"(u[1] ^ 0x80008000u),
+                         "r"(u[2] ^ 0x80008000u), "r"(u[3] ^ 0x80008000u)
+                         : "memory");
+        }
+    } else {
+        const int32_t D = A.pool.dim, rows = it.nt * P.G, tile_rows = P.tokens * P.G;
+        const T* q = (const T*)A.q + (int64_t)(it.row0 + it.t0) * A.q_stride + (int64_t)it.h * P.G * D;
+        // half a warp a row, eight elements a lane; eight rows of loads under way
+        const int c = lane & 15;
+        for (int32_t r0 = lane >> 4; r0 - (lane >> 4) < rows; r0 += 16) {
+            uint4 u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int32_t r = r0 + 2 * k;
+                u[k] = make_uint4(0, 0, 0, 0);
+                if (r < rows && c * 8 < D) {
+                    const int32_t t = r / P.G, g = r - t * P.G;
+                    u[k] = *reinterpret_cast<const uint4*>(q + t * A.q_stride + (int64_t)g * D + c * 8);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int32_t r = r0 + 2 * k;
+                const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                float2 f[4];
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f[i] = to_float2<T>(w[i]);
+                    top = fmaxf(top, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
+                }
+                for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+                int e = 0;
+                if (top > 0.f && top < INFINITY) e = max(-120, min(120, 7 - ilogbf(top)));
+                const float up = __int_as_float((127 + e) << 23);
+                uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // an infinite query has no finite parts: its row is NaN, as its softmax is
+                    const float x = isinf(f[i].x) ? NAN : flip ? -f[i].x * up : f[i].x * up;
+                    const float y = isinf(f[i].y) ? NAN : flip ? -f[i].y * up : f[i].y * up;
+                    const uint32_t a = e4m3x2(x, y);
+                    const float2 b = from_e4m3x2(a);
+                    hi[i >> 1] |= a << (16 * (i & 1));
+                    lo[i >> 1] |= e4m3x2(x - b.x, y - b.y) << (16 * (i & 1));
+                }
+                if (r < rows) {
+                    const int32_t at = r < tile_rows ? r : r - tile_rows;
+                    const uint32_t dst = q_smem + (r < tile_rows ? 0 : 2 * kHalf) + at * 128 +
+                                         (((c >> 1) ^ (at & 7)) << 4) + (c & 1) * 8;
+                    asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
+                    asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst + kHalf), "r"(lo[0]), "r"(lo[1]) : "memory");
+                    if (c == 0)
+                        sh.q_down[(items & 1) * 2 * kTile + (r < tile_rows ? 0 : kTile) + at] = __int_as_float((127 - e) << 23);
+                }
+            }
+        }
+    }
+    fence_async();
+    __syncwarp();
+    if (lane == 0) bar_arrive(q_full);
+    return true;
+}
+
+// Rows [lo, hi) of a value tile set to zero. A whole row is the same 128 bytes under any swizzle.
+template <int NH>
+__device__ __forceinline__ void clear_rows(uint32_t at, int32_t lo, int32_t hi) {
+    lo = max(lo, 0);
+    hi = min(hi, kTile);
+    for (int32_t i = lo * 8 + (threadIdx.x & 31); i < hi * 8; i += 32)
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at + h * kHalf + i * 16), "r"(0) : "memory");
+}
+
+// Non-finite elements of rows [lo, hi): cleared, and their rows noted.
+template <int K, int NH>
+__device__ __forceinline__ void scan_rows(uint32_t at, int32_t lo, int32_t hi, uint32_t bad, uint32_t* odd) {
+    constexpr int bits = K == kE4m3 ? 8 : 16;
+    constexpr uint32_t unit = K == kE4m3 ? 0x01010101u : 0x00010001u;
+    constexpr uint32_t top = unit * (K == kE4m3 ? 0x7fu : K == kBf16 ? 0x7f80u : 0x7c00u), high = unit << (bits - 1);
+#pragma unroll 4
+    for (int32_t i = lo * 8 + (threadIdx.x & 31); i < hi * 8; i += 32)
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            const uint32_t a = at + h * kHalf + i * 16;
+            uint32_t u[4], any = 0;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(a));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t t = ~u[e] & top;  // an element of zeros: its exponent is all ones
+                any |= (t - unit) & ~t & high;
+            }
+            if (any && !(bad >> (i >> 6) & 1u)) {
+                bool found = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int by = 0; by < 32; by += bits) {
+                        constexpr uint32_t one = (1u << bits) - 1u;
+                        if ((u[e] >> by & top & one) == (top & one)) {
+                            u[e] &= ~(one << by);
+                            found = true;
+                        }
+                    }
+                if (found) {
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
+                                 : "memory");
+                    atomicOr(&odd[i >> 8], 1u << (i >> 3 & 31));
+                }
+            }
+        }
+}
+
+// Queries, and value tiles before they are multiplied: rows of slots that no row of the item sees are cleared
+// (they may hold anything, and a weight of zero times NaN is NaN), and so are single non-finite values that only
+// some rows see; those are noted for the rows that do.
+template <int K, int NH>
+__device__ __forceinline__ void value_role(const Params& P, Shared& sh, uint32_t q_smem, uint32_t v_smem,
+                                           const CUtensorMap* qm) {
+    const int lane = threadIdx.x & 31;
     volatile int* gave_up = &sh.gave_up;
-    uint32_t v = 0;
+    uint32_t v = 0, items = 0;
+    Ring ring;
     Walk walk(P, sh.start);
     Item it;
-    while (walk.next(it)) {
-        for (int32_t j = 0; j < it.n; ++j, ++v) {
-            const uint32_t load = 2 * v + 1, slot = load % P.slots, ring = v % kBadRing;
-            if (!wait(smem_u32(&sh.full[slot]), (load / P.slots) & 1, gave_up)) return;
+    for (; walk.next(it); ++items) {
+        if (items > 0 && !wait(smem_u32(&sh.q_empty), (items - 1) & 1, gave_up)) return;
+        if (!load_queries<K, NH>(P, sh, it, q_smem, qm, items)) return;
+        int32_t mixed_lo, mixed_hi;
+        mixed_slots(P, it, mixed_lo, mixed_hi);
+        for (int32_t j = 0; j < it.n; ++j, ++v, ring.step(P.v_slots)) {
+            if (!wait(smem_u32(&sh.v_full[ring.i]), ring.parity, gave_up)) return;
             const int32_t k0 = (it.tile + j) * kTile;
-            const uint32_t bad = sh.bad[ring];
-            const bool edge = bad || k0 < it.lo || k0 + kTile > it.end, mixed = mixed_tile(P, it, k0);
-            uint32_t odd[2] = {0, 0};
-            if (edge || mixed) {
-                const uint32_t at = kv_smem + slot * (NH * kHalf) + (lane & 7) * 16;
-                for (int i = 0; i < 16; ++i) {  // four rows at a time, eight lanes each
-                    const int row = half * 64 + i * 4 + (lane >> 3);
-                    const int32_t s = k0 + row;
-                    const bool clear = s < it.lo || s >= it.end || (bad >> (row >> 3) & 1u);
-                    bool found = false;
-#pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        const uint32_t a = at + h * kHalf + row * 128;
-                        uint32_t u[4];
-                        bool write = clear;
-                        if (clear) u[0] = u[1] = u[2] = u[3] = 0;
-                        else if (mixed) {
-                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                                         : "r"(a)
-                                         : "memory");
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (K == kE4m3) {
-#pragma unroll
-                                    for (int by = 0; by < 32; by += 8)
-                                        if ((u[e] >> by & 0x7fu) == 0x7fu) {
-                                            u[e] &= ~(0xffu << by);
-                                            write = found = true;
-                                        }
-                                } else {
-                                    constexpr uint32_t top = K == kBf16 ? 0x7f80u : 0x7c00u;
-#pragma unroll
-                                    for (int by = 0; by < 32; by += 16)
-                                        if ((u[e] >> by & top) == top) {
-                                            u[e] &= ~(0xffffu << by);
-                                            write = found = true;
-                                        }
-                                }
-                            }
-                        }
-                        if (write)
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(u[0]), "r"(u[1]), "r"(u[2]),
-                                         "r"(u[3])
-                                         : "memory");
-                    }
-                    const unsigned f = __ballot_sync(kAll, found);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (f >> (8 * k) & 0xffu) odd[i >> 3] |= 1u << ((i & 7) * 4 + k);
+            const uint32_t bad = sh.bad[1][v % kBadRing];
+            const bool mixed = mixed_tile(it, k0, mixed_lo, mixed_hi);
+            if (bad || k0 < it.lo || k0 + kTile > it.end || mixed) {
+                const uint32_t at = v_smem + ring.i * (NH * kHalf);
+                // rows no one sees lie before the first and after the last one that is seen
+                clear_rows<NH>(at, 0, it.lo - k0);
+                clear_rows<NH>(at, it.end - k0, kTile);
+                if (bad)
+                    for (int g = 0; g < 16; ++g)
+                        if (bad >> g & 1u) clear_rows<NH>(at, 8 * g, 8 * g + 8);
+                if (mixed) {
+                    if (lane < 4) sh.odd[v % kBadRing][lane] = 0;
+                    __syncwarp();
+                    const int32_t lo = max(0, it.lo - k0), hi = min(kTile, it.end - k0);
+                    scan_rows<K, NH>(at, lo, min(hi, mixed_lo - k0), bad, sh.odd[v % kBadRing]);
+                    scan_rows<K, NH>(at, max(lo, mixed_hi - k0), hi, bad, sh.odd[v % kBadRing]);
                 }
                 fence_async();
             }
-            if (lane == 0) {
-                sh.odd[ring][2 * half] = odd[0];
-                sh.odd[ring][2 * half + 1] = odd[1];
-            }
             __syncwarp();
-            if (lane == 0) bar_arrive(smem_u32(&sh.value[v % P.slots]));
+            if (lane == 0) bar_arrive(smem_u32(&sh.value[ring.i]));
         }
     }
 }
 
 template <int K, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_attend(const __grid_constant__ Params P, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
+    k_attend(const __grid_constant__ Params P, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
+             const __grid_constant__ CUtensorMap qm) {
     constexpr int NH = K == kE4m3 ? 1 : DP / 64;
-    extern __shared__ char raw[];
-    __shared__ Shared sh;
-    const uint32_t q_smem = (smem_u32(raw) + 1023u) & ~1023u;
-    const uint32_t kv_smem = q_smem + P.q_tiles * (K == kE4m3 ? 2 : NH) * kHalf;
+    extern __shared__ __align__(1024) char raw[];
+    const uint32_t q_smem = smem_u32(raw), k_smem = q_smem + P.q_tiles * (K == kE4m3 ? 2 : NH) * kHalf,
+                   v_smem = k_smem + P.k_slots * NH * kHalf;
+    Shared& sh = *reinterpret_cast<Shared*>(raw + (v_smem - q_smem) + P.v_slots * NH * kHalf);
+    if (q_smem & 1023u) {  // the tiles' swizzle counts on it
+        if (threadIdx.x == 0) report(P.a.status, 1u << SV_ERR_CUDA);
+        return;
+    }
     const int tid = threadIdx.x, w = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;");
     if (tid == 0) {
         for (int i = 0; i < kMaxSlots; ++i) {
-            bar_init(smem_u32(&sh.full[i]), 1);
-            bar_init(smem_u32(&sh.empty[i]), 1);
-            bar_init(smem_u32(&sh.value[i]), 2);
+            bar_init(smem_u32(&sh.k_full[i]), 1);
+            bar_init(smem_u32(&sh.k_empty[i]), 1);
+            bar_init(smem_u32(&sh.v_full[i]), 1);
+            bar_init(smem_u32(&sh.v_empty[i]), 1);
+            bar_init(smem_u32(&sh.value[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_u32(&sh.s_full[i]), 1);
             bar_init(smem_u32(&sh.p_ready[i]), 4);
             bar_init(smem_u32(&sh.pv_done[i]), 1);
         }
-        bar_init(smem_u32(&sh.q_full), 8);
+        bar_init(smem_u32(&sh.q_in), 1);
+        bar_init(smem_u32(&sh.q_full), 1);
         bar_init(smem_u32(&sh.q_empty), 1);
         bar_init(smem_u32(&sh.meet), 8);
         bar_init(smem_u32(&sh.part), 8);
@@ -1066,36 +1219,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (w == 9)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
-    // sequences that fail: their findings, and zeros in their rows
-    for (int32_t b = blockIdx.x; b < P.a.chunk.B; b += gridDim.x) {
-        const Seq s = checked_seq(P, b);
-        if (!s.err) continue;
-        if (tid == 0) report(P.a.status, s.err);
-        if (!s.rows_ok) continue;
-        const int64_t row = (int64_t)P.a.q_heads * P.a.pool.dim / 8;
-        uint4* out = (uint4*)P.a.out + s.row0 * row;
-        for (int64_t i = tid; i < s.T * row; i += kThreads) out[i] = make_uint4(0, 0, 0, 0);
-        if (P.a.lse)
-            for (int64_t i = tid; i < (int64_t)s.T * P.a.q_heads; i += kThreads)
-                P.a.lse[(int64_t)s.row0 * P.a.q_heads + i] = -INFINITY;
-    }
+    plan(P, sh);
     if (blockIdx.x == 0 && tid == 0) {
         const int64_t end = (int64_t)P.a.chunk.offs[P.a.chunk.B] + P.a.chunk.B;
         if (end > P.a.chunk.rows || P.a.chunk.offs[0] != 0) report(P.a.status, 1u << SV_ERR_BAD_OFFSETS);
     }
-    plan(P, sh);
     tc_before();
     __syncthreads();
     tc_after();
-    if (w < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        softmax_role<K, DP>(P, sh, q_smem);
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        if (w == 8) load_role<NH>(P, sh, kv_smem, &km, &vm);
-        else if (w == 9) product_role<K, NH>(P, sh, q_smem, kv_smem);
-        else value_role<K, NH>(P, sh, kv_smem);
-    }
+    // sequences that fail: their findings, and zeros in their rows
+    if (sh.failing)
+        for (int32_t b = blockIdx.x; b < P.a.chunk.B; b += gridDim.x) {
+            const Seq s = checked_seq(P, b);
+            if (!s.err) continue;
+            if (tid == 0) report(P.a.status, s.err);
+            if (!s.rows_ok) continue;
+            const int64_t row = (int64_t)P.a.q_heads * P.a.pool.dim / 8;
+            uint4* out = (uint4*)P.a.out + s.row0 * row;
+            for (int64_t i = tid; i < s.T * row; i += kThreads) out[i] = make_uint4(0, 0, 0, 0);
+            if (P.a.lse)
+                for (int64_t i = tid; i < (int64_t)s.T * P.a.q_heads; i += kThreads)
+                    P.a.lse[(int64_t)s.row0 * P.a.q_heads + i] = -INFINITY;
+        }
+    if (w < 8) softmax_role<K, DP>(P, sh);
+    else if (w == 8) load_role<NH>(P, sh, k_smem, &km, 0);
+    else if (w == 9) product_role<K, NH>(P, sh, q_smem, k_smem, v_smem);
+    else if (w == 10) load_role<NH>(P, sh, v_smem, &vm, 1);
+    else value_role<K, NH>(P, sh, q_smem, v_smem, &qm);
     tc_before();
     __syncthreads();
     tc_after();
@@ -1194,6 +1344,17 @@ bool encode(CUtensorMap* m, const Pool& p, char* base, int esize, int kind, int 
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries as (dim, head, row), copied in boxes of 128 bytes by the heads of a group by q_box rows.
+bool encode_queries(CUtensorMap* m, const AttendArgs& A, int kind, int G, int q_box) {
+    const cuuint64_t dims[3] = {(cuuint64_t)A.pool.dim, (cuuint64_t)A.q_heads, (cuuint64_t)A.chunk.rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)A.pool.dim * 2, (cuuint64_t)A.q_stride * 2};
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)G, (cuuint32_t)q_box}, ones[3] = {1, 1, 1};
+    return encoder()(m, kind == kFp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                     const_cast<void*>(A.q), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int K, int DP>
 cudaError_t launch(const AttendArgs& A, cudaStream_t st) {
     constexpr int NH = K == kE4m3 ? 1 : DP / 64, q_bytes = (K == kE4m3 ? 2 : NH) * kHalf;
@@ -1202,7 +1363,10 @@ cudaError_t launch(const AttendArgs& A, cudaStream_t st) {
     P.G = A.q_heads / A.pool.heads;
     P.tokens = kTile / P.G;
     P.q_tiles = A.chunk.max_gamma + 1 > P.tokens ? 2 : 1;
-    P.slots = min(kMaxSlots, (kSmem - 1024 - (int)sizeof(Shared) - P.q_tiles * q_bytes) / (NH * kHalf));
+    P.q_box = min(P.tokens, A.chunk.max_gamma + 1);
+    const int slots = min(2 * kMaxSlots, (kSmem - shared_bytes<K>() - P.q_tiles * q_bytes) / (NH * kHalf));
+    P.k_slots = slots / 2;
+    P.v_slots = slots - P.k_slots;
     P.box = kTile;
     while (A.pool.page_size % P.box) P.box /= 2;
     char* ws = (char*)A.workspace;
@@ -1215,13 +1379,14 @@ cudaError_t launch(const AttendArgs& A, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int n = min(sms, kMaxCtas);
     if (!encoder()) return cudaErrorNotSupported;
-    CUtensorMap km, vm;
+    CUtensorMap km, vm, qm;
+    if (K != kE4m3 && !encode_queries(&qm, A, K, P.G, P.q_box)) return cudaErrorInvalidValue;
     if (!encode(&km, A.pool, A.pool.k, KindOf<K>::kBytes, K, P.box) || !encode(&vm, A.pool, A.pool.v, KindOf<K>::kBytes, K, P.box))
         return cudaErrorInvalidValue;
-    const int smem = 1024 + P.q_tiles * q_bytes + P.slots * NH * kHalf;
-    e = cudaFuncSetAttribute(k_attend<K, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem - (int)sizeof(Shared));
+    const int smem = P.q_tiles * q_bytes + slots * NH * kHalf + shared_bytes<K>();
+    e = cudaFuncSetAttribute(k_attend<K, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    k_attend<K, DP><<<n, kThreads, smem, st>>>(P, km, vm);
+    k_attend<K, DP><<<n, kThreads, smem, st>>>(P, km, vm, qm);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
