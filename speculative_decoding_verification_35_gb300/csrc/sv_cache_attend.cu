@@ -29,11 +29,12 @@ namespace sv {
 namespace cache {
 namespace {
 
-constexpr int kThreads = 384;   // two softmax warpgroups, then warps for loads, products and value tiles
+constexpr int kThreads = 512;   // two softmax warpgroups, then a warp for each other role
 constexpr int kTile = 128;      // slots of a tile, and rows of a query tile
 constexpr int kMaxSlots = 6;    // key tiles in flight, and value tiles
 constexpr int kBadRing = 16;
 constexpr int kMaxCtas = 160;
+constexpr int kItems = 4;       // items that are known ahead
 constexpr int kHalf = kTile * 128;  // bytes of 128 rows of 128 bytes, the unit of an operand in shared memory
 constexpr int kSmem = 227 * 1024;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -108,37 +109,29 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// True once the phase is over; may sleep for it, half a microsecond at most.
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "n"(500)
         : "memory");
     return ok;
 }
-__device__ __forceinline__ unsigned long long now_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-// A whole warp waits; false once the CTA has given up (after two seconds without the phase).
+// A whole warp waits; false once the CTA has given up (a wait of at least a tenth of a second and a few at most).
+constexpr uint32_t kPolls = 1u << 24;
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
     bool ok = bar_try(bar, parity);
-    if (!__all_sync(kAll, ok)) {
-        unsigned long long t0 = 0;
-        for (uint32_t i = 1; !ok; ++i) {
-            ok = bar_try(bar, parity);
-            if (!ok && (i & 63u) == 0) {
-                const unsigned long long t = now_ns();
-                if (!t0) t0 = t;
-                if (t - t0 > 2000000000ull) *gave_up = 1;
-                if (*gave_up) break;
-            }
+#pragma unroll 1
+    for (uint32_t i = 1; !__all_sync(kAll, ok); ++i) {
+        if (!ok) ok = bar_try(bar, parity);
+        if ((i & 255u) == 0) {
+            if (i >= kPolls) *gave_up = 1;
+            if (__any_sync(kAll, *gave_up)) return false;
         }
-        ok = __all_sync(kAll, ok);
     }
-    return ok;
+    return true;
 }
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int d, int token, int head, int page,
                                          uint32_t bar) {
@@ -255,14 +248,16 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t u) {
 // ---------------------------------------------------------------------------------------------------------
 // work items
 // ---------------------------------------------------------------------------------------------------------
-struct Item {
-    int32_t b, h, row0;       // sequence, key head, the sequence's first row
-    int32_t t0, nt;           // its chunk tokens
+struct alignas(16) Item {
+    int32_t b, h, row0;           // sequence, key head, the sequence's first row
+    int32_t t0, nt;               // its chunk tokens
     int32_t past;
-    int32_t lo, end;          // the slots [lo, end) that some row of it sees
-    int32_t tile, n;          // the CTA's tiles: the first (absolute), how many
-    bool two;                 // 129 to 256 rows: a query tile per stream
-    bool begins, finishes;    // its first and last tiles are among the CTA's
+    int32_t lo, end;              // the slots [lo, end) that some row of it sees
+    int32_t tile, n;              // the CTA's tiles: the first (absolute), how many; 0: no more items
+    int32_t mixed_lo, mixed_hi;   // slots below mixed_lo and from mixed_hi on are seen by some of its rows only
+    int32_t two;                  // 129 to 256 rows: a query tile per stream
+    int32_t begins, finishes;     // its first and last tiles are among the CTA's
+    int32_t pad;
 };
 
 __device__ __forceinline__ void span(const Params& P, int32_t T, int32_t past, int32_t p, Item& it, int32_t& first,
@@ -286,6 +281,7 @@ __device__ __forceinline__ void span(const Params& P, int32_t T, int32_t past, i
 __device__ __forceinline__ bool tree_ok(const Chunk& c, int32_t b, int32_t T) {
     const int32_t* par = c.parents + c.offs[b];
     bool ok = true;
+#pragma unroll 4
     for (int j = 1; j < T; ++j) ok &= (uint32_t)par[j - 1] < (uint32_t)j;
     return ok;
 }
@@ -300,6 +296,7 @@ __device__ __forceinline__ Seq checked_seq(const Params& P, int32_t b) {
 __device__ __forceinline__ void size_of(const Params& P, const Seq& s, long long& tiles, long long& blocks) {
     tiles = blocks = 0;
     if (s.err) return;
+#pragma unroll 1
     for (int32_t p = 0; p * 2 * P.tokens < s.T; ++p) {
         Item it;
         int32_t first, count;
@@ -317,60 +314,13 @@ struct Start {
     long long left;
 };
 
-// The items of a CTA, one after the other. Every warp walks by itself.
-struct Walk {
-    const Params& P;
-    int32_t b, p, h, x, T, past, row0;
-    const int32_t lead;
-    long long left;
-    __device__ Walk(const Params& P_, const Start& s)
-        : P(P_), b(s.b), p(s.p), h(s.h), x(s.x), T(s.T), past(s.past), row0(s.row0), lead(s.lead), left(s.left) {}
-    __device__ bool next(Item& it) {
-        if (left <= 0) return false;
-        if (T < 0) {  // past the last sequence
-            for (; b < P.a.chunk.B; ++b) {
-                const Seq s = checked_seq(P, b);
-                if (!s.err) {
-                    T = s.T;
-                    past = s.past;
-                    row0 = s.row0;
-                    break;
-                }
-            }
-            if (T < 0) return false;
-        }
-        left -= max(0, lead - x);
-        if (left <= 0) return false;
-        int32_t first, count;
-        span(P, T, past, p, it, first, count);
-        const int32_t j = max(0, x - lead);
-        it.b = b;
-        it.h = h;
-        it.row0 = row0;
-        it.tile = first + j;
-        it.begins = j == 0;
-        it.n = (int32_t)min((long long)(count - j), left);
-        it.finishes = j + it.n == count;
-        left -= it.n;
-        x = 0;
-        if (++h == P.a.pool.heads) {
-            h = 0;
-            ++p;
-            if (p * 2 * P.tokens >= T) {
-                p = 0;
-                ++b;
-                T = -1;
-            }
-        }
-        return true;
-    }
-};
-
 struct Shared {  // behind the operand tiles
     uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
     uint64_t value[kMaxSlots];  // a value tile is in and clean
     uint64_t s_full[2], p_ready[2], pv_done[2];
     uint64_t q_in, q_full, q_empty, meet, part, drain;
+    uint64_t item_full[kItems], item_empty[kItems];
+    Item item[kItems];
     uint32_t tmem;
     int gave_up;
     Start start;
@@ -399,6 +349,7 @@ __device__ __forceinline__ void plan(const Params& P, Shared& sh) {
         if (c > 0) P.records[c].parts = 0;
     }
     bool fails = false;
+#pragma unroll 1
     for (int32_t b = tid; b < B; b += kThreads) {
         const Seq s = checked_seq(P, b);
         long long t, n;
@@ -435,6 +386,7 @@ __device__ __forceinline__ void plan(const Params& P, Shared& sh) {
     if (c >= n) return;  // the same for the whole CTA
     const long long u0 = W * c / n, u1 = W * (c + 1) / n;
     long long base = 0;
+#pragma unroll 1
     for (int32_t b0 = 0; b0 < B && base <= u0; b0 += kThreads) {
         const int32_t b = b0 + tid;
         if (b0 > 0) {
@@ -463,6 +415,7 @@ __device__ __forceinline__ void plan(const Params& P, Shared& sh) {
             long long rest = u0 - begin;
             Item it;
             int32_t first, count, p = 0;
+#pragma unroll 1
             for (;; ++p) {
                 span(P, mine.T, mine.past, p, it, first, count);
                 const long long block = (long long)(count + lead) * heads;
@@ -492,6 +445,82 @@ __device__ __forceinline__ void plan(const Params& P, Shared& sh) {
 // ---------------------------------------------------------------------------------------------------------
 // the softmax warpgroups
 // ---------------------------------------------------------------------------------------------------------
+// The CTA's items, one after the other, by one warp; a last one of no tiles ends them.
+__device__ __forceinline__ void item_role(const Params& P, Shared& sh) {
+    const int lane = threadIdx.x & 31;
+    const bool tree = P.a.chunk.parents != nullptr;
+    const int32_t lead = sh.start.lead;
+    int32_t b = sh.start.b, p = sh.start.p, h = sh.start.h, x = sh.start.x;
+    int32_t T = sh.start.T, past = sh.start.past, row0 = sh.start.row0;
+    long long left = sh.start.left;
+    Ring ring;
+#pragma unroll 1
+    for (uint32_t i = 0;; ++i, ring.step(kItems)) {
+        Item it{};
+        left -= max(0, lead - x);
+        if (left > 0 && T < 0) {  // the next sequence
+#pragma unroll 1
+            for (; b < P.a.chunk.B; ++b) {
+                const Seq s = checked_seq(P, b);
+                if (!s.err) {
+                    T = s.T;
+                    past = s.past;
+                    row0 = s.row0;
+                    break;
+                }
+            }
+        }
+        if (left > 0 && T > 0) {
+            int32_t first, count;
+            span(P, T, past, p, it, first, count);
+            const int32_t j = max(0, x - lead);
+            it.b = b;
+            it.h = h;
+            it.row0 = row0;
+            it.tile = first + j;
+            it.begins = j == 0;
+            it.n = (int32_t)min((long long)(count - j), left);
+            it.finishes = j + it.n == count;
+            it.mixed_hi = past + (tree ? 0 : it.t0 + 1);
+            it.mixed_lo = P.a.window > 0 && (tree || it.nt > 1) ? it.lo + it.nt + (tree ? it.t0 : 0) : 0;
+            left -= it.n;
+            x = 0;
+            if (++h == P.a.pool.heads) {
+                h = 0;
+                ++p;
+                if (p * 2 * P.tokens >= T) {
+                    p = 0;
+                    ++b;
+                    T = -1;
+                }
+            }
+        }
+        if (i >= kItems && !wait(smem_u32(&sh.item_empty[ring.i]), ring.parity ^ 1, &sh.gave_up)) return;
+        if (lane == 0) {
+            sh.item[ring.i] = it;
+            bar_arrive(smem_u32(&sh.item_full[ring.i]));
+        }
+        __syncwarp();
+        if (it.n == 0) return;
+    }
+}
+
+// A role's view of the items.
+struct Items {
+    Shared& sh;
+    Ring ring;
+    __device__ __forceinline__ Items(Shared& s) : sh(s) {}
+    __device__ __forceinline__ bool next(Item& it) {
+        if (!wait(smem_u32(&sh.item_full[ring.i]), ring.parity, &sh.gave_up)) return false;
+        it = sh.item[ring.i];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) bar_arrive(smem_u32(&sh.item_empty[ring.i]));
+        ring.step(kItems);
+        return it.n > 0;
+    }
+};
+constexpr int kItemReaders = 8 + 2 + 2 + 1;
+
 // A row of a query tile as its thread knows it.
 struct Row {
     bool real;
@@ -509,6 +538,19 @@ __device__ __forceinline__ float score_unit(const AttendArgs& A, int32_t h, bool
     return fmaxf(fabsf(sl), 1e-30f);
 }
 
+// The nodes that a tree's node t sees (itself and those above it, as far as the window reaches), and its depth.
+__device__ __forceinline__ uint32_t lineage(const int32_t* par, int32_t t, int32_t window, int32_t& depth) {
+    uint32_t above = 0;
+    int32_t d = 0;
+#pragma unroll 1
+    for (;; t = par[t - 1], ++d) {
+        if (window <= 0 || d < window) above |= 1u << t;
+        if (t == 0) break;
+    }
+    depth = d;
+    return above;
+}
+
 // tl: the row's token within its tile.
 __device__ __forceinline__ Row row_of(const Params& P, const Item& it, int stream, int32_t tl) {
     const AttendArgs& A = P.a;
@@ -519,13 +561,7 @@ __device__ __forceinline__ Row row_of(const Params& P, const Item& it, int strea
     int32_t depth = row.token;
     if (A.chunk.parents) {
         const int32_t* par = A.chunk.parents + (it.row0 - it.b);
-        depth = -1;
-        if (row.real)
-            for (int32_t t = row.token;; t = par[t - 1]) {
-                ++depth;
-                if (A.window <= 0 || depth < A.window) row.above |= 1u << t;
-                if (t == 0) break;
-            }
+        if (row.real) row.above = lineage(par, row.token, A.window, depth);
     }
     const int32_t pos = it.past + depth;
     row.low = A.window > 0 ? max(0, pos - A.window + 1) : 0;
@@ -563,15 +599,125 @@ __device__ __forceinline__ void hide(uint32_t* s, uint32_t seen) {
         if (!(seen >> i & 1u)) s[i] = 0xff800000u;
 }
 
-// Slots of the item that some of its rows see and others do not: those below lo and those from hi on. Only there
-// can a value meet a weight of zero, and a NaN or infinity be carried into a row that does not see it.
-__device__ __forceinline__ void mixed_slots(const Params& P, const Item& it, int32_t& lo, int32_t& hi) {
-    const bool tree = P.a.chunk.parents != nullptr;
-    hi = it.past + (tree ? 0 : it.t0 + 1);
-    lo = P.a.window > 0 && (tree || it.nt > 1) ? it.lo + it.nt + (tree ? it.t0 : 0) : 0;
+// Only among slots that some rows of the item see and others do not can a value meet a weight of zero, and a NaN
+// or infinity be carried into a row that does not see it.
+__device__ __forceinline__ bool mixed_tile(const Item& it, int32_t k0) {
+    return k0 < it.mixed_lo || max(k0, it.mixed_hi) < min(k0 + kTile, it.end);
 }
-__device__ __forceinline__ bool mixed_tile(const Item& it, int32_t k0, int32_t lo, int32_t hi) {
-    return k0 < lo || max(k0, hi) < min(k0 + kTile, it.end);
+
+// Adds the non-finite values of the slots in odd that a row sees (and its product met as zero) to its output.
+template <int K, int DP>
+__device__ __forceinline__ void add_odd(const AttendArgs& A, const Item& it, uint32_t o_col, int32_t k0, const uint32_t* odd,
+                                     const uint32_t* seen) {
+    using T = typename KindOf<K>::T;
+#pragma unroll 1
+    for (int c = 0; c < DP; c += 32) {
+        uint32_t o[32];
+        tc_ld32(o_col + c, o);
+        tc_wait_ld();
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i)
+            for (uint32_t w = odd[i] & seen[i]; w; w &= w - 1) {
+                const int32_t slot = k0 + 32 * i + __ffs(w) - 1;
+                const int64_t at = place_of(A.pool, it.b, slot) + it.h * A.pool.s_head;
+#pragma unroll
+                for (int d = 0; d < 32; ++d) {
+                    float x = 0.f;
+                    if (c + d < A.pool.dim) {
+                        if (K == kE4m3) x = (((const uint8_t*)A.pool.v)[at + c + d] & 0x7f) == 0x7f ? NAN : 0.f;
+                        else x = (float)((const T*)A.pool.v)[at + c + d];
+                    }
+                    if (!isfinite(x)) o[d] = __float_as_uint(__uint_as_float(o[d]) + x);
+                }
+            }
+        tc_st32(o_col + c, o);
+    }
+}
+
+// A step: the tile's maximum, then its weights in place of its scores (and their sum). The scores are read from
+// tensor memory twice, which is cheaper than the registers it takes to keep them, and the loops are rolled: unrolled,
+// the roles' code misses the instruction cache in every step (measured: 1500 cycles a step, 2200 unrolled).
+__device__ __forceinline__ float tile_max(uint32_t s_col, bool masked, const uint32_t* seen) {
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+    for (int q = 0; q < 4; q += 2) {
+        uint32_t s[2][32];
+        tc_ld32(s_col + 32 * q, s[0]);
+        tc_ld32(s_col + 32 * q + 32, s[1]);
+        tc_wait_ld();
+        if (masked) {
+            hide(s[0], q ? seen[2] : seen[0]);
+            hide(s[1], q ? seen[3] : seen[1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                top[e] = fmaxf(top[e], fmaxf(__uint_as_float(s[0][i + e]), __uint_as_float(s[1][i + e])));
+    }
+    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+template <int K>
+__device__ __forceinline__ void weights32(uint32_t* x, F2 sl2, F2 off2, F2* sum, uint32_t* pk) {
+    using T = typename KindOf<K>::T;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            unpack2(fma2(pack2(__uint_as_float(x[i + e]), __uint_as_float(x[i + e + 1])), sl2, off2), p[e], p[e + 1]);
+            p[e] = exp2_fast(p[e]);
+            p[e + 1] = exp2_fast(p[e + 1]);
+            sum[e >> 1] = add2(sum[e >> 1], pack2(p[e], p[e + 1]));
+        }
+        if (K != kE4m3) {
+            pk[i >> 1] = from_float2<T>(p[0], p[1]);
+            pk[(i >> 1) + 1] = from_float2<T>(p[2], p[3]);
+        } else {
+            const uint32_t a = e4m3x2(p[0], p[1]), b = e4m3x2(p[2], p[3]);
+            const float2 u = from_e4m3x2(a), w = from_e4m3x2(b);
+            pk[i >> 2] = a | b << 16;
+            pk[8 + (i >> 2)] = e4m3x2(p[0] - u.x, p[1] - u.y) | e4m3x2(p[2] - w.x, p[3] - w.y) << 16;
+        }
+    }
+}
+template <int K>
+__device__ __forceinline__ float tile_weights(uint32_t s_col, bool masked, const uint32_t* seen, float sl, float off) {
+    const F2 sl2 = pack2(sl, sl), off2 = pack2(off, off);
+    F2 sum[2] = {0, 0};
+    uint32_t s[2][32];
+    tc_ld32(s_col, s[0]);
+#pragma unroll 1
+    for (int q = 0; q < 4; q += 2) {
+        uint32_t pk[16];
+        tc_wait_ld();
+        tc_ld32(s_col + 32 * q + 32, s[1]);
+        if (masked) hide(s[0], q ? seen[2] : seen[0]);
+        weights32<K>(s[0], sl2, off2, sum, pk);
+        tc_st16(s_col + 16 * q, pk);
+        tc_wait_ld();
+        tc_ld32(s_col + (q ? 96 : 64), s[0]);  // the last one is read for nothing
+        if (masked) hide(s[1], q ? seen[3] : seen[1]);
+        weights32<K>(s[1], sl2, off2, sum, pk);
+        tc_st16(s_col + 16 * q + 16, pk);
+    }
+    tc_wait_ld();
+    float a, b;
+    unpack2(add2(sum[0], sum[1]), a, b);
+    return a + b;
+}
+// O times f, a factor per row.
+template <int DP>
+__device__ __forceinline__ void rescale(uint32_t o_col, float f) {
+#pragma unroll 1
+    for (int c = 0; c < DP; c += 32) {
+        uint32_t o[32];
+        tc_ld32(o_col + c, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tc_st32(o_col + c, o);
+    }
 }
 
 template <int K, int DP>
@@ -593,16 +739,16 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
     uint32_t tiles = 0;   // of the CTA, before this item
     uint32_t items = 0, merges = 0;
 
-    Walk walk(P, sh.start);
+    Items walk(sh);
     Item it;
+#pragma unroll 1
     for (; walk.next(it); ++items) {
         Row row = row_of(P, it, stream, tl);
         float m = -INFINITY, l = 0.f;
         const bool busy = __any_sync(kAll, row.real);
         const int32_t first = it.two ? 0 : stream, by = it.two ? 1 : 2;
         uint32_t done = 0;
-        int32_t mixed_lo, mixed_hi;
-        mixed_slots(P, it, mixed_lo, mixed_hi);
+#pragma unroll 1
         for (int32_t j = first; j < it.n; j += by, ++done, ++steps) {
             if (!wait(s_full, steps & 1, gave_up)) return;
             tc_after();
@@ -616,26 +762,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
                 const bool whole = (k0 + kTile <= row.limit && row.low <= k0 && !bad) || !row.real;
                 const bool masked = !__all_sync(kAll, whole);
                 if (masked) seen_of(row, it, k0, bad, tree, seen);
-                uint32_t s[2][32];
-                // the tile's maximum
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    tc_ld32(s_col + 32 * q, s[0]);
-                    tc_ld32(s_col + 32 * q + 32, s[1]);
-                    tc_wait_ld();
-                    if (masked) {
-                        hide(s[0], seen[q]);
-                        hide(s[1], seen[q + 1]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            top[e] = fmaxf(top[e], fmaxf(__uint_as_float(s[0][i + e]), __uint_as_float(s[1][i + e])));
-                }
-                tc_ld32(s_col, s[0]);
-                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                const float mx = tile_max(s_col, masked, seen);
                 const bool move = row.real && ((mx - m) * row.sl > KT::kSlack || (m == -INFINITY && mx > m));
                 if (__any_sync(kAll, move)) {
                     const float old = m;
@@ -645,56 +772,14 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
                     if (__any_sync(kAll, move && old != -INFINITY)) {
                         if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
                         tc_after();
-                        tc_wait_ld();
-                        for (int c = 0; c < DP; c += 32) {
-                            tc_ld32(o_col[stream] + c, s[1]);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) s[1][i] = __float_as_uint(__uint_as_float(s[1][i]) * f);
-                            tc_st32(o_col[stream] + c, s[1]);
-                        }
+                        rescale<DP>(o_col[stream], f);
                     }
                 }
-                // its weights, in place of the scores
                 const float off = KT::kShift - (m == -INFINITY ? 0.f : m * row.sl);
-                const F2 sl2 = pack2(row.sl, row.sl), off2 = pack2(off, off);
-                F2 sum[2] = {0, 0};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    tc_wait_ld();
-                    uint32_t* x = s[q & 1];
-                    if (q < 3) tc_ld32(s_col + 32 * q + 32, s[(q + 1) & 1]);
-                    if (masked) hide(x, seen[q]);
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        float p[4];
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            unpack2(fma2(pack2(__uint_as_float(x[i + e]), __uint_as_float(x[i + e + 1])), sl2, off2), p[e],
-                                    p[e + 1]);
-                            p[e] = exp2_fast(p[e]);
-                            p[e + 1] = exp2_fast(p[e + 1]);
-                            sum[e >> 1] = add2(sum[e >> 1], pack2(p[e], p[e + 1]));
-                        }
-                        if (K != kE4m3) {
-                            pk[i >> 1] = from_float2<T>(p[0], p[1]);
-                            pk[(i >> 1) + 1] = from_float2<T>(p[2], p[3]);
-                        } else {
-                            const uint32_t a = e4m3x2(p[0], p[1]), b = e4m3x2(p[2], p[3]);
-                            const float2 u = from_e4m3x2(a), w = from_e4m3x2(b);
-                            pk[i >> 2] = a | b << 16;
-                            pk[8 + (i >> 2)] = e4m3x2(p[0] - u.x, p[1] - u.y) | e4m3x2(p[2] - w.x, p[3] - w.y) << 16;
-                        }
-                    }
-                    tc_st16(s_col + 16 * q, pk);
-                }
-                float a, b;
-                unpack2(add2(sum[0], sum[1]), a, b);
-                l += a + b;
+                l += tile_weights<K>(s_col, masked, seen, row.sl, off);
                 tc_wait_st();
             }
-            const bool mixed = mixed_tile(it, k0, mixed_lo, mixed_hi);
+            const bool mixed = mixed_tile(it, k0);
             if (mixed) {  // before p_ready: the tile cannot be released, nor its barrier move on, until then
                 const uint32_t v = tiles + j;
                 if (!wait(smem_u32(&sh.value[v % P.v_slots]), (v / P.v_slots) & 1, gave_up)) return;
@@ -704,36 +789,14 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
             if (lane == 0) bar_arrive(p_ready);
             if (mixed) {
                 // rows that see a non-finite value, which the product met as zero, get it added here
+                const uint32_t none[4] = {0, 0, 0, 0};
                 uint32_t odd[4], any = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) any |= odd[i] = sh.odd[ring][i];
                 if (any && busy) {
                     if (!wait(pv_done, steps & 1, gave_up)) return;
                     tc_after();
-                    for (int c = 0; c < DP; c += 32) {
-                        uint32_t o[32];
-                        tc_ld32(o_col[stream] + c, o);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            for (uint32_t w = row.real ? odd[i] & seen[i] : 0u; w; w &= w - 1) {
-                                const int32_t slot = k0 + 32 * i + __ffs(w) - 1;
-                                const int64_t at = place_of(A.pool, it.b, slot) + it.h * A.pool.s_head;
-#pragma unroll
-                                for (int d = 0; d < 32; ++d) {
-                                    if (c + d >= D) break;
-                                    float x;
-                                    if (K == kE4m3) {
-                                        const uint8_t u = ((const uint8_t*)A.pool.v)[at + c + d];
-                                        x = (u & 0x7f) == 0x7f ? NAN : 0.f;
-                                    } else {
-                                        x = (float)((const T*)A.pool.v)[at + c + d];
-                                    }
-                                    if (!isfinite(x)) o[d] = __float_as_uint(__uint_as_float(o[d]) + x);
-                                }
-                            }
-                        tc_st32(o_col[stream] + c, o);
-                    }
+                    add_odd<K, DP>(A, it, o_col[stream], k0, row.real ? odd : none, seen);
                     tc_wait_st();
                     tc_before();
                 }
@@ -773,6 +836,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
         const int c_begin = it.two ? 0 : stream * (DP / 2), c_end = it.two ? DP : c_begin + DP / 2;
         const size_t prow = (size_t)(2 * blockIdx.x + (it.begins ? 1 : 0)) * 256 + (it.two && stream ? kTile : 0) + r;
         if (busy) {
+#pragma unroll 1
             for (int c = c_begin; c < c_end; c += 32) {
                 uint32_t o[32];
                 tc_ld32(it.two ? o_col[stream] + c : o_col[0] + c, o);
@@ -838,12 +902,14 @@ __device__ __forceinline__ void load_role(const Params& P, Shared& sh, uint32_t 
     const int32_t box = P.box, boxes = kTile / box, ps = P.a.pool.page_size;
     const uint32_t full = smem_u32(kv ? sh.v_full : sh.k_full), empty = smem_u32(kv ? sh.v_empty : sh.k_empty);
     const uint32_t slots = kv ? P.v_slots : P.k_slots;
+    const bool leader = elect();
     volatile int* gave_up = &sh.gave_up;
     uint32_t tile = 0;
     Ring ring;
     bool ok = true;
-    Walk walk(P, sh.start);
+    Items walk(sh);
     Item it;
+#pragma unroll 1
     while (ok && walk.next(it)) {
         const int32_t* table = P.a.pool.table + (int64_t)it.b * P.a.pool.table_stride;
         // where a lane's box of a tile lies; read a tile ahead
@@ -861,6 +927,7 @@ __device__ __forceinline__ void load_role(const Params& P, Shared& sh, uint32_t 
         bool next_need;
         int32_t next_page, next_at;
         look(0, next_need, next_page, next_at);
+#pragma unroll 1
         for (int32_t j = 0; j < it.n; ++j, ++tile, ring.step(slots)) {
             bool need = next_need;
             const int32_t page = next_page, at = next_at;
@@ -886,23 +953,32 @@ __device__ __forceinline__ void load_role(const Params& P, Shared& sh, uint32_t 
                 bar_expect(bar, bytes);
             }
             __syncwarp();
-            if (need) {
-                const uint32_t dst = smem + ring.i * (NH * kHalf) + lane * box * 128;
+            const uint32_t dst = smem + ring.i * (NH * kHalf), todo = __ballot_sync(kAll, need);
+            const int32_t head = __shfl_sync(kAll, it.h, 0);
+#pragma unroll 1
+            for (int i = 0; i < boxes; ++i) {  // one thread issues: from many, each copy would wait for the last
+                const int32_t p = __shfl_sync(kAll, page, i), a = __shfl_sync(kAll, at, i);
+                if (leader && (todo >> i & 1u)) {
 #pragma unroll
-                for (int h = 0; h < NH; ++h) copy_box(dst + h * kHalf, map, h * 64, at, it.h, page, bar);
+                    for (int h = 0; h < NH; ++h) copy_box(dst + i * box * 128 + h * kHalf, map, h * 64, a, head, p, bar);
+                }
             }
             __syncwarp();
         }
     }
     // copies still under way land before the CTA ends, also where another role gave up
+#pragma unroll 1
     for (uint32_t i = tile > slots ? tile - slots : 0; i < tile; ++i) {
         int none = 0;
         wait(full + 8 * (i % slots), (i / slots) & 1, &none);
     }
 }
 
+// A stream's products, by one thread: S = Q K^T of its next tile follows O += P V of this one, whose P lies where that
+// S will. Tiles of the other stream's alone are passed on.
 template <int K, int NH>
-__device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem) {
+__device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem,
+                                             const uint32_t st) {
     constexpr bool k8 = K == kE4m3;
     constexpr int parts = k8 ? 2 : 1, slot_bytes = NH * kHalf, steps_max = k8 ? 4 : 4 * NH;
     constexpr uint32_t fmt = K == kBf16 ? 1u : 0u;
@@ -916,73 +992,82 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
     constexpr uint32_t q_bytes = (k8 ? 2 : NH) * kHalf;
     constexpr uint32_t dp = NH == 1 && !k8 ? 64 : 128;
     const uint32_t tmem = __shfl_sync(kAll, sh.tmem, 0);
+    const uint32_t s_at = tmem + st * kTile, o_at = tmem + 256 + st * dp;
     const uint32_t k_full = smem_u32(sh.k_full), k_empty = smem_u32(sh.k_empty), v_empty = smem_u32(sh.v_empty),
-                   value = smem_u32(sh.value), s_full = smem_u32(sh.s_full), p_ready = smem_u32(sh.p_ready),
-                   pv_done = smem_u32(sh.pv_done), q_empty = smem_u32(&sh.q_empty);
+                   value = smem_u32(sh.value), s_full = smem_u32(&sh.s_full[st]), p_ready = smem_u32(&sh.p_ready[st]),
+                   pv_done = smem_u32(&sh.pv_done[st]), q_empty = smem_u32(&sh.q_empty);
     const bool leader = elect();
     volatile int* gave_up = &sh.gave_up;
-    uint32_t items = 0, p_parity = 0;  // p_parity: bit st for stream st
+    uint32_t items = 0, p_parity = 0;
     Ring kr, vr;
-    Walk walk(P, sh.start);
+    Items walk(sh);
     Item it;
     bool ok = true;
+#pragma unroll 1
     while (ok && walk.next(it)) {
         if (!(ok = wait(smem_u32(&sh.q_full), items & 1, gave_up))) break;
         tc_after();
         // the same in every lane; taken from one, so that the operands below live in uniform registers
-        const bool two = __shfl_sync(kAll, (int)it.two, 0);
-        const int32_t S = __shfl_sync(kAll, it.two ? 2 * it.n : it.n, 0);
-        auto scores = [&](int32_t n) {
-            const uint32_t st = n & 1;
-            const bool last_use = !two || st;
-            if (!(two && st) && !wait(k_full + 8 * kr.i, kr.parity, gave_up)) return false;
-            const uint32_t q = operand(q_smem + (two && st ? q_bytes : 0), 16), k = operand(k_smem + kr.i * slot_bytes, 16);
-            const uint32_t d = tmem + st * kTile;
+        const bool two = __shfl_sync(kAll, it.two, 0);
+        const int32_t n = __shfl_sync(kAll, it.n, 0);
+        const uint32_t q = operand(q_smem + (two && st ? q_bytes : 0), 16);
+        // this stream's tiles are first, first + by, ...; k_at and v_at: the next tile of either kind
+        const int32_t first = two ? 0 : (int32_t)st, by = two ? 1 : 2;
+        int32_t k_at = 0, v_at = 0;
+        auto pass = [&](int32_t to, int32_t& at, Ring& r, uint32_t full, uint32_t empty, uint32_t slots) {
+            for (; at < to; ++at, r.step(slots)) {
+                if (!wait(full + 8 * r.i, r.parity, gave_up)) return false;
+                if (leader) bar_arrive(empty + 8 * r.i);
+            }
+            return true;
+        };
+        auto scores = [&](int32_t t) {
+            if (!pass(t, k_at, kr, k_full, k_empty, P.k_slots) || !wait(k_full + 8 * kr.i, kr.parity, gave_up)) return false;
+            const uint32_t k = operand(k_smem + kr.i * slot_bytes, 16);
             if (leader) {
 #pragma unroll
                 for (int part = 0; part < parts; ++part)
 #pragma unroll
                     for (int i = 0; i < steps_max; ++i) {
                         const uint32_t off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
-                        if (i < depth) mma_ss<k8>(d, q + (part * kHalf >> 4) + off, k + off, id_s, part + i > 0);
+                        if (i < depth) mma_ss<k8>(s_at, q + (part * kHalf >> 4) + off, k + off, id_s, part + i > 0);
                     }
-                tc_commit(s_full + 8 * st);
-                if (last_use) tc_commit(k_empty + 8 * kr.i);
-                if (n == S - 1) tc_commit(q_empty);
+                tc_commit(s_full);
+                tc_commit(k_empty + 8 * kr.i);
+                if (t + by >= n) tc_commit(q_empty);
             }
             __syncwarp();
-            if (last_use) kr.step(P.k_slots);
+            ++k_at;
+            kr.step(P.k_slots);
             return true;
         };
-        auto outputs = [&](int32_t n) {
-            const uint32_t st = n & 1;
-            const bool last_use = !two || st;
-            if (!(two && st) && !wait(value + 8 * vr.i, vr.parity, gave_up)) return false;
-            if (!wait(p_ready + 8 * st, p_parity >> st & 1, gave_up)) return false;
-            p_parity ^= 1u << st;
+        if (first < n) ok = scores(first);
+        else if (leader) bar_arrive(q_empty);
+#pragma unroll 1
+        for (int32_t t = first; t < n && ok; t += by) {
+            if (!(ok = pass(t, v_at, vr, value, v_empty, P.v_slots))) break;
+            if (!(ok = wait(value + 8 * vr.i, vr.parity, gave_up))) break;
+            if (!(ok = wait(p_ready, p_parity, gave_up))) break;
+            p_parity ^= 1u;
             tc_after();
-            const uint32_t a = tmem + st * kTile, b = operand(v_smem + vr.i * slot_bytes, kHalf), d = tmem + 256 + st * dp;
-            const uint32_t add = n > 1;
+            const uint32_t b = operand(v_smem + vr.i * slot_bytes, kHalf);
+            const uint32_t add = t > first;
             if (leader) {
 #pragma unroll
                 for (int i = 0; i < kTile / KindOf<K>::kStep; ++i)
 #pragma unroll
                     for (int part = 0; part < parts; ++part)
-                        mma_ts<k8>(d, a + (k8 ? part * 8 + i * 16 : i * 8), b + (i * KindOf<K>::kStep * 128 >> 4), id_o,
+                        mma_ts<k8>(o_at, s_at + (k8 ? part * 8 + i * 16 : i * 8), b + (i * KindOf<K>::kStep * 128 >> 4), id_o,
                                    part + i > 0 ? 1u : add);
-                tc_commit(pv_done + 8 * st);
-                if (last_use) tc_commit(v_empty + 8 * vr.i);
+                tc_commit(pv_done);
+                tc_commit(v_empty + 8 * vr.i);
             }
             __syncwarp();
-            if (last_use) vr.step(P.v_slots);
-            return true;
-        };
-        ok = scores(0);
-        if (ok && S > 1) ok = scores(1);
-        for (int32_t n = 0; n < S && ok; ++n) {
-            ok = outputs(n);
-            if (ok && n + 2 < S) ok = scores(n + 2);
+            ++v_at;
+            vr.step(P.v_slots);
+            if (t + by < n) ok = scores(t + by);
         }
+        if (ok) ok = pass(n, k_at, kr, k_full, k_empty, P.k_slots) && pass(n, v_at, vr, value, v_empty, P.v_slots);
         ++items;
     }
     // products under way end before the tensor memory is given back
@@ -1016,6 +1101,7 @@ __device__ __forceinline__ bool load_queries(const Params& P, Shared& sh, const 
         __syncwarp();
         if (!flip) return true;
         if (!wait(bar, items & 1, &sh.gave_up)) return false;
+#pragma unroll 1
         for (int i = lane; i < (it.two ? 2 : 1) * NH * kHalf / 16; i += 32) {
             uint32_t u[4];
             const uint32_t at = q_smem + i * 16;
@@ -1027,12 +1113,13 @@ __device__ __forceinline__ bool load_queries(const Params& P, Shared& sh, const 
     } else {
         const int32_t D = A.pool.dim, rows = it.nt * P.G, tile_rows = P.tokens * P.G;
         const T* q = (const T*)A.q + (int64_t)(it.row0 + it.t0) * A.q_stride + (int64_t)it.h * P.G * D;
-        // half a warp a row, eight elements a lane; eight rows of loads under way
+        // half a warp a row, eight elements a lane; eight rows under way
         const int c = lane & 15;
-        for (int32_t r0 = lane >> 4; r0 - (lane >> 4) < rows; r0 += 16) {
-            uint4 u[8];
+#pragma unroll 1
+        for (int32_t r0 = lane >> 4; r0 - (lane >> 4) < rows; r0 += 8) {
+            uint4 u[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 4; ++k) {
                 const int32_t r = r0 + 2 * k;
                 u[k] = make_uint4(0, 0, 0, 0);
                 if (r < rows && c * 8 < D) {
@@ -1041,7 +1128,7 @@ __device__ __forceinline__ bool load_queries(const Params& P, Shared& sh, const 
                 }
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 4; ++k) {
                 const int32_t r = r0 + 2 * k;
                 const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
                 float2 f[4];
@@ -1089,6 +1176,7 @@ template <int NH>
 __device__ __forceinline__ void clear_rows(uint32_t at, int32_t lo, int32_t hi) {
     lo = max(lo, 0);
     hi = min(hi, kTile);
+#pragma unroll 2
     for (int32_t i = lo * 8 + (threadIdx.x & 31); i < hi * 8; i += 32)
 #pragma unroll
         for (int h = 0; h < NH; ++h)
@@ -1144,32 +1232,33 @@ __device__ __forceinline__ void value_role(const Params& P, Shared& sh, uint32_t
     volatile int* gave_up = &sh.gave_up;
     uint32_t v = 0, items = 0;
     Ring ring;
-    Walk walk(P, sh.start);
+    Items walk(sh);
     Item it;
+#pragma unroll 1
     for (; walk.next(it); ++items) {
         if (items > 0 && !wait(smem_u32(&sh.q_empty), (items - 1) & 1, gave_up)) return;
         if (!load_queries<K, NH>(P, sh, it, q_smem, qm, items)) return;
-        int32_t mixed_lo, mixed_hi;
-        mixed_slots(P, it, mixed_lo, mixed_hi);
+#pragma unroll 1
         for (int32_t j = 0; j < it.n; ++j, ++v, ring.step(P.v_slots)) {
             if (!wait(smem_u32(&sh.v_full[ring.i]), ring.parity, gave_up)) return;
             const int32_t k0 = (it.tile + j) * kTile;
             const uint32_t bad = sh.bad[1][v % kBadRing];
-            const bool mixed = mixed_tile(it, k0, mixed_lo, mixed_hi);
+            const bool mixed = mixed_tile(it, k0);
             if (bad || k0 < it.lo || k0 + kTile > it.end || mixed) {
                 const uint32_t at = v_smem + ring.i * (NH * kHalf);
                 // rows no one sees lie before the first and after the last one that is seen
                 clear_rows<NH>(at, 0, it.lo - k0);
                 clear_rows<NH>(at, it.end - k0, kTile);
                 if (bad)
+#pragma unroll 1
                     for (int g = 0; g < 16; ++g)
                         if (bad >> g & 1u) clear_rows<NH>(at, 8 * g, 8 * g + 8);
                 if (mixed) {
                     if (lane < 4) sh.odd[v % kBadRing][lane] = 0;
                     __syncwarp();
                     const int32_t lo = max(0, it.lo - k0), hi = min(kTile, it.end - k0);
-                    scan_rows<K, NH>(at, lo, min(hi, mixed_lo - k0), bad, sh.odd[v % kBadRing]);
-                    scan_rows<K, NH>(at, max(lo, mixed_hi - k0), hi, bad, sh.odd[v % kBadRing]);
+                    scan_rows<K, NH>(at, lo, min(hi, it.mixed_lo - k0), bad, sh.odd[v % kBadRing]);
+                    scan_rows<K, NH>(at, max(lo, it.mixed_hi - k0), hi, bad, sh.odd[v % kBadRing]);
                 }
                 fence_async();
             }
@@ -1197,9 +1286,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kMaxSlots; ++i) {
             bar_init(smem_u32(&sh.k_full[i]), 1);
-            bar_init(smem_u32(&sh.k_empty[i]), 1);
+            bar_init(smem_u32(&sh.k_empty[i]), 2);
             bar_init(smem_u32(&sh.v_full[i]), 1);
-            bar_init(smem_u32(&sh.v_empty[i]), 1);
+            bar_init(smem_u32(&sh.v_empty[i]), 2);
             bar_init(smem_u32(&sh.value[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -1209,10 +1298,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bar_init(smem_u32(&sh.q_in), 1);
         bar_init(smem_u32(&sh.q_full), 1);
-        bar_init(smem_u32(&sh.q_empty), 1);
+        bar_init(smem_u32(&sh.q_empty), 2);
         bar_init(smem_u32(&sh.meet), 8);
         bar_init(smem_u32(&sh.part), 8);
-        bar_init(smem_u32(&sh.drain), 1);
+        bar_init(smem_u32(&sh.drain), 2);
+        for (int i = 0; i < kItems; ++i) {
+            bar_init(smem_u32(&sh.item_full[i]), 1);
+            bar_init(smem_u32(&sh.item_empty[i]), kItemReaders);
+        }
         sh.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
@@ -1229,6 +1322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_after();
     // sequences that fail: their findings, and zeros in their rows
     if (sh.failing)
+#pragma unroll 1
         for (int32_t b = blockIdx.x; b < P.a.chunk.B; b += gridDim.x) {
             const Seq s = checked_seq(P, b);
             if (!s.err) continue;
@@ -1236,16 +1330,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!s.rows_ok) continue;
             const int64_t row = (int64_t)P.a.q_heads * P.a.pool.dim / 8;
             uint4* out = (uint4*)P.a.out + s.row0 * row;
+#pragma unroll 1
             for (int64_t i = tid; i < s.T * row; i += kThreads) out[i] = make_uint4(0, 0, 0, 0);
             if (P.a.lse)
+#pragma unroll 1
                 for (int64_t i = tid; i < (int64_t)s.T * P.a.q_heads; i += kThreads)
                     P.a.lse[(int64_t)s.row0 * P.a.q_heads + i] = -INFINITY;
         }
-    if (w < 8) softmax_role<K, DP>(P, sh);
-    else if (w == 8) load_role<NH>(P, sh, k_smem, &km, 0);
-    else if (w == 9) product_role<K, NH>(P, sh, q_smem, k_smem, v_smem);
-    else if (w == 10) load_role<NH>(P, sh, v_smem, &vm, 1);
-    else value_role<K, NH>(P, sh, q_smem, v_smem, &qm);
+    // 128 registers a thread at launch: 192 + 192 + 64 + 64 for the four warpgroups
+    if (w < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        softmax_role<K, DP>(P, sh);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (w == 8 || w == 10) load_role<NH>(P, sh, w == 8 ? k_smem : v_smem, w == 8 ? &km : &vm, w == 10);
+        else if (w == 9 || w == 13) product_role<K, NH>(P, sh, q_smem, k_smem, v_smem, w == 13);
+        else if (w == 11) value_role<K, NH>(P, sh, q_smem, v_smem, &qm);
+        else if (w == 12) item_role(P, sh);
+    }
     tc_before();
     __syncthreads();
     tc_after();
@@ -1267,6 +1369,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_attend_merge(const __grid_con
     const int lane = threadIdx.x & 31;
     const int32_t D = P.a.pool.dim, rows = rec.tokens * P.G;
     constexpr int kPer = DP / 32;
+#pragma unroll 1
     for (int32_t i = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); i < rows;
          i += gridDim.y * (kMergeThreads / 32)) {
         const int32_t t = i / P.G, g = i - t * P.G;
@@ -1274,10 +1377,12 @@ __global__ void __launch_bounds__(kMergeThreads) k_attend_merge(const __grid_con
         // the first part is the last item of CTA c - 1, the others the first items of c, c + 1, ...
         auto slot = [&](int32_t part) { return (size_t)(part ? 2 * (c + part - 1) : 2 * (c - 1) + 1) * 256 + r; };
         float top = -INFINITY;
+#pragma unroll 1
         for (int32_t p = lane; p < rec.parts; p += 32) top = fmaxf(top, P.part_ml[slot(p)].x);
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
         const float base = top == -INFINITY ? 0.f : top;
         float l = 0.f, acc[kPer] = {};
+#pragma unroll 1
         for (int32_t p0 = 0; p0 < rec.parts; p0 += 32) {
             float wt = 0.f, pl = 0.f;
             if (p0 + lane < rec.parts) {
