@@ -44,11 +44,12 @@ constexpr unsigned kAll = 0xffffffffu;
 // element kinds
 // ---------------------------------------------------------------------------------------------------------
 // kShift: weights are held as 2^kShift w, so that those far below the largest keep their precision in a narrow
-// type; kSlack: how far (log2) a weight may exceed the reference before the reference moves. 2^(kShift + kSlack)
-// is within the type's range.
+// type; kSlack: how far (log2) a weight may exceed the reference before the reference moves. A tile's 128 weights
+// sum to 2^(kShift + kSlack + 7) at most, within the type's range: bfloat16 has float's, and its reference hardly
+// ever moves after the first tile. (e4m3: every weight, 2^(kShift + kSlack) <= 448.)
 // kE4m3: the cache is 8 bits wide and the products are too. A bfloat16 query has 8 significant bits and an
 // e4m3 value 4, so q 2^k = hi + lo exactly, but for elements under 2^-11 of the row's largest (k brings it to
-// [128, 256)); a weight is hi + lo to 2^-9 of itself. Each product then runs twice, at twice the 16-bit rate,
+// [128, 256)); a weight is hi + lo to about 2^-9 of itself. Each product then runs twice, at twice the 16-bit rate,
 // and no key or value is converted.
 enum Kind { kBf16 = 0, kFp16 = 1, kE4m3 = 2 };
 template <int K>
@@ -56,19 +57,19 @@ struct KindOf;
 template <>
 struct KindOf<kBf16> {
     using T = __nv_bfloat16;
-    static constexpr float kShift = 0.f, kSlack = 8.f;
+    static constexpr float kShift = 0.f, kSlack = 56.f;
     static constexpr int kBytes = 2, kStep = 16;  // of an element; elements a product step takes along its depth
 };
 template <>
 struct KindOf<kFp16> {
     using T = __half;
-    static constexpr float kShift = 7.f, kSlack = 8.f;
+    static constexpr float kShift = 7.f, kSlack = 1.f;
     static constexpr int kBytes = 2, kStep = 16;
 };
 template <>
 struct KindOf<kE4m3> {
     using T = __nv_bfloat16;
-    static constexpr float kShift = 8.f, kSlack = 0.75f;
+    static constexpr float kShift = 7.f, kSlack = 1.75f;
     static constexpr int kBytes = 1, kStep = 32;
 };
 
@@ -89,6 +90,7 @@ struct Params {
     int32_t q_box;      // tokens of one copy into a query tile
     int32_t k_slots, v_slots;  // key and value tiles that shared memory has room for
     int32_t box;        // slots of one copy, a divisor of the page size and of kTile
+    int32_t wide;       // output rows lie on 32 bytes
     float* part_o;      // [2 n][256][DP]
     float2* part_ml;    // [2 n][256]
     Record* records;    // [n]
@@ -240,9 +242,17 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t u) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)u, __NV_E4M3);
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+__device__ __forceinline__ __half2 half_pair(uint32_t e4m3) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)e4m3, __NV_E4M3);
+    return *reinterpret_cast<const __half2*>(&h);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t u) { return __half22float2(half_pair(u)); }
+// The parts hi and lo of two weights, by way of their half-precision values (2^-11 of them off, where hi + lo is 2^-9).
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const __half2 x = __floats2half2_rn(a, b);
+    hi = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&x), __NV_SATFINITE, __NV_E4M3);
+    const __half2 r = __hsub2(x, half_pair(hi));
+    lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&r), __NV_SATFINITE, __NV_E4M3);
 }
 
 // ---------------------------------------------------------------------------------------------------------
@@ -318,6 +328,7 @@ struct Shared {  // behind the operand tiles
     uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
     uint64_t value[kMaxSlots];  // a value tile is in and clean
     uint64_t s_full[2], p_ready[2], pv_done[2];
+    uint64_t turn[2];           // the streams' products take turns
     uint64_t q_in, q_full, q_empty, meet, part, drain;
     uint64_t item_full[kItems], item_empty[kItems];
     Item item[kItems];
@@ -337,7 +348,7 @@ constexpr int shared_bytes() {
 }
 
 // Where the CTA begins, and the record of an item that its predecessor began. All threads.
-constexpr int32_t kLead = 3;  // measured: about three tiles' time between an item's last tile and the next one's pace
+constexpr int32_t kLead = 5;  // measured: about five tiles' time between an item's last tile and the next one's pace
 __device__ __forceinline__ void plan(const Params& P, Shared& sh) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int32_t B = P.a.chunk.B, c = (int32_t)blockIdx.x, heads = P.a.pool.heads;
@@ -592,13 +603,6 @@ __device__ __forceinline__ void seen_of(const Row& row, const Item& it, int32_t 
     }
 }
 
-// Scores of slots that are not seen.
-__device__ __forceinline__ void hide(uint32_t* s, uint32_t seen) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (!(seen >> i & 1u)) s[i] = 0xff800000u;
-}
-
 // Only among slots that some rows of the item see and others do not can a value meet a weight of zero, and a NaN
 // or infinity be carried into a row that does not see it.
 __device__ __forceinline__ bool mixed_tile(const Item& it, int32_t k0) {
@@ -634,10 +638,12 @@ __device__ __forceinline__ void add_odd(const AttendArgs& A, const Item& it, uin
     }
 }
 
-// A step: the tile's maximum, then its weights in place of its scores (and their sum). The scores are read from
-// tensor memory twice, which is cheaper than the registers it takes to keep them, and the loops are rolled: unrolled,
-// the roles' code misses the instruction cache in every step (measured: 1500 cycles a step, 2200 unrolled).
-__device__ __forceinline__ float tile_max(uint32_t s_col, bool masked, const uint32_t* seen) {
+// A step turns a tile's scores into its weights, in their place, and sums them. quick_weights reads the scores once
+// and counts on the row's reference; where a weight would be too large for it nothing is written, the tile's
+// maximum is taken, the reference moves and the step begins again. A row's first tile and the narrow e4m3 weights
+// begin with the maximum. What few tiles need (tile_max, hide_tile) is rolled: unrolled, the roles' code misses the
+// instruction cache in every step (measured: 1500 cycles a step, 2200 with all unrolled).
+__device__ __forceinline__ float tile_max(uint32_t s_col) {
     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
     for (int q = 0; q < 4; q += 2) {
@@ -645,10 +651,6 @@ __device__ __forceinline__ float tile_max(uint32_t s_col, bool masked, const uin
         tc_ld32(s_col + 32 * q, s[0]);
         tc_ld32(s_col + 32 * q + 32, s[1]);
         tc_wait_ld();
-        if (masked) {
-            hide(s[0], q ? seen[2] : seen[0]);
-            hide(s[1], q ? seen[3] : seen[1]);
-        }
 #pragma unroll
         for (int i = 0; i < 32; i += 4)
 #pragma unroll
@@ -657,8 +659,24 @@ __device__ __forceinline__ float tile_max(uint32_t s_col, bool masked, const uin
     }
     return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
 }
+// Scores of slots that a row does not see become -inf.
+__device__ __forceinline__ void hide_tile(uint32_t s_col, const uint32_t* seen) {
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t m = q == 0 ? seen[0] : q == 1 ? seen[1] : q == 2 ? seen[2] : seen[3];
+        if (__all_sync(kAll, m == ~0u)) continue;
+        uint32_t s[32];
+        tc_ld32(s_col + 32 * q, s);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!(m >> i & 1u)) s[i] = 0xff800000u;
+        tc_st32(s_col + 32 * q, s);
+    }
+    tc_wait_st();
+}
 template <int K>
-__device__ __forceinline__ void weights32(uint32_t* x, F2 sl2, F2 off2, F2* sum, uint32_t* pk) {
+__device__ __forceinline__ void weights32(const uint32_t* x, F2 sl2, F2 off2, F2* sum, uint32_t* pk) {
     using T = typename KindOf<K>::T;
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
@@ -674,37 +692,34 @@ __device__ __forceinline__ void weights32(uint32_t* x, F2 sl2, F2 off2, F2* sum,
             pk[i >> 1] = from_float2<T>(p[0], p[1]);
             pk[(i >> 1) + 1] = from_float2<T>(p[2], p[3]);
         } else {
-            const uint32_t a = e4m3x2(p[0], p[1]), b = e4m3x2(p[2], p[3]);
-            const float2 u = from_e4m3x2(a), w = from_e4m3x2(b);
+            uint32_t a, b, c, d;
+            split_pair(p[0], p[1], a, c);
+            split_pair(p[2], p[3], b, d);
             pk[i >> 2] = a | b << 16;
-            pk[8 + (i >> 2)] = e4m3x2(p[0] - u.x, p[1] - u.y) | e4m3x2(p[2] - w.x, p[3] - w.y) << 16;
+            pk[8 + (i >> 2)] = c | d << 16;
         }
     }
 }
+// False if the weights of some row sum to more than their type holds.
 template <int K>
-__device__ __forceinline__ float tile_weights(uint32_t s_col, bool masked, const uint32_t* seen, float sl, float off) {
+__device__ __forceinline__ bool quick_weights(uint32_t s_col, float sl, float off, bool real, float& total) {
     const F2 sl2 = pack2(sl, sl), off2 = pack2(off, off);
     F2 sum[2] = {0, 0};
-    uint32_t s[2][32];
+    uint32_t s[2][32], pk[4][16];
     tc_ld32(s_col, s[0]);
-#pragma unroll 1
-    for (int q = 0; q < 4; q += 2) {
-        uint32_t pk[16];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
         tc_wait_ld();
-        tc_ld32(s_col + 32 * q + 32, s[1]);
-        if (masked) hide(s[0], q ? seen[2] : seen[0]);
-        weights32<K>(s[0], sl2, off2, sum, pk);
-        tc_st16(s_col + 16 * q, pk);
-        tc_wait_ld();
-        tc_ld32(s_col + (q ? 96 : 64), s[0]);  // the last one is read for nothing
-        if (masked) hide(s[1], q ? seen[3] : seen[1]);
-        weights32<K>(s[1], sl2, off2, sum, pk);
-        tc_st16(s_col + 16 * q + 16, pk);
+        if (q < 3) tc_ld32(s_col + 32 * q + 32, s[(q + 1) & 1]);
+        weights32<K>(s[q & 1], sl2, off2, sum, pk[q]);
     }
-    tc_wait_ld();
     float a, b;
     unpack2(add2(sum[0], sum[1]), a, b);
-    return a + b;
+    total = a + b;
+    if (K != kE4m3 && __any_sync(kAll, real && total > (K == kBf16 ? 0x1p64f : 0x1p15f))) return false;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tc_st16(s_col + 16 * q, pk[q]);
+    return true;
 }
 // O times f, a factor per row.
 template <int DP>
@@ -762,21 +777,29 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
                 const bool whole = (k0 + kTile <= row.limit && row.low <= k0 && !bad) || !row.real;
                 const bool masked = !__all_sync(kAll, whole);
                 if (masked) seen_of(row, it, k0, bad, tree, seen);
-                const float mx = tile_max(s_col, masked, seen);
-                const bool move = row.real && ((mx - m) * row.sl > KT::kSlack || (m == -INFINITY && mx > m));
-                if (__any_sync(kAll, move)) {
-                    const float old = m;
-                    if (move) m = mx;
-                    const float f = !move || old == -INFINITY ? 1.f : exp2_fast((old - m) * row.sl);
-                    l *= f;
-                    if (__any_sync(kAll, move && old != -INFINITY)) {
-                        if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
-                        tc_after();
-                        rescale<DP>(o_col[stream], f);
+                if (masked) hide_tile(s_col, seen);
+                float sum;
+                bool first = K == kE4m3 || __any_sync(kAll, row.real && m == -INFINITY);
+#pragma unroll 1
+                for (int attempt = 0; attempt < 2; ++attempt, first = true) {
+                    if (first) {
+                        const float mx = tile_max(s_col);
+                        const bool move = row.real && ((mx - m) * row.sl > KT::kSlack || (m == -INFINITY && mx > m));
+                        if (__any_sync(kAll, move)) {
+                            const float old = m;
+                            if (move) m = mx;
+                            const float f = !move || old == -INFINITY ? 1.f : exp2_fast((old - m) * row.sl);
+                            l *= f;
+                            if (__any_sync(kAll, move && old != -INFINITY)) {
+                                if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
+                                tc_after();
+                                rescale<DP>(o_col[stream], f);
+                            }
+                        }
                     }
+                    if (quick_weights<K>(s_col, row.sl, KT::kShift - (m == -INFINITY ? 0.f : m * row.sl), row.real, sum)) break;
                 }
-                const float off = KT::kShift - (m == -INFINITY ? 0.f : m * row.sl);
-                l += tile_weights<K>(s_col, masked, seen, row.sl, off);
+                l += sum;
                 tc_wait_st();
             }
             const bool mixed = mixed_tile(it, k0);
@@ -853,25 +876,30 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
                 if (row.real) {
                     if (alone) {
                         T* out = (T*)A.out + ((int64_t)row_at * A.q_heads + head) * D;
+                        uint32_t u[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            if (c + i < D) {
-                                uint4 u;
-                                u.x = from_float2<T>(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-                                u.y = from_float2<T>(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-                                u.z = from_float2<T>(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
-                                u.w = from_float2<T>(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
-                                *reinterpret_cast<uint4*>(out + c + i) = u;
+                        for (int i = 0; i < 16; ++i)
+                            u[i] = from_float2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                        // lanes write to rows of their own: whole 32-byte sectors halve what that costs
+#pragma unroll
+                        for (int i = 0; i < 32; i += 16) {
+                            const uint32_t* w = u + i / 2;
+                            if (P.wide && c + i < D) {
+                                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + c + i), SV_W8(w, 0)
+                                             : "memory");
+                            } else {
+                                if (c + i < D) *reinterpret_cast<uint4*>(out + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                                if (c + i + 8 < D)
+                                    *reinterpret_cast<uint4*>(out + c + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
                             }
                         }
                     } else {
                         float* out = P.part_o + prow * DP + c;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
+                        for (int i = 0; i < 32; i += 8)
                             if (c + i < D)
-                                *reinterpret_cast<float4*>(out + i) =
-                                    make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
-                                                __uint_as_float(o[i + 3]));
+                                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + i), SV_W8(o, i)
+                                             : "memory");
                     }
                 }
             }
@@ -975,7 +1003,9 @@ __device__ __forceinline__ void load_role(const Params& P, Shared& sh, uint32_t 
 }
 
 // A stream's products, by one thread: S = Q K^T of its next tile follows O += P V of this one, whose P lies where that
-// S will. Tiles of the other stream's alone are passed on.
+// S will. Tiles of the other stream's alone are passed on. The streams take turns, each turn both products: left to
+// themselves they fall into step, both at their products and then both at their exponentials (measured: 4200 cycles
+// a tile of 256 rows).
 template <int K, int NH>
 __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem,
                                              const uint32_t st) {
@@ -998,7 +1028,8 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
                    pv_done = smem_u32(&sh.pv_done[st]), q_empty = smem_u32(&sh.q_empty);
     const bool leader = elect();
     volatile int* gave_up = &sh.gave_up;
-    uint32_t items = 0, p_parity = 0;
+    const uint32_t turn[2] = {smem_u32(&sh.turn[st]), smem_u32(&sh.turn[st ^ 1])};
+    uint32_t items = 0, p_parity = 0, turns = 0;
     Ring kr, vr;
     Items walk(sh);
     Item it;
@@ -1021,8 +1052,10 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
             }
             return true;
         };
+        auto ready = [&](int32_t t) {  // the tile's keys
+            return pass(t, k_at, kr, k_full, k_empty, P.k_slots) && wait(k_full + 8 * kr.i, kr.parity, gave_up);
+        };
         auto scores = [&](int32_t t) {
-            if (!pass(t, k_at, kr, k_full, k_empty, P.k_slots) || !wait(k_full + 8 * kr.i, kr.parity, gave_up)) return false;
             const uint32_t k = operand(k_smem + kr.i * slot_bytes, 16);
             if (leader) {
 #pragma unroll
@@ -1032,6 +1065,7 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
                         const uint32_t off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
                         if (i < depth) mma_ss<k8>(s_at, q + (part * kHalf >> 4) + off, k + off, id_s, part + i > 0);
                     }
+                bar_arrive(turn[1]);
                 tc_commit(s_full);
                 tc_commit(k_empty + 8 * kr.i);
                 if (t + by >= n) tc_commit(q_empty);
@@ -1039,16 +1073,38 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
             __syncwarp();
             ++k_at;
             kr.step(P.k_slots);
+        };
+        auto idle = [&](bool last) {  // a turn without work
+            if (!wait(turn[0], turns, gave_up)) return false;
+            turns ^= 1u;
+            if (leader) {
+                bar_arrive(turn[1]);
+                if (last) bar_arrive(q_empty);
+            }
             return true;
         };
-        if (first < n) ok = scores(first);
-        else if (leader) bar_arrive(q_empty);
+        if (first < n) {
+            if (!(ok = ready(first) && wait(turn[0], turns, gave_up))) break;
+            turns ^= 1u;
+            scores(first);
+        } else if (!(ok = idle(true))) {
+            break;
+        }
+        const int32_t rounds = two ? n : (n + 1) / 2;
 #pragma unroll 1
-        for (int32_t t = first; t < n && ok; t += by) {
-            if (!(ok = pass(t, v_at, vr, value, v_empty, P.v_slots))) break;
-            if (!(ok = wait(value + 8 * vr.i, vr.parity, gave_up))) break;
+        for (int32_t k = 0; k < rounds; ++k) {
+            const int32_t t = first + k * by;
+            if (t >= n) {
+                ok = idle(false);
+                break;  // only ever the last round
+            }
+            const bool more = t + by < n;
+            if (!(ok = pass(t, v_at, vr, value, v_empty, P.v_slots) && wait(value + 8 * vr.i, vr.parity, gave_up))) break;
+            if (more && !(ok = ready(t + by))) break;
             if (!(ok = wait(p_ready, p_parity, gave_up))) break;
             p_parity ^= 1u;
+            if (!(ok = wait(turn[0], turns, gave_up))) break;
+            turns ^= 1u;
             tc_after();
             const uint32_t b = operand(v_smem + vr.i * slot_bytes, kHalf);
             const uint32_t add = t > first;
@@ -1059,13 +1115,14 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
                     for (int part = 0; part < parts; ++part)
                         mma_ts<k8>(o_at, s_at + (k8 ? part * 8 + i * 16 : i * 8), b + (i * KindOf<K>::kStep * 128 >> 4), id_o,
                                    part + i > 0 ? 1u : add);
+                if (!more) bar_arrive(turn[1]);
                 tc_commit(pv_done);
                 tc_commit(v_empty + 8 * vr.i);
             }
             __syncwarp();
             ++v_at;
             vr.step(P.v_slots);
-            if (t + by < n) ok = scores(t + by);
+            if (more) scores(t + by);
         }
         if (ok) ok = pass(n, k_at, kr, k_full, k_empty, P.k_slots) && pass(n, v_at, vr, value, v_empty, P.v_slots);
         ++items;
@@ -1295,6 +1352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(smem_u32(&sh.s_full[i]), 1);
             bar_init(smem_u32(&sh.p_ready[i]), 4);
             bar_init(smem_u32(&sh.pv_done[i]), 1);
+            bar_init(smem_u32(&sh.turn[i]), 1);
         }
         bar_init(smem_u32(&sh.q_in), 1);
         bar_init(smem_u32(&sh.q_full), 1);
@@ -1309,6 +1367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sh.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
+        bar_arrive(smem_u32(&sh.turn[0]));
     }
     if (w == 9)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
@@ -1474,6 +1533,7 @@ cudaError_t launch(const AttendArgs& A, cudaStream_t st) {
     P.v_slots = slots - P.k_slots;
     P.box = kTile;
     while (A.pool.page_size % P.box) P.box /= 2;
+    P.wide = A.pool.dim % 16 == 0 && (uintptr_t)A.out % 32 == 0;
     char* ws = (char*)A.workspace;
     P.part_o = (float*)ws;
     P.part_ml = (float2*)(ws + part_rows() * DP * sizeof(float));
