@@ -23,6 +23,8 @@
 // on the device, so the host needs to know none of them.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "sv_cache.cuh"
 
 namespace sv {
@@ -347,6 +349,12 @@ constexpr int shared_bytes() {
     return (int)sizeof(Shared) + (K == kE4m3 ? 2 * 2 * kTile * 4 : 0);
 }
 
+// a * b / c of small numbers without the long division.
+__device__ __forceinline__ long long share(long long a, int32_t b, int32_t c) {
+    const unsigned long long x = (unsigned long long)a * (uint32_t)b;
+    return x >> 32 ? (long long)(x / (uint32_t)c) : (long long)((uint32_t)x / (uint32_t)c);
+}
+
 // Where the CTA begins, and the record of an item that its predecessor began. All threads.
 constexpr int32_t kLead = 5;  // measured: about five tiles' time between an item's last tile and the next one's pace
 __device__ __forceinline__ void plan(const Params& P, Shared& sh) {
@@ -395,7 +403,7 @@ __device__ __forceinline__ void plan(const Params& P, Shared& sh) {
     const long long W = tiles + lead * blocks;
     const int32_t n = (int32_t)min((long long)gridDim.x, tiles);
     if (c >= n) return;  // the same for the whole CTA
-    const long long u0 = W * c / n, u1 = W * (c + 1) / n;
+    const long long u0 = share(W, c, n), u1 = share(W, c + 1, n);
     long long base = 0;
 #pragma unroll 1
     for (int32_t b0 = 0; b0 < B && base <= u0; b0 += kThreads) {
@@ -413,13 +421,21 @@ __device__ __forceinline__ void plan(const Params& P, Shared& sh) {
             const long long x = __shfl_up_sync(kAll, incl, o);
             if (lane >= o) incl += x;
         }
-        __syncthreads();
-        if (lane == 31) sh.scan[w] = incl;
-        __syncthreads();
+        if (B > kThreads) {  // else the warps' sums are there already
+            __syncthreads();
+            if (lane == 31) {
+                sh.scan[w] = incl;
+                sh.scan2[w] = 0;
+            }
+            __syncthreads();
+        }
+        const int32_t sc = B > kThreads ? 1 : heads, lc = B > kThreads ? 0 : lead * heads;
         long long before = base, total = 0;
+#pragma unroll 1
         for (int i = 0; i < kThreads / 32; ++i) {
-            if (i < w) before += sh.scan[i];
-            total += sh.scan[i];
+            const long long x = sh.scan[i] * sc + sh.scan2[i] * lc;
+            if (i < w) before += x;
+            total += x;
         }
         const long long begin = before + incl - u;
         if (u > 0 && u0 >= begin && u0 < begin + u) {
@@ -438,7 +454,7 @@ __device__ __forceinline__ void plan(const Params& P, Shared& sh) {
             if (x > lead) {
                 // the item's first tile is unit `from`; if the CTA before this one had it, this one records the item
                 const long long from = u0 - x + lead;
-                if (from >= W * (c - 1) / n) {
+                if (from >= share(W, c - 1, n)) {
                     Record r{};
                     r.parts = (int32_t)(((from + count) * n - 1) / W - c) + 2;  // to the CTA of its last tile
                     r.row0 = mine.row0 + it.t0;
@@ -1339,7 +1355,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     const int tid = threadIdx.x, w = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;");
     if (tid == 0) {
         for (int i = 0; i < kMaxSlots; ++i) {
             bar_init(smem_u32(&sh.k_full[i]), 1);
@@ -1369,8 +1384,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_async();
         bar_arrive(smem_u32(&sh.turn[0]));
     }
+    if (w == 8 && (tid & 31) == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&km));
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&vm));
+        if (K != kE4m3) asm volatile("prefetch.tensormap [%0];" ::"l"(&qm));
+    }
     if (w == 9)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+    // what is above may run while the stream's previous kernel ends
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     plan(P, sh);
     if (blockIdx.x == 0 && tid == 0) {
         const int64_t end = (int64_t)P.a.chunk.offs[P.a.chunk.B] + P.a.chunk.B;
@@ -1421,6 +1444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kMergeThreads = 256;
 template <typename T, int DP>
 __global__ void __launch_bounds__(kMergeThreads) k_attend_merge(const __grid_constant__ Params P) {
+    asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t c = blockIdx.x + 1;
     const Record rec = P.records[c];
@@ -1549,20 +1573,28 @@ cudaError_t launch(const AttendArgs& A, cudaStream_t st) {
     if (!encode(&km, A.pool, A.pool.k, KindOf<K>::kBytes, K, P.box) || !encode(&vm, A.pool, A.pool.v, KindOf<K>::kBytes, K, P.box))
         return cudaErrorInvalidValue;
     const int smem = P.q_tiles * q_bytes + slots * NH * kHalf + shared_bytes<K>();
-    e = cudaFuncSetAttribute(k_attend<K, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    k_attend<K, DP><<<n, kThreads, smem, st>>>(P, km, vm, qm);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(n - 1, 4);
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.stream = st;
+    static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use all shared memory
+    if (dev >= 64 || !(allowed.load() >> dev & 1u)) {
+        e = cudaFuncSetAttribute(k_attend<K, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) allowed.fetch_or((uint64_t)1 << dev);
+    }
+    // both launches may begin before the one ahead of them has ended; they wait for it where they need it
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_attend<K, DP>, P, km, vm, qm);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(n - 1, 4);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, k_attend_merge<typename KindOf<K>::T, DP>, P);
 }
 

@@ -19,6 +19,8 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from .specverify import SV_BF16, _ptr, lib
 
 SV_F16, SV_E4M3 = 2, 3
@@ -94,54 +96,50 @@ def spec_cache_compact(cache, chunk, out_num_accepted, out_path, out_cached, dev
 # ------------------------------------------------------------------------------------------------
 # torch marshalling helpers
 # ------------------------------------------------------------------------------------------------
-def _codes():
-    import torch
-    return {torch.bfloat16: SV_BF16, torch.float16: SV_F16, torch.float8_e4m3fn: SV_E4M3}
+_ACTIVATIONS = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}
+_CACHES = {**_ACTIVATIONS, torch.float8_e4m3fn: SV_E4M3}
 
 
 def _check(t, name, dtypes, shape=None, device=None):
-    """A tensor argument's type, shape (None: any extent) and device."""
+    """A tensor argument's type, shape (None: any extent) and device number."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape))):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-
-
-def _stream(stream):
-    import torch
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    if shape is not None:
+        got = t.shape
+        if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(got)}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} must be on device {device}, got {t.device}")
 
 
 class Chunk:
     """One batch of chunks in the verify step's layout (device int32 tensors; see sv_chunk)."""
 
     def __init__(self, seq_offsets, cached, rows: int, max_gamma: int, parents=None):
-        import torch
         B = cached.numel()
         _check(cached, "cached", (torch.int32,), (B,))
-        _check(seq_offsets, "seq_offsets", (torch.int32,), (B + 1,), cached.device)
+        _check(seq_offsets, "seq_offsets", (torch.int32,), (B + 1,), cached.get_device())
         if parents is not None:
-            _check(parents, "parents", (torch.int32,), (None,), cached.device)
+            _check(parents, "parents", (torch.int32,), (None,), cached.get_device())
         for t, name in ((seq_offsets, "seq_offsets"), (cached, "cached"), (parents, "parents")):
             if t is not None and not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
         self.seq_offsets, self.cached, self.parents = seq_offsets, cached, parents
         self.B, self.rows, self.max_gamma = B, rows, max_gamma
         self.struct = SvChunk(_ptr(seq_offsets), _ptr(cached), _ptr(parents), B, rows, max_gamma, 0)
+        self.at = ctypes.addressof(self.struct)
 
 
 class Rope:
     """Rotary positions: a float32 table [positions, dim], cosines then sines (see sv_rope)."""
 
     def __init__(self, table, interleaved: bool = False):
-        import torch
         _check(table, "table", (torch.float32,), (None, None))
         if not table.is_contiguous():
             raise ValueError("table must be contiguous")
         self.table = table
         self.struct = SvRope(_ptr(table), table.shape[0], table.shape[1], int(interleaved), 0)
+        self.at = ctypes.addressof(self.struct)
 
 
 class PagedCache:
@@ -154,19 +152,18 @@ class PagedCache:
     """
 
     def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
-        import torch
-        codes = _codes()
+        codes = _CACHES
         _check(k, "k", tuple(codes), (None,) * 5)
-        _check(v, "v", (k.dtype,), k.shape, k.device)
+        _check(v, "v", (k.dtype,), k.shape, k.get_device())
         if k.stride() != v.stride() or k.stride(4) != 1:
             raise ValueError("k and v must have equal strides and contiguous heads")
-        _check(page_table, "page_table", (torch.int32,), (None, None), k.device)
+        _check(page_table, "page_table", (torch.int32,), (None, None), k.get_device())
         if page_table.shape[0] > 1 and page_table.stride(0) < page_table.shape[1] or page_table.stride(1) != 1:
             raise ValueError("page_table's rows must be contiguous")
         layers, pages, page_size, heads, dim = k.shape
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if t is not None:
-                _check(t, name, (torch.float32,), (layers, heads), k.device)
+                _check(t, name, (torch.float32,), (layers, heads), k.get_device())
                 if not t.is_contiguous():
                     raise ValueError(f"{name} must be contiguous")
         self.k, self.v, self.page_table, self.k_scale, self.v_scale = k, v, page_table, k_scale, v_scale
@@ -181,65 +178,78 @@ class PagedCache:
         self.ws_bytes = spec_cache_workspace_size(self.struct)
         self.workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=k.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
-        self._types = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}
+        # addresses that no call changes
+        self._at, self._status, self._ws = ctypes.addressof(self.struct), _ptr(self.status), _ptr(self.workspace)
+        self._device = k.get_device()
 
-    def _heads(self, t, name, rows, heads=None):
-        """Rows of [heads, head_dim], contiguous within a row: the row stride."""
-        if t.dim() != 3 or t.shape[0] < rows or t.shape[2] != self.head_dim or (heads and t.shape[1] != heads):
+    def _rows(self, t, name, rows, heads=None):
+        """Rows of [heads, head_dim], contiguous within a row: the row stride. These checks and the launch are all
+        that a call costs the host, a few microseconds."""
+        n, h, d = t.shape if t.dim() == 3 else (0, 0, 0)
+        if n < rows or d != self.head_dim or (heads is not None and h != heads):
             raise ValueError(f"{name} must be [{rows}, {heads or 'heads'}, {self.head_dim}], got {tuple(t.shape)}")
-        if t.stride(2) != 1 or (t.stride(1) != self.head_dim and t.shape[1] > 1):
+        if t.get_device() != self._device:
+            raise ValueError(f"{name} must be on {self.k.device}, got {t.device}")
+        s0, s1, s2 = t.stride()
+        if s2 != 1 or (s1 != d and h > 1):
             raise ValueError(f"{name}'s heads must be contiguous within a row")
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * self.head_dim
+        return s0 if n > 1 else h * d
 
     def _type(self, *ts):
-        code = self._types.get(ts[0].dtype)
-        if code is None or any(t.dtype != ts[0].dtype for t in ts):
-            raise TypeError(f"tensors must share bfloat16 or float16, got {[str(t.dtype) for t in ts]}")
-        return code
+        raise TypeError(f"tensors must share bfloat16 or float16, got {[str(t.dtype) for t in ts]}")
+
+    def _stream(self, stream):
+        if stream is not None:
+            return stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self._device)  # the current stream's handle alone
 
     def append(self, chunk: Chunk, q, k, v, q_out, rope: Rope | None = None, layer: int = 0, stream=None) -> int:
         """Enqueue spec_cache_append: rotated queries to q_out, rotated keys and values to the cache. q and
         q_out may be None."""
-        code = self._type(k, v) if q is None else self._type(k, v, q, q_out)
-        ks = self._heads(k, "k", chunk.rows, self.heads)
-        if self._heads(v, "v", chunk.rows, self.heads) != ks:
+        rows, kind = chunk.rows, k.dtype
+        code = _ACTIVATIONS.get(kind)
+        if code is None or v.dtype != kind or (q is not None and (q.dtype != kind or q_out.dtype != kind)):
+            self._type(*(t for t in (q, k, v, q_out) if t is not None))
+        ks = self._rows(k, "k", rows, self.heads)
+        if self._rows(v, "v", rows, self.heads) != ks:
             raise ValueError("k and v must have equal row strides")
         qh, qs = 0, 0
         if q is not None:
-            qh, qs = q.shape[1], self._heads(q, "q", chunk.rows)
-            if self._heads(q_out, "q_out", chunk.rows, qh) != qh * self.head_dim:
+            qs, qh = self._rows(q, "q", rows), q.shape[1]
+            if self._rows(q_out, "q_out", rows, qh) != qh * self.head_dim:
                 raise ValueError("q_out must be contiguous")
-        return spec_cache_append(self.struct, layer, chunk.struct, None if rope is None else rope.struct, code, qh,
-                                 _ptr(q), qs, _ptr(k), _ptr(v), ks, _ptr(q_out), _ptr(self.status), _stream(stream))
+        return lib.spec_cache_append(self._at, layer, chunk.at, None if rope is None else rope.at, code, qh, _ptr(q), qs,
+                                     k.data_ptr(), v.data_ptr(), ks, _ptr(q_out), self._status, self._stream(stream))
 
     def attend(self, chunk: Chunk, q, out, lse=None, scale: float | None = None, window: int = 0, layer: int = 0,
                stream=None) -> int:
         """Enqueue spec_cache_attend: attention of the chunk's rotated queries into out (and lse, float32
         [rows, q_heads]). scale: 1 / sqrt(head_dim) by default."""
-        import torch
-        code = self._type(q, out)
-        qh, qs = q.shape[1], self._heads(q, "q", chunk.rows)
-        if self._heads(out, "out", chunk.rows, qh) != qh * self.head_dim:
+        rows, kind = chunk.rows, q.dtype
+        code = _ACTIVATIONS.get(kind)
+        if code is None or out.dtype != kind:
+            self._type(q, out)
+        qs, qh = self._rows(q, "q", rows), q.shape[1]
+        if self._rows(out, "out", rows, qh) != qh * self.head_dim:
             raise ValueError("out must be contiguous")
         if lse is not None:
-            _check(lse, "lse", (torch.float32,), (None, qh))
-            if lse.shape[0] < chunk.rows or not lse.is_contiguous():
+            _check(lse, "lse", (torch.float32,), (None, qh), self._device)
+            if lse.shape[0] < rows or not lse.is_contiguous():
                 raise ValueError("lse must be contiguous with a row for every chunk row")
         if scale is None:
             scale = self.head_dim ** -0.5
-        return spec_cache_attend(self.struct, layer, chunk.struct, code, qh, _ptr(q), qs, scale, window, _ptr(out),
-                                 _ptr(lse), _ptr(self.status), _ptr(self.workspace), self.ws_bytes, _stream(stream))
+        return lib.spec_cache_attend(self._at, layer, chunk.at, code, qh, q.data_ptr(), qs, scale, window, out.data_ptr(),
+                                     _ptr(lse), self._status, self._ws, self.ws_bytes, self._stream(stream))
 
     def compact(self, chunk: Chunk, out_num_accepted, out_path, out_cached, stream=None) -> int:
         """Enqueue spec_cache_compact on a verify call's outputs. out_path None: linear drafts. out_cached may
         be the chunk's `cached`."""
-        import torch
-        _check(out_num_accepted, "out_num_accepted", (torch.int32,), (chunk.B,))
-        _check(out_cached, "out_cached", (torch.int32,), (chunk.B,))
+        _check(out_num_accepted, "out_num_accepted", (torch.int32,), (chunk.B,), self._device)
+        _check(out_cached, "out_cached", (torch.int32,), (chunk.B,), self._device)
         if out_path is not None:
-            _check(out_path, "out_path", (torch.int32,), (None,))
-        return spec_cache_compact(self.struct, chunk.struct, _ptr(out_num_accepted), _ptr(out_path), _ptr(out_cached),
-                                  _ptr(self.status), _stream(stream))
+            _check(out_path, "out_path", (torch.int32,), (None,), self._device)
+        return lib.spec_cache_compact(self._at, chunk.at, out_num_accepted.data_ptr(), _ptr(out_path),
+                                      out_cached.data_ptr(), self._status, self._stream(stream))
 
     def status_bits(self) -> int:
         return int(self.status.item()) & 0xFFFFFFFF
