@@ -1,0 +1,591 @@
+// spec_cache_attend for chunks of up to 64 rows (a row is a token and a query head of the group): plain decoding and
+// drafts. The mathematics, the numbering of the work and its split over the CTAs are sv_cache_attend.cu's.
+//
+// Such a chunk is bound by the bytes of its keys and values: a tile of 128 slots takes an SM about 2800 cycles to
+// bring in at the HBM rate (16 bits, D = 128), half of that with D = 64 or 8 bits, so whatever is done per tile has
+// to fit beneath. With the rows as the first dimension of a product (128 lanes) most of a softmax is padding, and
+// the few real rows sit in one warp, 128 scores each: 1300 to 3000 cycles a tile measured, more than the loads.
+// The products are therefore turned around,
+//     S^T = K Q^T  (128 slots x rows),   O^T += V^T P^T  (D x rows),
+// with the slots on the lanes: every thread has one slot and as many scores as there are rows, all four warps of a
+// group work, and rows are rounded up to 16, 32 or 64 columns only. The weights go to shared memory, the product's
+// other operand; a row's sum stays spread over the lanes until the item ends. All threads hold their weights against
+// the rows' references, and one word tells the four warps of a group when a reference has to move (a first tile, or
+// a weight too large for its type), which costs three more barriers and a pass of maxima.
+//
+// Up to 32 rows a CTA has one softmax warpgroup, and two CTAs share an SM: one's beginnings and endings of items (a
+// fifth of the time of an item of ten tiles) lie under the other's tiles. Above that two operand sets would leave an
+// SM four tiles of 16 bits and D = 128, too few in flight, so there is one CTA, whose two warpgroups have half of the
+// rows each. Measured at 6.7 TB/s of copy rate, bfloat16, D = 128: 64 sequences of 6 tokens, 512 to 8192 long, 4
+// heads a group, 139 us (0.81 of the copy rate; 133 to 141 us with the rows on the lanes
+// and tiles taken by two warpgroups in turn); 2 sequences of 8 tokens, 8 heads a group, 164 us (0.90; two CTAs an SM
+// 213 us, rows on the lanes 180 us). 128 sequences of one token with a window of 1024: 74 us (128 us before). e4m3
+// cache, 32 sequences of 4 tokens: 121 us (150 us before).
+#include "sv_cache_attend.cuh"
+
+#include <type_traits>
+
+namespace sv {
+namespace cache {
+namespace {
+
+// The weights' tile: a slot's weights lie side by side, NR of them (e4m3: NR bytes for hi, then another tile for lo).
+template <int K, int NR>
+struct Weights {
+    static constexpr int kPitch = NR * KindOf<K>::kBytes;  // 32, 64 or 128 bytes, the width of the swizzle
+    static constexpr int kPart = kTile * kPitch;
+    static constexpr int kBytes = kPart * (K == kE4m3 ? 2 : 1);
+    static constexpr uint32_t kSwizzle = kPitch == 128 ? 2u : kPitch == 64 ? 4u : 6u;
+    static constexpr uint32_t kHigh = (uint32_t)(8 * kPitch) >> 4 | 1u << 14 | kSwizzle << 29;
+    static_assert(kPitch >= 32 && kPitch <= 128, "a swizzle's width");
+    // where the 16 bytes c of a slot lie
+    static __device__ __forceinline__ uint32_t at(uint32_t slot, uint32_t c) {
+        return slot * kPitch + ((c ^ ((slot * kPitch >> 7) & (kPitch / 16 - 1))) << 4);
+    }
+};
+
+// With G softmax warpgroups each has NR / G rows of every tile; then comes a warp for each other role.
+template <int G>
+constexpr int kThreads = (G + 1) * 128;
+constexpr int kReaders = 1 + 1 + 1;  // of an item, besides the softmax warps: loader, products, values
+constexpr int kHalfSm = 113 * 1024;  // of shared memory
+
+// What a group's warps tell each other now and then: when the references move, and at an item's end.
+template <int N>
+struct Notes {
+    float part[4][N];  // per warp: a row's maximum; at the end its sum
+    float sub[N];      // by how much the reference moves; at the end what O is scaled by
+    float fac[N];      // 2^-sub
+    float off[N];      // what is added to a row's scaled scores: kShift - reference
+};
+struct Nothing {};
+
+// One group's notes lie in the weights' place, while no product reads that. Two groups are not at the same step.
+template <int N, int G>
+struct alignas(16) Group : std::conditional<G == 1, Nothing, Notes<N>>::type {
+    float ref[N];  // the rows' references (log2)
+    uint64_t vote;
+    int again[3];  // votes in turn: some weight is too large
+    int unset;     // some row has no reference yet
+    int moved;     // some row's O is to be scaled
+};
+
+template <int NR, int G>
+struct alignas(16) Shared : Common {
+    uint64_t s_full[2], p_ready, pv_done;
+    Group<NR / G, G> group[G];
+};
+
+// A barrier of the softmax warps.
+struct Vote {
+    uint32_t bar, parity;
+    volatile int* gave_up;
+    __device__ __forceinline__ bool operator()() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) bar_arrive(bar);
+        const bool ok = wait(bar, parity, gave_up);
+        parity ^= 1u;
+        return ok;
+    }
+};
+
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t prefix32(int32_t n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+__device__ __forceinline__ void tc_ld16(uint32_t col, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : SV_R8(r, 0), SV_R8(r, 8)
+                 : "r"(col));
+}
+__device__ __forceinline__ void tc_ld1(uint32_t col, uint32_t& r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(col));
+}
+__device__ __forceinline__ void tc_st1(uint32_t col, uint32_t r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(col), "r"(r) : "memory");
+}
+
+// The rows that see a slot, as bits, the first of them row0.
+__device__ __forceinline__ uint32_t rows_seeing(const Params& P, const Item& it, const Tree* tree, int32_t slot, uint32_t bad,
+                                                int32_t row0) {
+    if (slot < it.lo || slot >= it.end || (bad >> (slot % kTile >> 3) & 1u)) return 0;
+    const int32_t i = slot - it.past, w = P.a.window;  // its place in the chunk, if it has one
+    if (!tree) {
+        const int32_t first = max(0, i), last = w > 0 ? min(it.nt - 1, i + w - 1) : it.nt - 1;
+        return prefix32((last + 1) * P.G - row0) & ~prefix32(first * P.G - row0);
+    }
+    if (i < 0 && w <= 0) return prefix32(it.nt * P.G - row0);
+    uint32_t m = 0;
+#pragma unroll 1
+    for (int32_t t = 0; t < it.nt; ++t)
+        if (i < 0 ? tree->depth[t] - i < w : tree->above[t] >> i & 1u) m |= prefix32((t + 1) * P.G - row0) & ~prefix32(t * P.G - row0);
+    return m;
+}
+
+template <int K, int NR, int G>
+__device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh, char* weights) {
+    using KT = KindOf<K>;
+    using T = typename KT::T;
+    using Wt = Weights<K, NR>;
+    const AttendArgs& A = P.a;
+    constexpr int N = NR / G;  // the group's rows, from row0 on
+    const int k = threadIdx.x & 127, lane = threadIdx.x & 31, warp = k >> 5, row0 = threadIdx.x / 128 * N;
+    Group<N, G>& mine = sh.group[threadIdx.x / 128];
+    const uint32_t lanes = (uint32_t)(k & ~31) << 16, tmem = sh.tmem + lanes + row0, p_smem = smem_u32(weights);
+    const uint32_t o_col = tmem + 2 * NR;
+    const uint32_t p_ready = smem_u32(&sh.p_ready), pv_done = smem_u32(&sh.pv_done);
+    Notes<N>& notes = *(G == 1 ? reinterpret_cast<Notes<N>*>(weights) : reinterpret_cast<Notes<N>*>(&mine));
+    static_assert(sizeof(Notes<N>) <= Wt::kBytes, "the notes fit");
+    const int32_t D = A.pool.dim;
+    volatile int* gave_up = &sh.gave_up;
+    Vote vote{smem_u32(&mine.vote), 0, gave_up};
+    uint32_t steps = 0, tiles = 0, items = 0, votes = 0;  // votes: on weights, modulo 3
+    Items walk(sh);
+    Item it;
+#pragma unroll 1
+    for (; walk.next(it); ++items) {
+        const Tree* tree = A.chunk.parents ? &walk.tree() : nullptr;
+        const int32_t rows = min(N, it.nt * P.G - row0);  // none or less: a group without work
+        bool flip;
+        const float unit = score_unit(A, it.h, flip);
+        float l[N], off[N], u[K == kE4m3 ? N : 1];
+        u[0] = unit;
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+            l[r] = 0.f;
+            off[r] = KT::kShift;
+        }
+#pragma unroll 1
+        for (int32_t j = 0; j < it.n; ++j, ++steps) {
+            const uint32_t buf = steps & 1;
+            if (!wait(smem_u32(&sh.s_full[buf]), steps >> 1 & 1, gave_up)) return;
+            tc_after();
+            if (K == kE4m3 && j == 0)
+#pragma unroll
+                for (int r = 0; r < (K == kE4m3 ? N : 1); ++r) u[r] = unit * sh.q_down[(items & 1) * sh.q_rows + row0 + r];
+            const uint32_t s_col = tmem + buf * NR;
+            const int32_t k0 = (it.tile + j) * kTile;
+            const uint32_t ring = (tiles + j) % kNotes;
+            const uint32_t bad = sh.bad[0][ring];
+            uint32_t s[N];
+#pragma unroll
+            for (int c = 0; c < N; c += 16) tc_ld16(s_col + c, s + c);
+            tc_wait_ld();
+            if (k0 < max(it.lo, it.mixed_lo) || k0 + kTile > min(it.mixed_hi, it.end) || bad) {
+                const uint32_t seen = rows_seeing(P, it, tree, k0 + k, bad, row0);
+#pragma unroll
+                for (int r = 0; r < N; ++r)
+                    if (!(seen >> r & 1u)) s[r] = 0xff800000u;
+            }
+            // the weights' logarithms against the references (a first tile's: against none)
+            float top = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+                const float y = fmaf(__uint_as_float(s[r]), u[K == kE4m3 ? r : 0], off[r]);
+                s[r] = __float_as_uint(y);
+                top = fmaxf(top, y);
+            }
+            bool fresh = j == 0 || mine.unset;
+            if (!fresh) {
+                // before anyone can pass this vote, everyone has read the last one's word but two
+                constexpr float most = K == kBf16 ? 64.f : K == kFp16 ? 15.f : 8.75f;
+                if (k == 0) mine.again[votes == 2 ? 0 : votes + 1] = 0;
+                if (__any_sync(kAll, top > most) && lane == 0) mine.again[votes] = 1;
+                if (!vote()) return;
+                fresh = mine.again[votes];
+                votes = votes == 2 ? 0 : votes + 1;
+            }
+            if (fresh) {
+                if (j > 0) {  // O is whole, and the notes' place free, once the last step's product has been
+                    if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
+                    tc_after();
+                }
+                // the rows' maxima, by warp, then by one thread a row
+#pragma unroll
+                for (int r = 0; r < N; ++r) {
+                    const float x = warp_max(__uint_as_float(s[r]));
+                    if (lane == r) notes.part[warp][r] = x;
+                }
+                if (!vote()) return;
+                if (warp == 0) {
+                    const int r = lane % N;
+                    const float old = j == 0 ? -INFINITY : mine.ref[r];
+                    const float mx = fmaxf(fmaxf(notes.part[0][r], notes.part[1][r]), fmaxf(notes.part[2][r], notes.part[3][r])) -
+                                     KT::kShift;
+                    // against none: to the maximum, if there is one; else upwards only
+                    const bool has = old != -INFINITY, any = mx != -INFINITY;
+                    const float d = has ? fmaxf(mx, 0.f) : any ? mx : 0.f;
+                    const float ref = has ? old + d : any ? d : -INFINITY;
+                    __syncwarp();
+                    mine.ref[r] = ref;
+                    notes.sub[r] = d;
+                    notes.off[r] = KT::kShift - (ref == -INFINITY ? 0.f : ref);
+                    notes.fac[r] = has ? exp2_fast(-d) : 1.f;
+                    const bool unset = __any_sync(kAll, r < rows && ref == -INFINITY), moved = __any_sync(kAll, has && d > 0.f);
+                    if (lane == 0) {
+                        mine.unset = unset;
+                        mine.moved = moved;
+                    }
+                }
+                if (!vote()) return;
+                const bool moved = mine.moved;
+#pragma unroll
+                for (int r = 0; r < N; ++r) {
+                    s[r] = __float_as_uint(__uint_as_float(s[r]) - notes.sub[r]);
+                    off[r] = notes.off[r];
+                    l[r] *= notes.fac[r];
+                }
+                if (moved)
+#pragma unroll 1
+                    for (int c = 0; c < rows; ++c) {
+                        uint32_t o;
+                        tc_ld1(o_col + c, o);
+                        tc_wait_ld();
+                        tc_st1(o_col + c, __float_as_uint(__uint_as_float(o) * notes.fac[c]));
+                    }
+                tc_wait_st();
+                if (!vote()) return;  // the notes have been read
+            }
+            uint32_t pk[N / 2];  // 16 bits: pairs; e4m3: hi in the first half, lo in the second
+#pragma unroll
+            for (int r = 0; r < N; r += 4) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = exp2_fast(__uint_as_float(s[r + e]));
+                    l[r + e] += p[e];
+                }
+                if (K != kE4m3) {
+                    pk[r / 2] = from_float2<T>(p[0], p[1]);
+                    pk[r / 2 + 1] = from_float2<T>(p[2], p[3]);
+                } else {
+                    uint32_t a, b, c, d;
+                    split_pair(p[0], p[1], a, c);
+                    split_pair(p[2], p[3], b, d);
+                    pk[r / 4] = a | b << 16;
+                    pk[N / 4 + r / 4] = c | d << 16;
+                }
+            }
+            // the weights' place is free once the last step's product has been
+            if (j > 0 && !wait(pv_done, (steps - 1) & 1, gave_up)) return;
+            constexpr int kWide = N * KT::kBytes / 16;
+#pragma unroll
+            for (int c = 0; c < kWide; ++c)
+#pragma unroll
+                for (int part = 0; part < (K == kE4m3 ? 2 : 1); ++part) {
+                    const uint32_t* u = pk + part * (N / 4) + 4 * c;
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(p_smem + part * Wt::kPart + Wt::at(k, row0 / N * kWide + c)), "r"(u[0]),
+                                 "r"(u[1]), "r"(u[2]), "r"(u[3])
+                                 : "memory");
+                }
+            const bool mixed = mixed_tile(it, k0);
+            if (mixed) {  // before p_ready: the tile cannot be released, nor its barrier move on, until then
+                const uint32_t v = tiles + j;
+                if (!wait(smem_u32(&sh.value[v % P.v_slots]), (v / P.v_slots) & 1, gave_up)) return;
+            }
+            fence_async();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(p_ready);
+            if (mixed) {
+                // rows that see a non-finite value, which the product met as zero, get it added here
+                uint32_t any = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) any |= sh.odd[ring][i];
+                if (any) {
+                    if (!wait(pv_done, steps & 1, gave_up)) return;
+                    tc_after();
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+                        for (uint32_t w = sh.odd[ring][i]; w; w &= w - 1) {
+                            const int32_t slot = k0 + 32 * i + __ffs(w) - 1;
+                            const int64_t at = place_of(A.pool, it.b, slot) + it.h * A.pool.s_head + k;
+                            float x = 0.f;
+                            if (k < D) {
+                                if (K == kE4m3) x = (((const uint8_t*)A.pool.v)[at] & 0x7f) == 0x7f ? NAN : 0.f;
+                                else x = (float)((const T*)A.pool.v)[at];
+                            }
+                            if (isfinite(x)) x = 0.f;
+                            const uint32_t m = rows_seeing(P, it, tree, slot, bad, row0);
+#pragma unroll 1
+                            for (int c = 0; c < rows; ++c) {
+                                uint32_t o;
+                                tc_ld1(o_col + c, o);
+                                tc_wait_ld();
+                                if (m >> c & 1u) o = __float_as_uint(__uint_as_float(o) + x);
+                                __syncwarp();
+                                tc_st1(o_col + c, o);
+                                tc_wait_st();
+                            }
+                        }
+                    tc_before();
+                }
+            }
+        }
+        tiles += it.n;
+
+        // the item's end: the rows' sums over the lanes
+        // lanes exchange halves of what they hold until each has one row's sum over the warp
+#pragma unroll
+        for (int e = 0; e < 5; ++e) {
+            const int o = 16 >> e, half = N >> (e + 1);
+            if (half == 0) l[0] += __shfl_xor_sync(kAll, l[0], o);
+#pragma unroll
+            for (int r = 0; r < half; ++r) {
+                const bool up = lane & o;
+                const float give = up ? l[r] : l[r + half], keep = up ? l[r + half] : l[r];
+                l[r] = keep + __shfl_xor_sync(kAll, give, o);
+            }
+        }
+        if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
+        tc_after();
+        if (N == 32) {
+            notes.part[warp][(lane >> 4 & 1) * 16 + (lane >> 3 & 1) * 8 + (lane >> 2 & 1) * 4 + (lane >> 1 & 1) * 2 + (lane & 1)] =
+                l[0];
+        } else if (!(lane & 1)) {
+            notes.part[warp][(lane >> 4 & 1) * 8 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2 + (lane >> 1 & 1)] = l[0];
+        }
+        if (!vote()) return;
+        const bool alone = it.begins && it.finishes;
+        const size_t part = (size_t)(2 * blockIdx.x + (it.begins ? 1 : 0)) * P.part_rows + row0;
+        if (k < rows) {
+            const float total = (notes.part[0][k] + notes.part[1][k]) + (notes.part[2][k] + notes.part[3][k]),
+                        ref = mine.ref[k] - KT::kShift;
+            float f = 1.f;
+            if (alone) {
+                const float vs = A.pool.v_scale ? A.pool.v_scale[it.h] : 1.f;
+                const int32_t row = row0 + k, t = row / P.G;
+                f = total == 0.f ? 0.f : vs / total;
+                if (A.lse)
+                    A.lse[(int64_t)(it.row0 + it.t0 + t) * A.q_heads + it.h * P.G + row - t * P.G] =
+                        total == 0.f ? -INFINITY : ref * kLn2 + logf(total);
+            } else {
+                P.part_ml[part + k] = make_float2(ref, total);
+            }
+            notes.sub[k] = f;
+        }
+        if (!vote()) return;
+        const int32_t dp = K == kE4m3 || D > 64 ? 128 : 64;
+        const int32_t t0 = row0 / P.G;
+        int32_t g = row0 - t0 * P.G;
+        T* out = (T*)A.out + ((int64_t)(it.row0 + it.t0 + t0) * A.q_heads + it.h * P.G + g) * D + k;
+        float* out_part = P.part_o + part * dp + k;
+#pragma unroll 1
+        for (int c = 0; c < rows; c += 4) {
+            uint32_t o[4];
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+                         : "r"(o_col + c));
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = __uint_as_float(o[i]) * notes.sub[c + i];
+                if (k < D && c + i < rows) {
+                    if (alone) *out = (T)x;
+                    else out_part[(c + i) * dp] = x;
+                }
+                out += D;
+                if (++g == P.G) {  // the next token's heads
+                    g = 0;
+                    out += (int64_t)(A.q_heads - P.G) * D;
+                }
+            }
+        }
+        tc_before();
+    }
+}
+
+// The products, by one thread. Scores run two tiles ahead of outputs, in two buffers.
+template <int K, int NR, int G>
+__device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh, uint32_t q_smem, uint32_t p_smem, uint32_t k_smem,
+                                             uint32_t v_smem) {
+    constexpr bool k8 = K == kE4m3;
+    constexpr int parts = k8 ? 2 : 1;
+    constexpr uint32_t fmt = K == kBf16 ? 1u : 0u;
+    using Wt = Weights<K, NR>;
+    const int32_t D = P.a.pool.dim;
+    const int32_t depth = (D + KindOf<K>::kStep - 1) / KindOf<K>::kStep;
+    const uint32_t slot_bytes = P.halves * kHalf;
+    // float accumulators, 128 lanes, NR columns; of O both operands' rows lie along the depth
+    const uint32_t id_s = 1u << 4 | fmt << 7 | fmt << 10 | (uint32_t)(NR >> 3) << 17 | (uint32_t)(kTile >> 4) << 24;
+    const uint32_t id_o = id_s | 3u << 15;
+    const uint32_t tmem = __shfl_sync(kAll, sh.tmem, 0), o_at = tmem + 2 * NR;
+    const uint32_t k_full = smem_u32(sh.k_full), k_empty = smem_u32(sh.k_empty), v_empty = smem_u32(sh.v_empty),
+                   value = smem_u32(sh.value), s_full = smem_u32(sh.s_full), p_ready = smem_u32(&sh.p_ready),
+                   pv_done = smem_u32(&sh.pv_done), q_empty = smem_u32(&sh.q_empty);
+    const uint32_t q = operand(q_smem, 16), q_part = (uint32_t)P.q_part >> 4, p = operand(p_smem, 16);
+    const bool leader = elect();
+    volatile int* gave_up = &sh.gave_up;
+    uint32_t items = 0, p_parity = 0, buf = 0;  // buf: of the next scores
+    Ring kr, vr;
+    Items walk(sh);
+    Item it;
+    bool ok = true;
+#pragma unroll 1
+    while (ok && walk.next(it)) {
+        if (!(ok = wait(smem_u32(&sh.q_full), items & 1, gave_up))) break;
+        tc_after();
+        const int32_t n = __shfl_sync(kAll, it.n, 0);
+#pragma unroll 1
+        for (int32_t t = -2; t < n; ++t) {  // outputs of tile t, scores of the next but one
+            if (t >= 0) {
+                if (!(ok = wait(value + 8 * vr.i, vr.parity, gave_up) && wait(p_ready, p_parity, gave_up))) break;
+                p_parity ^= 1u;
+                tc_after();
+                // D <= 64: the upper 64 lanes repeat the lower ones' columns
+                const uint32_t a = operand(v_smem + vr.i * slot_bytes, slot_bytes > kHalf ? kHalf : 0);
+                if (leader) {
+#pragma unroll 2
+                    for (int i = 0; i < kTile / KindOf<K>::kStep; ++i)
+#pragma unroll
+                        for (int part = 0; part < parts; ++part)
+                            mma_mixed<k8, Wt::kHigh>(o_at, a + (i * KindOf<K>::kStep * 128 >> 4),
+                                                     p + (part * Wt::kPart + i * KindOf<K>::kStep * Wt::kPitch >> 4), id_o,
+                                                     (uint32_t)(t + part + i > 0));
+                    tc_commit(pv_done);
+                    tc_commit(v_empty + 8 * vr.i);
+                }
+                __syncwarp();
+                vr.step(P.v_slots);
+            }
+            if (t + 2 < n) {
+                if (!(ok = wait(k_full + 8 * kr.i, kr.parity, gave_up))) break;
+                const uint32_t a = operand(k_smem + kr.i * slot_bytes, 16), d = tmem + buf * NR;
+                if (leader) {
+#pragma unroll
+                    for (int part = 0; part < parts; ++part)
+#pragma unroll 2
+                        for (int i = 0; i < depth; ++i) {
+                            const uint32_t in = (i & 3) * 32 >> 4;
+                            mma_ss<k8>(d, a + (i >> 2) * (kHalf >> 4) + in, q + (k8 ? part : i >> 2) * q_part + in, id_s,
+                                       part + i > 0);
+                        }
+                    tc_commit(s_full + 8 * buf);
+                    tc_commit(k_empty + 8 * kr.i);
+                    if (t + 3 == n) tc_commit(q_empty);
+                }
+                __syncwarp();
+                kr.step(P.k_slots);
+                buf ^= 1u;
+            }
+        }
+        ++items;
+    }
+    // products under way end before the tensor memory is given back
+    if (leader) tc_commit(smem_u32(&sh.drain));
+    __syncwarp();
+    int none = 0;
+    wait(smem_u32(&sh.drain), 0, &none);
+}
+
+template <int K, int NR, int G>
+__global__ void __launch_bounds__(kThreads<G>, G == 1 ? 2 : 1)
+    k_attend_few(const __grid_constant__ Params P, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
+                 const __grid_constant__ CUtensorMap qm) {
+    constexpr int columns = 4 * NR;  // three times NR are used
+    extern __shared__ __align__(1024) char raw[];
+    const uint32_t slot_bytes = P.halves * kHalf;
+    const uint32_t q_smem = smem_u32(raw), p_smem = q_smem + P.q_tile, k_smem = p_smem + Weights<K, NR>::kBytes,
+                   v_smem = k_smem + P.k_slots * slot_bytes;
+    char* behind = raw + (v_smem - q_smem) + P.v_slots * slot_bytes;
+    Shared<NR, G>& sh = *reinterpret_cast<Shared<NR, G>*>(behind);
+    if (q_smem & 1023u) {  // the tiles' swizzle counts on it
+        if (threadIdx.x == 0) report(P.a.status, 1u << SV_ERR_CUDA);
+        return;
+    }
+    const int tid = threadIdx.x, w = tid >> 5;
+    if (tid == 0) {
+        init_common(sh, 1, 4 * G + kReaders);
+        bar_init(smem_u32(&sh.s_full[0]), 1);
+        bar_init(smem_u32(&sh.s_full[1]), 1);
+        bar_init(smem_u32(&sh.p_ready), 4 * G);
+        bar_init(smem_u32(&sh.pv_done), 1);
+        for (int g = 0; g < G; ++g) {
+            bar_init(smem_u32(&sh.group[g].vote), 4);
+            sh.group[g].again[0] = 0;
+        }
+        sh.q_rows = NR;
+        sh.tree = reinterpret_cast<Tree*>(behind + (sizeof(sh) + 15) / 16 * 16);
+        sh.q_down = reinterpret_cast<float*>(sh.tree + (P.a.chunk.parents ? kItems : 0));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // query rows past the copies' last one stay zero
+    for (int i = tid; i < P.q_tile / 16; i += kThreads<G>) reinterpret_cast<uint4*>(raw)[i] = make_uint4(0, 0, 0, 0);
+    fence_async();
+    const int role = w - 4 * G;
+    if (role == 0 && (tid & 31) == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&km));
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&vm));
+        if (K != kE4m3) asm volatile("prefetch.tensormap [%0];" ::"l"(&qm));
+    }
+    if (role == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "n"(columns)
+                     : "memory");
+        // else the SM's other CTA could not allocate before this one ends
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    begin<kThreads<G>>(P, sh);
+    // at launch 128 registers a thread for one group, 168 for two
+    if (role < 0) {
+        if (G == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        softmax_role<K, NR, G>(P, sh, raw + P.q_tile);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (role == 0) load_role(P, sh, k_smem, v_smem, &km, &vm, 0, 1);
+        else if (role == 1) product_role<K, NR, G>(P, sh, q_smem, p_smem, k_smem, v_smem);
+        else if (role == 2) value_role<K>(P, sh, q_smem, v_smem, &qm);
+        else item_role(P, sh);
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (role == 1) {
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "n"(columns));
+    }
+    if (tid == 0 && sh.gave_up) report(P.a.status, 1u << SV_ERR_TIMEOUT);
+}
+
+template <int K, int NR, int G>
+cudaError_t launch(Params& P, int sms, cudaStream_t st) {
+    const AttendArgs& A = P.a;
+    P.ctas = G == 1 ? 2 * sms : sms;
+    const int halves = P.halves = K == kE4m3 || A.pool.dim <= 64 ? 1 : 2;
+    P.tokens = P.block = A.chunk.max_gamma + 1;
+    P.q_box = P.tokens;
+    P.q_part = NR * 128;
+    P.q_tile = (K == kE4m3 ? 2 : halves) * P.q_part;
+    const int own = (int)(sizeof(Shared<NR, G>) + 15) / 16 * 16 + (A.chunk.parents ? kItems * (int)sizeof(Tree) : 0) +
+                    (K == kE4m3 ? 2 * NR * 4 : 0);
+    const int rest = P.q_tile + Weights<K, NR>::kBytes + own;
+    const int slots = min(2 * kMaxSlots, ((G == 1 ? kHalfSm : kSmem) - rest) / (halves * kHalf));
+    P.k_slots = slots / 2;
+    P.v_slots = slots - P.k_slots;
+    CUtensorMap km, vm, qm;
+    if (K != kE4m3 && !encode_queries(&qm, A, K, P.G, P.q_box)) return cudaErrorInvalidValue;
+    if (!encode_pool(&km, A.pool, A.pool.k, KindOf<K>::kBytes, K, P.box) ||
+        !encode_pool(&vm, A.pool, A.pool.v, KindOf<K>::kBytes, K, P.box))
+        return cudaErrorInvalidValue;
+    static std::atomic<unsigned long long> allowed{0};
+    void* args[] = {&P, &km, &vm, &qm};
+    return launch_early((const void*)k_attend_few<K, NR, G>, &allowed, dim3(P.ctas), kThreads<G>, rest + slots * halves * kHalf, st, args);
+}
+
+template <int K>
+cudaError_t choose(Params& P, int rows, int sms, cudaStream_t st) {
+    P.part_rows = kFewRows;
+    if (K != kE4m3 && rows <= 16) return launch<K, K == kE4m3 ? 32 : 16, 1>(P, sms, st);
+    return rows <= 32 ? launch<K, 32, 1>(P, sms, st) : launch<K, 64, 2>(P, sms, st);
+}
+
+}  // namespace
+
+cudaError_t launch_few(Params& P, int kind, int rows, int sms, cudaStream_t st) {
+    return kind == kE4m3 ? choose<kE4m3>(P, rows, sms, st) : kind == kFp16 ? choose<kFp16>(P, rows, sms, st) : choose<kBf16>(P, rows, sms, st);
+}
+
+}  // namespace cache
+}  // namespace sv
