@@ -227,12 +227,11 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
     const int32_t tl = r / P.G, g = r - tl * P.G;
     uint32_t steps = 0;   // of this stream, over all items
     uint32_t tiles = 0;   // of the CTA, before this item
-    uint32_t items = 0;
 
     Items walk(sh);
     Item it;
 #pragma unroll 1
-    for (; walk.next(it); ++items) {
+    while (walk.next(it)) {
         Row row = row_of(P, it, walk, stream, tl);
         float m = -INFINITY, l = 0.f;
         const bool busy = __any_sync(kAll, row.real);
@@ -240,7 +239,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
         for (int32_t j = 0; j < it.n; ++j, ++steps) {
             if (!wait(s_full, steps & 1, gave_up)) return;
             tc_after();
-            if (K == kE4m3 && j == 0) row.sl *= sh.q_down[(items & 1) * sh.q_rows + stream * kTile + r];
+            if (K == kE4m3 && j == 0) row.sl *= sh.q_down[walk.ring.i * sh.q_rows + stream * kTile + r];
             const int32_t k0 = (it.tile + j) * kTile;
             const uint32_t ring = (tiles + j) % kNotes;
             uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
@@ -499,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (w == 8 || w == 10) load_role(P, sh, k_smem, v_smem, &km, &vm, w == 10, w == 10);
         else if (w == 9 || w == 13) product_role<K, NH>(P, sh, q_smem, k_smem, v_smem, w == 13);
-        else if (w == 11) value_role<K>(P, sh, q_smem, v_smem, &qm);
-        else if (w == 12) item_role(P, sh);
+        else if (w == 11) value_role<K>(P, sh, v_smem);
+        else if (w == 12) item_role<K>(P, sh, q_smem, &qm);
     }
     tc_before();
     __syncthreads();
@@ -581,10 +580,11 @@ cudaError_t launch(Params P, int n, cudaStream_t st) {
     P.block = 2 * P.tokens;
     P.q_box = min(P.tokens, A.chunk.max_gamma + 1);
     P.q_part = kHalf;
+    P.lead = 5;  // measured, as the other launch's
     P.halves = NH;
     P.q_tile = (K == kE4m3 ? 2 : NH) * kHalf;
     const int own = (int)(sizeof(Shared) + 15) / 16 * 16 + (A.chunk.parents ? kItems * (int)sizeof(Tree) : 0) +
-                    (K == kE4m3 ? 2 * 2 * kTile * 4 : 0);
+                    (K == kE4m3 ? kItems * 2 * kTile * 4 : 0);
     const int slots = min(2 * kMaxSlots, (kSmem - own - 2 * P.q_tile) / (NH * kHalf));
     P.k_slots = slots / 2;
     P.v_slots = slots - P.k_slots;

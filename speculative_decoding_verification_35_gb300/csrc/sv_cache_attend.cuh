@@ -15,7 +15,7 @@ constexpr int kTile = 128;      // slots of a tile
 constexpr int kMaxSlots = 6;    // key tiles in flight, and value tiles
 constexpr int kNotes = 8;       // tiles whose notes (bad pages, non-finite values) are kept: as many as are in flight,
                                 // with those whose scores run ahead
-constexpr int kItems = 2;       // items that are known ahead
+constexpr int kItems = 3;       // items that are known ahead
 constexpr int kMaxCtas = 320;   // of any launch
 constexpr int kHalf = kTile * 128;  // bytes of 128 rows of 128 bytes, the unit of an operand in shared memory
 constexpr int kSmem = 227 * 1024;
@@ -79,6 +79,7 @@ struct Params {
     int32_t wide;       // output rows lie on 32 bytes
     int32_t ctas;       // of the launch
     int32_t part_rows;  // rows of a partial result
+    int32_t lead;       // what an item's beginning and end cost, in tiles
     float* part_o;      // [2 n][part_rows][64 or 128]
     float2* part_ml;    // [2 n][part_rows]
     Record* records;    // [n]
@@ -120,6 +121,15 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
         }
     }
     return true;
+}
+// Whether the phase is over, for a whole warp.
+__device__ __forceinline__ bool ready(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return __all_sync(kAll, ok);
 }
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int d, int token, int head, int page,
                                          uint32_t bar) {
@@ -340,7 +350,7 @@ struct Common {  // of both kernels, behind the operand tiles
     uint32_t bad[2][kNotes];    // per key and per value tile: groups of 8 slots that lie on a bad page
     uint32_t odd[kNotes][4];    // per value tile: slots with a non-finite value that was cleared
     uint32_t scan[2][16];
-    float* q_down;  // e4m3 caches: [2][query rows], what a row's scores are scaled by, for even and odd items
+    float* q_down;  // e4m3 caches: [kItems][q_rows], what a row's scores are scaled by
     Tree* tree;     // trees: [kItems]
     int32_t q_rows;
 };
@@ -348,7 +358,6 @@ struct Common {  // of both kernels, behind the operand tiles
 // a b / c, rounded down, without the long division: a = q c + r gives q b + r b / c. b and c below 2^15.
 __device__ __forceinline__ uint32_t share(uint32_t a, uint32_t b, uint32_t c) { return a / c * b + a % c * b / c; }
 
-constexpr int32_t kLead = 5;  // measured: about five tiles' time between an item's last tile and the next one's pace
 // Where the CTA begins, and the record of an item that its predecessor began: by all threads, in the end by one,
 // whose sequence b it is, `rest` units into it.
 __device__ __forceinline__ void begin_at(const Params& P, Common& sh, const Seq& s, int32_t b, uint32_t rest, uint32_t lead,
@@ -470,7 +479,7 @@ __device__ __forceinline__ void plan(const Params& P, Common& sh) {
         tiles *= heads;
         blocks *= heads;
         // With few tiles there is a CTA for each, and an item's beginning is nobody's but its own.
-        lead = tiles <= 2 * gridDim.x ? 0 : kLead;
+        lead = tiles <= 2 * gridDim.x ? 0 : P.lead;
         if (tiles + lead * blocks >> 31) {
             if (c == 0 && tid == 0) report(P.a.status, 1u << SV_ERR_CAPACITY);
             return;
@@ -480,90 +489,6 @@ __device__ __forceinline__ void plan(const Params& P, Common& sh) {
         if (c >= n) return;  // the same for the whole CTA
         u0 = share(W, c, n);
         u1 = share(W, c + 1, n);
-    }
-}
-
-// The CTA's items, one after the other, by one warp; a last one of no tiles ends them.
-__device__ __forceinline__ void item_role(const Params& P, Common& sh) {
-    const int lane = threadIdx.x & 31;
-    const bool tree = P.a.chunk.parents != nullptr;
-    const int32_t lead = sh.start.lead;
-    int32_t b = sh.start.b, p = sh.start.p, h = sh.start.h, x = sh.start.x, left = sh.start.left;
-    int32_t T = sh.start.T, past = sh.start.past, row0 = sh.start.row0;
-    Ring ring;
-#pragma unroll 1
-    for (uint32_t i = 0;; ++i, ring.step(kItems)) {
-        Item it{};
-        left -= max(0, lead - x);
-        if (left > 0 && T < 0) {  // the next sequence
-#pragma unroll 1
-            for (; b < P.a.chunk.B; ++b) {
-                const Seq s = seq_of(P.a.chunk, capacity_of(P.a.pool), b);
-                bool ok = !s.err;
-                if (ok && tree) {
-                    int32_t d;
-                    uint32_t m;
-                    tree_of(P.a.chunk, b, s.T, d, m, ok);
-                }
-                if (ok) {
-                    T = s.T;
-                    past = s.past;
-                    row0 = s.row0;
-                    break;
-                }
-            }
-        }
-        const int32_t tb = b;
-        if (left > 0 && T > 0) {
-            int32_t first, count;
-            span(P, T, past, p, it, first, count);
-            const int32_t j = max(0, x - lead);
-            it.b = b;
-            it.h = h;
-            it.row0 = row0;
-            it.tile = first + j;
-            it.begins = j == 0;
-            it.n = min(count - j, left);
-            it.finishes = j + it.n == count;
-            it.mixed_hi = past + (tree ? 0 : it.t0 + 1);
-            it.mixed_lo = P.a.window > 0 && (tree || it.nt > 1) ? it.lo + it.nt + (tree ? it.t0 : 0) : 0;
-            left -= it.n;
-            x = 0;
-        }
-        if (i >= kItems && !wait(smem_u32(&sh.item_empty[ring.i]), ring.parity ^ 1, &sh.gave_up)) return;
-        if (tree && it.n > 0) {
-            int32_t depth, par = 0;
-            uint32_t above;
-            bool ok;
-            tree_of(P.a.chunk, tb, T, depth, above, ok);
-            if (P.a.window > 0 && P.a.window < 32) {  // as far as the window reaches, a step at a time
-                if (lane > 0 && lane < T) par = P.a.chunk.parents[(int64_t)P.a.chunk.offs[tb] + lane - 1];
-                int32_t at = lane;
-                above = 1u << lane;
-                for (int d = 1; d < P.a.window; ++d) {
-                    at = __shfl_sync(kAll, par, at);
-                    above |= 1u << at;
-                }
-            }
-            sh.tree[ring.i].above[lane] = above;
-            sh.tree[ring.i].depth[lane] = depth;
-            __syncwarp();
-        }
-        if (it.n > 0 && ++h == P.a.pool.heads) {
-            h = 0;
-            ++p;
-            if (p * P.block >= T) {
-                p = 0;
-                ++b;
-                T = -1;
-            }
-        }
-        if (lane == 0) {
-            sh.item[ring.i] = it;
-            bar_arrive(smem_u32(&sh.item_full[ring.i]));
-        }
-        __syncwarp();
-        if (it.n == 0) return;
     }
 }
 
@@ -701,7 +626,7 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
 // into the parts hi and lo, each row brought to [128, 256) by a power of two.
 template <int K>
 __device__ __forceinline__ bool load_queries(const Params& P, Common& sh, const Item& it, uint32_t q_smem,
-                                             const CUtensorMap* qm, uint32_t items) {
+                                             const CUtensorMap* qm, uint32_t items, uint32_t entry) {
     using T = typename KindOf<K>::T;
     const AttendArgs& A = P.a;
     const int lane = threadIdx.x & 31;
@@ -779,7 +704,7 @@ __device__ __forceinline__ bool load_queries(const Params& P, Common& sh, const 
                     asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
                     asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst + P.q_part), "r"(lo[0]), "r"(lo[1]) : "memory");
                     if (c == 0)
-                        sh.q_down[(items & 1) * sh.q_rows + (r < tile_rows ? 0 : kTile) + at] = __int_as_float((127 - e) << 23);
+                        sh.q_down[entry * sh.q_rows + (r < tile_rows ? 0 : kTile) + at] = __int_as_float((127 - e) << 23);
                 }
             }
         }
@@ -833,22 +758,114 @@ __device__ __forceinline__ void scan_rows(int halves, uint32_t at, int32_t lo, i
         }
 }
 
-// Queries, and value tiles before they are multiplied: rows of slots that no row of the item sees are cleared
+// The CTA's items, one after the other, by one warp, and their queries; a last one of no tiles ends them.
+template <int K>
+__device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t q_smem, const CUtensorMap* qm) {
+    const int lane = threadIdx.x & 31;
+    const bool tree = P.a.chunk.parents != nullptr;
+    const int32_t lead = sh.start.lead;
+    int32_t b = sh.start.b, p = sh.start.p, h = sh.start.h, x = sh.start.x, left = sh.start.left;
+    int32_t T = sh.start.T, past = sh.start.past, row0 = sh.start.row0;
+    Ring ring;
+    uint32_t loads = 0;
+#pragma unroll 1
+    for (uint32_t i = 0;; ++i, ring.step(kItems)) {
+        Item it{};
+        left -= max(0, lead - x);
+        if (left > 0 && T < 0) {  // the next sequence
+#pragma unroll 1
+            for (; b < P.a.chunk.B; ++b) {
+                const Seq s = seq_of(P.a.chunk, capacity_of(P.a.pool), b);
+                bool ok = !s.err;
+                if (ok && tree) {
+                    int32_t d;
+                    uint32_t m;
+                    tree_of(P.a.chunk, b, s.T, d, m, ok);
+                }
+                if (ok) {
+                    T = s.T;
+                    past = s.past;
+                    row0 = s.row0;
+                    break;
+                }
+            }
+        }
+        const int32_t tb = b;
+        if (left > 0 && T > 0) {
+            int32_t first, count;
+            span(P, T, past, p, it, first, count);
+            const int32_t j = max(0, x - lead);
+            it.b = b;
+            it.h = h;
+            it.row0 = row0;
+            it.tile = first + j;
+            it.begins = j == 0;
+            it.n = min(count - j, left);
+            it.finishes = j + it.n == count;
+            it.mixed_hi = past + (tree ? 0 : it.t0 + 1);
+            it.mixed_lo = P.a.window > 0 && (tree || it.nt > 1) ? it.lo + it.nt + (tree ? it.t0 : 0) : 0;
+            left -= it.n;
+            x = 0;
+        }
+        if (i >= kItems && !wait(smem_u32(&sh.item_empty[ring.i]), ring.parity ^ 1, &sh.gave_up)) break;
+        if (tree && it.n > 0) {
+            int32_t depth, par = 0;
+            uint32_t above;
+            bool ok;
+            tree_of(P.a.chunk, tb, T, depth, above, ok);
+            if (P.a.window > 0 && P.a.window < 32) {  // as far as the window reaches, a step at a time
+                if (lane > 0 && lane < T) par = P.a.chunk.parents[(int64_t)P.a.chunk.offs[tb] + lane - 1];
+                int32_t at = lane;
+                above = 1u << lane;
+                for (int d = 1; d < P.a.window; ++d) {
+                    at = __shfl_sync(kAll, par, at);
+                    above |= 1u << at;
+                }
+            }
+            sh.tree[ring.i].above[lane] = above;
+            sh.tree[ring.i].depth[lane] = depth;
+            __syncwarp();
+        }
+        if (it.n > 0 && ++h == P.a.pool.heads) {
+            h = 0;
+            ++p;
+            if (p * P.block >= T) {
+                p = 0;
+                ++b;
+                T = -1;
+            }
+        }
+        if (lane == 0) {
+            sh.item[ring.i] = it;
+            bar_arrive(smem_u32(&sh.item_full[ring.i]));
+        }
+        __syncwarp();
+        if (it.n == 0) break;
+        if (i > 0 && !wait(smem_u32(&sh.q_empty), (i - 1) & 1, &sh.gave_up)) break;
+        ++loads;
+        if (!load_queries<K>(P, sh, it, q_smem, qm, i, ring.i)) break;
+    }
+    if (K != kE4m3 && loads > 0) {  // its copies land before the CTA ends, whoever gave up
+        int none = 0;
+        bool flip;
+        score_unit(P.a, 0, flip);
+        wait(smem_u32(flip ? &sh.q_in : &sh.q_full), (loads - 1) & 1, &none);
+    }
+}
+
+// Value tiles before they are multiplied: rows of slots that no row of the item sees are cleared
 // (they may hold anything, and a weight of zero times NaN is NaN), and so are single non-finite values that only
 // some rows see; those are noted for the rows that do.
 template <int K>
-__device__ __forceinline__ void value_role(const Params& P, Common& sh, uint32_t q_smem, uint32_t v_smem,
-                                           const CUtensorMap* qm) {
+__device__ __forceinline__ void value_role(const Params& P, Common& sh, uint32_t v_smem) {
     const int lane = threadIdx.x & 31;
     volatile int* gave_up = &sh.gave_up;
-    uint32_t v = 0, items = 0;
+    uint32_t v = 0;
     Ring ring;
     Items walk(sh);
     Item it;
 #pragma unroll 1
-    for (; walk.next(it); ++items) {
-        if (items > 0 && !wait(smem_u32(&sh.q_empty), (items - 1) & 1, gave_up)) return;
-        if (!load_queries<K>(P, sh, it, q_smem, qm, items)) return;
+    while (walk.next(it)) {
 #pragma unroll 1
         for (int32_t j = 0; j < it.n; ++j, ++v, ring.step(P.v_slots)) {
             if (!wait(smem_u32(&sh.v_full[ring.i]), ring.parity, gave_up)) return;

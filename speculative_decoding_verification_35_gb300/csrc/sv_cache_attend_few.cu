@@ -29,14 +29,20 @@ namespace sv {
 namespace cache {
 namespace {
 
-// The weights' tile: a slot's weights lie side by side, NR of them (e4m3: NR bytes for hi, then another tile for lo).
+// The weights' tile: a slot's weights lie side by side, NR of them. e4m3: NR bytes for what rounding gives, hi, and NR
+// for what it leaves, 2^kLow lo; a product of twice the columns then has both, O = O_hi + 2^-kLow O_lo. A weight
+// 2^-n of the largest, which is 2^kShift or more, is kept to 2^-8 of itself, from n = 13 on to 2^-18 of the largest.
 template <int K, int NR>
 struct Weights {
-    static constexpr int kPitch = NR * KindOf<K>::kBytes;  // 32, 64 or 128 bytes, the width of the swizzle
-    static constexpr int kPart = kTile * kPitch;
-    static constexpr int kBytes = kPart * (K == kE4m3 ? 2 : 1);
+    static constexpr int kPitch = 2 * NR;  // 32, 64 or 128 bytes, the width of the swizzle
+    static constexpr int kBytes = kTile * kPitch;
+    static constexpr int kColumns = K == kE4m3 ? 2 * NR : NR;  // of O
+    static constexpr int kLow = 4;
     static constexpr uint32_t kSwizzle = kPitch == 128 ? 2u : kPitch == 64 ? 4u : 6u;
     static constexpr uint32_t kHigh = (uint32_t)(8 * kPitch) >> 4 | 1u << 14 | kSwizzle << 29;
+    // weights are 2^kShift at a new reference, which stays until one is above 2^kMost: e4m3 ends at 448, fp16 at 65504
+    static constexpr float kShift = K == kBf16 ? 0.f : K == kFp16 ? 7.f : 4.f;
+    static constexpr float kMost = K == kBf16 ? 64.f : K == kFp16 ? 15.f : 8.75f;
     static_assert(kPitch >= 32 && kPitch <= 128, "a swizzle's width");
     // where the 16 bytes c of a slot lie
     static __device__ __forceinline__ uint32_t at(uint32_t slot, uint32_t c) {
@@ -50,24 +56,17 @@ constexpr int kThreads = (G + 1) * 128;
 constexpr int kReaders = 1 + 1 + 1;  // of an item, besides the softmax warps: loader, products, values
 constexpr int kHalfSm = 113 * 1024;  // of shared memory
 
-// What a group's warps tell each other now and then: when the references move, and at an item's end.
+// What a group's warps tell each other when the references move and at an item's end: per warp a row's maximum, or
+// sum. One group's notes lie in the weights' place, while no product reads that; two groups are not at the same step.
 template <int N>
 struct Notes {
-    float part[4][N];  // per warp: a row's maximum; at the end its sum
-    float sub[N];      // by how much the reference moves; at the end what O is scaled by
-    float fac[N];      // 2^-sub
-    float off[N];      // what is added to a row's scaled scores: kShift - reference
+    float part[4][N];
 };
 struct Nothing {};
-
-// One group's notes lie in the weights' place, while no product reads that. Two groups are not at the same step.
 template <int N, int G>
 struct alignas(16) Group : std::conditional<G == 1, Nothing, Notes<N>>::type {
-    float ref[N];  // the rows' references (log2)
     uint64_t vote;
     int again[3];  // votes in turn: some weight is too large
-    int unset;     // some row has no reference yet
-    int moved;     // some row's O is to be scaled
 };
 
 template <int NR, int G>
@@ -76,13 +75,15 @@ struct alignas(16) Shared : Common {
     Group<NR / G, G> group[G];
 };
 
-// A barrier of the softmax warps.
+// A barrier of a group's warps; what lies between the two calls needs no one.
 struct Vote {
     uint32_t bar, parity;
     volatile int* gave_up;
-    __device__ __forceinline__ bool operator()() {
+    __device__ __forceinline__ void arrive() {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) bar_arrive(bar);
+    }
+    __device__ __forceinline__ bool pass() {
         const bool ok = wait(bar, parity, gave_up);
         parity ^= 1u;
         return ok;
@@ -105,6 +106,25 @@ __device__ __forceinline__ void tc_ld1(uint32_t col, uint32_t& r) {
 }
 __device__ __forceinline__ void tc_st1(uint32_t col, uint32_t r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(col), "r"(r) : "memory");
+}
+
+__device__ __forceinline__ void tc_st16(uint32_t col, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(col),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+__device__ __forceinline__ void tc_ld4(uint32_t col, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(col));
+}
+// e4m3 weights in pairs: what rounding gives, and 2^kLow of what it leaves
+template <int kLow>
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = e4m3x2(a, b);
+    const float2 x = from_e4m3x2(hi);
+    lo = e4m3x2((a - x.x) * (1 << kLow), (b - x.y) * (1 << kLow));
 }
 
 // The rows that see a slot, as bits, the first of them row0.
@@ -138,10 +158,12 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
     const uint32_t p_ready = smem_u32(&sh.p_ready), pv_done = smem_u32(&sh.pv_done);
     Notes<N>& notes = *(G == 1 ? reinterpret_cast<Notes<N>*>(weights) : reinterpret_cast<Notes<N>*>(&mine));
     static_assert(sizeof(Notes<N>) <= Wt::kBytes, "the notes fit");
+    constexpr int kParts = K == kE4m3 ? 2 : 1;
     const int32_t D = A.pool.dim;
     volatile int* gave_up = &sh.gave_up;
     Vote vote{smem_u32(&mine.vote), 0, gave_up};
     uint32_t steps = 0, tiles = 0, items = 0, votes = 0;  // votes: on weights, modulo 3
+    bool owed = false;  // a vote of the last item's end has been given and not passed: others may still read the notes
     Items walk(sh);
     Item it;
 #pragma unroll 1
@@ -150,13 +172,17 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
         const int32_t rows = min(N, it.nt * P.G - row0);  // none or less: a group without work
         bool flip;
         const float unit = score_unit(A, it.h, flip);
-        float l[N], off[N], u[K == kE4m3 ? N : 1];
+        float l[N], off[N], u[K == kE4m3 ? N : 1];  // weights are 2^(u s + off)
         u[0] = unit;
 #pragma unroll
         for (int r = 0; r < N; ++r) {
             l[r] = 0.f;
-            off[r] = KT::kShift;
+            off[r] = Wt::kShift;
         }
+        // every warp settles the references by itself, from the same notes: a lane has a row's (off again, and whether
+        // there is a reference at all)
+        float own_off = Wt::kShift;
+        bool own = false, unset = true;
 #pragma unroll 1
         for (int32_t j = 0; j < it.n; ++j, ++steps) {
             const uint32_t buf = steps & 1;
@@ -164,89 +190,95 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
             tc_after();
             if (K == kE4m3 && j == 0)
 #pragma unroll
-                for (int r = 0; r < (K == kE4m3 ? N : 1); ++r) u[r] = unit * sh.q_down[(items & 1) * sh.q_rows + row0 + r];
+                for (int r = 0; r < (K == kE4m3 ? N : 1); ++r) u[r] = unit * sh.q_down[walk.ring.i * sh.q_rows + row0 + r];
             const uint32_t s_col = tmem + buf * NR;
             const int32_t k0 = (it.tile + j) * kTile;
             const uint32_t ring = (tiles + j) % kNotes;
             const uint32_t bad = sh.bad[0][ring];
+            const bool cut = k0 < max(it.lo, it.mixed_lo) || k0 + kTile > min(it.mixed_hi, it.end) || bad;
+            const uint32_t seen = cut ? rows_seeing(P, it, tree, k0 + k, bad, row0) : ~0u;
             uint32_t s[N];
+            // Once, mostly: while the votes come in that no weight is too large, the weights are taken as if none were.
+            bool fresh = unset;
+#pragma unroll 1
+            for (;;) {
 #pragma unroll
-            for (int c = 0; c < N; c += 16) tc_ld16(s_col + c, s + c);
-            tc_wait_ld();
-            if (k0 < max(it.lo, it.mixed_lo) || k0 + kTile > min(it.mixed_hi, it.end) || bad) {
-                const uint32_t seen = rows_seeing(P, it, tree, k0 + k, bad, row0);
+                for (int c = 0; c < N; c += 16) tc_ld16(s_col + c, s + c);
+                tc_wait_ld();
+                if (cut)
 #pragma unroll
-                for (int r = 0; r < N; ++r)
-                    if (!(seen >> r & 1u)) s[r] = 0xff800000u;
-            }
-            // the weights' logarithms against the references (a first tile's: against none)
-            float top = -INFINITY;
+                    for (int r = 0; r < N; ++r)
+                        if (!(seen >> r & 1u)) s[r] = 0xff800000u;
+                // the weights' logarithms against the references (where there is none yet, against 0)
+                float top = -INFINITY;
 #pragma unroll
-            for (int r = 0; r < N; ++r) {
-                const float y = fmaf(__uint_as_float(s[r]), u[K == kE4m3 ? r : 0], off[r]);
-                s[r] = __float_as_uint(y);
-                top = fmaxf(top, y);
-            }
-            bool fresh = j == 0 || mine.unset;
-            if (!fresh) {
-                // before anyone can pass this vote, everyone has read the last one's word but two
-                constexpr float most = K == kBf16 ? 64.f : K == kFp16 ? 15.f : 8.75f;
-                if (k == 0) mine.again[votes == 2 ? 0 : votes + 1] = 0;
-                if (__any_sync(kAll, top > most) && lane == 0) mine.again[votes] = 1;
-                if (!vote()) return;
+                for (int r = 0; r < N; ++r) {
+                    const float y = fmaf(__uint_as_float(s[r]), u[K == kE4m3 ? r : 0], off[r]);
+                    s[r] = __float_as_uint(y);
+                    top = fmaxf(top, y);
+                }
+                if (!fresh) {
+                    // no one passes this vote before everyone has read the last but one's word
+                    if (k == 0) mine.again[votes == 2 ? 0 : votes + 1] = 0;
+                    if (__any_sync(kAll, top > Wt::kMost) && lane == 0) mine.again[votes] = 1;
+                    vote.arrive();
+                } else {
+                    if (owed && !vote.pass()) return;
+                    owed = false;
+                    if (j > 0) {  // O is whole, and the notes' place free, once the last step's product has been
+                        if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
+                        tc_after();
+                    }
+                    // the rows' maxima, by warp, then of all
+#pragma unroll
+                    for (int r = 0; r < N; ++r) {
+                        const float x = warp_max(__uint_as_float(s[r]));
+                        if (lane == r) notes.part[warp][r] = x;
+                    }
+                    vote.arrive();
+                    if (!vote.pass()) return;
+                    const int r0 = lane % N;
+                    const float mx = fmaxf(fmaxf(notes.part[0][r0], notes.part[1][r0]), fmaxf(notes.part[2][r0], notes.part[3][r0])) -
+                                     Wt::kShift;
+                    vote.arrive();
+                    // from none to the maximum, if there is one; else upwards only
+                    const float d = own ? fmaxf(mx, 0.f) : mx != -INFINITY ? mx : 0.f;
+                    const bool moved = __any_sync(kAll, own && d > 0.f);
+                    const float fac = own ? exp2_fast(-d) : 1.f;
+                    own_off -= d;
+                    own = own || mx != -INFINITY;
+                    unset = __any_sync(kAll, r0 < rows && !own);
+#pragma unroll
+                    for (int r = 0; r < N; ++r) {
+                        const float x = __shfl_sync(kAll, d, r);
+                        s[r] = __float_as_uint(__uint_as_float(s[r]) - x);
+                        off[r] -= x;
+                    }
+                    if (moved) {
+#pragma unroll
+                        for (int r = 0; r < N; ++r) l[r] *= __shfl_sync(kAll, fac, r);
+#pragma unroll 1
+                        for (int c = 0; c < kParts * N; c += 16) {
+                            if (c % N >= rows) continue;
+                            const uint32_t col = o_col + (c >= N ? NR - N : 0) + c;
+                            uint32_t o[16];
+                            tc_ld16(col, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(kAll, fac, c % N + i));
+                            tc_st16(col, o);
+                        }
+                        tc_wait_st();
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < N; ++r) s[r] = __float_as_uint(exp2_fast(__uint_as_float(s[r])));
+                if (!vote.pass()) return;
+                if (fresh) break;
                 fresh = mine.again[votes];
                 votes = votes == 2 ? 0 : votes + 1;
-            }
-            if (fresh) {
-                if (j > 0) {  // O is whole, and the notes' place free, once the last step's product has been
-                    if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
-                    tc_after();
-                }
-                // the rows' maxima, by warp, then by one thread a row
-#pragma unroll
-                for (int r = 0; r < N; ++r) {
-                    const float x = warp_max(__uint_as_float(s[r]));
-                    if (lane == r) notes.part[warp][r] = x;
-                }
-                if (!vote()) return;
-                if (warp == 0) {
-                    const int r = lane % N;
-                    const float old = j == 0 ? -INFINITY : mine.ref[r];
-                    const float mx = fmaxf(fmaxf(notes.part[0][r], notes.part[1][r]), fmaxf(notes.part[2][r], notes.part[3][r])) -
-                                     KT::kShift;
-                    // against none: to the maximum, if there is one; else upwards only
-                    const bool has = old != -INFINITY, any = mx != -INFINITY;
-                    const float d = has ? fmaxf(mx, 0.f) : any ? mx : 0.f;
-                    const float ref = has ? old + d : any ? d : -INFINITY;
-                    __syncwarp();
-                    mine.ref[r] = ref;
-                    notes.sub[r] = d;
-                    notes.off[r] = KT::kShift - (ref == -INFINITY ? 0.f : ref);
-                    notes.fac[r] = has ? exp2_fast(-d) : 1.f;
-                    const bool unset = __any_sync(kAll, r < rows && ref == -INFINITY), moved = __any_sync(kAll, has && d > 0.f);
-                    if (lane == 0) {
-                        mine.unset = unset;
-                        mine.moved = moved;
-                    }
-                }
-                if (!vote()) return;
-                const bool moved = mine.moved;
-#pragma unroll
-                for (int r = 0; r < N; ++r) {
-                    s[r] = __float_as_uint(__uint_as_float(s[r]) - notes.sub[r]);
-                    off[r] = notes.off[r];
-                    l[r] *= notes.fac[r];
-                }
-                if (moved)
-#pragma unroll 1
-                    for (int c = 0; c < rows; ++c) {
-                        uint32_t o;
-                        tc_ld1(o_col + c, o);
-                        tc_wait_ld();
-                        tc_st1(o_col + c, __float_as_uint(__uint_as_float(o) * notes.fac[c]));
-                    }
-                tc_wait_st();
-                if (!vote()) return;  // the notes have been read
+                if (!fresh) break;
             }
             uint32_t pk[N / 2];  // 16 bits: pairs; e4m3: hi in the first half, lo in the second
 #pragma unroll
@@ -254,7 +286,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                 float p[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    p[e] = exp2_fast(__uint_as_float(s[r + e]));
+                    p[e] = __uint_as_float(s[r + e]);
                     l[r + e] += p[e];
                 }
                 if (K != kE4m3) {
@@ -262,22 +294,23 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                     pk[r / 2 + 1] = from_float2<T>(p[2], p[3]);
                 } else {
                     uint32_t a, b, c, d;
-                    split_pair(p[0], p[1], a, c);
-                    split_pair(p[2], p[3], b, d);
+                    split_weights<Wt::kLow>(p[0], p[1], a, c);
+                    split_weights<Wt::kLow>(p[2], p[3], b, d);
                     pk[r / 4] = a | b << 16;
                     pk[N / 4 + r / 4] = c | d << 16;
                 }
             }
             // the weights' place is free once the last step's product has been
             if (j > 0 && !wait(pv_done, (steps - 1) & 1, gave_up)) return;
-            constexpr int kWide = N * KT::kBytes / 16;
+            constexpr int kWide = N * KT::kBytes / 16;  // 16 bytes of a part
 #pragma unroll
-            for (int c = 0; c < kWide; ++c)
+            for (int part = 0; part < kParts; ++part)
 #pragma unroll
-                for (int part = 0; part < (K == kE4m3 ? 2 : 1); ++part) {
-                    const uint32_t* u = pk + part * (N / 4) + 4 * c;
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(p_smem + part * Wt::kPart + Wt::at(k, row0 / N * kWide + c)), "r"(u[0]),
-                                 "r"(u[1]), "r"(u[2]), "r"(u[3])
+                for (int c = 0; c < kWide; ++c) {
+                    const uint32_t* v = pk + part * (N / 4) + 4 * c;
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                     p_smem + Wt::at(k, part * (NR / 16) + row0 / N * kWide + c)),
+                                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
                                  : "memory");
                 }
             const bool mixed = mixed_tile(it, k0);
@@ -348,26 +381,26 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
         } else if (!(lane & 1)) {
             notes.part[warp][(lane >> 4 & 1) * 8 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2 + (lane >> 1 & 1)] = l[0];
         }
-        if (!vote()) return;
+        vote.arrive();
+        if (!vote.pass()) return;
+        const int r0 = lane % N;
+        const float total = (notes.part[0][r0] + notes.part[1][r0]) + (notes.part[2][r0] + notes.part[3][r0]);
+        vote.arrive();
+        owed = true;
         const bool alone = it.begins && it.finishes;
         const size_t part = (size_t)(2 * blockIdx.x + (it.begins ? 1 : 0)) * P.part_rows + row0;
-        if (k < rows) {
-            const float total = (notes.part[0][k] + notes.part[1][k]) + (notes.part[2][k] + notes.part[3][k]),
-                        ref = mine.ref[k] - KT::kShift;
-            float f = 1.f;
+        float f = 1.f;  // what a row's O is scaled by
+        if (alone) f = total == 0.f ? 0.f : (A.pool.v_scale ? A.pool.v_scale[it.h] : 1.f) / total;
+        if (k < rows && k < N) {
             if (alone) {
-                const float vs = A.pool.v_scale ? A.pool.v_scale[it.h] : 1.f;
                 const int32_t row = row0 + k, t = row / P.G;
-                f = total == 0.f ? 0.f : vs / total;
                 if (A.lse)
                     A.lse[(int64_t)(it.row0 + it.t0 + t) * A.q_heads + it.h * P.G + row - t * P.G] =
-                        total == 0.f ? -INFINITY : ref * kLn2 + logf(total);
+                        total == 0.f ? -INFINITY : fmaf(-own_off, kLn2, logf(total));
             } else {
-                P.part_ml[part + k] = make_float2(ref, total);
+                P.part_ml[part + k] = make_float2(own ? -own_off : -INFINITY, total);
             }
-            notes.sub[k] = f;
         }
-        if (!vote()) return;
         const int32_t dp = K == kE4m3 || D > 64 ? 128 : 64;
         const int32_t t0 = row0 / P.G;
         int32_t g = row0 - t0 * P.G;
@@ -375,14 +408,15 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
         float* out_part = P.part_o + part * dp + k;
 #pragma unroll 1
         for (int c = 0; c < rows; c += 4) {
-            uint32_t o[4];
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-                         : "r"(o_col + c));
+            uint32_t o[4], o_low[4];
+            tc_ld4(o_col + c, o);
+            if (K == kE4m3) tc_ld4(o_col + NR + c, o_low);
             tc_wait_ld();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x = __uint_as_float(o[i]) * notes.sub[c + i];
+                float x = __uint_as_float(o[i]);
+                if (K == kE4m3) x = fmaf(__uint_as_float(o_low[i]), 1.f / (1 << Wt::kLow), x);
+                x *= __shfl_sync(kAll, f, c + i);
                 if (k < D && c + i < rows) {
                     if (alone) *out = (T)x;
                     else out_part[(c + i) * dp] = x;
@@ -398,7 +432,9 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
     }
 }
 
-// The products, by one thread. Scores run two tiles ahead of outputs, in two buffers.
+// The products, by one thread, in the order in which they become possible: a tile's scores, into one of two buffers, once
+// its keys are in (an item's first: its queries too); its outputs, once its weights and values are. Scores run up to two
+// tiles ahead, also into the next item.
 template <int K, int NR, int G>
 __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh, uint32_t q_smem, uint32_t p_smem, uint32_t k_smem,
                                              uint32_t v_smem) {
@@ -410,69 +446,73 @@ __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh,
     const int32_t depth = (D + KindOf<K>::kStep - 1) / KindOf<K>::kStep;
     const uint32_t slot_bytes = P.halves * kHalf;
     // float accumulators, 128 lanes, NR columns; of O both operands' rows lie along the depth
-    const uint32_t id_s = 1u << 4 | fmt << 7 | fmt << 10 | (uint32_t)(NR >> 3) << 17 | (uint32_t)(kTile >> 4) << 24;
-    const uint32_t id_o = id_s | 3u << 15;
+    const uint32_t id = 1u << 4 | fmt << 7 | fmt << 10 | (uint32_t)(kTile >> 4) << 24;
+    const uint32_t id_s = id | (uint32_t)(NR >> 3) << 17, id_o = id | (uint32_t)(Wt::kColumns >> 3) << 17 | 3u << 15;
     const uint32_t tmem = __shfl_sync(kAll, sh.tmem, 0), o_at = tmem + 2 * NR;
     const uint32_t k_full = smem_u32(sh.k_full), k_empty = smem_u32(sh.k_empty), v_empty = smem_u32(sh.v_empty),
                    value = smem_u32(sh.value), s_full = smem_u32(sh.s_full), p_ready = smem_u32(&sh.p_ready),
-                   pv_done = smem_u32(&sh.pv_done), q_empty = smem_u32(&sh.q_empty);
+                   pv_done = smem_u32(&sh.pv_done), q_full = smem_u32(&sh.q_full), q_empty = smem_u32(&sh.q_empty);
     const uint32_t q = operand(q_smem, 16), q_part = (uint32_t)P.q_part >> 4, p = operand(p_smem, 16);
     const bool leader = elect();
     volatile int* gave_up = &sh.gave_up;
-    uint32_t items = 0, p_parity = 0, buf = 0;  // buf: of the next scores
+    uint32_t items = 0, ahead = 0, scores = 0, outputs = 0, first = 0, polls = 0;  // first: by buffer, an item's first tile
+    int32_t j = 0, n = 0;
     Ring kr, vr;
     Items walk(sh);
     Item it;
-    bool ok = true;
+    bool more = walk.next(it);
+    n = __shfl_sync(kAll, it.n, 0);
 #pragma unroll 1
-    while (ok && walk.next(it)) {
-        if (!(ok = wait(smem_u32(&sh.q_full), items & 1, gave_up))) break;
-        tc_after();
-        const int32_t n = __shfl_sync(kAll, it.n, 0);
-#pragma unroll 1
-        for (int32_t t = -2; t < n; ++t) {  // outputs of tile t, scores of the next but one
-            if (t >= 0) {
-                if (!(ok = wait(value + 8 * vr.i, vr.parity, gave_up) && wait(p_ready, p_parity, gave_up))) break;
-                p_parity ^= 1u;
-                tc_after();
-                // D <= 64: the upper 64 lanes repeat the lower ones' columns
-                const uint32_t a = operand(v_smem + vr.i * slot_bytes, slot_bytes > kHalf ? kHalf : 0);
-                if (leader) {
-#pragma unroll 2
-                    for (int i = 0; i < kTile / KindOf<K>::kStep; ++i)
+    while (more || ahead > 0) {
+        if (more && ahead < 2 && (j > 0 || ready(q_full, items & 1)) && ready(k_full + 8 * kr.i, kr.parity)) {
+            tc_after();
+            const uint32_t buf = scores & 1, a = operand(k_smem + kr.i * slot_bytes, 16), d = tmem + buf * NR;
+            if (leader) {
 #pragma unroll
-                        for (int part = 0; part < parts; ++part)
-                            mma_mixed<k8, Wt::kHigh>(o_at, a + (i * KindOf<K>::kStep * 128 >> 4),
-                                                     p + (part * Wt::kPart + i * KindOf<K>::kStep * Wt::kPitch >> 4), id_o,
-                                                     (uint32_t)(t + part + i > 0));
-                    tc_commit(pv_done);
-                    tc_commit(v_empty + 8 * vr.i);
-                }
-                __syncwarp();
-                vr.step(P.v_slots);
-            }
-            if (t + 2 < n) {
-                if (!(ok = wait(k_full + 8 * kr.i, kr.parity, gave_up))) break;
-                const uint32_t a = operand(k_smem + kr.i * slot_bytes, 16), d = tmem + buf * NR;
-                if (leader) {
-#pragma unroll
-                    for (int part = 0; part < parts; ++part)
+                for (int part = 0; part < parts; ++part)
 #pragma unroll 2
-                        for (int i = 0; i < depth; ++i) {
-                            const uint32_t in = (i & 3) * 32 >> 4;
-                            mma_ss<k8>(d, a + (i >> 2) * (kHalf >> 4) + in, q + (k8 ? part : i >> 2) * q_part + in, id_s,
-                                       part + i > 0);
-                        }
-                    tc_commit(s_full + 8 * buf);
-                    tc_commit(k_empty + 8 * kr.i);
-                    if (t + 3 == n) tc_commit(q_empty);
-                }
-                __syncwarp();
-                kr.step(P.k_slots);
-                buf ^= 1u;
+                    for (int i = 0; i < depth; ++i) {
+                        const uint32_t in = (i & 3) * 32 >> 4;
+                        mma_ss<k8>(d, a + (i >> 2) * (kHalf >> 4) + in, q + (k8 ? part : i >> 2) * q_part + in, id_s, part + i > 0);
+                    }
+                tc_commit(s_full + 8 * buf);
+                tc_commit(k_empty + 8 * kr.i);
+                if (j + 1 == n) tc_commit(q_empty);
             }
+            __syncwarp();
+            first = (first & ~(1u << buf)) | (uint32_t)(j == 0) << buf;
+            kr.step(P.k_slots);
+            ++scores;
+            ++ahead;
+            polls = 0;
+            if (++j == n) {
+                j = 0;
+                ++items;
+                more = walk.next(it);
+                n = __shfl_sync(kAll, it.n, 0);
+            }
+        } else if (ahead > 0 && ready(p_ready, outputs & 1) && ready(value + 8 * vr.i, vr.parity)) {
+            tc_after();
+            // D <= 64: the upper 64 lanes repeat the lower ones' columns
+            const uint32_t a = operand(v_smem + vr.i * slot_bytes, slot_bytes > kHalf ? kHalf : 0);
+            const uint32_t fresh = first >> (outputs & 1) & 1u;
+            if (leader) {
+#pragma unroll 2
+                for (int i = 0; i < kTile / KindOf<K>::kStep; ++i)
+                    mma_mixed<k8, Wt::kHigh>(o_at, a + (i * KindOf<K>::kStep * 128 >> 4), p + (i * KindOf<K>::kStep * Wt::kPitch >> 4), id_o,
+                                             i > 0 ? 1u : fresh ^ 1u);
+                tc_commit(pv_done);
+                tc_commit(v_empty + 8 * vr.i);
+            }
+            __syncwarp();
+            vr.step(P.v_slots);
+            ++outputs;
+            --ahead;
+            polls = 0;
+        } else if ((++polls & 255u) == 0) {
+            if (polls >= kPolls) *gave_up = 1;
+            if (__any_sync(kAll, *gave_up)) break;
         }
-        ++items;
     }
     // products under way end before the tensor memory is given back
     if (leader) tc_commit(smem_u32(&sh.drain));
@@ -485,7 +525,7 @@ template <int K, int NR, int G>
 __global__ void __launch_bounds__(kThreads<G>, G == 1 ? 2 : 1)
     k_attend_few(const __grid_constant__ Params P, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
                  const __grid_constant__ CUtensorMap qm) {
-    constexpr int columns = 4 * NR;  // three times NR are used
+    constexpr int columns = 4 * NR;  // twice NR for scores, NR (e4m3: twice) for O
     extern __shared__ __align__(1024) char raw[];
     const uint32_t slot_bytes = P.halves * kHalf;
     const uint32_t q_smem = smem_u32(raw), p_smem = q_smem + P.q_tile, k_smem = p_smem + Weights<K, NR>::kBytes,
@@ -537,8 +577,8 @@ __global__ void __launch_bounds__(kThreads<G>, G == 1 ? 2 : 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (role == 0) load_role(P, sh, k_smem, v_smem, &km, &vm, 0, 1);
         else if (role == 1) product_role<K, NR, G>(P, sh, q_smem, p_smem, k_smem, v_smem);
-        else if (role == 2) value_role<K>(P, sh, q_smem, v_smem, &qm);
-        else item_role(P, sh);
+        else if (role == 2) value_role<K>(P, sh, v_smem);
+        else item_role<K>(P, sh, q_smem, &qm);
     }
     tc_before();
     __syncthreads();
@@ -557,9 +597,10 @@ cudaError_t launch(Params& P, int sms, cudaStream_t st) {
     P.tokens = P.block = A.chunk.max_gamma + 1;
     P.q_box = P.tokens;
     P.q_part = NR * 128;
+    P.lead = 2;
     P.q_tile = (K == kE4m3 ? 2 : halves) * P.q_part;
     const int own = (int)(sizeof(Shared<NR, G>) + 15) / 16 * 16 + (A.chunk.parents ? kItems * (int)sizeof(Tree) : 0) +
-                    (K == kE4m3 ? 2 * NR * 4 : 0);
+                    (K == kE4m3 ? kItems * NR * 4 : 0);
     const int rest = P.q_tile + Weights<K, NR>::kBytes + own;
     const int slots = min(2 * kMaxSlots, ((G == 1 ? kHalfSm : kSmem) - rest) / (halves * kHalf));
     P.k_slots = slots / 2;
@@ -577,7 +618,7 @@ cudaError_t launch(Params& P, int sms, cudaStream_t st) {
 template <int K>
 cudaError_t choose(Params& P, int rows, int sms, cudaStream_t st) {
     P.part_rows = kFewRows;
-    if (K != kE4m3 && rows <= 16) return launch<K, K == kE4m3 ? 32 : 16, 1>(P, sms, st);
+    if (rows <= 16) return launch<K, 16, 1>(P, sms, st);
     return rows <= 32 ? launch<K, 32, 1>(P, sms, st) : launch<K, 64, 2>(P, sms, st);
 }
 
