@@ -173,5 +173,21 @@ __device__ __forceinline__ uint32_t from_float2<__half>(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// A launch whose CTAs may be brought in while the kernel before it in the stream ends: they wait for its end, and
+// its writes, with griddepcontrol.wait before they read anything.
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t st, Args... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace cache
 }  // namespace sv

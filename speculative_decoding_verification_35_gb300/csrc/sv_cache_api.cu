@@ -1,4 +1,5 @@
 // C ABI of the cache calls (include/speccache.h): host-side validation and the launches.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -63,7 +64,7 @@ Chunk chunk_of(const sv_chunk* c) {
     r.parents = c->max_gamma > 0 ? c->parents : nullptr;
     r.B = c->B;
     r.rows = c->rows;
-    r.max_gamma = c->max_gamma;
+    r.max_gamma = std::min(c->max_gamma, std::max(c->rows, 1) - 1);  // as many as there can be
     return r;
 }
 

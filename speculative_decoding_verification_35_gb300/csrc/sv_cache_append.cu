@@ -13,8 +13,7 @@ namespace {
 constexpr int kThreads = 256;
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(const uint4 u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -49,10 +48,49 @@ __device__ __forceinline__ void store8_e4m3(char* p, const float (&x)[8], float 
 }
 
 // One CTA per row. A unit is 8 elements, or a pair of 8 that rotate into one another; head hh of the row is a
-// query head, then a key head, then a value head.
+// query head, then a key head, then a value head. A thread reads some units before it is known where they go: finding
+// the row's sequence, length and page takes four dependent reads, as long as the data does (prompts of 5933 rows, 60
+// heads of 96, fp16: 41 us one after the other).
+template <bool kInter>
+constexpr int kAhead = kInter ? 4 : 2;  // 64 bytes a thread
+
 template <typename T, bool kE4m3, bool kInter>
-__global__ void __launch_bounds__(kThreads) k_cache_append(const AppendArgs A) {
-    const int32_t row = blockIdx.x;
+__global__ void __launch_bounds__(kThreads) k_cache_append(const __grid_constant__ AppendArgs A) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t row = blockIdx.x, rot = A.rot, D = A.pool.dim;
+    const int32_t paired = kInter ? 0 : rot >> 4;
+    const int32_t units = paired + ((D - (kInter ? 0 : rot)) >> 3), all = (A.q_heads + 2 * A.pool.heads) * units;
+    struct Unit {
+        int32_t h, d0, d1;  // d1 < 0: no pair
+        bool is_q, is_v;
+    };
+    auto unit = [&](int32_t i) {
+        const int32_t hh = i / units, u = i - hh * units;
+        Unit r;
+        r.is_q = hh < A.q_heads;
+        r.is_v = hh >= A.q_heads + A.pool.heads;
+        r.h = r.is_q ? hh : r.is_v ? hh - A.q_heads - A.pool.heads : hh - A.q_heads;
+        r.d0 = u < paired ? 8 * u : kInter ? 8 * u : rot + 8 * (u - paired);
+        r.d1 = u < paired ? r.d0 + (rot >> 1) : -1;
+        return r;
+    };
+    constexpr int n = kAhead<kInter>;
+    uint4 x[n], y[kInter ? 1 : n];
+    auto read = [&](int32_t i0) {
+#pragma unroll
+        for (int a = 0; a < n; ++a) {
+            const int32_t i = i0 + a * kThreads;
+            if (i >= all) break;
+            const Unit u = unit(i);
+            const T* src = u.is_q ? (const T*)A.q + row * A.q_stride : (const T*)(u.is_v ? A.v : A.k) + row * A.kv_stride;
+            src += (int64_t)u.h * D;
+            x[a] = *reinterpret_cast<const uint4*>(src + u.d0);
+            if (!kInter && u.d1 >= 0) y[kInter ? 0 : a] = *reinterpret_cast<const uint4*>(src + u.d1);
+        }
+    };
+    read(threadIdx.x);
+
     if (row == 0 && threadIdx.x == 0) {
         const int64_t end = (int64_t)A.chunk.offs[A.chunk.B] + A.chunk.B;
         if (end > A.chunk.rows || A.chunk.offs[0] != 0) report(A.status, 1u << SV_ERR_BAD_OFFSETS);
@@ -80,76 +118,76 @@ __global__ void __launch_bounds__(kThreads) k_cache_append(const AppendArgs A) {
     const bool store = place >= 0;
     if (!store && threadIdx.x == 0) report(A.status, 1u << SV_ERR_BAD_OFFSETS);
 
-    const int32_t rot = A.rot, D = A.pool.dim;
-    const int32_t paired = kInter ? 0 : rot >> 4;
-    const int32_t units = paired + ((D - (kInter ? 0 : rot)) >> 3);
     const float* cs = A.rope + (int64_t)(s.past + depth) * rot;
-    const int32_t heads = A.q_heads + 2 * A.pool.heads;
-    for (int32_t i = threadIdx.x; i < heads * units; i += kThreads) {
-        const int32_t hh = i / units, u = i - hh * units;
-        const bool is_q = hh < A.q_heads, is_v = hh >= A.q_heads + A.pool.heads;
-        const int32_t h = is_q ? hh : is_v ? hh - A.q_heads - A.pool.heads : hh - A.q_heads;
-        const T* src = is_q   ? (const T*)A.q + row * A.q_stride
-                       : is_v ? (const T*)A.v + row * A.kv_stride
-                              : (const T*)A.k + row * A.kv_stride;
-        src += (int64_t)h * D;
-        const int32_t d0 = u < paired ? 8 * u : (kInter ? 8 * u : rot + 8 * (u - paired));
-        const int32_t d1 = u < paired ? d0 + (rot >> 1) : -1;
-        float x[8], y[8];
-        load8(src + d0, x);
-        if (d1 >= 0) load8(src + d1, y);
-        if (!is_v) {
-            if (d1 >= 0) {
+#pragma unroll 1
+    for (int32_t i0 = threadIdx.x; i0 < all; i0 += n * kThreads) {
+        if (i0 != threadIdx.x) read(i0);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float c = __ldg(cs + d0 + e), sn = __ldg(cs + (rot >> 1) + d0 + e);
-                    const float a = x[e], w = y[e];
-                    x[e] = a * c - w * sn;
-                    y[e] = w * c + a * sn;
-                }
-            } else if (kInter && d0 < rot) {
+        for (int a = 0; a < n; ++a) {
+            const int32_t i = i0 + a * kThreads;
+            if (i >= all) break;
+            const Unit u = unit(i);
+            float p[8], q[8];
+            unpack8<T>(x[a], p);
+            if (!kInter && u.d1 >= 0) unpack8<T>(y[kInter ? 0 : a], q);
+            if (!u.is_v) {
+                if (!kInter && u.d1 >= 0) {
+                    float c[8], sn[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float c = __ldg(cs + (d0 >> 1) + e), sn = __ldg(cs + (rot >> 1) + (d0 >> 1) + e);
-                    const float a = x[2 * e], w = x[2 * e + 1];
-                    x[2 * e] = a * c - w * sn;
-                    x[2 * e + 1] = w * c + a * sn;
+                    for (int e = 0; e < 8; e += 4) {
+                        *reinterpret_cast<float4*>(c + e) = __ldg(reinterpret_cast<const float4*>(cs + u.d0 + e));
+                        *reinterpret_cast<float4*>(sn + e) = __ldg(reinterpret_cast<const float4*>(cs + (rot >> 1) + u.d0 + e));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = p[e], w = q[e];
+                        p[e] = v * c[e] - w * sn[e];
+                        q[e] = w * c[e] + v * sn[e];
+                    }
+                } else if (kInter && u.d0 < rot) {
+                    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + (u.d0 >> 1)));
+                    const float4 sn = __ldg(reinterpret_cast<const float4*>(cs + (rot >> 1) + (u.d0 >> 1)));
+                    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = p[2 * e], w = p[2 * e + 1];
+                        p[2 * e] = v * cc[e] - w * ss[e];
+                        p[2 * e + 1] = w * cc[e] + v * ss[e];
+                    }
                 }
             }
-        }
-        if (is_q) {
-            T* dst = (T*)A.q_out + ((int64_t)row * A.q_heads + h) * D;
-            store8(dst + d0, x);
-            if (d1 >= 0) store8(dst + d1, y);
-        } else if (store) {
-            const int64_t at = place + h * A.pool.s_head;
-            char* base = is_v ? A.pool.v : A.pool.k;
-            if (kE4m3) {
-                const float* scales = is_v ? A.pool.v_scale : A.pool.k_scale;
-                const float sc = scales ? __ldg(scales + h) : 1.f;
-                store8_e4m3(base + at + d0, x, sc);
-                if (d1 >= 0) store8_e4m3(base + at + d1, y, sc);
-            } else {
-                store8((T*)base + at + d0, x);
-                if (d1 >= 0) store8((T*)base + at + d1, y);
+            if (u.is_q) {
+                T* dst = (T*)A.q_out + ((int64_t)row * A.q_heads + u.h) * D;
+                store8(dst + u.d0, p);
+                if (!kInter && u.d1 >= 0) store8(dst + u.d1, q);
+            } else if (store) {
+                const int64_t at = place + u.h * A.pool.s_head;
+                char* base = u.is_v ? A.pool.v : A.pool.k;
+                if (kE4m3) {
+                    const float* scales = u.is_v ? A.pool.v_scale : A.pool.k_scale;
+                    const float sc = scales ? __ldg(scales + u.h) : 1.f;
+                    store8_e4m3(base + at + u.d0, p, sc);
+                    if (!kInter && u.d1 >= 0) store8_e4m3(base + at + u.d1, q, sc);
+                } else {
+                    store8((T*)base + at + u.d0, p);
+                    if (!kInter && u.d1 >= 0) store8((T*)base + at + u.d1, q);
+                }
             }
         }
     }
 }
 
 template <typename T, bool kE4m3>
-void launch(const AppendArgs& A, bool inter, cudaStream_t st) {
-    if (inter) k_cache_append<T, kE4m3, true><<<A.chunk.rows, kThreads, 0, st>>>(A);
-    else k_cache_append<T, kE4m3, false><<<A.chunk.rows, kThreads, 0, st>>>(A);
+cudaError_t launch(const AppendArgs& A, bool inter, cudaStream_t st) {
+    const auto kernel = inter ? k_cache_append<T, kE4m3, true> : k_cache_append<T, kE4m3, false>;
+    return launch_chained(kernel, dim3(A.chunk.rows), dim3(kThreads), st, A);
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& A, int dtype, int cache_dtype, bool interleaved, cudaStream_t st) {
-    if (cache_dtype == SV_E4M3) launch<__nv_bfloat16, true>(A, interleaved, st);
-    else if (dtype == SV_F16) launch<__half, false>(A, interleaved, st);
-    else launch<__nv_bfloat16, false>(A, interleaved, st);
-    return cudaGetLastError();
+    if (cache_dtype == SV_E4M3) return launch<__nv_bfloat16, true>(A, interleaved, st);
+    return dtype == SV_F16 ? launch<__half, false>(A, interleaved, st) : launch<__nv_bfloat16, false>(A, interleaved, st);
 }
 
 }  // namespace cache

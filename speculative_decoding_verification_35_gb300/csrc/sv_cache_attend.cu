@@ -19,6 +19,8 @@
 // on the device, so the host needs to know none of them.
 #include "sv_cache_attend.cuh"
 
+#include <algorithm>
+
 namespace sv {
 namespace cache {
 namespace {
@@ -510,7 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0 && sh.gave_up) report(P.a.status, 1u << SV_ERR_TIMEOUT);
 }
 
-// Items that several CTAs worked on: one warp a row, the parts in their order.
+// Items that several CTAs worked on: one warp a row, the parts in their order. Bound by the latency of a few dependent
+// reads from L2, so the first parts are read along with the references, and there are warps for every row at once.
 constexpr int kMergeThreads = 256;
 template <typename T, int DP>
 __global__ void __launch_bounds__(kMergeThreads) k_attend_merge(const __grid_constant__ Params P) {
@@ -518,58 +521,62 @@ __global__ void __launch_bounds__(kMergeThreads) k_attend_merge(const __grid_con
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t c = blockIdx.x + 1;
     const Record rec = P.records[c];
-    if (!rec.parts) return;
+    const int32_t i = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);  // the item's row
+    if (!rec.parts || i >= rec.tokens * P.G) return;
     const int lane = threadIdx.x & 31;
-    const int32_t D = P.a.pool.dim, rows = rec.tokens * P.G;
-    constexpr int kPer = DP / 32;
+    constexpr int kPer = DP / 32, kAtOnce = 4;
+    const bool in = lane * kPer < P.a.pool.dim;
+    const int32_t t = i / P.G, g = i - t * P.G;
+    const int32_t r = t < rec.split ? i : kTile + i - rec.split * P.G;
+    // the first part is the last item of CTA c - 1, the others the first items of c, c + 1, ...
+    auto slot = [&](int32_t part) { return (size_t)(part ? 2 * (c + part - 1) : 2 * (c - 1) + 1) * P.part_rows + r; };
+    float x[kAtOnce][kPer];
+    auto read = [&](int32_t p0) {
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) x[k][e] = 0.f;
+            if (p0 + k >= rec.parts || !in) continue;
+            const float* o = P.part_o + slot(p0 + k) * DP + lane * kPer;
+            if (kPer == 4) *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(o);
+            else *reinterpret_cast<float2*>(x[k]) = *reinterpret_cast<const float2*>(o);
+        }
+    };
+    read(0);
+    float2 ml = lane < rec.parts ? P.part_ml[slot(lane)] : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
 #pragma unroll 1
-    for (int32_t i = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); i < rows;
-         i += gridDim.y * (kMergeThreads / 32)) {
-        const int32_t t = i / P.G, g = i - t * P.G;
-        const int32_t r = t < rec.split ? i : kTile + i - rec.split * P.G;
-        // the first part is the last item of CTA c - 1, the others the first items of c, c + 1, ...
-        auto slot = [&](int32_t part) { return (size_t)(part ? 2 * (c + part - 1) : 2 * (c - 1) + 1) * P.part_rows + r; };
-        float top = -INFINITY;
+    for (int32_t p = 32 + lane; p < rec.parts; p += 32) top = fmaxf(top, P.part_ml[slot(p)].x);
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    const float base = top == -INFINITY ? 0.f : top;
+    float l = 0.f, acc[kPer] = {}, wt = 0.f;
 #pragma unroll 1
-        for (int32_t p = lane; p < rec.parts; p += 32) top = fmaxf(top, P.part_ml[slot(p)].x);
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-        const float base = top == -INFINITY ? 0.f : top;
-        float l = 0.f, acc[kPer] = {};
-#pragma unroll 1
-        for (int32_t p0 = 0; p0 < rec.parts; p0 += 32) {
-            float wt = 0.f, pl = 0.f;
-            if (p0 + lane < rec.parts) {
-                const float2 ml = P.part_ml[slot(p0 + lane)];
-                wt = top == -INFINITY ? 1.f : exp2_fast(ml.x - base);
-                pl = ml.y * wt;
-            }
+    for (int32_t p = 0; p < rec.parts; p += kAtOnce) {
+        if (p % 32 == 0) {
+            if (p > 0) ml = p + lane < rec.parts ? P.part_ml[slot(p + lane)] : make_float2(-INFINITY, 0.f);
+            wt = p + lane >= rec.parts ? 0.f : top == -INFINITY ? 1.f : exp2_fast(ml.x - base);
+            float pl = ml.y * wt;
             for (int o = 16; o; o >>= 1) pl += __shfl_xor_sync(kAll, pl, o);
             l += pl;
-            const int32_t n = min(32, rec.parts - p0);
-#pragma unroll 4
-            for (int32_t k = 0; k < n; ++k) {
-                const float f = __shfl_sync(kAll, wt, k);
-                const float* o = P.part_o + slot(p0 + k) * DP + lane * kPer;
-                if (lane * kPer < D) {
-                    float x[kPer];
-                    if (kPer == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(o);
-                    else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(o);
-#pragma unroll
-                    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(f, x[e], acc[e]);
-                }
-            }
         }
-        const float vs = P.a.pool.v_scale ? P.a.pool.v_scale[rec.head] : 1.f;
-        const float inv = l == 0.f ? 0.f : vs / l;
-        const int64_t at = (int64_t)(rec.row0 + t) * P.a.q_heads + rec.head * P.G + g;
-        if (lane * kPer < D) {
-            T* out = (T*)P.a.out + at * D + lane * kPer;
 #pragma unroll
-            for (int e = 0; e < kPer; e += 2)
-                *reinterpret_cast<uint32_t*>(out + e) = from_float2<T>(acc[e] * inv, acc[e + 1] * inv);
+        for (int k = 0; k < kAtOnce; ++k) {
+            const float f = __shfl_sync(kAll, wt, (p + k) & 31);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[e] = p + k < rec.parts ? fmaf(f, x[k][e], acc[e]) : acc[e];
         }
-        if (P.a.lse && lane == 0) P.a.lse[at] = l == 0.f ? -INFINITY : top * kLn2 + logf(l);
+        if (p + kAtOnce < rec.parts) read(p + kAtOnce);
     }
+    const float vs = P.a.pool.v_scale ? P.a.pool.v_scale[rec.head] : 1.f;
+    const float inv = l == 0.f ? 0.f : vs / l;
+    const int64_t at = (int64_t)(rec.row0 + t) * P.a.q_heads + rec.head * P.G + g;
+    if (in) {
+        T* out = (T*)P.a.out + at * P.a.pool.dim + lane * kPer;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2)
+            *reinterpret_cast<uint32_t*>(out + e) = from_float2<T>(acc[e] * inv, acc[e + 1] * inv);
+    }
+    if (P.a.lse && lane == 0) P.a.lse[at] = l == 0.f ? -INFINITY : top * kLn2 + logf(l);
 }
 
 template <int K, int DP>
@@ -603,7 +610,8 @@ cudaError_t merge(Params& P, cudaStream_t st, bool narrow) {
     static std::atomic<unsigned long long> allowed{~0ull};  // it asks for no shared memory
     void* args[] = {&P};
     const void* k = narrow ? (const void*)k_attend_merge<T, 64> : (const void*)k_attend_merge<T, 128>;
-    return launch_early(k, &allowed, dim3(P.ctas - 1, 4), kMergeThreads, 0, st, args);
+    const int warps = kMergeThreads / 32, rows = (int)std::min((int64_t)(P.a.chunk.max_gamma + 1) * P.G, (int64_t)P.part_rows);
+    return launch_early(k, &allowed, dim3(P.ctas - 1, (rows + warps - 1) / warps), kMergeThreads, 0, st, args);
 }
 
 }  // namespace

@@ -16,7 +16,9 @@ constexpr int kThreads = 128;
 constexpr int kAhead = 8;
 
 // grid: (B, layers * 2, columns of a token / kThreads)
-__global__ void __launch_bounds__(kThreads) k_cache_compact(const CompactArgs A, bool write_now) {
+__global__ void __launch_bounds__(kThreads) k_cache_compact(const __grid_constant__ CompactArgs A, bool write_now) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
     const int32_t b = blockIdx.x, layer = blockIdx.y >> 1;
     const Seq s = seq_of(A.chunk, capacity_of(A.pool), b);
@@ -80,7 +82,9 @@ __global__ void __launch_bounds__(kThreads) k_cache_compact(const CompactArgs A,
 }
 
 // The new lengths, written after the moves where they replace the lengths that the moves read.
-__global__ void __launch_bounds__(kThreads) k_cache_advance(const CompactArgs A) {
+__global__ void __launch_bounds__(kThreads) k_cache_advance(const __grid_constant__ CompactArgs A) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t warp = (blockIdx.x * kThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
     if (warp >= A.chunk.B) return;
     const Seq s = seq_of(A.chunk, capacity_of(A.pool), warp);
@@ -101,9 +105,9 @@ cudaError_t launch_compact(const CompactArgs& A, cudaStream_t st) {
     const int32_t cols = A.pool.heads * (A.pool.dim * A.esize / 16);
     const dim3 grid((unsigned)A.chunk.B, A.path ? 2u * (unsigned)A.pool.layers : 1u,
                     A.path ? (unsigned)((cols + kThreads - 1) / kThreads) : 1u);
-    k_cache_compact<<<grid, kThreads, 0, st>>>(A, !in_place);
-    if (in_place) k_cache_advance<<<(A.chunk.B + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, st>>>(A);
-    return cudaGetLastError();
+    const cudaError_t e = launch_chained(k_cache_compact, grid, dim3(kThreads), st, A, !in_place);
+    if (e != cudaSuccess || !in_place) return e;
+    return launch_chained(k_cache_advance, dim3((A.chunk.B + kThreads / 32 - 1) / (kThreads / 32)), dim3(kThreads), st, A);
 }
 
 }  // namespace cache
