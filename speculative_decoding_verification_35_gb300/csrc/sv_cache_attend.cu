@@ -212,6 +212,23 @@ __device__ __forceinline__ void rescale(uint32_t o_col, float f) {
     }
 }
 
+// Among four lanes: what was block b (8 of 32) of lane i becomes block i of lane b.
+__device__ __forceinline__ void trade(uint32_t* u, int lane) {
+#pragma unroll
+    for (int o = 1; o <= 2; o *= 2)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            if (!(b & o))
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t &lo = u[8 * b + i], &hi = u[8 * (b + o) + i];
+                    const bool up = lane & o;
+                    const uint32_t got = __shfl_xor_sync(kAll, up ? lo : hi, o);
+                    lo = up ? got : lo;
+                    hi = up ? hi : got;
+                }
+}
+
 template <int K, int DP>
 __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
     using KT = KindOf<K>;
@@ -312,38 +329,47 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
         // a row that carries NaN or infinity in its sum stays so: inv is then NaN or zero
         const size_t prow = (size_t)(2 * blockIdx.x + (it.begins ? 1 : 0)) * P.part_rows + stream * kTile + r;
         if (busy) {
+            // A lane has a row; four lanes trade, so that they write 128 bytes of one row and then of the next.
+            const int64_t at = alone ? ((int64_t)row_at * A.q_heads + head) * D : (int64_t)prow * DP;
+            const uint32_t real = __ballot_sync(kAll, row.real) >> (lane & ~3);
+            const int part = (lane & 3) * 8;
+            const int step = alone ? 64 : 32;  // columns of 128 bytes
 #pragma unroll 1
-            for (int c = 0; c < DP; c += 32) {
-                uint32_t o[32];
-                tc_ld32(o_col + c, o);
+            for (int c = 0; c < D; c += step) {
+                uint32_t u[32];
+                tc_ld32(o_col + c, u);
+                if (alone) {
+                    uint32_t o[32];
+                    tc_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        u[i] = from_float2<T>(__uint_as_float(u[2 * i]) * inv, __uint_as_float(u[2 * i + 1]) * inv);
+                    tc_ld32(o_col + c + 32, o);  // past D: columns that are not written
+                    tc_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        u[16 + i] = from_float2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                }
                 tc_wait_ld();
-                if (row.real) {
-                    if (alone) {
-                        T* out = (T*)A.out + ((int64_t)row_at * A.q_heads + head) * D;
-                        uint32_t u[16];
+                trade(u, lane);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            u[i] = from_float2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-                        // lanes write to rows of their own: whole 32-byte sectors halve what that costs
-#pragma unroll
-                        for (int i = 0; i < 32; i += 16) {
-                            const uint32_t* w = u + i / 2;
-                            if (P.wide && c + i < D) {
-                                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + c + i), SV_W8(w, 0)
-                                             : "memory");
-                            } else {
-                                if (c + i < D) *reinterpret_cast<uint4*>(out + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
-                                if (c + i + 8 < D)
-                                    *reinterpret_cast<uint4*>(out + c + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                            }
-                        }
+                for (int b = 0; b < 4; ++b) {
+                    const int64_t to = __shfl_sync(kAll, at, (lane & ~3) + b);
+                    const uint32_t* v = u + 8 * b;
+                    if (!(real >> b & 1u)) continue;
+                    if (!alone) {
+                        if (c + part < D)
+                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(P.part_o + to + c + part), SV_W8(v, 0)
+                                         : "memory");
+                        continue;
+                    }
+                    const int d = c + 2 * part;
+                    T* out = (T*)A.out + to + d;
+                    if (P.wide && d < D) {
+                        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out), SV_W8(v, 0) : "memory");
                     } else {
-                        float* out = P.part_o + prow * DP + c;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            if (c + i < D)
-                                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + i), SV_W8(o, i)
-                                             : "memory");
+                        if (d < D) *reinterpret_cast<uint4*>(out) = make_uint4(v[0], v[1], v[2], v[3]);
+                        if (d + 8 < D) *reinterpret_cast<uint4*>(out + 8) = make_uint4(v[4], v[5], v[6], v[7]);
                     }
                 }
             }
