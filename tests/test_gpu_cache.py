@@ -373,6 +373,127 @@ def test_streams_graphs_and_repeats(sc):
     b.compare(out, lse)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("tokens,group", [(4, 4), (17, 1), (8, 4), (33, 1), (8, 8), (13, 5), (32, 4), (43, 3), (256, 1),
+                                          (65, 4), (2, 128), (3, 127)])
+def test_rows_of_a_group(sc, tokens, group, kind, cache, D):
+    """tokens x group rows read the same keys: 16, 32, 64, 128, 256 of them, and just past those."""
+    Batch(sc, [tokens, 1, (tokens + 1) // 2], [290, 0, 127], 2 * group, 2, D, 32, kind, cache, seed=tokens).check()
+
+
+@pytest.mark.parametrize("kind,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("group,window", [(1, 0), (1, 5), (2, 0), (2, 40), (4, 0), (4, 3), (8, 200)])
+def test_trees_of_a_group(sc, group, window, kind, cache):
+    rng = np.random.default_rng(group)
+    chunks = [32, 5, 1, 17]
+    par = [tree(rng, n) for n in chunks]
+    Batch(sc, chunks, [250, 128, 40, 0], 2 * group, 2, 128, 16, kind, cache, parents=par, seed=group).check(window)
+
+
+@pytest.mark.parametrize("kind,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("tokens,group", [(3, 2), (6, 4), (7, 8), (100, 2)])
+@pytest.mark.parametrize("value", [40.0, -40.0, 300.0])
+def test_moving_references(sc, value, tokens, group, kind, cache):
+    """Scores that climb (or fall) along the cache past what a weight's type holds, so that a row's reference moves."""
+    b = Batch(sc, [tokens], [900], 2 * group, 2, 64, 16, kind, cache, qscale=1.0)
+    b.q[..., 0] = 64.0
+    slots = torch.arange(900 + tokens, device="cuda")
+    ramp = value / 8 * slots / 900  # times 64 / sqrt(64)
+    pages = torch.tensor(b.table_h[0].astype(np.int64), device="cuda")[slots // 16]
+    for h in range(2):
+        x = ramp if b.ks is None else ramp / b.ks[0, h]
+        b.k[0, pages, slots % 16, h, 0] = x.clamp(-448, 448).to(b.k.dtype)
+    b.check()
+
+
+@pytest.mark.parametrize("kind,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("tokens,group", [(6, 2), (9, 6), (90, 2)])
+def test_scales_of_either_sign_and_zero(sc, tokens, group, kind, cache):
+    b = Batch(sc, [tokens, 1], [200, 30], 2 * group, 2, 64, 16, kind, cache)
+
+    def run(q, scale):
+        out = torch.empty((b.rows, b.hq, b.D), dtype=TYPES[kind], device="cuda")
+        lse = torch.empty((b.rows, b.hq), device="cuda")
+        assert b.cache.attend(b.chunk, q, out, lse, scale=scale) == 0
+        return out, lse
+    for (q1, s1), (q2, s2) in (((b.q, -0.11), (-b.q, 0.11)), ((b.q, 0.0), (0 * b.q, 0.11))):
+        for x, y in zip(run(q1, s1), run(q2, s2)):
+            torch.cuda.synchronize()
+            assert torch.equal(x, y)
+    assert b.cache.status_bits() == 0
+    # with a scale of zero every slot weighs the same
+    want = torch.log(torch.tensor([200.0 + t + 1 for t in range(tokens)] + [31.0], device="cuda"))
+    assert (run(b.q, 0.0)[1] - want[:, None]).abs().max() <= 2.0 ** -18 + 2.0 ** -22 * 6
+
+
+@pytest.mark.parametrize("kind,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("tokens,group,window", [(6, 2, 0), (12, 4, 0), (12, 4, 20), (140, 2, 0), (140, 2, 150)])
+def test_nonfinite_values_of_a_chain(sc, tokens, group, window, kind, cache):
+    """A token's NaN changes the rows that see the token, those at or after it and within the window, and no others."""
+    b = Batch(sc, [tokens], [131], 2 * group, 2, 64, 16, kind, cache)
+    good, gl = b.attend(window)
+    seen = []
+    for slot in (131 + tokens // 2, 131 + tokens - 1) + ((112 + tokens // 2,) if window == 20 else ()):
+        pg, at = int(b.table_h[0][slot // 16]), slot % 16
+        if cache == "e4m3":
+            b.v.view(torch.uint8)[0, pg, at, :, 9] = 0x7F
+        else:
+            b.v[0, pg, at, :, 9] = float("nan") if slot % 2 else float("inf")
+        seen.append(slot)
+    out, lse = b.attend(window)
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == 0 and torch.equal(lse, gl)
+    pos = 131 + np.arange(tokens)
+    hit = np.zeros(tokens, dtype=bool)
+    for slot in seen:
+        hit |= (slot <= pos) & ((window == 0) | (slot > pos - window))
+    hit = torch.tensor(hit, device="cuda")
+    other = torch.arange(64, device="cuda") != 9
+    assert torch.equal(out[~hit], good[~hit]) and torch.equal(out[:, :, other], good[:, :, other])
+    assert not torch.isfinite(out[hit][:, :, 9]).any()
+
+
+def test_many_long_chunks(sc):
+    """More sequences than a launch has threads, in chunks of more rows than one query tile."""
+    rng = np.random.default_rng(4)
+    Batch(sc, [int(x) for x in rng.integers(60, 80, 530)], [int(x) for x in rng.integers(0, 30, 530)], 2, 1, 64, 8).check()
+
+
+def test_bad_pages_of_prompts(sc):
+    b = Batch(sc, [150, 70], [60, 200], 4, 2, 64, 16, "fp16", "fp16")
+    b.table_h[0, 2] = -1
+    b.table_h[1, :] = b.k.shape[1] + 5
+    b.table.copy_(torch.tensor(b.table_h))
+    b.check(status=BAD_OFFSETS)
+
+
+@pytest.mark.parametrize("chunks", [[3, 1], [130, 70]])
+def test_outputs_on_16_bytes(sc, chunks):
+    b = Batch(sc, chunks, [300, 20], 4, 2, 64, 16)
+    good, _ = b.attend()
+    room = torch.full((good.numel() + 8,), 7.0, dtype=good.dtype, device="cuda")
+    out = room[8:].view(good.shape)
+    assert b.cache.attend(b.chunk, b.q, out, None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, good) and (room[:8] == 7).all()
+
+
+def test_calls_in_a_row_on_one_workspace(sc):
+    """Launches that begin while the last one ends wait for what it writes."""
+    b = Batch(sc, [6, 2, 40], [2000, 300, 0], 8, 2, 128, 16)
+    other = Batch(sc, [90, 1], [10, 5000], 8, 2, 128, 16, seed=7)
+    want = [x.attend()[0] for x in (b, other)]
+    torch.cuda.synchronize()
+    other.cache.workspace, other.cache._ws = b.cache.workspace, b.cache._ws
+    got = []
+    for _ in range(20):
+        got.append((b.attend()[0], other.attend()[0]))
+    torch.cuda.synchronize()
+    for pair in got:
+        assert torch.equal(pair[0], want[0]) and torch.equal(pair[1], want[1])
+
+
 # ------------------------------------------------------------------------------------------------
 # append
 # ------------------------------------------------------------------------------------------------
