@@ -23,7 +23,9 @@
  * the device set bit (1u << code) of *device_status (nullable; the caller clears it):
  *   SV_ERR_BAD_OFFSETS  seq_offsets[0] != 0, T_b outside 1 .. max_gamma + 1, rows past `rows`, a parent
  *                       outside [0, j), a page id outside [0, pages), an accepted path that is none
- *   SV_ERR_CAPACITY     cached[b] < 0, or slots cached[b] + T_b past the page table or the rotation table
+ *   SV_ERR_CAPACITY     cached[b] < 0, or slots cached[b] + T_b past the page table or the rotation table; or a
+ *                       batch too long for one spec_cache_attend call (2^31 pieces of 128 slots, over all kv heads;
+ *                       nothing is written then)
  *   SV_ERR_TIMEOUT      a bounded wait inside the launch gave up (the outputs are then undefined)
  * A sequence with a finding fails alone: append writes nothing of it, attend writes zeros and an lse of -inf
  * (nothing where the rows themselves are bad), compact moves nothing. A bad page id fails only its tokens:
@@ -124,7 +126,8 @@ size_t spec_cache_workspace_size(const sv_cache* cache);
  * of the chunk sees, and whatever lies in pages beyond a sequence's last token, are never read into a result,
  * NaN and infinities included. A token that sees nothing (bad pages) gets zeros and an lse of -inf.
  * Scores, the softmax's statistics and the accumulators are float; the weights w_s are rounded to the
- * precision of dtype before the product with v.
+ * precision of dtype before the product with v (for fp16 to 2^-24, with an SV_E4M3 cache to 2^-17 of the row's
+ * largest where they are smaller than that allows).
  * q as in spec_cache_append (rotated), q_heads a multiple of cache->heads by at most 128; out is
  * [rows][q_heads][head_dim], lse (nullable) float[rows][q_heads]; rows outside every sequence are not
  * written. workspace: spec_cache_workspace_size(cache) bytes aligned to 256, not shared by calls that may
