@@ -293,20 +293,20 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
                 tc_wait_st();
             }
             const bool mixed = mixed_tile(it, k0);
-            if (mixed) {  // before p_ready: the tile cannot be released, nor its barrier move on, until then
+            if (rarely(mixed)) {  // before p_ready: the tile cannot be released, nor its barrier move on, until then
                 const uint32_t v = tiles + j;
                 if (!wait(smem_u32(&sh.value[v % P.v_slots]), (v / P.v_slots) & 1, gave_up)) return;
             }
             tc_before();
             __syncwarp();
             if (lane == 0) bar_arrive(p_ready);
-            if (mixed) {
+            if (rarely(mixed)) {
                 // rows that see a non-finite value, which the product met as zero, get it added here
                 const uint32_t none[4] = {0, 0, 0, 0};
                 uint32_t odd[4], any = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) any |= odd[i] = sh.odd[ring][i];
-                if (any && busy) {
+                if (rarely(any && busy)) {
                     if (!wait(pv_done, steps & 1, gave_up)) return;
                     tc_after();
                     add_odd<K, DP>(A, it, o_col, k0, row.real ? odd : none, seen);
@@ -436,13 +436,16 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
             if (t >= 0) {
                 const uint32_t b = operand(v_smem + vr.i * slot_bytes, kHalf);
                 const uint32_t add = t > 0;
+                int32_t lo, hi;
+                steps_of<K>(it, (it.tile + t) * kTile, lo, hi);
                 if (leader) {
 #pragma unroll
                     for (int i = 0; i < kTile / KindOf<K>::kStep; ++i)
+                        if (i >= lo && i < hi)
 #pragma unroll
                         for (int part = 0; part < parts; ++part)
                             mma_ts<k8>(o_at, s_at + (k8 ? part * 8 + i * 16 : i * 8), b + (i * KindOf<K>::kStep * 128 >> 4), id_o,
-                                       part + i > 0 ? 1u : add);
+                                       i > lo || part > 0 ? 1u : add);
                     if (!more) bar_arrive(turn[1]);
                     tc_commit(pv_done);
                     tc_commit(v_empty + 8 * vr.i);

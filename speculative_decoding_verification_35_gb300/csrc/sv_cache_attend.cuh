@@ -22,6 +22,9 @@ constexpr int kSmem = 227 * 1024;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr unsigned kAll = 0xffffffffu;
 
+// What is rarely so: its code is put aside, so that what runs lies closer together in the instruction cache.
+__device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, 0); }
+
 // ---------------------------------------------------------------------------------------------------------
 // element kinds
 // ---------------------------------------------------------------------------------------------------------
@@ -112,6 +115,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 constexpr uint32_t kPolls = 1u << 24;
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
     bool ok = bar_try(bar, parity);
+    if (!rarely(!__all_sync(kAll, ok))) return true;
 #pragma unroll 1
     for (uint32_t i = 1; !__all_sync(kAll, ok); ++i) {
         if (!ok) ok = bar_try(bar, parity);
@@ -569,7 +573,7 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
             need = need && !miss;
             const uint32_t todo = __ballot_sync(kAll, need), bytes = __popc(todo) * box * 128 * P.halves;
             uint32_t bad = 0;
-            if (__any_sync(kAll, miss)) {
+            if (rarely(__any_sync(kAll, miss))) {
                 if (miss) {
                     report(P.a.status, 1u << SV_ERR_BAD_OFFSETS);
                     bad = ((1u << (box / 8)) - 1u) << (lane * (box / 8));
@@ -643,7 +647,7 @@ __device__ __forceinline__ bool load_queries(const Params& P, Common& sh, const 
                     copy_queries(q_smem + t * P.q_tile + h * P.q_part, qm, h * 64, it.h * P.G, it.row0 + it.t0 + t * it.split, bar);
         }
         __syncwarp();
-        if (!flip) return true;
+        if (!rarely(flip)) return true;
         if (!wait(bar, items & 1, &sh.gave_up)) return false;
 #pragma unroll 1
         for (int i = lane; i < q_tiles * P.q_tile / 16; i += 32) {
@@ -715,46 +719,72 @@ __device__ __forceinline__ bool load_queries(const Params& P, Common& sh, const 
     return true;
 }
 
+// The steps of a tile's depth that O += P V takes: those with a slot that some row of the item sees.
+template <int K>
+__device__ __forceinline__ void steps_of(const Item& it, int32_t k0, int32_t& lo, int32_t& hi) {
+    constexpr int step = KindOf<K>::kStep;
+    lo = max(0, it.lo - k0) / step;
+    hi = (min(kTile, it.end - k0) + step - 1) / step;
+}
+
 // Rows [lo, hi) of a value tile set to zero. A whole row is the same 128 bytes under any swizzle.
 __device__ __forceinline__ void clear_rows(int halves, uint32_t at, int32_t lo, int32_t hi) {
-    lo = max(lo, 0);
-    hi = min(hi, kTile);
 #pragma unroll 1
     for (int32_t i = lo * 8 + (threadIdx.x & 31); i < hi * 8; i += 32)
         for (int h = 0; h < halves; ++h)
             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at + h * kHalf + i * 16), "r"(0) : "memory");
 }
 
-// Non-finite elements of rows [lo, hi): cleared, and their rows noted.
+// 16 bytes' non-finite elements cleared; whether there were any.
+template <int K>
+__device__ __forceinline__ bool clean16(uint32_t a) {
+    constexpr int bits = K == kE4m3 ? 8 : 16;
+    constexpr uint32_t one = (1u << bits) - 1u, top = K == kE4m3 ? 0x7fu : K == kBf16 ? 0x7f80u : 0x7c00u;
+    bool any = false;
+#pragma unroll 1
+    for (int e = 0; e < 16; e += 4) {
+        uint32_t x, clear = 0;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a + e));
+#pragma unroll 1
+        for (int by = 0; by < 32; by += bits)
+            if ((x >> by & top) == top) clear |= one << by;
+        if (!clear) continue;
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(a + e), "r"(x & ~clear) : "memory");
+        any = true;
+    }
+    return any;
+}
+
+// Non-finite elements of rows [lo, hi): cleared, and their rows noted. A product with zero finds them, for 16 bits:
+// x 0 + a is NaN from the first one on. Four reads are under way at a time (one after the other they took 7000 cycles
+// of a tile of 128 rows of 256 bytes).
 template <int K>
 __device__ __forceinline__ void scan_rows(int halves, uint32_t at, int32_t lo, int32_t hi, uint32_t bad, uint32_t* odd) {
-    constexpr int bits = K == kE4m3 ? 8 : 16;
-    constexpr uint32_t unit = K == kE4m3 ? 0x01010101u : 0x00010001u, one = (1u << bits) - 1u;
-    constexpr uint32_t top = unit * (K == kE4m3 ? 0x7fu : K == kBf16 ? 0x7f80u : 0x7c00u), high = unit << (bits - 1);
 #pragma unroll 1
-    for (int32_t i = lo * 8 + (threadIdx.x & 31); i < hi * 8; i += 32)
+    for (int h = 0; h < halves; ++h, at += kHalf)
 #pragma unroll 1
-        for (int h = 0; h < halves; ++h) {
-            const uint32_t a = at + h * kHalf + i * 16;
-            uint32_t u[4], any = 0;
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(a));
+        for (int32_t i = lo * 8 + (threadIdx.x & 31); i < hi * 8; i += 128) {
+            uint32_t u[4][4], any = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t t = ~u[e] & top;  // an element of zeros: its exponent is all ones (or one below it is)
-                any |= (t - unit) & ~t & high;
+            for (int k = 0; k < 4; ++k) {
+                u[k][0] = u[k][1] = u[k][2] = u[k][3] = 0;
+                if (i + 32 * k < hi * 8)
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(u[k][0]), "=r"(u[k][1]), "=r"(u[k][2]), "=r"(u[k][3])
+                                 : "r"(at + (i + 32 * k) * 16));
             }
-            if (!any || (bad >> (i >> 6) & 1u)) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (K == kE4m3) any |= ((u[k][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                    else if (K == kBf16) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(any) : "r"(u[k][e]), "r"(0));
+                    else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(any) : "r"(u[k][e]), "r"(0));
+                }
+            if (!rarely(K == kE4m3 ? any != 0 : (any & 0x7fff7fffu) != 0)) continue;
 #pragma unroll 1
-            for (int e = 0; e < 16; e += 4) {
-                uint32_t x, clear = 0;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a + e));
-#pragma unroll 1
-                for (int by = 0; by < 32; by += bits)
-                    if ((x >> by & top & one) == (top & one)) clear |= one << by;
-                if (!clear) continue;
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(a + e), "r"(x & ~clear) : "memory");
-                atomicOr(&odd[i >> 8], 1u << (i >> 3 & 31));
-            }
+            for (int32_t c = i; c < min(hi * 8, i + 128); c += 32)
+                if (!(bad >> (c >> 6) & 1u) && clean16<K>(at + c * 16)) atomicOr(&odd[c >> 8], 1u << (c >> 3 & 31));
         }
 }
 
@@ -772,7 +802,7 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
     for (uint32_t i = 0;; ++i, ring.step(kItems)) {
         Item it{};
         left -= max(0, lead - x);
-        if (left > 0 && T < 0) {  // the next sequence
+        if (rarely(left > 0 && T < 0)) {  // the next sequence
 #pragma unroll 1
             for (; b < P.a.chunk.B; ++b) {
                 const Seq s = seq_of(P.a.chunk, capacity_of(P.a.pool), b);
@@ -808,7 +838,7 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
             x = 0;
         }
         if (i >= kItems && !wait(smem_u32(&sh.item_empty[ring.i]), ring.parity ^ 1, &sh.gave_up)) break;
-        if (tree && it.n > 0) {
+        if (rarely(tree && it.n > 0)) {
             int32_t depth, par = 0;
             uint32_t above;
             bool ok;
@@ -872,18 +902,21 @@ __device__ __forceinline__ void value_role(const Params& P, Common& sh, uint32_t
             const int32_t k0 = (it.tile + j) * kTile;
             const uint32_t bad = sh.bad[1][v % kNotes];
             const bool mixed = mixed_tile(it, k0);
-            if (bad || k0 < it.lo || k0 + kTile > it.end || mixed) {
+            if (rarely(bad || k0 < it.lo || k0 + kTile > it.end || mixed)) {
                 const uint32_t at = v_smem + ring.i * (P.halves * kHalf);
                 uint32_t* odd = sh.odd[v % kNotes];
                 if (lane < 4) odd[lane] = 0;
                 __syncwarp();
                 const int32_t lo = max(0, it.lo - k0), hi = min(kTile, it.end - k0);
+                int32_t from, to;
+                steps_of<K>(it, k0, from, to);
                 // rows no one sees lie before the first and after the last one that is seen, or on bad pages
+                constexpr int step = KindOf<K>::kStep;
 #pragma unroll 1
                 for (int g = -2; g < (bad ? 16 : 0); ++g)
                     if (g < 0 || (bad >> g & 1u))
-                        clear_rows(P.halves, at, g == -2 ? 0 : g == -1 ? hi : 8 * g, g == -2 ? lo : g == -1 ? kTile : 8 * g + 8);
-                if (mixed)
+                        clear_rows(P.halves, at, g == -2 ? from * step : g == -1 ? hi : 8 * g, g == -2 ? lo : g == -1 ? to * step : 8 * g + 8);
+                if (rarely(mixed))
 #pragma unroll 1
                     for (int g = 0; g < 2; ++g)
                         scan_rows<K>(P.halves, at, g ? max(lo, it.mixed_hi - k0) : lo, g ? hi : min(hi, it.mixed_lo - k0), bad, odd);

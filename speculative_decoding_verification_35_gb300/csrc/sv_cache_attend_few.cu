@@ -132,7 +132,7 @@ __device__ __forceinline__ uint32_t rows_seeing(const Params& P, const Item& it,
                                                 int32_t row0) {
     if (slot < it.lo || slot >= it.end || (bad >> (slot % kTile >> 3) & 1u)) return 0;
     const int32_t i = slot - it.past, w = P.a.window;  // its place in the chunk, if it has one
-    if (!tree) {
+    if (!rarely(tree)) {
         const int32_t first = max(0, i), last = w > 0 ? min(it.nt - 1, i + w - 1) : it.nt - 1;
         return prefix32((last + 1) * P.G - row0) & ~prefix32(first * P.G - row0);
     }
@@ -196,7 +196,8 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
             const uint32_t ring = (tiles + j) % kNotes;
             const uint32_t bad = sh.bad[0][ring];
             const bool cut = k0 < max(it.lo, it.mixed_lo) || k0 + kTile > min(it.mixed_hi, it.end) || bad;
-            const uint32_t seen = cut ? rows_seeing(P, it, tree, k0 + k, bad, row0) : ~0u;
+            uint32_t seen = ~0u;
+            if (rarely(cut)) seen = rows_seeing(P, it, tree, k0 + k, bad, row0);
             uint32_t s[N];
             // Once, mostly: while the votes come in that no weight is too large, the weights are taken as if none were.
             bool fresh = unset;
@@ -205,7 +206,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
 #pragma unroll
                 for (int c = 0; c < N; c += 16) tc_ld16(s_col + c, s + c);
                 tc_wait_ld();
-                if (cut)
+                if (rarely(cut))
 #pragma unroll
                     for (int r = 0; r < N; ++r)
                         if (!(seen >> r & 1u)) s[r] = 0xff800000u;
@@ -254,7 +255,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                         s[r] = __float_as_uint(__uint_as_float(s[r]) - x);
                         off[r] -= x;
                     }
-                    if (moved) {
+                    if (rarely(moved)) {
 #pragma unroll
                         for (int r = 0; r < N; ++r) l[r] *= __shfl_sync(kAll, fac, r);
 #pragma unroll 1
@@ -314,7 +315,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                                  : "memory");
                 }
             const bool mixed = mixed_tile(it, k0);
-            if (mixed) {  // before p_ready: the tile cannot be released, nor its barrier move on, until then
+            if (rarely(mixed)) {  // before p_ready: the tile cannot be released, nor its barrier move on, until then
                 const uint32_t v = tiles + j;
                 if (!wait(smem_u32(&sh.value[v % P.v_slots]), (v / P.v_slots) & 1, gave_up)) return;
             }
@@ -322,12 +323,12 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
             tc_before();
             __syncwarp();
             if (lane == 0) bar_arrive(p_ready);
-            if (mixed) {
+            if (rarely(mixed)) {
                 // rows that see a non-finite value, which the product met as zero, get it added here
                 uint32_t any = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) any |= sh.odd[ring][i];
-                if (any) {
+                if (rarely(any)) {
                     if (!wait(pv_done, steps & 1, gave_up)) return;
                     tc_after();
 #pragma unroll 1
@@ -455,7 +456,8 @@ __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh,
     const uint32_t q = operand(q_smem, 16), q_part = (uint32_t)P.q_part >> 4, p = operand(p_smem, 16);
     const bool leader = elect();
     volatile int* gave_up = &sh.gave_up;
-    uint32_t items = 0, ahead = 0, scores = 0, outputs = 0, first = 0, polls = 0;  // first: by buffer, an item's first tile
+    uint32_t items = 0, ahead = 0, scores = 0, outputs = 0, polls = 0;
+    uint32_t notes = 0;  // 16 bits a buffer: the first and last step of the outputs' depth, an item's first tile
     int32_t j = 0, n = 0;
     Ring kr, vr;
     Items walk(sh);
@@ -480,7 +482,9 @@ __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh,
                 if (j + 1 == n) tc_commit(q_empty);
             }
             __syncwarp();
-            first = (first & ~(1u << buf)) | (uint32_t)(j == 0) << buf;
+            int32_t lo, hi;
+            steps_of<K>(it, (it.tile + j) * kTile, lo, hi);
+            notes = (notes & ~(0xffffu << 16 * buf)) | (uint32_t)(lo | hi << 4 | (j == 0) << 8) << 16 * buf;
             kr.step(P.k_slots);
             ++scores;
             ++ahead;
@@ -495,12 +499,14 @@ __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh,
             tc_after();
             // D <= 64: the upper 64 lanes repeat the lower ones' columns
             const uint32_t a = operand(v_smem + vr.i * slot_bytes, slot_bytes > kHalf ? kHalf : 0);
-            const uint32_t fresh = first >> (outputs & 1) & 1u;
+            const uint32_t note = __shfl_sync(kAll, notes, 0) >> 16 * (outputs & 1);
+            const int32_t lo = note & 15u, hi = note >> 4 & 15u;
+            const uint32_t add = (note >> 8 & 1u) ^ 1u;
             if (leader) {
 #pragma unroll 2
-                for (int i = 0; i < kTile / KindOf<K>::kStep; ++i)
+                for (int i = lo; i < hi; ++i)
                     mma_mixed<k8, Wt::kHigh>(o_at, a + (i * KindOf<K>::kStep * 128 >> 4), p + (i * KindOf<K>::kStep * Wt::kPitch >> 4), id_o,
-                                             i > 0 ? 1u : fresh ^ 1u);
+                                             i > lo ? 1u : add);
                 tc_commit(pv_done);
                 tc_commit(v_empty + 8 * vr.i);
             }
