@@ -405,22 +405,22 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
     const uint32_t s_at = tmem + st * kTile, o_at = tmem + 256 + st * dp;
     const uint32_t k_full = smem_u32(sh.k_full), k_empty = smem_u32(sh.k_empty), v_empty = smem_u32(sh.v_empty),
                    value = smem_u32(sh.value), s_full = smem_u32(&sh.s_full[st]), p_ready = smem_u32(&sh.p_ready[st]),
-                   pv_done = smem_u32(&sh.pv_done[st]), q_empty = smem_u32(&sh.q_empty);
+                   pv_done = smem_u32(&sh.pv_done[st]), q_empty = smem_u32(sh.q_empty), q_full = smem_u32(sh.q_full);
     const bool leader = elect();
     volatile int* gave_up = &sh.gave_up;
     const uint32_t turn[2] = {smem_u32(&sh.turn[st]), smem_u32(&sh.turn[st ^ 1])};
-    uint32_t items = 0, p_parity = 0, turns = 0;
-    Ring kr, vr;
+    uint32_t p_parity = 0, turns = 0;
+    Ring kr, vr, qr;
     Items walk(sh);
     Item it;
     bool ok = true;
 #pragma unroll 1
     while (ok && walk.next(it)) {
-        if (!(ok = wait(smem_u32(&sh.q_full), items & 1, gave_up))) break;
+        if (!(ok = wait(q_full + 8 * qr.i, qr.parity, gave_up))) break;
         tc_after();
         // the same in every lane; taken from one, so that the operands below live in uniform registers
         const int32_t n = __shfl_sync(kAll, it.n, 0);
-        const uint32_t q = operand(q_smem + st * q_bytes, 16);
+        const uint32_t q = operand(q_smem + qr.i * P.q_bytes + st * q_bytes, 16), q_done = q_empty + 8 * qr.i;
 #pragma unroll 1
         for (int32_t t = -1; t < n; ++t) {  // outputs of tile t, scores of the next
             const bool more = t + 1 < n;
@@ -466,13 +466,13 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
                     bar_arrive(turn[1]);
                     tc_commit(s_full);
                     tc_commit(k_empty + 8 * kr.i);
-                    if (t + 2 == n) tc_commit(q_empty);
+                    if (t + 2 == n) tc_commit(q_done);
                 }
                 __syncwarp();
                 kr.step(P.k_slots);
             }
         }
-        ++items;
+        qr.step(P.q_bufs);
     }
     // products under way end before the tensor memory is given back
     if (leader) tc_commit(smem_u32(&sh.drain));
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
              const __grid_constant__ CUtensorMap qm) {
     constexpr int NH = K == kE4m3 ? 1 : DP / 64;
     extern __shared__ __align__(1024) char raw[];
-    const uint32_t q_smem = smem_u32(raw), k_smem = q_smem + 2 * P.q_tile, v_smem = k_smem + P.k_slots * NH * kHalf;
+    const uint32_t q_smem = smem_u32(raw), k_smem = q_smem + P.q_bufs * P.q_bytes, v_smem = k_smem + P.k_slots * NH * kHalf;
     char* behind = raw + (v_smem - q_smem) + P.v_slots * NH * kHalf;
     Shared& sh = *reinterpret_cast<Shared*>(behind);
     if (q_smem & 1023u) {  // the tiles' swizzle counts on it
@@ -619,9 +619,11 @@ cudaError_t launch(Params P, int n, cudaStream_t st) {
     P.lead = 5;  // measured, as the other launch's
     P.halves = NH;
     P.q_tile = (K == kE4m3 ? 2 : NH) * kHalf;
+    P.q_bytes = 2 * P.q_tile;
+    P.q_bufs = K == kE4m3 ? 2 : 1;  // the next item's are split into parts, 256 rows by one warp, under this one's tiles
     const int own = (int)(sizeof(Shared) + 15) / 16 * 16 + (A.chunk.parents ? kItems * (int)sizeof(Tree) : 0) +
                     (K == kE4m3 ? kItems * 2 * kTile * 4 : 0);
-    const int slots = min(2 * kMaxSlots, (kSmem - own - 2 * P.q_tile) / (NH * kHalf));
+    const int slots = min(2 * kMaxSlots, (kSmem - own - P.q_bufs * P.q_bytes) / (NH * kHalf));
     P.k_slots = slots / 2;
     P.v_slots = slots - P.k_slots;
     CUtensorMap km, vm, qm;
@@ -631,7 +633,7 @@ cudaError_t launch(Params P, int n, cudaStream_t st) {
         return cudaErrorInvalidValue;
     static std::atomic<unsigned long long> allowed{0};
     void* args[] = {&P, &km, &vm, &qm};
-    return launch_early((const void*)k_attend<K, DP>, &allowed, dim3(n), kThreads, 2 * P.q_tile + slots * NH * kHalf + own, st, args);
+    return launch_early((const void*)k_attend<K, DP>, &allowed, dim3(n), kThreads, P.q_bufs * P.q_bytes + slots * NH * kHalf + own, st, args);
 }
 
 template <typename T>

@@ -77,6 +77,7 @@ struct Params {
     int32_t halves;     // 128-byte columns of a row of keys, values and 16-bit queries: 1 or 2
     int32_t q_part;     // bytes from a query tile's hi part to its lo part (e4m3)
     int32_t q_tile;     // bytes from a query tile to the next
+    int32_t q_bytes, q_bufs;  // of an item's query tiles; how many items' there is room for, 1 or 2
     int32_t k_slots, v_slots;  // key and value tiles that shared memory has room for
     int32_t box;        // slots of one copy, a divisor of the page size and of kTile
     int32_t wide;       // output rows lie on 32 bytes
@@ -344,7 +345,7 @@ struct Tree {
 struct Common {  // of both kernels, behind the operand tiles
     uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
     uint64_t value[kMaxSlots];  // a value tile is in and clean
-    uint64_t q_in, q_full, q_empty, drain;
+    uint64_t q_in, q_full[2], q_empty[2], drain;
     uint64_t item_full[kItems], item_empty[kItems];
     Item item[kItems];
     uint32_t tmem;
@@ -537,7 +538,7 @@ __device__ __forceinline__ bool mixed_tile(const Item& it, int32_t k0) {
 __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t k_smem, uint32_t v_smem, const CUtensorMap* km,
                                           const CUtensorMap* vm, int first, int last) {
     const int lane = threadIdx.x & 31;
-    const int32_t box = P.box, boxes = kTile / box, ps = P.a.pool.page_size;
+    const int32_t box = P.box, boxes = kTile / box, ps = P.a.pool.page_size, tile_pages = kTile / ps, tile_rest = kTile % ps;
     const bool leader = elect();
     volatile int* gave_up = &sh.gave_up;
     uint32_t tile = 0, issued[2] = {0, 0};
@@ -548,27 +549,26 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
 #pragma unroll 1
     while (ok && walk.next(it)) {
         const int32_t* table = P.a.pool.table + (int64_t)it.b * P.a.pool.table_stride;
-        const int32_t head = __shfl_sync(kAll, it.h, 0);
-        // where a lane's box of a tile lies; read a tile ahead
-        auto look = [&](int32_t j, bool& need, int32_t& page, int32_t& at) {
-            const int32_t slot = (it.tile + j) * kTile + lane * box;
-            need = j < it.n && lane < boxes && slot < it.end && slot + box > it.lo;
-            page = -1;
-            at = 0;
-            if (need) {
-                const int32_t i = slot / ps;
-                at = slot - i * ps;
-                page = table[i];
-            }
-        };
-        bool next_need;
-        int32_t next_page, next_at;
-        look(0, next_need, next_page, next_at);
+        const int32_t head = __shfl_sync(kAll, it.h, 0), n = __shfl_sync(kAll, it.n, 0);
+        // where a lane's box of a tile lies; its page's id is read a tile ahead
+        int32_t slot = it.tile * kTile + lane * box, i = slot / ps, in = slot - i * ps;
+        bool next_need = false;
+        int32_t next_page = -1, next_at = 0;
 #pragma unroll 1
-        for (int32_t j = 0; j < it.n && ok; ++j, ++tile) {
+        for (int32_t j = -1; j < n && ok; ++j) {
             bool need = next_need;
             const int32_t page = next_page, at = next_at;
-            look(j + 1, next_need, next_page, next_at);
+            next_need = j + 1 < n && lane < boxes && slot < it.end && slot + box > it.lo;
+            next_at = in;
+            next_page = next_need ? table[i] : -1;
+            slot += kTile;
+            i += tile_pages;
+            in += tile_rest;
+            if (in >= ps) {
+                in -= ps;
+                ++i;
+            }
+            if (j < 0) continue;
             const bool miss = need && (page < 0 || page >= P.a.pool.pages);
             need = need && !miss;
             const uint32_t todo = __ballot_sync(kAll, need), bytes = __popc(todo) * box * 128 * P.halves;
@@ -594,13 +594,24 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
                 __syncwarp();
                 const CUtensorMap* map = kv ? vm : km;
                 const uint32_t dst = (kv ? v_smem : k_smem) + r.i * (P.halves * kHalf);
+                // one thread issues: from many, each copy would wait for the last
 #pragma unroll 1
-                for (int i = 0; i < boxes; ++i) {  // one thread issues: from many, each copy would wait for the last
-                    const int32_t p = __shfl_sync(kAll, page, i), a = __shfl_sync(kAll, at, i);
-                    if (leader && (todo >> i & 1u)) {
-                        copy_box(dst + i * box * 128, map, 0, a, head, p, full);
-                        if (P.halves > 1) copy_box(dst + i * box * 128 + kHalf, map, 64, a, head, p, full);
+                for (int i = 0; i < boxes; i += 4) {
+                    int32_t p[4], a[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        p[k] = __shfl_sync(kAll, page, i + k);
+                        a[k] = __shfl_sync(kAll, at, i + k);
                     }
+                    if (leader)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (todo >> (i + k) & 1u) {
+                                const uint32_t to = dst + (i + k) * box * 128;
+                                copy_box(to, map, 0, a[k], head, p[k], full);
+                                if (P.halves > 1) copy_box(to + kHalf, map, 64, a[k], head, p[k], full);
+                            }
+                    __syncwarp();
                 }
                 r.step(slots);
                 if (kv) {
@@ -611,6 +622,7 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
                     ++issued[0];
                 }
             }
+            ++tile;
         }
     }
     // copies still under way land before the CTA ends, also where another role gave up
@@ -630,11 +642,10 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
 // into the parts hi and lo, each row brought to [128, 256) by a power of two.
 template <int K>
 __device__ __forceinline__ bool load_queries(const Params& P, Common& sh, const Item& it, uint32_t q_smem,
-                                             const CUtensorMap* qm, uint32_t items, uint32_t entry) {
+                                             const CUtensorMap* qm, uint32_t items, uint32_t entry, uint32_t q_full) {
     using T = typename KindOf<K>::T;
     const AttendArgs& A = P.a;
     const int lane = threadIdx.x & 31;
-    const uint32_t q_full = smem_u32(&sh.q_full);
     const int q_tiles = P.tokens < P.block ? 2 : 1;
     bool flip;
     score_unit(A, it.h, flip);
@@ -797,6 +808,7 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
     int32_t b = sh.start.b, p = sh.start.p, h = sh.start.h, x = sh.start.x, left = sh.start.left;
     int32_t T = sh.start.T, past = sh.start.past, row0 = sh.start.row0;
     Ring ring;
+    Ring qr;
     uint32_t loads = 0;
 #pragma unroll 1
     for (uint32_t i = 0;; ++i, ring.step(kItems)) {
@@ -871,15 +883,20 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
         }
         __syncwarp();
         if (it.n == 0) break;
-        if (i > 0 && !wait(smem_u32(&sh.q_empty), (i - 1) & 1, &sh.gave_up)) break;
+        if (i >= (uint32_t)P.q_bufs && !wait(smem_u32(&sh.q_empty[qr.i]), qr.parity ^ 1, &sh.gave_up)) break;
         ++loads;
-        if (!load_queries<K>(P, sh, it, q_smem, qm, i, ring.i)) break;
+        if (!load_queries<K>(P, sh, it, q_smem + qr.i * P.q_bytes, qm, i, ring.i, smem_u32(&sh.q_full[qr.i]))) break;
+        qr.step(P.q_bufs);
     }
     if (K != kE4m3 && loads > 0) {  // its copies land before the CTA ends, whoever gave up
         int none = 0;
         bool flip;
         score_unit(P.a, 0, flip);
-        wait(smem_u32(flip ? &sh.q_in : &sh.q_full), (loads - 1) & 1, &none);
+        if (flip) wait(smem_u32(&sh.q_in), (loads - 1) & 1, &none);
+        else
+#pragma unroll 1
+            for (uint32_t k = loads > (uint32_t)P.q_bufs ? loads - P.q_bufs : 0; k < loads; ++k)
+                wait(smem_u32(&sh.q_full[k % P.q_bufs]), k / P.q_bufs & 1, &none);
     }
 }
 
@@ -942,8 +959,10 @@ __device__ __forceinline__ void init_common(Common& sh, int streams, int readers
         bar_init(smem_u32(&sh.value[i]), 1);
     }
     bar_init(smem_u32(&sh.q_in), 1);
-    bar_init(smem_u32(&sh.q_full), 1);
-    bar_init(smem_u32(&sh.q_empty), streams);
+    for (int i = 0; i < 2; ++i) {
+        bar_init(smem_u32(&sh.q_full[i]), 1);
+        bar_init(smem_u32(&sh.q_empty[i]), streams);
+    }
     bar_init(smem_u32(&sh.drain), streams);
     for (int i = 0; i < kItems; ++i) {
         bar_init(smem_u32(&sh.item_full[i]), 1);

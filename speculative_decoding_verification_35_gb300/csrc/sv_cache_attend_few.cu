@@ -162,14 +162,15 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
     const int32_t D = A.pool.dim;
     volatile int* gave_up = &sh.gave_up;
     Vote vote{smem_u32(&mine.vote), 0, gave_up};
-    uint32_t steps = 0, tiles = 0, items = 0, votes = 0;  // votes: on weights, modulo 3
+    uint32_t steps = 0, tiles = 0, votes = 0;  // votes: on weights, modulo 3
     bool owed = false;  // a vote of the last item's end has been given and not passed: others may still read the notes
     Items walk(sh);
     Item it;
 #pragma unroll 1
-    for (; walk.next(it); ++items) {
+    while (walk.next(it)) {
         const Tree* tree = A.chunk.parents ? &walk.tree() : nullptr;
-        const int32_t rows = min(N, it.nt * P.G - row0);  // none or less: a group without work
+        // taken from one lane: the same in all, so that the branches on it are the warp's. None or less: a group without work
+        const int32_t rows = __shfl_sync(kAll, min(N, it.nt * P.G - row0), 0);
         bool flip;
         const float unit = score_unit(A, it.h, flip);
         float l[N], off[N], u[K == kE4m3 ? N : 1];  // weights are 2^(u s + off)
@@ -190,7 +191,11 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
             tc_after();
             if (K == kE4m3 && j == 0)
 #pragma unroll
-                for (int r = 0; r < (K == kE4m3 ? N : 1); ++r) u[r] = unit * sh.q_down[walk.ring.i * sh.q_rows + row0 + r];
+                for (int r = 0; r < (K == kE4m3 ? N : 1); r += 4) {
+                    if (r >= rows) break;
+#pragma unroll
+                    for (int e = 0; e < (K == kE4m3 ? 4 : 1); ++e) u[r + e] = unit * sh.q_down[walk.ring.i * sh.q_rows + row0 + r + e];
+                }
             const uint32_t s_col = tmem + buf * NR;
             const int32_t k0 = (it.tile + j) * kTile;
             const uint32_t ring = (tiles + j) % kNotes;
@@ -204,19 +209,30 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
 #pragma unroll 1
             for (;;) {
 #pragma unroll
-                for (int c = 0; c < N; c += 16) tc_ld16(s_col + c, s + c);
+                for (int c = 0; c < N; c += 16) {
+                    if (c > 0 && c >= rows) break;
+                    tc_ld16(s_col + c, s + c);
+                }
                 tc_wait_ld();
                 if (rarely(cut))
 #pragma unroll
-                    for (int r = 0; r < N; ++r)
-                        if (!(seen >> r & 1u)) s[r] = 0xff800000u;
+                    for (int r = 0; r < N; r += 4) {
+                        if (r >= rows) break;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!(seen >> (r + e) & 1u)) s[r + e] = 0xff800000u;
+                    }
                 // the weights' logarithms against the references (where there is none yet, against 0)
                 float top = -INFINITY;
 #pragma unroll
-                for (int r = 0; r < N; ++r) {
-                    const float y = fmaf(__uint_as_float(s[r]), u[K == kE4m3 ? r : 0], off[r]);
-                    s[r] = __float_as_uint(y);
-                    top = fmaxf(top, y);
+                for (int r = 0; r < N; r += 4) {
+                    if (r >= rows) break;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = fmaf(__uint_as_float(s[r + e]), u[K == kE4m3 ? r + e : 0], off[r + e]);
+                        s[r + e] = __float_as_uint(y);
+                        top = fmaxf(top, y);
+                    }
                 }
                 if (!fresh) {
                     // no one passes this vote before everyone has read the last but one's word
@@ -232,9 +248,13 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                     }
                     // the rows' maxima, by warp, then of all
 #pragma unroll
-                    for (int r = 0; r < N; ++r) {
-                        const float x = warp_max(__uint_as_float(s[r]));
-                        if (lane == r) notes.part[warp][r] = x;
+                    for (int r = 0; r < N; r += 4) {
+                        if (r >= rows) break;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = warp_max(__uint_as_float(s[r + e]));
+                            if (lane == r + e) notes.part[warp][r + e] = x;
+                        }
                     }
                     vote.arrive();
                     if (!vote.pass()) return;
@@ -243,17 +263,21 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                                      Wt::kShift;
                     vote.arrive();
                     // from none to the maximum, if there is one; else upwards only
-                    const float d = own ? fmaxf(mx, 0.f) : mx != -INFINITY ? mx : 0.f;
+                    const float d = r0 >= rows ? 0.f : own ? fmaxf(mx, 0.f) : mx != -INFINITY ? mx : 0.f;
                     const bool moved = __any_sync(kAll, own && d > 0.f);
                     const float fac = own ? exp2_fast(-d) : 1.f;
                     own_off -= d;
                     own = own || mx != -INFINITY;
                     unset = __any_sync(kAll, r0 < rows && !own);
 #pragma unroll
-                    for (int r = 0; r < N; ++r) {
-                        const float x = __shfl_sync(kAll, d, r);
-                        s[r] = __float_as_uint(__uint_as_float(s[r]) - x);
-                        off[r] -= x;
+                    for (int r = 0; r < N; r += 4) {
+                        if (r >= rows) break;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = __shfl_sync(kAll, d, r + e);
+                            s[r + e] = __float_as_uint(__uint_as_float(s[r + e]) - x);
+                            off[r + e] -= x;
+                        }
                     }
                     if (rarely(moved)) {
 #pragma unroll
@@ -274,7 +298,11 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                     }
                 }
 #pragma unroll
-                for (int r = 0; r < N; ++r) s[r] = __float_as_uint(exp2_fast(__uint_as_float(s[r])));
+                for (int r = 0; r < N; r += 4) {
+                    if (r >= rows) break;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[r + e] = __float_as_uint(exp2_fast(__uint_as_float(s[r + e])));
+                }
                 if (!vote.pass()) return;
                 if (fresh) break;
                 fresh = mine.again[votes];
@@ -284,6 +312,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
             uint32_t pk[N / 2];  // 16 bits: pairs; e4m3: hi in the first half, lo in the second
 #pragma unroll
             for (int r = 0; r < N; r += 4) {
+                if (r >= rows) break;
                 float p[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -308,6 +337,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
             for (int part = 0; part < kParts; ++part)
 #pragma unroll
                 for (int c = 0; c < kWide; ++c) {
+                    if (c * (16 / KT::kBytes) >= rows) break;
                     const uint32_t* v = pk + part * (N / 4) + 4 * c;
                     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
                                      p_smem + Wt::at(k, part * (NR / 16) + row0 / N * kWide + c)),
@@ -362,26 +392,29 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
         tiles += it.n;
 
         // the item's end: the rows' sums over the lanes
-        // lanes exchange halves of what they hold until each has one row's sum over the warp
+        // of four rows at a time: lanes trade until each has one row's, then add it up
+        float sum[N / 4];
 #pragma unroll
-        for (int e = 0; e < 5; ++e) {
-            const int o = 16 >> e, half = N >> (e + 1);
-            if (half == 0) l[0] += __shfl_xor_sync(kAll, l[0], o);
+        for (int q = 0; q < N / 4; ++q) {
+            sum[q] = 0.f;
+            if (4 * q >= rows) break;
+            float* x = l + 4 * q;
+            const bool up = lane & 16, right = lane & 8;
 #pragma unroll
-            for (int r = 0; r < half; ++r) {
-                const bool up = lane & o;
-                const float give = up ? l[r] : l[r + half], keep = up ? l[r + half] : l[r];
-                l[r] = keep + __shfl_xor_sync(kAll, give, o);
+            for (int e = 0; e < 2; ++e) {
+                const float give = up ? x[e] : x[e + 2], keep = up ? x[e + 2] : x[e];
+                x[e] = keep + __shfl_xor_sync(kAll, give, 16);
             }
+            const float give = right ? x[0] : x[1], keep = right ? x[1] : x[0];
+            sum[q] = keep + __shfl_xor_sync(kAll, give, 8);
+#pragma unroll
+            for (int o = 4; o; o >>= 1) sum[q] += __shfl_xor_sync(kAll, sum[q], o);
         }
         if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
         tc_after();
-        if (N == 32) {
-            notes.part[warp][(lane >> 4 & 1) * 16 + (lane >> 3 & 1) * 8 + (lane >> 2 & 1) * 4 + (lane >> 1 & 1) * 2 + (lane & 1)] =
-                l[0];
-        } else if (!(lane & 1)) {
-            notes.part[warp][(lane >> 4 & 1) * 8 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2 + (lane >> 1 & 1)] = l[0];
-        }
+        if (!(lane & 7))
+#pragma unroll
+            for (int q = 0; q < N / 4; ++q) notes.part[warp][4 * q + (lane >> 3 & 2) + (lane >> 3 & 1)] = sum[q];
         vote.arrive();
         if (!vote.pass()) return;
         const int r0 = lane % N;
@@ -391,13 +424,13 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
         const bool alone = it.begins && it.finishes;
         const size_t part = (size_t)(2 * blockIdx.x + (it.begins ? 1 : 0)) * P.part_rows + row0;
         float f = 1.f;  // what a row's O is scaled by
-        if (alone) f = total == 0.f ? 0.f : (A.pool.v_scale ? A.pool.v_scale[it.h] : 1.f) / total;
+        if (alone) f = total == 0.f ? 0.f : __fdividef(A.pool.v_scale ? A.pool.v_scale[it.h] : 1.f, total);
         if (k < rows && k < N) {
             if (alone) {
                 const int32_t row = row0 + k, t = row / P.G;
                 if (A.lse)
                     A.lse[(int64_t)(it.row0 + it.t0 + t) * A.q_heads + it.h * P.G + row - t * P.G] =
-                        total == 0.f ? -INFINITY : fmaf(-own_off, kLn2, logf(total));
+                        total == 0.f ? -INFINITY : (__log2f(total) - own_off) * kLn2;
             } else {
                 P.part_ml[part + k] = make_float2(own ? -own_off : -INFINITY, total);
             }
@@ -452,22 +485,23 @@ __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh,
     const uint32_t tmem = __shfl_sync(kAll, sh.tmem, 0), o_at = tmem + 2 * NR;
     const uint32_t k_full = smem_u32(sh.k_full), k_empty = smem_u32(sh.k_empty), v_empty = smem_u32(sh.v_empty),
                    value = smem_u32(sh.value), s_full = smem_u32(sh.s_full), p_ready = smem_u32(&sh.p_ready),
-                   pv_done = smem_u32(&sh.pv_done), q_full = smem_u32(&sh.q_full), q_empty = smem_u32(&sh.q_empty);
-    const uint32_t q = operand(q_smem, 16), q_part = (uint32_t)P.q_part >> 4, p = operand(p_smem, 16);
+                   pv_done = smem_u32(&sh.pv_done), q_full = smem_u32(sh.q_full), q_empty = smem_u32(sh.q_empty);
+    const uint32_t q_part = (uint32_t)P.q_part >> 4, p = operand(p_smem, 16);
     const bool leader = elect();
     volatile int* gave_up = &sh.gave_up;
-    uint32_t items = 0, ahead = 0, scores = 0, outputs = 0, polls = 0;
+    uint32_t ahead = 0, scores = 0, outputs = 0, polls = 0;
     uint32_t notes = 0;  // 16 bits a buffer: the first and last step of the outputs' depth, an item's first tile
     int32_t j = 0, n = 0;
-    Ring kr, vr;
+    Ring kr, vr, qr;
     Items walk(sh);
     Item it;
     bool more = walk.next(it);
     n = __shfl_sync(kAll, it.n, 0);
 #pragma unroll 1
     while (more || ahead > 0) {
-        if (more && ahead < 2 && (j > 0 || ready(q_full, items & 1)) && ready(k_full + 8 * kr.i, kr.parity)) {
+        if (more && ahead < 2 && (j > 0 || ready(q_full + 8 * qr.i, qr.parity)) && ready(k_full + 8 * kr.i, kr.parity)) {
             tc_after();
+            const uint32_t q = operand(q_smem + qr.i * P.q_bytes, 16);
             const uint32_t buf = scores & 1, a = operand(k_smem + kr.i * slot_bytes, 16), d = tmem + buf * NR;
             if (leader) {
 #pragma unroll
@@ -479,7 +513,7 @@ __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh,
                     }
                 tc_commit(s_full + 8 * buf);
                 tc_commit(k_empty + 8 * kr.i);
-                if (j + 1 == n) tc_commit(q_empty);
+                if (j + 1 == n) tc_commit(q_empty + 8 * qr.i);
             }
             __syncwarp();
             int32_t lo, hi;
@@ -491,7 +525,7 @@ __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh,
             polls = 0;
             if (++j == n) {
                 j = 0;
-                ++items;
+                qr.step(P.q_bufs);
                 more = walk.next(it);
                 n = __shfl_sync(kAll, it.n, 0);
             }
@@ -534,7 +568,7 @@ __global__ void __launch_bounds__(kThreads<G>, G == 1 ? 2 : 1)
     constexpr int columns = 4 * NR;  // twice NR for scores, NR (e4m3: twice) for O
     extern __shared__ __align__(1024) char raw[];
     const uint32_t slot_bytes = P.halves * kHalf;
-    const uint32_t q_smem = smem_u32(raw), p_smem = q_smem + P.q_tile, k_smem = p_smem + Weights<K, NR>::kBytes,
+    const uint32_t q_smem = smem_u32(raw), p_smem = q_smem + P.q_bufs * P.q_bytes, k_smem = p_smem + Weights<K, NR>::kBytes,
                    v_smem = k_smem + P.k_slots * slot_bytes;
     char* behind = raw + (v_smem - q_smem) + P.v_slots * slot_bytes;
     Shared<NR, G>& sh = *reinterpret_cast<Shared<NR, G>*>(behind);
@@ -559,7 +593,7 @@ __global__ void __launch_bounds__(kThreads<G>, G == 1 ? 2 : 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // query rows past the copies' last one stay zero
-    for (int i = tid; i < P.q_tile / 16; i += kThreads<G>) reinterpret_cast<uint4*>(raw)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < P.q_bufs * P.q_bytes / 16; i += kThreads<G>) reinterpret_cast<uint4*>(raw)[i] = make_uint4(0, 0, 0, 0);
     fence_async();
     const int role = w - 4 * G;
     if (role == 0 && (tid & 31) == 0) {
@@ -578,7 +612,7 @@ __global__ void __launch_bounds__(kThreads<G>, G == 1 ? 2 : 1)
     if (role < 0) {
         if (G == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        softmax_role<K, NR, G>(P, sh, raw + P.q_tile);
+        softmax_role<K, NR, G>(P, sh, raw + P.q_bufs * P.q_bytes);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (role == 0) load_role(P, sh, k_smem, v_smem, &km, &vm, 0, 1);
@@ -607,8 +641,14 @@ cudaError_t launch(Params& P, int sms, cudaStream_t st) {
     P.q_tile = (K == kE4m3 ? 2 : halves) * P.q_part;
     const int own = (int)(sizeof(Shared<NR, G>) + 15) / 16 * 16 + (A.chunk.parents ? kItems * (int)sizeof(Tree) : 0) +
                     (K == kE4m3 ? kItems * NR * 4 : 0);
-    const int rest = P.q_tile + Weights<K, NR>::kBytes + own;
-    const int slots = min(2 * kMaxSlots, ((G == 1 ? kHalfSm : kSmem) - rest) / (halves * kHalf));
+    P.q_bytes = P.q_tile;
+    auto slots_of = [&](int bufs) {
+        const int rest = (G == 1 ? kHalfSm : kSmem) - bufs * P.q_bytes - Weights<K, NR>::kBytes - own;
+        return min(2 * kMaxSlots, rest / (halves * kHalf));
+    };
+    // The next item's queries are fetched (e4m3: and split into parts) under this one's tiles, where that costs no slot.
+    P.q_bufs = K == kE4m3 || slots_of(2) == slots_of(1) ? 2 : 1;
+    const int slots = slots_of(P.q_bufs), rest = P.q_bufs * P.q_bytes + Weights<K, NR>::kBytes + own;
     P.k_slots = slots / 2;
     P.v_slots = slots - P.k_slots;
     CUtensorMap km, vm, qm;
