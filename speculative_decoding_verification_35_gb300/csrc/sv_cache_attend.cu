@@ -733,6 +733,9 @@ cudaError_t launch_attend(const AttendArgs& A, int dtype, int cache_dtype, cudaS
     P.G = A.q_heads / A.pool.heads;
     P.box = kTile;
     while (A.pool.page_size % P.box) P.box /= 2;
+    P.boxes = kTile / P.box;
+    P.tile_pages = kTile / A.pool.page_size;
+    P.tile_rest = kTile % A.pool.page_size;
     P.wide = A.pool.dim % 16 == 0 && (uintptr_t)A.out % 32 == 0;
     char* ws = (char*)A.workspace;
     P.part_o = (float*)ws;

@@ -79,7 +79,8 @@ struct Params {
     int32_t q_tile;     // bytes from a query tile to the next
     int32_t q_bytes, q_bufs;  // of an item's query tiles; how many items' there is room for, 1 or 2
     int32_t k_slots, v_slots;  // key and value tiles that shared memory has room for
-    int32_t box;        // slots of one copy, a divisor of the page size and of kTile
+    int32_t box, boxes; // slots of one copy, a divisor of the page size and of kTile; copies of a tile
+    int32_t tile_pages, tile_rest;  // kTile in whole pages, and the slots left over
     int32_t wide;       // output rows lie on 32 bytes
     int32_t ctas;       // of the launch
     int32_t part_rows;  // rows of a partial result
@@ -112,20 +113,15 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok;
 }
-// A whole warp waits; false once the CTA has given up (a wait of at least a tenth of a second and a few at most).
-constexpr uint32_t kPolls = 1u << 24;
+// A whole warp waits, a tenth of a second at least and a few seconds at most; false, and the CTA gives up, if that was
+// not enough. (Short, as it stands in some thirty places.)
+constexpr uint32_t kPolls = 1u << 22;
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-    bool ok = bar_try(bar, parity);
-    if (!rarely(!__all_sync(kAll, ok))) return true;
 #pragma unroll 1
-    for (uint32_t i = 1; !__all_sync(kAll, ok); ++i) {
-        if (!ok) ok = bar_try(bar, parity);
-        if ((i & 255u) == 0) {
-            if (i >= kPolls) *gave_up = 1;
-            if (__any_sync(kAll, *gave_up)) return false;
-        }
-    }
-    return true;
+    for (uint32_t i = 0; i < kPolls; ++i)
+        if (__all_sync(kAll, bar_try(bar, parity))) return true;
+    *gave_up = 1;
+    return false;
 }
 // Whether the phase is over, for a whole warp.
 __device__ __forceinline__ bool ready(uint32_t bar, uint32_t parity) {
@@ -538,7 +534,7 @@ __device__ __forceinline__ bool mixed_tile(const Item& it, int32_t k0) {
 __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t k_smem, uint32_t v_smem, const CUtensorMap* km,
                                           const CUtensorMap* vm, int first, int last) {
     const int lane = threadIdx.x & 31;
-    const int32_t box = P.box, boxes = kTile / box, ps = P.a.pool.page_size, tile_pages = kTile / ps, tile_rest = kTile % ps;
+    const int32_t box = P.box, boxes = P.boxes, ps = P.a.pool.page_size;
     const bool leader = elect();
     volatile int* gave_up = &sh.gave_up;
     uint32_t tile = 0, issued[2] = {0, 0};
@@ -562,8 +558,8 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
             next_at = in;
             next_page = next_need ? table[i] : -1;
             slot += kTile;
-            i += tile_pages;
-            in += tile_rest;
+            i += P.tile_pages;
+            in += P.tile_rest;
             if (in >= ps) {
                 in -= ps;
                 ++i;
@@ -594,24 +590,13 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
                 __syncwarp();
                 const CUtensorMap* map = kv ? vm : km;
                 const uint32_t dst = (kv ? v_smem : k_smem) + r.i * (P.halves * kHalf);
-                // one thread issues: from many, each copy would wait for the last
 #pragma unroll 1
-                for (int i = 0; i < boxes; i += 4) {
-                    int32_t p[4], a[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        p[k] = __shfl_sync(kAll, page, i + k);
-                        a[k] = __shfl_sync(kAll, at, i + k);
+                for (int i = 0; i < boxes; ++i) {  // one thread issues: from many, each copy would wait for the last
+                    const int32_t p = __shfl_sync(kAll, page, i), a = __shfl_sync(kAll, at, i);
+                    if (leader && (todo >> i & 1u)) {
+                        copy_box(dst + i * box * 128, map, 0, a, head, p, full);
+                        if (P.halves > 1) copy_box(dst + i * box * 128 + kHalf, map, 64, a, head, p, full);
                     }
-                    if (leader)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (todo >> (i + k) & 1u) {
-                                const uint32_t to = dst + (i + k) * box * 128;
-                                copy_box(to, map, 0, a[k], head, p[k], full);
-                                if (P.halves > 1) copy_box(to + kHalf, map, 64, a[k], head, p[k], full);
-                            }
-                    __syncwarp();
                 }
                 r.step(slots);
                 if (kv) {

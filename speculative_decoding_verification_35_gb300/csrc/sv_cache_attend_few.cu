@@ -506,7 +506,7 @@ __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh,
             if (leader) {
 #pragma unroll
                 for (int part = 0; part < parts; ++part)
-#pragma unroll 2
+#pragma unroll 1
                     for (int i = 0; i < depth; ++i) {
                         const uint32_t in = (i & 3) * 32 >> 4;
                         mma_ss<k8>(d, a + (i >> 2) * (kHalf >> 4) + in, q + (k8 ? part : i >> 2) * q_part + in, id_s, part + i > 0);
@@ -537,7 +537,7 @@ __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh,
             const int32_t lo = note & 15u, hi = note >> 4 & 15u;
             const uint32_t add = (note >> 8 & 1u) ^ 1u;
             if (leader) {
-#pragma unroll 2
+#pragma unroll 1
                 for (int i = lo; i < hi; ++i)
                     mma_mixed<k8, Wt::kHigh>(o_at, a + (i * KindOf<K>::kStep * 128 >> 4), p + (i * KindOf<K>::kStep * Wt::kPitch >> 4), id_o,
                                              i > lo ? 1u : add);
