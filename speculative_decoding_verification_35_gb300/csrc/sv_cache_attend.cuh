@@ -794,20 +794,29 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
     int32_t T = sh.start.T, past = sh.start.past, row0 = sh.start.row0;
     Ring ring;
     Ring qr;
-    uint32_t loads = 0;
+    uint32_t loads = 0, above = 0;
+    int32_t depth = 0;
 #pragma unroll 1
     for (uint32_t i = 0;; ++i, ring.step(kItems)) {
         Item it{};
         left -= max(0, lead - x);
-        if (rarely(left > 0 && T < 0)) {  // the next sequence
+        if (rarely(left > 0 && (T < 0 || (tree && i == 0)))) {  // the next sequence (a tree's lanes: nodes)
 #pragma unroll 1
             for (; b < P.a.chunk.B; ++b) {
                 const Seq s = seq_of(P.a.chunk, capacity_of(P.a.pool), b);
                 bool ok = !s.err;
                 if (ok && tree) {
-                    int32_t d;
-                    uint32_t m;
-                    tree_of(P.a.chunk, b, s.T, d, m, ok);
+                    tree_of(P.a.chunk, b, s.T, depth, above, ok);
+                    if (P.a.window > 0 && P.a.window < 32) {  // as far as the window reaches, a step at a time
+                        int32_t at = lane, par = 0;
+                        if (ok && lane > 0 && lane < s.T) par = P.a.chunk.parents[(int64_t)P.a.chunk.offs[b] + lane - 1];
+                        above = 1u << lane;
+#pragma unroll 1
+                        for (int d = 1; d < P.a.window; ++d) {
+                            at = __shfl_sync(kAll, par, at);
+                            above |= 1u << at;
+                        }
+                    }
                 }
                 if (ok) {
                     T = s.T;
@@ -817,7 +826,6 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
                 }
             }
         }
-        const int32_t tb = b;
         if (left > 0 && T > 0) {
             int32_t first, count;
             span(P, T, past, p, it, first, count);
@@ -835,20 +843,7 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
             x = 0;
         }
         if (i >= kItems && !wait(smem_u32(&sh.item_empty[ring.i]), ring.parity ^ 1, &sh.gave_up)) break;
-        if (rarely(tree && it.n > 0)) {
-            int32_t depth, par = 0;
-            uint32_t above;
-            bool ok;
-            tree_of(P.a.chunk, tb, T, depth, above, ok);
-            if (P.a.window > 0 && P.a.window < 32) {  // as far as the window reaches, a step at a time
-                if (lane > 0 && lane < T) par = P.a.chunk.parents[(int64_t)P.a.chunk.offs[tb] + lane - 1];
-                int32_t at = lane;
-                above = 1u << lane;
-                for (int d = 1; d < P.a.window; ++d) {
-                    at = __shfl_sync(kAll, par, at);
-                    above |= 1u << at;
-                }
-            }
+        if (tree) {
             sh.tree[ring.i].above[lane] = above;
             sh.tree[ring.i].depth[lane] = depth;
             __syncwarp();
