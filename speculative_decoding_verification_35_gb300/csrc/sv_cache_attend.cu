@@ -17,6 +17,11 @@
 // tiles with one long sequence or hundreds of short ones, and a CTA leaves at most two items unfinished. Their
 // partials go to the workspace, and a second small launch merges them in a fixed order. Lengths are read
 // on the device, so the host needs to know none of them.
+//
+// Bound by the chain of a stream's tile: scores (512 cycles of the tensor cores at D = 128), softmax (some 1450), outputs
+// (512) and what lies between; two streams in turn keep the tensor cores busy 1024 of every 1560 cycles. Measured:
+// bfloat16, D = 128, 3 prompts of 700 to 2048 tokens over 1 to 8192 cached, 32 heads in 8 groups: 244 us, 1.21 PFLOP/s
+// of what the mask leaves (0.64 of a library product's 1.89), 3 us of them the merge.
 #include "sv_cache_attend.cuh"
 
 #include <algorithm>
@@ -616,7 +621,7 @@ cudaError_t launch(Params P, int n, cudaStream_t st) {
     P.block = 2 * P.tokens;
     P.q_box = min(P.tokens, A.chunk.max_gamma + 1);
     P.q_part = kHalf;
-    P.lead = 5;  // measured, as the other launch's
+    P.lead = 5;  // measured on prompts of 700 to 2048 tokens: 2, 3 and 8 are 2 to 7 % slower
     P.halves = NH;
     P.q_tile = (K == kE4m3 ? 2 : NH) * kHalf;
     P.q_bytes = 2 * P.q_tile;

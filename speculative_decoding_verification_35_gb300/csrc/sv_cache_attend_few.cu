@@ -14,13 +14,22 @@
 // a weight too large for its type), which costs three more barriers and a pass of maxima.
 //
 // Up to 32 rows a CTA has one softmax warpgroup, and two CTAs share an SM: one's beginnings and endings of items (a
-// fifth of the time of an item of ten tiles) lie under the other's tiles. Above that two operand sets would leave an
-// SM four tiles of 16 bits and D = 128, too few in flight, so there is one CTA, whose two warpgroups have half of the
-// rows each. Measured at 6.7 TB/s of copy rate, bfloat16, D = 128: 64 sequences of 6 tokens, 512 to 8192 long, 4
-// heads a group, 139 us (0.81 of the copy rate; 133 to 141 us with the rows on the lanes
-// and tiles taken by two warpgroups in turn); 2 sequences of 8 tokens, 8 heads a group, 164 us (0.90; two CTAs an SM
-// 213 us, rows on the lanes 180 us). 128 sequences of one token with a window of 1024: 74 us (128 us before). e4m3
-// cache, 32 sequences of 4 tokens: 121 us (150 us before).
+// fifth of the time of an item of ten tiles) lie under the other's tiles. (Three an SM, where registers and shared
+// memory allow it, measured the same: 62 against 63 us for the window below.) Above 32 rows two operand sets would leave
+// an SM four tiles of 16 bits and D = 128, too few in flight, so there is one CTA, whose two warpgroups have half of the
+// rows each.
+//
+// What bounds it beside the bytes is code: eight roles' instructions pass through one instruction cache, and what is
+// not in it takes some 16 cycles an instruction. So waits are short, loops rolled where they need not be fast, rare
+// paths put aside, and columns past an item's rows are branched over.
+//
+// Measured (one copy reads and writes 6.7 TB/s): bfloat16, D = 128, pages of 16, 8 key heads: 64 sequences of 6 tokens,
+// 500 to 8000 cached, 4 heads a group, 129 us (0.87 of the copy rate; with the rows on the lanes 133 to 141); 2
+// sequences of 8 tokens, 60000 to 131072 cached, 8 heads a group, 155 us (0.95; two CTAs an SM 213, rows on the lanes
+// 180). float16, D = 64, 16 heads of their own, 128 sequences of one token with a window of 1024: 60 us (0.44; rows on
+// the lanes 128), of which some 10 are the launches and the first tiles' way; its 128-byte pieces lie 2 KB apart, and
+// more than half of its items have one tile. e4m3, D = 128, 32 sequences of 4 tokens, 2000 to 16384 cached: 92 us (0.80;
+// rows on the lanes 150).
 #include "sv_cache_attend.cuh"
 
 #include <type_traits>
@@ -637,7 +646,7 @@ cudaError_t launch(Params& P, int sms, cudaStream_t st) {
     P.tokens = P.block = A.chunk.max_gamma + 1;
     P.q_box = P.tokens;
     P.q_part = NR * 128;
-    P.lead = 2;
+    P.lead = 2;  // measured on the cases above: 0, 1, 3 and 4 are up to a third slower
     P.q_tile = (K == kE4m3 ? 2 : halves) * P.q_part;
     const int own = (int)(sizeof(Shared<NR, G>) + 15) / 16 * 16 + (A.chunk.parents ? kItems * (int)sizeof(Tree) : 0) +
                     (K == kE4m3 ? kItems * NR * 4 : 0);
