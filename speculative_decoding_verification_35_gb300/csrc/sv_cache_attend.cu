@@ -259,22 +259,26 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
         Row row = row_of(P, it, walk, stream, tl);
         float m = -INFINITY, l = 0.f;
         const bool busy = __any_sync(kAll, row.real);
+        bool unset = busy;  // some row has no reference yet
 #pragma unroll 1
         for (int32_t j = 0; j < it.n; ++j, ++steps) {
+            // what needs no scores, before them
+            const int32_t k0 = (it.tile + j) * kTile;
+            const uint32_t ring = (tiles + j) % kNotes;
+            const bool whole = __all_sync(kAll, (k0 + kTile <= row.limit && row.low <= k0) || !row.real);
+            const bool mixed = mixed_tile(it, k0);
             if (!wait(s_full, steps & 1, gave_up)) return;
             tc_after();
             if (K == kE4m3 && j == 0) row.sl *= sh.q_down[walk.ring.i * sh.q_rows + stream * kTile + r];
-            const int32_t k0 = (it.tile + j) * kTile;
-            const uint32_t ring = (tiles + j) % kNotes;
             uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
             if (busy) {
                 const uint32_t bad = sh.bad[0][ring];
-                const bool whole = (k0 + kTile <= row.limit && row.low <= k0 && !bad) || !row.real;
-                const bool masked = !__all_sync(kAll, whole);
-                if (masked) seen_of(row, it, k0, bad, tree, seen);
-                if (masked) hide_tile(s_col, seen);
+                if (!whole || bad) {
+                    seen_of(row, it, k0, bad, tree, seen);
+                    hide_tile(s_col, seen);
+                }
                 float sum;
-                bool first = K == kE4m3 || __any_sync(kAll, row.real && m == -INFINITY);
+                bool first = K == kE4m3 || unset;
 #pragma unroll 1
                 for (int attempt = 0; attempt < 2; ++attempt, first = true) {
                     if (first) {
@@ -283,6 +287,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
                         if (__any_sync(kAll, move)) {
                             const float old = m;
                             if (move) m = mx;
+                            unset = __any_sync(kAll, row.real && m == -INFINITY);
                             const float f = !move || old == -INFINITY ? 1.f : exp2_fast((old - m) * row.sl);
                             l *= f;
                             if (__any_sync(kAll, move && old != -INFINITY)) {
@@ -297,7 +302,6 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
                 l += sum;
                 tc_wait_st();
             }
-            const bool mixed = mixed_tile(it, k0);
             if (rarely(mixed)) {  // before p_ready: the tile cannot be released, nor its barrier move on, until then
                 const uint32_t v = tiles + j;
                 if (!wait(smem_u32(&sh.value[v % P.v_slots]), (v / P.v_slots) & 1, gave_up)) return;
