@@ -20,8 +20,8 @@
 //
 // Bound by the chain of a stream's tile: scores (512 cycles of the tensor cores at D = 128), softmax (some 1450), outputs
 // (512) and what lies between; two streams in turn keep the tensor cores busy 1024 of every 1560 cycles. Measured:
-// bfloat16, D = 128, 3 prompts of 700 to 2048 tokens over 1 to 8192 cached, 32 heads in 8 groups: 244 us, 1.21 PFLOP/s
-// of what the mask leaves (0.64 of a library product's 1.89), 3 us of them the merge.
+// bfloat16, D = 128, 3 prompts of 700 to 2048 tokens over 1 to 8192 cached, 32 heads in 8 groups: 234 us, 1.27 PFLOP/s
+// of what the mask leaves (0.67 of a library product's 1.89), 3 us of them the merge.
 #include "sv_cache_attend.cuh"
 
 #include <algorithm>
@@ -625,7 +625,7 @@ cudaError_t launch(Params P, int n, cudaStream_t st) {
     P.block = 2 * P.tokens;
     P.q_box = min(P.tokens, A.chunk.max_gamma + 1);
     P.q_part = kHalf;
-    P.lead = 5;  // measured on prompts of 700 to 2048 tokens: 2, 3 and 8 are 2 to 7 % slower
+    P.lead = 3;  // measured on prompts of 700 to 2048 tokens: 235 us, with 1, 2, 4 and 5 272, 238, 238 and 240
     P.halves = NH;
     P.q_tile = (K == kE4m3 ? 2 : NH) * kHalf;
     P.q_bytes = 2 * P.q_tile;

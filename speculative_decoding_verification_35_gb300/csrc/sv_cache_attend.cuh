@@ -422,8 +422,25 @@ __device__ __forceinline__ void plan(const Params& P, Common& sh) {
             const int32_t b = b0 + tid;
             if (round == 0 || B > kThreads) {
                 my_tiles = my_blocks = 0;
+                uint32_t* wrong = &sh.odd[0][0];  // bits: trees of this turn that are none
+                if (P.a.chunk.parents) {
+                    static_assert(kThreads / 32 <= kNotes * 4, "a word a warp");
+                    if (b0 > 0) __syncthreads();  // the last turn's have been read
+                    if (tid < kThreads / 32) wrong[tid] = 0;
+                    __syncthreads();
+#pragma unroll 1
+                    for (int i = w; i < min(kThreads, B - b0); i += kThreads / 32) {  // a warp a tree
+                        const Seq s = seq_of(P.a.chunk, capacity_of(P.a.pool), b0 + i);
+                        int32_t par = 0;
+                        if (!s.err && lane > 0 && lane < s.T) par = P.a.chunk.parents[s.row0 - (b0 + i) + lane - 1];
+                        const bool ok = __all_sync(kAll, (uint32_t)par < (uint32_t)max(lane, 1));
+                        if (!ok && lane == 0) atomicOr(&wrong[i >> 5], 1u << (i & 31));
+                    }
+                    __syncthreads();
+                }
                 if (b < B) {
-                    mine = checked_seq(P, b);
+                    mine = seq_of(P.a.chunk, capacity_of(P.a.pool), b);
+                    if (!mine.err && P.a.chunk.parents && (wrong[tid >> 5] >> (tid & 31) & 1u)) mine.err = 1u << SV_ERR_BAD_OFFSETS;
                     size_of(P, mine, my_tiles, my_blocks);
                 }
             }

@@ -646,7 +646,7 @@ cudaError_t launch(Params& P, int sms, cudaStream_t st) {
     P.tokens = P.block = A.chunk.max_gamma + 1;
     P.q_box = P.tokens;
     P.q_part = NR * 128;
-    P.lead = 2;  // measured on the cases above: 0, 1, 3 and 4 are up to a third slower
+    P.lead = halves == 2 ? 1 : 2;  // measured on the cases above: others of 0 to 4 are 1 to 30 % slower
     P.q_tile = (K == kE4m3 ? 2 : halves) * P.q_part;
     const int own = (int)(sizeof(Shared<NR, G>) + 15) / 16 * 16 + (A.chunk.parents ? kItems * (int)sizeof(Tree) : 0) +
                     (K == kE4m3 ? kItems * NR * 4 : 0);

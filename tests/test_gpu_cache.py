@@ -460,6 +460,31 @@ def test_many_long_chunks(sc):
     Batch(sc, [int(x) for x in rng.integers(60, 80, 530)], [int(x) for x in rng.integers(0, 30, 530)], 2, 1, 64, 8).check()
 
 
+@pytest.mark.parametrize("tokens,group", [(4, 2), (20, 8)])
+def test_wrong_trees_among_many(sc, tokens, group):
+    """More trees than a launch has threads; those whose parents are none fail alone, wherever they stand."""
+    rng = np.random.default_rng(tokens)
+    B = 1100
+    chunks = [int(x) for x in rng.integers(2, tokens + 1, B)]
+    par = [tree(rng, n) for n in chunks]
+    b = Batch(sc, chunks, [int(x) for x in rng.integers(0, 40, B)], 2 * group, 2, 64, 8, parents=par)
+    good, gl = b.attend()
+    wrong = [0, 31, 255, 256, 511, 512, 700, 1099]
+    bad = b.parents_h.copy()
+    for i in wrong:
+        bad[int(b.offs_h[i]) + chunks[i] - 2] = chunks[i] - 1  # the last node under itself
+    b.parents.copy_(torch.tensor(bad))
+    out, lse = b.attend()
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == BAD_OFFSETS
+    r = np.cumsum([0] + chunks)
+    failed = torch.zeros(b.rows, dtype=torch.bool, device="cuda")
+    for i in wrong:
+        failed[r[i]:r[i + 1]] = True
+    assert torch.equal(out[~failed], good[~failed]) and torch.equal(lse[~failed], gl[~failed])
+    assert not out[failed].any() and (lse[failed] == -float("inf")).all()
+
+
 def test_bad_pages_of_prompts(sc):
     b = Batch(sc, [150, 70], [60, 200], 4, 2, 64, 16, "fp16", "fp16")
     b.table_h[0, 2] = -1
