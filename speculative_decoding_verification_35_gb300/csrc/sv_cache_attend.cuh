@@ -320,7 +320,7 @@ __device__ __forceinline__ void size_of(const Params& P, const Seq& s, uint32_t&
         Item it;
         int32_t first, count;
         span(P, s.T, s.past, p, it, first, count);
-        tiles += count;
+        if (tiles >> 31 == 0) tiles += count;  // more are refused, so they need not be counted
         ++blocks;
     }
 }
@@ -330,6 +330,7 @@ __device__ __forceinline__ void size_of(const Params& P, const Seq& s, uint32_t&
 struct Start {
     int32_t b, p, h, T, past, row0;
     int32_t lead, x, left;
+    uint32_t W, n, u0;  // units in all, CTAs that have some, and this CTA's first
 };
 
 // A tree's nodes: what each sees (bits: itself and those above it, as far as the window reaches), and its depth.
@@ -359,11 +360,11 @@ struct Common {  // of both kernels, behind the operand tiles
 // a b / c, rounded down, without the long division: a = q c + r gives q b + r b / c. b and c below 2^15.
 __device__ __forceinline__ uint32_t share(uint32_t a, uint32_t b, uint32_t c) { return a / c * b + a % c * b / c; }
 
-// Where the CTA begins, and the record of an item that its predecessor began: by all threads, in the end by one,
+// Where the CTA begins: by all threads, in the end by one,
 // whose sequence b it is, `rest` units into it.
 __device__ __forceinline__ void begin_at(const Params& P, Common& sh, const Seq& s, int32_t b, uint32_t rest, uint32_t lead,
                                          uint32_t W, uint32_t n, uint32_t u0, uint32_t u1) {
-    const uint32_t c = blockIdx.x, heads = P.a.pool.heads;
+    const uint32_t heads = P.a.pool.heads;
     Item it;
     int32_t first, count, p = 0;
 #pragma unroll 1
@@ -374,27 +375,37 @@ __device__ __forceinline__ void begin_at(const Params& P, Common& sh, const Seq&
         rest -= all;
     }
     const uint32_t h = rest / (count + lead), x = rest - h * (count + lead);
-    sh.start = {b, p, (int32_t)h, s.T, s.past, s.row0, (int32_t)lead, (int32_t)x, (int32_t)(u1 - u0)};
+    sh.start = {b, p, (int32_t)h, s.T, s.past, s.row0, (int32_t)lead, (int32_t)x, (int32_t)(u1 - u0), W, n, u0};
     // its page ids on their way here
     const int32_t slot = (first + (x > lead ? (int32_t)(x - lead) : 0)) * kTile;
     asm volatile("prefetch.global.L1 [%0];" ::"l"(P.a.pool.table + (int64_t)b * P.a.pool.table_stride +
                                                   min(slot / P.a.pool.page_size, P.a.pool.table_stride - 1)));
-    if (x <= lead) return;
+}
+
+// The record of the item that the CTA begins in, if it is the second one to work on it. Late, by one thread: only the
+// merge needs it.
+__device__ __forceinline__ void record(const Params& P, const Common& sh) {
+    const Start& s = sh.start;
+    const uint32_t c = blockIdx.x;
+    if (s.left == 0 || s.x <= s.lead) return;
+    Item it;
+    int32_t first, count;
+    span(P, s.T, s.past, s.p, it, first, count);
     // the item's first tile is unit `from`; if the CTA before this one had it, this one records the item
-    const uint32_t from = u0 - x + lead;
-    if (from < share(W, c - 1, n)) return;
-    uint32_t lo = c, hi = n - 1;  // the CTA of its last tile
+    const uint32_t from = s.u0 - s.x + s.lead;
+    if (from < share(s.W, c - 1, s.n)) return;
+    uint32_t lo = c, hi = s.n - 1;  // the CTA of its last tile
 #pragma unroll 1
     while (lo < hi) {
         const uint32_t mid = (lo + hi + 1) / 2;
-        if (share(W, mid, n) <= from + count - 1) lo = mid;
+        if (share(s.W, mid, s.n) <= from + count - 1) lo = mid;
         else hi = mid - 1;
     }
     Record r{};
     r.parts = (int32_t)(lo - c) + 2;
     r.row0 = s.row0 + it.t0;
     r.tokens = it.nt;
-    r.head = (int32_t)h;
+    r.head = s.h;
     r.split = it.split;
     P.records[c] = r;
 }
@@ -411,6 +422,7 @@ __device__ __forceinline__ void plan(const Params& P, Common& sh) {
     }
     // Twice over the sequences, kThreads at a time: their sums, then the one that the CTA begins in. (As two rounds of
     // one loop: the code runs once a launch and is fetched from afar.)
+    const int used = (min(kThreads, B) + 31) / 32;  // warps that have sequences
     Seq mine{};
     uint32_t my_tiles = 0, my_blocks = 0, lead = 0, W = 0, n = 0, u0 = 0, u1 = 0, base = 0;
     unsigned long long tiles = 0, blocks = 0;
@@ -468,7 +480,7 @@ __device__ __forceinline__ void plan(const Params& P, Common& sh) {
             const uint32_t sc = B > kThreads ? 1 : heads, lc = B > kThreads ? 0 : lead * heads;
             uint32_t before = base, total = 0;
 #pragma unroll 4
-            for (int i = 0; i < kThreads / 32; ++i) {
+            for (int i = 0; i < used; ++i) {
                 const uint32_t x = sh.scan[0][i] * sc + sh.scan[1][i] * lc;
                 if (i < w) before += x;
                 total += x;
@@ -478,11 +490,13 @@ __device__ __forceinline__ void plan(const Params& P, Common& sh) {
             base += total;
         }
         if (round > 0) break;
-#pragma unroll 1
-        for (int o = 16; o; o >>= 1) {
-            tiles += __shfl_xor_sync(kAll, tiles, o);
-            blocks += __shfl_xor_sync(kAll, blocks, o);
-        }
+        // over the warp, 16 bits and the rest: what is clamped there is far too large below
+        auto sum = [](unsigned long long v) {
+            return __reduce_add_sync(kAll, (uint32_t)v & 0xffffu) +
+                   ((unsigned long long)__reduce_add_sync(kAll, (uint32_t)min(v >> 16, 0x3ffffffull)) << 16);
+        };
+        tiles = sum(tiles);
+        blocks = sum(blocks);
         if (lane == 0) {  // a sum too large for 32 bits is kept as too large for what is allowed below
             sh.scan[0][w] = (uint32_t)min(tiles, 0xffffffffull);
             sh.scan[1][w] = (uint32_t)min(blocks, 0xffffffffull);
@@ -490,7 +504,7 @@ __device__ __forceinline__ void plan(const Params& P, Common& sh) {
         if (__syncthreads_or(fails) && tid == 0) sh.failing = 1;
         tiles = blocks = 0;
 #pragma unroll 4
-        for (int i = 0; i < kThreads / 32; ++i) {
+        for (int i = 0; i < used; ++i) {
             tiles += sh.scan[0][i];
             blocks += sh.scan[1][i];
         }
@@ -885,6 +899,7 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
         if (!load_queries<K>(P, sh, it, q_smem + qr.i * P.q_bytes, qm, i, ring.i, smem_u32(&sh.q_full[qr.i]))) break;
         qr.step(P.q_bufs);
     }
+    if (lane == 0) record(P, sh);
     if (K != kE4m3 && loads > 0) {  // its copies land before the CTA ends, whoever gave up
         int none = 0;
         bool flip;
