@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kThreads = 512;  // two softmax warpgroups, then a warp for each other role
 constexpr int kReaders = 8 + 2 + 2 + 1;
+constexpr int kSplitters = 2;  // warps that split the queries for e4m3 caches
 
 struct Shared : Common {
     uint64_t s_full[2], p_ready[2], pv_done[2];
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int tid = threadIdx.x, w = tid >> 5;
     if (tid == 0) {
-        init_common(sh, 2, kReaders);
+        init_common(sh, 2, kReaders + (K == kE4m3 ? kSplitters : 0), K == kE4m3 ? kSplitters : 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_u32(&sh.s_full[i]), 1);
             bar_init(smem_u32(&sh.p_ready[i]), 4);
@@ -539,7 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w == 8 || w == 10) load_role(P, sh, k_smem, v_smem, &km, &vm, w == 10, w == 10);
         else if (w == 9 || w == 13) product_role<K, NH>(P, sh, q_smem, k_smem, v_smem, w == 13);
         else if (w == 11) value_role<K>(P, sh, v_smem);
-        else if (w == 12) item_role<K>(P, sh, q_smem, &qm);
+        else if (w == 12) item_role<K, K != kE4m3>(P, sh, q_smem, &qm);
+        else if (K == kE4m3 && w >= 14) query_role(P, sh, q_smem, w - 14, kSplitters);
     }
     tc_before();
     __syncthreads();

@@ -653,97 +653,114 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
     }
 }
 
-// The rows of an item's query tiles. 16-bit caches: copied, G heads of q_box tokens at once (rows past the
-// sequence's end are another sequence's, or zero: a product's row depends on its own row only). e4m3: split
-// into the parts hi and lo, each row brought to [128, 256) by a power of two.
-template <int K>
-__device__ __forceinline__ bool load_queries(const Params& P, Common& sh, const Item& it, uint32_t q_smem,
-                                             const CUtensorMap* qm, uint32_t items, uint32_t entry, uint32_t q_full) {
-    using T = typename KindOf<K>::T;
+// The rows of an item's query tiles, 16-bit caches: copied, G heads of q_box tokens at once (rows past the sequence's end
+// are another sequence's, or zero: a product's row depends on its own row only).
+__device__ __forceinline__ bool copy_item_queries(const Params& P, Common& sh, const Item& it, uint32_t q_smem, const CUtensorMap* qm,
+                                                  uint32_t items, uint32_t q_full) {
     const AttendArgs& A = P.a;
     const int lane = threadIdx.x & 31;
     const int q_tiles = P.tokens < P.block ? 2 : 1;
     bool flip;
     score_unit(A, it.h, flip);
-    if (K != kE4m3) {
-        const uint32_t bar = flip ? smem_u32(&sh.q_in) : q_full;
-        if (lane == 0) {
-            bar_expect(bar, q_tiles * P.halves * P.q_box * P.G * 128);
-            for (int t = 0; t < q_tiles; ++t)
-                for (int h = 0; h < P.halves; ++h)
-                    copy_queries(q_smem + t * P.q_tile + h * P.q_part, qm, h * 64, it.h * P.G, it.row0 + it.t0 + t * it.split, bar);
-        }
-        __syncwarp();
-        if (!rarely(flip)) return true;
-        if (!wait(bar, items & 1, &sh.gave_up)) return false;
+    const uint32_t bar = flip ? smem_u32(&sh.q_in) : q_full;
+    if (lane == 0) {
+        bar_expect(bar, q_tiles * P.halves * P.q_box * P.G * 128);
+        for (int t = 0; t < q_tiles; ++t)
+            for (int h = 0; h < P.halves; ++h)
+                copy_queries(q_smem + t * P.q_tile + h * P.q_part, qm, h * 64, it.h * P.G, it.row0 + it.t0 + t * it.split, bar);
+    }
+    __syncwarp();
+    if (!rarely(flip)) return true;
+    if (!wait(bar, items & 1, &sh.gave_up)) return false;
 #pragma unroll 1
-        for (int i = lane; i < q_tiles * P.q_tile / 16; i += 32) {
-            uint32_t u[4];
-            const uint32_t at = q_smem + i * 16;
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(at));
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(u[0] ^ 0x80008000u), "r"(u[1] ^ 0x80008000u),
-                         "r"(u[2] ^ 0x80008000u), "r"(u[3] ^ 0x80008000u)
-                         : "memory");
-        }
-    } else {
-        const int32_t D = A.pool.dim, rows = it.nt * P.G, tile_rows = q_tiles == 2 ? it.split * P.G : rows;
-        const T* q = (const T*)A.q + (int64_t)(it.row0 + it.t0) * A.q_stride + (int64_t)it.h * P.G * D;
-        // half a warp a row, eight elements a lane; eight rows under way
-        const int c = lane & 15;
+    for (int i = lane; i < q_tiles * P.q_tile / 16; i += 32) {
+        uint32_t u[4];
+        const uint32_t at = q_smem + i * 16;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(at));
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(u[0] ^ 0x80008000u), "r"(u[1] ^ 0x80008000u),
+                     "r"(u[2] ^ 0x80008000u), "r"(u[3] ^ 0x80008000u)
+                     : "memory");
+    }
+    fence_async();
+    __syncwarp();
+    if (lane == 0) bar_arrive(q_full);
+    return true;
+}
+
+// e4m3 caches: split into the parts hi and lo, each row brought to [128, 256) by a power of two, by `of` warps, of which
+// this is number `who`. Bound by the instructions of a row (some 100 for half a warp), so wide chunks have two warps.
+__device__ __forceinline__ void split_queries(const Params& P, Common& sh, const Item& it, uint32_t q_smem, uint32_t entry, uint32_t q_full,
+                                              int who, int of) {
+    using T = __nv_bfloat16;
+    const AttendArgs& A = P.a;
+    const int lane = threadIdx.x & 31;
+    bool flip;
+    score_unit(A, it.h, flip);
+    const int32_t D = A.pool.dim, rows = it.nt * P.G, tile_rows = P.tokens < P.block ? it.split * P.G : rows;
+    const T* q = (const T*)A.q + (int64_t)(it.row0 + it.t0) * A.q_stride + (int64_t)it.h * P.G * D;
+    // half a warp a row, eight elements a lane; eight rows under way
+    const int c = lane & 15;
 #pragma unroll 1
-        for (int32_t r0 = lane >> 4; r0 - (lane >> 4) < rows; r0 += 8) {
-            uint4 u[4];
+    for (int32_t r8 = 8 * who; r8 < rows; r8 += 8 * of) {
+        uint4 u[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int32_t r = r0 + 2 * k;
-                u[k] = make_uint4(0, 0, 0, 0);
-                if (r < rows && c * 8 < D) {
-                    const int32_t t = r / P.G, g = r - t * P.G;
-                    u[k] = *reinterpret_cast<const uint4*>(q + t * A.q_stride + (int64_t)g * D + c * 8);
-                }
+        for (int k = 0; k < 4; ++k) {
+            const int32_t r = r8 + (lane >> 4) + 2 * k;
+            u[k] = make_uint4(0, 0, 0, 0);
+            if (r < rows && c * 8 < D) {
+                const int32_t t = r / P.G, g = r - t * P.G;
+                u[k] = *reinterpret_cast<const uint4*>(q + t * A.q_stride + (int64_t)g * D + c * 8);
             }
+        }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int32_t r = r0 + 2 * k;
-                const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-                float2 f[4];
-                float top = 0.f;
+        for (int k = 0; k < 4; ++k) {
+            const int32_t r = r8 + (lane >> 4) + 2 * k;
+            const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+            uint32_t big = 0;  // magnitudes, in pairs
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f[i] = to_float2<T>(w[i]);
-                    top = fmaxf(top, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
-                }
-                for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-                int e = 0;
-                if (top > 0.f && top < INFINITY) e = max(-120, min(120, 7 - ilogbf(top)));
-                const float up = __int_as_float((127 + e) << 23);
-                uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+            for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(big) : "r"(w[i] & 0x7fff7fffu));
+            float top = fmaxf(__uint_as_float(big << 16), __uint_as_float(big & 0xffff0000u));
+            for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+            const int e = max(-120, min(120, 134 - (int)(__float_as_uint(top) >> 23)));
+            const float up = __int_as_float((127 + e) << 23), by = flip ? -up : up;
+            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // an infinite query has no finite parts: its row is NaN, as its softmax is
-                    const float x = isinf(f[i].x) ? NAN : flip ? -f[i].x * up : f[i].x * up;
-                    const float y = isinf(f[i].y) ? NAN : flip ? -f[i].y * up : f[i].y * up;
-                    const uint32_t a = e4m3x2(x, y);
-                    const float2 b = from_e4m3x2(a);
-                    hi[i >> 1] |= a << (16 * (i & 1));
-                    lo[i >> 1] |= e4m3x2(x - b.x, y - b.y) << (16 * (i & 1));
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = to_float2<T>(w[i]);
+                float x = f.x * by, y = f.y * by;
+                if (rarely(top == INFINITY)) {  // an infinite query has no finite parts: its row is NaN, as its softmax is
+                    if (isinf(f.x)) x = NAN;
+                    if (isinf(f.y)) y = NAN;
                 }
-                if (r < rows) {
-                    const int32_t at = r < tile_rows ? r : r - tile_rows;
-                    const uint32_t dst = q_smem + (r < tile_rows ? 0 : P.q_tile) + at * 128 +
-                                         (((c >> 1) ^ (at & 7)) << 4) + (c & 1) * 8;
-                    asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
-                    asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst + P.q_part), "r"(lo[0]), "r"(lo[1]) : "memory");
-                    if (c == 0)
-                        sh.q_down[entry * sh.q_rows + (r < tile_rows ? 0 : kTile) + at] = __int_as_float((127 - e) << 23);
-                }
+                const uint32_t a = e4m3x2(x, y);
+                const float2 b = from_e4m3x2(a);
+                hi[i >> 1] |= a << (16 * (i & 1));
+                lo[i >> 1] |= e4m3x2(x - b.x, y - b.y) << (16 * (i & 1));
+            }
+            if (r < rows) {
+                const int32_t at = r < tile_rows ? r : r - tile_rows;
+                const uint32_t dst = q_smem + (r < tile_rows ? 0 : P.q_tile) + at * 128 + (((c >> 1) ^ (at & 7)) << 4) + (c & 1) * 8;
+                asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
+                asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst + P.q_part), "r"(lo[0]), "r"(lo[1]) : "memory");
+                if (c == 0) sh.q_down[entry * sh.q_rows + (r < tile_rows ? 0 : kTile) + at] = __int_as_float((127 - e) << 23);
             }
         }
     }
     fence_async();
     __syncwarp();
     if (lane == 0) bar_arrive(q_full);
-    return true;
+}
+
+// Queries of e4m3 caches by warps of their own.
+__device__ __forceinline__ void query_role(const Params& P, Common& sh, uint32_t q_smem, int who, int of) {
+    Ring qr;
+    Items walk(sh);
+    Item it;
+#pragma unroll 1
+    for (uint32_t i = 0; walk.next(it); ++i, qr.step(P.q_bufs)) {
+        if (i >= (uint32_t)P.q_bufs && !wait(smem_u32(&sh.q_empty[qr.i]), qr.parity ^ 1, &sh.gave_up)) return;
+        split_queries(P, sh, it, q_smem + qr.i * P.q_bytes, walk.ring.i, smem_u32(&sh.q_full[qr.i]), who, of);
+    }
 }
 
 // The steps of a tile's depth that O += P V takes: those with a slot that some row of the item sees.
@@ -815,8 +832,9 @@ __device__ __forceinline__ void scan_rows(int halves, uint32_t at, int32_t lo, i
         }
 }
 
-// The CTA's items, one after the other, by one warp, and their queries; a last one of no tiles ends them.
-template <int K>
+// The CTA's items, one after the other, by one warp, and their queries (unless others see to those); a last one of no
+// tiles ends them.
+template <int K, bool kQueries>
 __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t q_smem, const CUtensorMap* qm) {
     const int lane = threadIdx.x & 31;
     const bool tree = P.a.chunk.parents != nullptr;
@@ -894,9 +912,12 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
         }
         __syncwarp();
         if (it.n == 0) break;
+        if (!kQueries) continue;
         if (i >= (uint32_t)P.q_bufs && !wait(smem_u32(&sh.q_empty[qr.i]), qr.parity ^ 1, &sh.gave_up)) break;
         ++loads;
-        if (!load_queries<K>(P, sh, it, q_smem + qr.i * P.q_bytes, qm, i, ring.i, smem_u32(&sh.q_full[qr.i]))) break;
+        const uint32_t at = q_smem + qr.i * P.q_bytes, q_full = smem_u32(&sh.q_full[qr.i]);
+        if (K == kE4m3) split_queries(P, sh, it, at, ring.i, q_full, 0, 1);
+        else if (!copy_item_queries(P, sh, it, at, qm, i, q_full)) break;
         qr.step(P.q_bufs);
     }
     if (lane == 0) record(P, sh);
@@ -960,8 +981,9 @@ __device__ __forceinline__ void value_role(const Params& P, Common& sh, uint32_t
 // ---------------------------------------------------------------------------------------------------------
 // the kernels' beginning and end
 // ---------------------------------------------------------------------------------------------------------
-// Barriers of the common part, by one thread. streams: warps at products; readers: warps that read the items.
-__device__ __forceinline__ void init_common(Common& sh, int streams, int readers) {
+// Barriers of the common part, by one thread. streams: warps at products; readers: warps that read the items; writers: of
+// the queries.
+__device__ __forceinline__ void init_common(Common& sh, int streams, int readers, int writers) {
 #pragma unroll 1
     for (int i = 0; i < kMaxSlots; ++i) {
         bar_init(smem_u32(&sh.k_full[i]), 1);
@@ -972,7 +994,7 @@ __device__ __forceinline__ void init_common(Common& sh, int streams, int readers
     }
     bar_init(smem_u32(&sh.q_in), 1);
     for (int i = 0; i < 2; ++i) {
-        bar_init(smem_u32(&sh.q_full[i]), 1);
+        bar_init(smem_u32(&sh.q_full[i]), writers);
         bar_init(smem_u32(&sh.q_empty[i]), streams);
     }
     bar_init(smem_u32(&sh.drain), streams);
