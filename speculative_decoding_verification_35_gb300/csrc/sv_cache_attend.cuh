@@ -688,7 +688,9 @@ __device__ __forceinline__ bool copy_item_queries(const Params& P, Common& sh, c
 }
 
 // e4m3 caches: split into the parts hi and lo, each row brought to [128, 256) by a power of two, by `of` warps, of which
-// this is number `who`. Bound by the instructions of a row (some 100 for half a warp), so wide chunks have two warps.
+// this is number `who`. A lane has a row and goes over it twice, for its largest element and for its parts; wide
+// chunks have two warps. (Half a warp a row, with its maximum over the lanes, took four times as long: 60000 cycles
+// for 256 rows.)
 __device__ __forceinline__ void split_queries(const Params& P, Common& sh, const Item& it, uint32_t q_smem, uint32_t entry, uint32_t q_full,
                                               int who, int of) {
     using T = __nv_bfloat16;
@@ -698,53 +700,59 @@ __device__ __forceinline__ void split_queries(const Params& P, Common& sh, const
     score_unit(A, it.h, flip);
     const int32_t D = A.pool.dim, rows = it.nt * P.G, tile_rows = P.tokens < P.block ? it.split * P.G : rows;
     const T* q = (const T*)A.q + (int64_t)(it.row0 + it.t0) * A.q_stride + (int64_t)it.h * P.G * D;
-    // half a warp a row, eight elements a lane; eight rows under way
-    const int c = lane & 15;
 #pragma unroll 1
-    for (int32_t r8 = 8 * who; r8 < rows; r8 += 8 * of) {
-        uint4 u[4];
+    for (int32_t r = 32 * who + lane; r - lane < rows; r += 32 * of) {
+        const int32_t t = r / P.G, g = r - t * P.G;
+        const T* row = q + t * A.q_stride + (int64_t)g * D;
+        const int32_t end = r < rows ? D : 0;
+        uint32_t big = 0;  // magnitudes, in pairs
+#pragma unroll 1
+        for (int32_t d = 0; d < end; d += 32) {
+            uint4 u[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int32_t r = r8 + (lane >> 4) + 2 * k;
-            u[k] = make_uint4(0, 0, 0, 0);
-            if (r < rows && c * 8 < D) {
-                const int32_t t = r / P.G, g = r - t * P.G;
-                u[k] = *reinterpret_cast<const uint4*>(q + t * A.q_stride + (int64_t)g * D + c * 8);
+            for (int k = 0; k < 4; ++k)
+                u[k] = d + 8 * k < end ? *reinterpret_cast<const uint4*>(row + d + 8 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(big) : "r"(w[i] & 0x7fff7fffu));
             }
         }
+        const float top = fmaxf(__uint_as_float(big << 16), __uint_as_float(big & 0xffff0000u));
+        const int e = max(-120, min(120, 134 - (int)(__float_as_uint(top) >> 23)));
+        const float up = __int_as_float((127 + e) << 23), by = flip ? -up : up;
+        const int32_t at = r < tile_rows ? r : r - tile_rows;
+        const uint32_t dst = q_smem + (r < tile_rows ? 0 : P.q_tile) + at * 128;
+#pragma unroll 1
+        for (int32_t c = 0; c < 8; ++c) {  // 16 elements, 16 bytes of each part
+            uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int32_t r = r8 + (lane >> 4) + 2 * k;
-            const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-            uint32_t big = 0;  // magnitudes, in pairs
+            for (int k = 0; k < 2; ++k) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (16 * c + 8 * k < end) u = *reinterpret_cast<const uint4*>(row + 16 * c + 8 * k);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(big) : "r"(w[i] & 0x7fff7fffu));
-            float top = fmaxf(__uint_as_float(big << 16), __uint_as_float(big & 0xffff0000u));
-            for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-            const int e = max(-120, min(120, 134 - (int)(__float_as_uint(top) >> 23)));
-            const float up = __int_as_float((127 + e) << 23), by = flip ? -up : up;
-            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = to_float2<T>(w[i]);
-                float x = f.x * by, y = f.y * by;
-                if (rarely(top == INFINITY)) {  // an infinite query has no finite parts: its row is NaN, as its softmax is
-                    if (isinf(f.x)) x = NAN;
-                    if (isinf(f.y)) y = NAN;
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = to_float2<T>(w[i]);
+                    float x = f.x * by, y = f.y * by;
+                    // an infinite query has no finite parts: its row is NaN, as its softmax is
+                    if (fabsf(x) == INFINITY) x = NAN;
+                    if (fabsf(y) == INFINITY) y = NAN;
+                    const uint32_t a = e4m3x2(x, y);
+                    const float2 b = from_e4m3x2(a);
+                    hi[2 * k + (i >> 1)] |= a << (16 * (i & 1));
+                    lo[2 * k + (i >> 1)] |= e4m3x2(x - b.x, y - b.y) << (16 * (i & 1));
                 }
-                const uint32_t a = e4m3x2(x, y);
-                const float2 b = from_e4m3x2(a);
-                hi[i >> 1] |= a << (16 * (i & 1));
-                lo[i >> 1] |= e4m3x2(x - b.x, y - b.y) << (16 * (i & 1));
             }
             if (r < rows) {
-                const int32_t at = r < tile_rows ? r : r - tile_rows;
-                const uint32_t dst = q_smem + (r < tile_rows ? 0 : P.q_tile) + at * 128 + (((c >> 1) ^ (at & 7)) << 4) + (c & 1) * 8;
-                asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
-                asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst + P.q_part), "r"(lo[0]), "r"(lo[1]) : "memory");
-                if (c == 0) sh.q_down[entry * sh.q_rows + (r < tile_rows ? 0 : kTile) + at] = __int_as_float((127 - e) << 23);
+                const uint32_t to = dst + ((c ^ (at & 7)) << 4);
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + P.q_part), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
+                             : "memory");
             }
         }
+        if (r < rows) sh.q_down[entry * sh.q_rows + (r < tile_rows ? 0 : kTile) + at] = __int_as_float((127 - e) << 23);
     }
     fence_async();
     __syncwarp();
