@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kThreads = 512;  // two softmax warpgroups, then a warp for each other role
 constexpr int kReaders = 8 + 2 + 2 + 1;
-constexpr int kSplitters = 2;  // warps that split the queries for e4m3 caches
+constexpr int kSplitters = 3;  // warps that split the queries for e4m3 caches: two of their own, and the items'
 
 struct Shared : Common {
     uint64_t s_full[2], p_ready[2], pv_done[2];
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int tid = threadIdx.x, w = tid >> 5;
     if (tid == 0) {
-        init_common(sh, 2, kReaders + (K == kE4m3 ? kSplitters : 0), K == kE4m3 ? kSplitters : 1);
+        init_common(sh, 2, kReaders + (K == kE4m3 ? kSplitters - 1 : 0), K == kE4m3 ? kSplitters : 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_u32(&sh.s_full[i]), 1);
             bar_init(smem_u32(&sh.p_ready[i]), 4);
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w == 8 || w == 10) load_role(P, sh, k_smem, v_smem, &km, &vm, w == 10, w == 10);
         else if (w == 9 || w == 13) product_role<K, NH>(P, sh, q_smem, k_smem, v_smem, w == 13);
         else if (w == 11) value_role<K>(P, sh, v_smem);
-        else if (w == 12) item_role<K, K != kE4m3>(P, sh, q_smem, &qm);
+        else if (w == 12) item_role<K, kSplitters>(P, sh, q_smem, &qm);
         else if (K == kE4m3 && w >= 14) query_role(P, sh, q_smem, w - 14, kSplitters);
     }
     tc_before();
@@ -627,7 +627,10 @@ cudaError_t launch(Params P, int n, cudaStream_t st) {
     P.block = 2 * P.tokens;
     P.q_box = min(P.tokens, A.chunk.max_gamma + 1);
     P.q_part = kHalf;
-    P.lead = 3;  // measured on prompts of 700 to 2048 tokens: 235 us, with 1, 2, 4 and 5 272, 238, 238 and 240
+    // measured on prompts of 700 to 2048 tokens: 235 us, with 1, 2, 4 and 5 272, 238, 238
+    // and 240. With an e4m3 cache the queries' parts take longer: 3, 6 and 10 make 476, 366 and 387 us of those prompts
+    // (and 54, 59 and 66 of 16 trees of 32 tokens).
+    P.lead = K == kE4m3 ? 6 : 3;
     P.halves = NH;
     P.q_tile = (K == kE4m3 ? 2 : NH) * kHalf;
     P.q_bytes = 2 * P.q_tile;

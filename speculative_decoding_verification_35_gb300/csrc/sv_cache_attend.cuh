@@ -689,7 +689,7 @@ __device__ __forceinline__ bool copy_item_queries(const Params& P, Common& sh, c
 
 // e4m3 caches: split into the parts hi and lo, each row brought to [128, 256) by a power of two, by `of` warps, of which
 // this is number `who`. A lane has a row and goes over it twice, for its largest element and for its parts; wide
-// chunks have two warps. (Half a warp a row, with its maximum over the lanes, took four times as long: 60000 cycles
+// chunks have three warps. (Half a warp a row, with its maximum over the lanes, took four times as long: 60000 cycles
 // for 256 rows.)
 __device__ __forceinline__ void split_queries(const Params& P, Common& sh, const Item& it, uint32_t q_smem, uint32_t entry, uint32_t q_full,
                                               int who, int of) {
@@ -707,13 +707,13 @@ __device__ __forceinline__ void split_queries(const Params& P, Common& sh, const
         const int32_t end = r < rows ? D : 0;
         uint32_t big = 0;  // magnitudes, in pairs
 #pragma unroll 1
-        for (int32_t d = 0; d < end; d += 32) {
-            uint4 u[4];
+        for (int32_t d = 0; d < end; d += 64) {
+            uint4 u[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 8; ++k)
                 u[k] = d + 8 * k < end ? *reinterpret_cast<const uint4*>(row + d + 8 * k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 8; ++k) {
                 const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(big) : "r"(w[i] & 0x7fff7fffu));
@@ -840,9 +840,9 @@ __device__ __forceinline__ void scan_rows(int halves, uint32_t at, int32_t lo, i
         }
 }
 
-// The CTA's items, one after the other, by one warp, and their queries (unless others see to those); a last one of no
-// tiles ends them.
-template <int K, bool kQueries>
+// The CTA's items, one after the other, by one warp, and their queries (e4m3: a part of them, where kSplitters warps do
+// that); a last one of no tiles ends them.
+template <int K, int kSplitters>
 __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t q_smem, const CUtensorMap* qm) {
     const int lane = threadIdx.x & 31;
     const bool tree = P.a.chunk.parents != nullptr;
@@ -920,11 +920,10 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
         }
         __syncwarp();
         if (it.n == 0) break;
-        if (!kQueries) continue;
         if (i >= (uint32_t)P.q_bufs && !wait(smem_u32(&sh.q_empty[qr.i]), qr.parity ^ 1, &sh.gave_up)) break;
         ++loads;
         const uint32_t at = q_smem + qr.i * P.q_bytes, q_full = smem_u32(&sh.q_full[qr.i]);
-        if (K == kE4m3) split_queries(P, sh, it, at, ring.i, q_full, 0, 1);
+        if (K == kE4m3) split_queries(P, sh, it, at, ring.i, q_full, kSplitters - 1, kSplitters);
         else if (!copy_item_queries(P, sh, it, at, qm, i, q_full)) break;
         qr.step(P.q_bufs);
     }

@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kThreads<G>, G == 1 ? 2 : 1)
         if (role == 0) load_role(P, sh, k_smem, v_smem, &km, &vm, 0, 1);
         else if (role == 1) product_role<K, NR, G>(P, sh, q_smem, p_smem, k_smem, v_smem);
         else if (role == 2) value_role<K>(P, sh, v_smem);
-        else item_role<K, true>(P, sh, q_smem, &qm);
+        else item_role<K, 1>(P, sh, q_smem, &qm);
     }
     tc_before();
     __syncthreads();
