@@ -147,7 +147,8 @@ class PagedCache:
 
     k, v: [layers, pages, page_size, heads, head_dim], bfloat16, float16 or float8_e4m3fn, of equal strides
     (views of another order, such as head-major pages, are fine; the last dimension is contiguous).
-    page_table: int32 [B, pages per sequence]. k_scale, v_scale: float32 [layers, heads] (float8_e4m3fn only).
+    page_table: int32 [sequences, pages per sequence]; a chunk has as many sequences, or the first of them.
+    k_scale, v_scale: float32 [layers, heads] (float8_e4m3fn only).
     Calls of one object share its workspace and must not overlap on the GPU.
     """
 
@@ -167,7 +168,7 @@ class PagedCache:
                 if not t.is_contiguous():
                     raise ValueError(f"{name} must be contiguous")
         self.k, self.v, self.page_table, self.k_scale, self.v_scale = k, v, page_table, k_scale, v_scale
-        self.heads, self.head_dim = heads, dim
+        self.heads, self.head_dim, self.sequences = heads, dim, page_table.shape[0]
         # of a dimension of extent one the stride says nothing: any valid one does
         st = [k.stride(i) if k.shape[i] > 1 else heads * page_size * dim for i in range(4)]
         width = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
@@ -181,6 +182,10 @@ class PagedCache:
         # addresses that no call changes
         self._at, self._status, self._ws = ctypes.addressof(self.struct), _ptr(self.status), _ptr(self.workspace)
         self._device = k.get_device()
+
+    def _chunk(self, chunk):
+        if chunk.B > self.sequences:
+            raise ValueError(f"page_table has {self.sequences} sequences, the chunk {chunk.B}")
 
     def _rows(self, t, name, rows, heads=None):
         """Rows of [heads, head_dim], contiguous within a row: the row stride. These checks and the launch are all
@@ -206,6 +211,7 @@ class PagedCache:
     def append(self, chunk: Chunk, q, k, v, q_out, rope: Rope | None = None, layer: int = 0, stream=None) -> int:
         """Enqueue spec_cache_append: rotated queries to q_out, rotated keys and values to the cache. q and
         q_out may be None."""
+        self._chunk(chunk)
         rows, kind = chunk.rows, k.dtype
         code = _ACTIVATIONS.get(kind)
         if code is None or v.dtype != kind or (q is not None and (q.dtype != kind or q_out.dtype != kind)):
@@ -225,6 +231,7 @@ class PagedCache:
                stream=None) -> int:
         """Enqueue spec_cache_attend: attention of the chunk's rotated queries into out (and lse, float32
         [rows, q_heads]). scale: 1 / sqrt(head_dim) by default."""
+        self._chunk(chunk)
         rows, kind = chunk.rows, q.dtype
         code = _ACTIVATIONS.get(kind)
         if code is None or out.dtype != kind:
@@ -244,6 +251,7 @@ class PagedCache:
     def compact(self, chunk: Chunk, out_num_accepted, out_path, out_cached, stream=None) -> int:
         """Enqueue spec_cache_compact on a verify call's outputs. out_path None: linear drafts. out_cached may
         be the chunk's `cached`."""
+        self._chunk(chunk)
         _check(out_num_accepted, "out_num_accepted", (torch.int32,), (chunk.B,), self._device)
         _check(out_cached, "out_cached", (torch.int32,), (chunk.B,), self._device)
         if out_path is not None:

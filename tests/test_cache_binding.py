@@ -1,0 +1,57 @@
+"""What the cache calls' binding refuses before the library is called (CPU)."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def sc():
+    from speculative_decoding_verification_35_gb300 import _build
+    _build.build()
+    from speculative_decoding_verification_35_gb300 import speccache
+    return speccache
+
+
+class Reached(Exception):
+    pass
+
+
+@pytest.fixture
+def calls(sc, monkeypatch):
+    """A cache of two sequences and its three calls on a chunk; Reached where the library would be called."""
+    for name in ("spec_cache_append", "spec_cache_attend", "spec_cache_compact"):
+        def stop(*args, name=name):
+            raise Reached(name, args)
+        monkeypatch.setattr(sc.lib, name, stop)
+    monkeypatch.setattr(sc.PagedCache, "_stream", lambda self, stream: None)
+    k = torch.zeros((1, 4, 8, 2, 16), dtype=torch.bfloat16)
+    cache = sc.PagedCache(k, k.clone(), torch.zeros((2, 2), dtype=torch.int32))
+    q = torch.zeros((3, 4, 16), dtype=torch.bfloat16)
+    kv = torch.zeros((3, 2, 16), dtype=torch.bfloat16)
+
+    def ints(n):
+        return torch.zeros(n, dtype=torch.int32)
+
+    def append(chunk, **kw):
+        cache.append(chunk, q, kv, kv, q.clone(), **kw)
+
+    def attend(chunk, **kw):
+        cache.attend(chunk, q, q.clone(), **kw)
+
+    def compact(chunk, accepted=None, path=None, now=None):
+        cache.compact(chunk, ints(chunk.B) if accepted is None else accepted, path,
+                      ints(chunk.B) if now is None else now)
+    return append, attend, compact
+
+
+def chunk(sc, B, **kw):
+    return sc.Chunk(torch.zeros(B + 1, dtype=torch.int32), torch.zeros(B, dtype=torch.int32), 3, 2, **kw)
+
+
+def test_more_sequences_than_the_page_table_has(sc, calls):
+    for call in calls:
+        for B in (0, 1, 2):
+            with pytest.raises(Reached):
+                call(chunk(sc, B))
+        for B in (3, 100):
+            with pytest.raises(ValueError, match="page_table"):
+                call(chunk(sc, B))
