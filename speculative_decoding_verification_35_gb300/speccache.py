@@ -256,6 +256,9 @@ class PagedCache:
         _check(out_cached, "out_cached", (torch.int32,), (chunk.B,), self._device)
         if out_path is not None:
             _check(out_path, "out_path", (torch.int32,), (None,), self._device)
+        for t, name in ((out_num_accepted, "out_num_accepted"), (out_path, "out_path"), (out_cached, "out_cached")):
+            if t is not None and not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
         return lib.spec_cache_compact(self._at, chunk.at, out_num_accepted.data_ptr(), _ptr(out_path),
                                       out_cached.data_ptr(), self._status, self._stream(stream))
 

@@ -55,3 +55,13 @@ def test_more_sequences_than_the_page_table_has(sc, calls):
         for B in (3, 100):
             with pytest.raises(ValueError, match="page_table"):
                 call(chunk(sc, B))
+
+
+def test_compact_wants_dense_tensors(sc, calls):
+    compact = calls[2]
+    wide = torch.zeros((2, 2), dtype=torch.int32)
+    for kw in (dict(accepted=wide[:, 0]), dict(now=wide[:, 1]), dict(path=torch.zeros(8, dtype=torch.int32)[::2])):
+        with pytest.raises(ValueError, match="contiguous"):
+            compact(chunk(sc, 2), **kw)
+    with pytest.raises(Reached):
+        compact(chunk(sc, 2), accepted=wide[0], path=torch.zeros(4, dtype=torch.int32), now=wide[1])
