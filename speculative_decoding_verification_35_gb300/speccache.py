@@ -125,7 +125,7 @@ class Chunk:
             if t is not None and not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
         self.seq_offsets, self.cached, self.parents = seq_offsets, cached, parents
-        self.B, self.rows, self.max_gamma = B, rows, max_gamma
+        self.B, self.rows, self.max_gamma, self.device = B, rows, max_gamma, cached.get_device()
         self.struct = SvChunk(_ptr(seq_offsets), _ptr(cached), _ptr(parents), B, rows, max_gamma, 0)
         self.at = ctypes.addressof(self.struct)
 
@@ -137,7 +137,7 @@ class Rope:
         _check(table, "table", (torch.float32,), (None, None))
         if not table.is_contiguous():
             raise ValueError("table must be contiguous")
-        self.table = table
+        self.table, self.device = table, table.get_device()
         self.struct = SvRope(_ptr(table), table.shape[0], table.shape[1], int(interleaved), 0)
         self.at = ctypes.addressof(self.struct)
 
@@ -186,6 +186,8 @@ class PagedCache:
     def _chunk(self, chunk):
         if chunk.B > self.sequences:
             raise ValueError(f"page_table has {self.sequences} sequences, the chunk {chunk.B}")
+        if chunk.device != self._device:
+            raise ValueError(f"chunk must be on {self.k.device}, got device {chunk.device}")
 
     def _rows(self, t, name, rows, heads=None):
         """Rows of [heads, head_dim], contiguous within a row: the row stride. These checks and the launch are all
@@ -216,6 +218,8 @@ class PagedCache:
         code = _ACTIVATIONS.get(kind)
         if code is None or v.dtype != kind or (q is not None and (q.dtype != kind or q_out.dtype != kind)):
             self._type(*(t for t in (q, k, v, q_out) if t is not None))
+        if rope is not None and rope.device != self._device:
+            raise ValueError(f"rope must be on {self.k.device}, got device {rope.device}")
         ks = self._rows(k, "k", rows, self.heads)
         if self._rows(v, "v", rows, self.heads) != ks:
             raise ValueError("k and v must have equal row strides")

@@ -65,3 +65,18 @@ def test_compact_wants_dense_tensors(sc, calls):
             compact(chunk(sc, 2), **kw)
     with pytest.raises(Reached):
         compact(chunk(sc, 2), accepted=wide[0], path=torch.zeros(4, dtype=torch.int32), now=wide[1])
+
+
+def test_chunks_and_rotations_of_another_device(sc, calls):
+    """(One device here: the numbers stand for two.)"""
+    other = chunk(sc, 2)
+    other.device = 1
+    for call in calls:
+        with pytest.raises(ValueError, match="chunk must be on"):
+            call(other)
+    rope = sc.Rope(torch.zeros((8, 16)))
+    with pytest.raises(Reached):
+        calls[0](chunk(sc, 2), rope=rope)
+    rope.device = 1
+    with pytest.raises(ValueError, match="rope must be on"):
+        calls[0](chunk(sc, 2), rope=rope)
