@@ -112,6 +112,13 @@ def _check(t, name, dtypes, shape=None, device=None):
         raise ValueError(f"{name} must be on device {device}, got {t.device}")
 
 
+def _int32(x, name):
+    """The library's sizes are int32; ctypes would wrap what is not."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must be an int32, got {x}")
+    return x
+
+
 class Chunk:
     """One batch of chunks in the verify step's layout (device int32 tensors; see sv_chunk)."""
 
@@ -126,7 +133,8 @@ class Chunk:
                 raise ValueError(f"{name} must be contiguous")
         self.seq_offsets, self.cached, self.parents = seq_offsets, cached, parents
         self.B, self.rows, self.max_gamma, self.device = B, rows, max_gamma, cached.get_device()
-        self.struct = SvChunk(_ptr(seq_offsets), _ptr(cached), _ptr(parents), B, rows, max_gamma, 0)
+        self.struct = SvChunk(_ptr(seq_offsets), _ptr(cached), _ptr(parents), B, _int32(rows, "rows"),
+                              _int32(max_gamma, "max_gamma"), 0)
         self.at = ctypes.addressof(self.struct)
 
 
@@ -228,13 +236,14 @@ class PagedCache:
             qs, qh = self._rows(q, "q", rows), q.shape[1]
             if self._rows(q_out, "q_out", rows, qh) != qh * self.head_dim:
                 raise ValueError("q_out must be contiguous")
-        return lib.spec_cache_append(self._at, layer, chunk.at, None if rope is None else rope.at, code, qh, _ptr(q), qs,
-                                     k.data_ptr(), v.data_ptr(), ks, _ptr(q_out), self._status, self._stream(stream))
+        return lib.spec_cache_append(self._at, _int32(layer, "layer"), chunk.at, None if rope is None else rope.at, code,
+                                     qh, _ptr(q), qs, k.data_ptr(), v.data_ptr(), ks, _ptr(q_out), self._status,
+                                     self._stream(stream))
 
     def attend(self, chunk: Chunk, q, out, lse=None, scale: float | None = None, window: int = 0, layer: int = 0,
                stream=None) -> int:
         """Enqueue spec_cache_attend: attention of the chunk's rotated queries into out (and lse, float32
-        [rows, q_heads]). scale: 1 / sqrt(head_dim) by default."""
+        [rows, q_heads]). scale: 1 / sqrt(head_dim) by default; window: 0 for none, as any past every length is."""
         self._chunk(chunk)
         rows, kind = chunk.rows, q.dtype
         code = _ACTIVATIONS.get(kind)
@@ -249,8 +258,10 @@ class PagedCache:
                 raise ValueError("lse must be contiguous with a row for every chunk row")
         if scale is None:
             scale = self.head_dim ** -0.5
-        return lib.spec_cache_attend(self._at, layer, chunk.at, code, qh, q.data_ptr(), qs, scale, window, out.data_ptr(),
-                                     _ptr(lse), self._status, self._ws, self.ws_bytes, self._stream(stream))
+        window = max(-2 ** 31, min(window, 2 ** 31 - 1))
+        return lib.spec_cache_attend(self._at, _int32(layer, "layer"), chunk.at, code, qh, q.data_ptr(), qs, scale, window,
+                                     out.data_ptr(), _ptr(lse), self._status, self._ws, self.ws_bytes,
+                                     self._stream(stream))
 
     def compact(self, chunk: Chunk, out_num_accepted, out_path, out_cached, stream=None) -> int:
         """Enqueue spec_cache_compact on a verify call's outputs. out_path None: linear drafts. out_cached may

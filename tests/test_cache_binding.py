@@ -80,3 +80,22 @@ def test_chunks_and_rotations_of_another_device(sc, calls):
     rope.device = 1
     with pytest.raises(ValueError, match="rope must be on"):
         calls[0](chunk(sc, 2), rope=rope)
+
+
+def test_integers_past_32_bits(sc, calls):
+    """Wrapped into the library's int32 they would be other layers, windows and sizes."""
+    append, attend, _ = calls
+    for call in (append, attend):
+        for layer in (2 ** 31, 2 ** 32, -2 ** 32, 2 ** 63):
+            with pytest.raises(ValueError, match="layer"):
+                call(chunk(sc, 2), layer=layer)
+    for window, passed in ((0, 0), (-1, -1), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                           (2 ** 32, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1), (2 ** 64, 2 ** 31 - 1),
+                           (-2 ** 32, -2 ** 31), (-2 ** 32 + 5, -2 ** 31)):
+        with pytest.raises(Reached) as got:
+            attend(chunk(sc, 2), window=window)
+        assert got.value.args[1][8] == passed
+    one = torch.zeros(2, dtype=torch.int32)
+    for rows, most in ((2 ** 32 + 1, 0), (1, 2 ** 32), (-2 ** 32, 0), (1, 2 ** 31)):
+        with pytest.raises(ValueError, match="int32"):
+            sc.Chunk(one, one[:1], rows, most)
