@@ -183,9 +183,11 @@ __device__ __forceinline__ void weights32(const uint32_t* x, F2 sl2, F2 off2, F2
         }
     }
 }
-// False if the weights of some row sum to more than their type holds.
+// False, with nothing written, if the weights of some row sum to more than their type may hold. bounded: the row's
+// reference has met the tile's maximum, so each weight is 2^(kShift + kSlack) at most and all are written. (Their sum is
+// no test then: 128 of that size sum to the limit itself, and as the arguments are rounded, to a little more.)
 template <int K>
-__device__ __forceinline__ bool quick_weights(uint32_t s_col, float sl, float off, bool real, float& total) {
+__device__ __forceinline__ bool quick_weights(uint32_t s_col, float sl, float off, bool real, bool bounded, float& total) {
     const F2 sl2 = pack2(sl, sl), off2 = pack2(off, off);
     F2 sum[2] = {0, 0};
     uint32_t s[2][32], pk[4][16];
@@ -199,7 +201,7 @@ __device__ __forceinline__ bool quick_weights(uint32_t s_col, float sl, float of
     float a, b;
     unpack2(add2(sum[0], sum[1]), a, b);
     total = a + b;
-    if (K != kE4m3 && __any_sync(kAll, real && total > (K == kBf16 ? 0x1p64f : 0x1p15f))) return false;
+    if (K != kE4m3 && !bounded && __any_sync(kAll, real && total > (K == kBf16 ? 0x1p64f : 0x1p15f))) return false;
 #pragma unroll
     for (int q = 0; q < 4; ++q) tc_st16(s_col + 16 * q, pk[q]);
     return true;
@@ -281,7 +283,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
                 float sum;
                 bool first = K == kE4m3 || unset;
 #pragma unroll 1
-                for (int attempt = 0; attempt < 2; ++attempt, first = true) {
+                for (;; first = true) {
                     if (first) {
                         const float mx = tile_max(s_col);
                         const bool move = row.real && ((mx - m) * row.sl > KT::kSlack || (m == -INFINITY && mx > m));
@@ -298,7 +300,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
                             }
                         }
                     }
-                    if (quick_weights<K>(s_col, row.sl, KT::kShift - (m == -INFINITY ? 0.f : m * row.sl), row.real, sum)) break;
+                    if (quick_weights<K>(s_col, row.sl, KT::kShift - (m == -INFINITY ? 0.f : m * row.sl), row.real, first, sum)) break;
                 }
                 l += sum;
                 tc_wait_st();

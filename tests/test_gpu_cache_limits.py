@@ -1,0 +1,47 @@
+"""The cache calls at the ends of their ranges: windows, lengths, scales, offsets and batches that are rare, on the GPU.
+
+Tolerances are those of test_gpu_cache.py, whose batches these tests use.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as oc
+from tests.test_gpu_cache import BAD_OFFSETS, CAPACITY, TYPES, Batch, f64, tree
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sc():
+    from speculative_decoding_verification_35_gb300 import speccache
+    return speccache
+
+
+@pytest.mark.parametrize("tokens", [9, 3])
+def test_fp16_weights_at_the_bound(sc, tokens):
+    """A tile of one score, then a tile of another that lies above it by as much as a reference allows: as the weights'
+    arguments are rounded, 128 of them sum to a little less or a little more than 2^15."""
+    rng = np.random.default_rng(tokens)
+    B, hkv, G = 64, 8, 8
+    b = Batch(sc, [tokens] * B, [256] * B, hkv * G, hkv, 64, 16, "fp16", seed=tokens)
+    b.q.zero_()
+    b.q[..., :3] = 1.0
+    # multiples of 2^-14 below 1024, in three parts that fp16 holds; scores are 1/8 of them
+    first = -rng.integers(256 << 14, 1008 << 14, (B, hkv))
+    second = first + 90852  # 8 / log2(e), rounded down
+    parts = np.zeros((B, 264 + tokens, hkv, 3))
+    for lo, hi, z in ((0, 128, first), (128, 256, second)):
+        whole = z >> 14
+        rest = z - (whole << 14)  # 14 bits
+        parts[:, lo:hi] = np.stack((whole, (rest >> 4 << 4) / 16384, (rest & 15) / 16384), -1)[:, None]
+    parts[:, 256:, :, 0] = -30000.0
+    slots = np.arange(256 + tokens)
+    for i in range(B):
+        pg = torch.tensor(b.table_h[i][slots // 16].astype(np.int64), device="cuda")
+        at = torch.tensor(slots % 16, device="cuda")
+        k = torch.zeros((len(slots), hkv, 64), dtype=torch.float16, device="cuda")
+        k[..., :3] = torch.tensor(parts[i, :len(slots)], device="cuda")
+        b.k[0, pg, at] = k
+        b.v[0, pg, at] = torch.where(torch.tensor(slots, device="cuda") < 128, 1.0, 3.0).half()[:, None, None]
+    b.check()
