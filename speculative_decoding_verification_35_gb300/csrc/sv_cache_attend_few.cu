@@ -142,7 +142,8 @@ __device__ __forceinline__ uint32_t rows_seeing(const Params& P, const Item& it,
     if (slot < it.lo || slot >= it.end || (bad >> (slot % kTile >> 3) & 1u)) return 0;
     const int32_t i = slot - it.past, w = P.a.window;  // its place in the chunk, if it has one
     if (!rarely(tree)) {
-        const int32_t first = max(0, i), last = w > 0 ? min(it.nt - 1, i + w - 1) : it.nt - 1;
+        // (compared without i + w, which a window near 2^31 takes past an int32)
+        const int32_t first = max(0, i), last = w > 0 && i < it.nt - w ? i + w - 1 : it.nt - 1;
         return prefix32((last + 1) * P.G - row0) & ~prefix32(first * P.G - row0);
     }
     if (i < 0 && w <= 0) return prefix32(it.nt * P.G - row0);

@@ -45,3 +45,17 @@ def test_fp16_weights_at_the_bound(sc, tokens):
         b.k[0, pg, at] = k
         b.v[0, pg, at] = torch.where(torch.tensor(slots, device="cuda") < 128, 1.0, 3.0).half()[:, None, None]
     b.check()
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31, 2 ** 32, 2 ** 32 + 1, 2 ** 40])
+@pytest.mark.parametrize("chunks,hq", [([5, 1, 6], 8), ([150, 1, 40], 8), ([32, 9, 1], 4)])
+@pytest.mark.parametrize("kind,cache", [("bf16", "bf16"), ("bf16", "e4m3")])
+def test_windows_past_every_length(sc, chunks, hq, kind, cache, window):
+    """The largest window there is, a usual way to say none, and those that no int32 holds."""
+    rng = np.random.default_rng(2)
+    par = [tree(rng, n) for n in chunks] if hq == 4 else None
+    b = Batch(sc, chunks, [300, 10, 128], hq, 2, 64, 16, kind, cache, parents=par)
+    out, lse = b.check(window)
+    want, wl = b.attend(0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
