@@ -272,7 +272,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
             const bool mixed = mixed_tile(it, k0);
             if (!wait(s_full, steps & 1, gave_up)) return;
             tc_after();
-            if (K == kE4m3 && j == 0) row.sl *= sh.q_down[walk.ring.i * sh.q_rows + stream * kTile + r];
+            if (K == kE4m3 && j == 0) row.sl = row_unit(row.sl, sh.q_down[walk.ring.i * sh.q_rows + stream * kTile + r]);
             uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
             if (busy) {
                 const uint32_t bad = sh.bad[0][ring];

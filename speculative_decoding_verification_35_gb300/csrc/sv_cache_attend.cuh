@@ -550,6 +550,9 @@ __device__ __forceinline__ float score_unit(const AttendArgs& A, int32_t h, bool
     flip = sl < 0.f;
     return fmaxf(fabsf(sl), 1e-30f);
 }
+// The same for a row whose queries were brought up by a power of two (e4m3): 2^-120 for a row of zeros, so that this
+// product, too, is kept above zero.
+__device__ __forceinline__ float row_unit(float unit, float down) { return fmaxf(unit * down, 1e-37f); }
 
 // Only among slots that some rows of the item see and others do not can a value meet a weight of zero, and a NaN
 // or infinity be carried into a row that does not see it.

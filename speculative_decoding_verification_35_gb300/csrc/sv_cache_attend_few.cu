@@ -204,7 +204,8 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                 for (int r = 0; r < (K == kE4m3 ? N : 1); r += 4) {
                     if (r >= rows) break;
 #pragma unroll
-                    for (int e = 0; e < (K == kE4m3 ? 4 : 1); ++e) u[r + e] = unit * sh.q_down[walk.ring.i * sh.q_rows + row0 + r + e];
+                    for (int e = 0; e < (K == kE4m3 ? 4 : 1); ++e)
+                        u[r + e] = row_unit(unit, sh.q_down[walk.ring.i * sh.q_rows + row0 + r + e]);
                 }
             const uint32_t s_col = tmem + buf * NR;
             const int32_t k0 = (it.tile + j) * kTile;

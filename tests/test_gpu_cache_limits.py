@@ -59,3 +59,22 @@ def test_windows_past_every_length(sc, chunks, hq, kind, cache, window):
     want, wl = b.attend(0)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("tokens,group", [(6, 2), (9, 6), (90, 2)])
+@pytest.mark.parametrize("scale,ks", [(0.0, None), (0.125, 1e-20), (0.125, 0.0), (1e-30, 1e-6)])
+def test_zero_queries_under_tiny_scales(sc, tokens, group, scale, ks):
+    """Rows of zeros weigh every slot alike, also where the factor of their scores is next to nothing."""
+    b = Batch(sc, [tokens, 1], [200, 30], 2 * group, 2, 64, 16, "bf16", "e4m3")
+    if ks is not None:
+        b.ks.fill_(ks)
+    b.q[::2] = 0
+    b.q[1, 0, 3] = 0
+    out = torch.empty((b.rows, b.hq, 64), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((b.rows, b.hq), device="cuda")
+    assert b.cache.attend(b.chunk, b.q, out, lse, scale=scale) == 0
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == 0
+    # the scores are under 1e-15 in every row
+    b.q = torch.zeros_like(b.q)
+    b.compare(out, lse)
