@@ -543,16 +543,18 @@ struct Items {
     }
     __device__ __forceinline__ const Tree& tree() const { return sh.tree[ring.i]; }
 };
+// x or the least, NaN for NaN (where fmaxf returns the other).
+__device__ __forceinline__ float at_least(float x, float least) { return x < least ? least : x; }
 // Scores to log2 of the weights. A negative factor changes the queries' signs; one of zero is kept above it, so
-// that -inf stays -inf.
+// that -inf stays -inf. A NaN stays one: a head whose scale is NaN has no weights.
 __device__ __forceinline__ float score_unit(const AttendArgs& A, int32_t h, bool& flip) {
     const float sl = A.scale * (A.pool.k_scale ? A.pool.k_scale[h] : 1.f) * kLog2e;
     flip = sl < 0.f;
-    return fmaxf(fabsf(sl), 1e-30f);
+    return at_least(fabsf(sl), 1e-30f);
 }
 // The same for a row whose queries were brought up by a power of two (e4m3): 2^-120 for a row of zeros, so that this
 // product, too, is kept above zero.
-__device__ __forceinline__ float row_unit(float unit, float down) { return fmaxf(unit * down, 1e-37f); }
+__device__ __forceinline__ float row_unit(float unit, float down) { return at_least(unit * down, 1e-37f); }
 
 // Only among slots that some rows of the item see and others do not can a value meet a weight of zero, and a NaN
 // or infinity be carried into a row that does not see it.

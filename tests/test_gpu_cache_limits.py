@@ -78,3 +78,17 @@ def test_zero_queries_under_tiny_scales(sc, tokens, group, scale, ks):
     # the scores are under 1e-15 in every row
     b.q = torch.zeros_like(b.q)
     b.compare(out, lse)
+
+
+@pytest.mark.parametrize("tokens,group", [(6, 2), (9, 6), (90, 2)])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_nan_scales_reach_their_heads(sc, tokens, group, which):
+    b = Batch(sc, [tokens, 1], [200, 30], 2 * group, 2, 64, 16, "bf16", "e4m3")
+    good, gl = b.attend()
+    (b.ks if which == "k" else b.vs)[0, 1] = float("nan")
+    out, lse = b.attend()
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == 0
+    assert torch.equal(out[:, :group], good[:, :group]) and torch.equal(lse[:, :group], gl[:, :group])
+    assert torch.isnan(out[:, group:]).all()
+    assert torch.isnan(lse[:, group:]).all() if which == "k" else torch.equal(lse[:, group:], gl[:, group:])
