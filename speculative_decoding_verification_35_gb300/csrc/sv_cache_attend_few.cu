@@ -185,10 +185,13 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
         const float unit = score_unit(A, it.h, flip);
         float l[N], off[N], u[K == kE4m3 ? N : 1];  // weights are 2^(u s + off)
         u[0] = unit;
+        // The loops below take four rows at a time. Those past the item's last have another sequence's queries, or what
+        // an earlier item left (e4m3: and an unset factor): their weights are zero, or nothing would keep their scores
+        // from voting on the references, and so from changing the roundings of the item's own rows.
 #pragma unroll
         for (int r = 0; r < N; ++r) {
             l[r] = 0.f;
-            off[r] = Wt::kShift;
+            off[r] = r < rows ? Wt::kShift : -INFINITY;
         }
         // every warp settles the references by itself, from the same notes: a lane has a row's (off again, and whether
         // there is a reference at all)

@@ -92,3 +92,21 @@ def test_nan_scales_reach_their_heads(sc, tokens, group, which):
     assert torch.equal(out[:, :group], good[:, :group]) and torch.equal(lse[:, :group], gl[:, :group])
     assert torch.isnan(out[:, group:]).all()
     assert torch.isnan(lse[:, group:]).all() if which == "k" else torch.equal(lse[:, group:], gl[:, group:])
+
+
+@pytest.mark.parametrize("kind,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("group,B", [(1, 2), (3, 2), (5, 40), (3, 900), (11, 700)])
+def test_other_sequences_queries_change_nothing(sc, group, B, kind, cache):
+    """Chunks of one and of two tokens: the outputs of the first are the same to the bit whatever the others' queries."""
+    chunks = [1 + i % 2 for i in range(B)]
+    b = Batch(sc, chunks, [400 + i % 3 * 150 for i in range(B)], group, 1, 64, 16, kind, cache, seed=group, qscale=1.0)
+    single = torch.tensor([n == 1 for n in chunks for _ in range(n)], device="cuda")
+    q = b.q.clone()
+    b.q = torch.where(single[:, None, None], q, q * 0.01)
+    want, wl = b.attend()
+    for factor in (40.0, -300.0):
+        b.q = torch.where(single[:, None, None], q, q * factor)
+        out, lse = b.attend()
+        torch.cuda.synchronize()
+        assert torch.equal(out[single], want[single]) and torch.equal(lse[single], wl[single])
+    assert b.cache.status_bits() == 0
