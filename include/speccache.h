@@ -29,7 +29,8 @@
  *   SV_ERR_TIMEOUT      a bounded wait inside the launch gave up (the outputs are then undefined)
  * A sequence with a finding fails alone: append writes nothing of it, attend writes zeros and an lse of -inf
  * (nothing where the rows themselves are bad), compact moves nothing. A bad page id fails only its tokens:
- * they are not stored, not moved, and not attended to.
+ * they are not stored, not moved, and not attended to. Where seq_offsets decreases, a row that two sequences claim
+ * holds either one's result, and the other's token may be missing from its cache; SV_ERR_BAD_OFFSETS is set.
  */
 #ifndef SPECCACHE_H
 #define SPECCACHE_H

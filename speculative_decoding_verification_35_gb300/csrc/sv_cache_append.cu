@@ -97,9 +97,12 @@ __global__ void __launch_bounds__(kThreads) k_cache_append(const __grid_constant
         if (end > A.chunk.rows || A.chunk.offs[0] != 0) report(A.status, 1u << SV_ERR_BAD_OFFSETS);
     }
     const int32_t b = find_seq(A.chunk, row);
-    if (b < 0) return;
     int32_t cap = capacity_of(A.pool);
     if (A.rot) cap = min(cap, A.positions);
+    // Every sequence's offsets are looked at, also of those that no row leads to.
+    if (threadIdx.x == kThreads - 1)
+        for (int32_t i = row; i < A.chunk.B; i += gridDim.x) report(A.status, seq_of(A.chunk, cap, i).err);
+    if (b < 0) return;
     Seq s = seq_of(A.chunk, cap, b);
     const int32_t j = row - s.row0;
     int32_t depth = j;

@@ -110,3 +110,51 @@ def test_other_sequences_queries_change_nothing(sc, group, B, kind, cache):
         torch.cuda.synchronize()
         assert torch.equal(out[single], want[single]) and torch.equal(lse[single], wl[single])
     assert b.cache.status_bits() == 0
+
+
+@pytest.mark.parametrize("offs,max_gamma,rows,stored", [
+    ([0, 5, 3, 8], 5, 11, [0, 2]),      # a sequence that ends before it begins; row 5 is claimed by two others
+    ([0, 5, 9, 8], 5, 11, [0, 1]),      # the last one does
+    ([0, 3, 9, 11], 5, 14, [0, 2]),     # one drafts too many
+    ([0, 2, 5, 8], 5, 10, [0, 1]),      # the last one's rows are not all there
+    ([0, 9, 2, 12, 14], 9, 18, [0, 3]),  # too long a sequence after one that ends before it begins
+])
+def test_append_reports_every_bad_sequence(sc, offs, max_gamma, rows, stored):
+    """The three calls find the same in a batch's offsets, also in sequences that own no row."""
+    B = len(offs) - 1
+    b = Batch(sc, [6] * B, [40] * B, 4, 2, 64, 8, poison=False)
+    for name in ("q", "kn", "vn"):
+        setattr(b, name, torch.randn((20, getattr(b, name).shape[1], 64), device="cuda").bfloat16())
+    b.table = torch.arange(B * 8, dtype=torch.int32, device="cuda").view(B, 8)
+    b.k = torch.randn((1, B * 8, 8, 2, 64), device="cuda").bfloat16()
+    b.v = b.k.clone()
+    b.offs = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    b.make(max_gamma)
+    b.chunk.struct.rows = b.chunk.rows = rows
+    q_out = torch.full((20, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    k0 = b.k.clone()
+    assert b.cache.append(b.chunk, b.q, b.kn, b.vn, q_out) == 0
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == BAD_OFFSETS
+    # a sequence's tokens, but for rows that another one claims as well
+    claims = [i for s in range(B) for i in range(offs[s] + s, offs[s + 1] + s + 1)]
+    for s in range(B):
+        at = b.k[0, b.table[s].long()].reshape(64, 2, 64)
+        was = k0[0, b.table[s].long()].reshape(64, 2, 64)
+        assert torch.equal(at[:40], was[:40])
+        if s not in stored:
+            assert torch.equal(at, was)
+            continue
+        T = offs[s + 1] - offs[s] + 1
+        assert torch.equal(at[40 + T:], was[40 + T:])
+        for j in range(T):
+            r = offs[s] + s + j
+            if claims.count(r) == 1:
+                assert torch.equal(at[40 + j], b.kn[r]) and torch.equal(q_out[r], b.q[r])
+    for call in (lambda: b.cache.attend(b.chunk, b.q, q_out),
+                 lambda: b.cache.compact(b.chunk, torch.zeros(B, dtype=torch.int32, device="cuda"), None,
+                                         torch.empty_like(b.cached))):
+        b.cache.status.zero_()
+        assert call() == 0
+        torch.cuda.synchronize()
+        assert b.cache.status_bits() == BAD_OFFSETS
