@@ -191,11 +191,15 @@ class PagedCache:
         self._at, self._status, self._ws = ctypes.addressof(self.struct), _ptr(self.status), _ptr(self.workspace)
         self._device = k.get_device()
 
-    def _chunk(self, chunk):
+    def _refuse(self, chunk, layer=0, rope=None):
+        """What is wrong with a call whose chunk, layer or rotation table is not for this cache. (The calls ask for that
+        in line: a function each would cost them half a microsecond.)"""
         if chunk.B > self.sequences:
             raise ValueError(f"page_table has {self.sequences} sequences, the chunk {chunk.B}")
         if chunk.device != self._device:
             raise ValueError(f"chunk must be on {self.k.device}, got device {chunk.device}")
+        _int32(layer, "layer")
+        raise ValueError(f"rope must be on {self.k.device}, got device {rope.device}")
 
     def _rows(self, t, name, rows, heads=None):
         """Rows of [heads, head_dim], contiguous within a row: the row stride. These checks and the launch are all
@@ -221,13 +225,13 @@ class PagedCache:
     def append(self, chunk: Chunk, q, k, v, q_out, rope: Rope | None = None, layer: int = 0, stream=None) -> int:
         """Enqueue spec_cache_append: rotated queries to q_out, rotated keys and values to the cache. q and
         q_out may be None."""
-        self._chunk(chunk)
+        if chunk.B > self.sequences or chunk.device != self._device or not -2 ** 31 <= layer < 2 ** 31 or (
+                rope is not None and rope.device != self._device):
+            self._refuse(chunk, layer, rope)
         rows, kind = chunk.rows, k.dtype
         code = _ACTIVATIONS.get(kind)
         if code is None or v.dtype != kind or (q is not None and (q.dtype != kind or q_out.dtype != kind)):
             self._type(*(t for t in (q, k, v, q_out) if t is not None))
-        if rope is not None and rope.device != self._device:
-            raise ValueError(f"rope must be on {self.k.device}, got device {rope.device}")
         ks = self._rows(k, "k", rows, self.heads)
         if self._rows(v, "v", rows, self.heads) != ks:
             raise ValueError("k and v must have equal row strides")
@@ -236,7 +240,7 @@ class PagedCache:
             qs, qh = self._rows(q, "q", rows), q.shape[1]
             if self._rows(q_out, "q_out", rows, qh) != qh * self.head_dim:
                 raise ValueError("q_out must be contiguous")
-        return lib.spec_cache_append(self._at, _int32(layer, "layer"), chunk.at, None if rope is None else rope.at, code,
+        return lib.spec_cache_append(self._at, layer, chunk.at, None if rope is None else rope.at, code,
                                      qh, _ptr(q), qs, k.data_ptr(), v.data_ptr(), ks, _ptr(q_out), self._status,
                                      self._stream(stream))
 
@@ -244,7 +248,8 @@ class PagedCache:
                stream=None) -> int:
         """Enqueue spec_cache_attend: attention of the chunk's rotated queries into out (and lse, float32
         [rows, q_heads]). scale: 1 / sqrt(head_dim) by default; window: 0 for none, as any past every length is."""
-        self._chunk(chunk)
+        if chunk.B > self.sequences or chunk.device != self._device or not -2 ** 31 <= layer < 2 ** 31:
+            self._refuse(chunk, layer)
         rows, kind = chunk.rows, q.dtype
         code = _ACTIVATIONS.get(kind)
         if code is None or out.dtype != kind:
@@ -258,22 +263,24 @@ class PagedCache:
                 raise ValueError("lse must be contiguous with a row for every chunk row")
         if scale is None:
             scale = self.head_dim ** -0.5
-        window = max(-2 ** 31, min(window, 2 ** 31 - 1))
-        return lib.spec_cache_attend(self._at, _int32(layer, "layer"), chunk.at, code, qh, q.data_ptr(), qs, scale, window,
+        if not -2 ** 31 <= window < 2 ** 31:
+            window = max(-2 ** 31, min(window, 2 ** 31 - 1))
+        return lib.spec_cache_attend(self._at, layer, chunk.at, code, qh, q.data_ptr(), qs, scale, window,
                                      out.data_ptr(), _ptr(lse), self._status, self._ws, self.ws_bytes,
                                      self._stream(stream))
 
     def compact(self, chunk: Chunk, out_num_accepted, out_path, out_cached, stream=None) -> int:
         """Enqueue spec_cache_compact on a verify call's outputs. out_path None: linear drafts. out_cached may
         be the chunk's `cached`."""
-        self._chunk(chunk)
+        if chunk.B > self.sequences or chunk.device != self._device:
+            self._refuse(chunk)
         _check(out_num_accepted, "out_num_accepted", (torch.int32,), (chunk.B,), self._device)
         _check(out_cached, "out_cached", (torch.int32,), (chunk.B,), self._device)
         if out_path is not None:
             _check(out_path, "out_path", (torch.int32,), (None,), self._device)
-        for t, name in ((out_num_accepted, "out_num_accepted"), (out_path, "out_path"), (out_cached, "out_cached")):
-            if t is not None and not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
+        if not (out_num_accepted.is_contiguous() and out_cached.is_contiguous() and
+                (out_path is None or out_path.is_contiguous())):
+            raise ValueError("out_num_accepted, out_path and out_cached must be contiguous")
         return lib.spec_cache_compact(self._at, chunk.at, out_num_accepted.data_ptr(), _ptr(out_path),
                                       out_cached.data_ptr(), self._status, self._stream(stream))
 
