@@ -142,8 +142,8 @@ int spec_cache_attend(const sv_cache* cache, int32_t layer, const sv_chunk* chun
  * After verification, in every layer: slot cached[b] + 1 + j gets the keys and values of slot
  * cached[b] + path[j], path[j] = out_path[seq_offsets[b] + j], for j < n_b = out_num_accepted[b] (as
  * spec_verify_tree wrote them: increasing nodes in 1 .. T_b - 1), and out_cached[b] = cached[b] + n_b + 1.
- * out_path NULL: linear drafts, nothing to move. A sequence with n_b < 0 (it failed verification) keeps its
- * cache and length. out_cached may be the chunk's own `cached` array (a second small launch then writes it).
+ * out_path NULL: linear drafts, any number of them (a prompt kept whole: n_b = T_b - 1), nothing to move. A
+ * sequence with n_b < 0 (it failed verification) keeps its cache and length. out_cached may be the chunk's own `cached` array (a second small launch then writes it).
  */
 int spec_cache_compact(const sv_cache* cache, const sv_chunk* chunk, const int32_t* out_num_accepted,
                        const int32_t* out_path, int32_t* out_cached, uint32_t* device_status, void* cuda_stream);

@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_compact(const __grid_constan
     bool moves = false;
     int32_t node = 0;
     if (!err && n >= 0) {
-        if (n >= s.T || n > SV_MAX_GAMMA) err = 1u << SV_ERR_BAD_OFFSETS;
+        if (n >= s.T || (A.path && n > SV_MAX_GAMMA)) err = 1u << SV_ERR_BAD_OFFSETS;
         else if (A.path) {
             if (lane < n) node = A.path[s.row0 - b + lane];
             const int32_t before = __shfl_up_sync(0xffffffffu, node, 1);
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_advance(const __grid_constan
     if (warp >= A.chunk.B) return;
     const Seq s = seq_of(A.chunk, capacity_of(A.pool), warp);
     const int32_t n = A.accepted[warp];
-    bool good = !s.err && n >= 0 && n < s.T && n <= SV_MAX_GAMMA;
+    bool good = !s.err && n >= 0 && n < s.T && (!A.path || n <= SV_MAX_GAMMA);
     if (good && A.path) {
         const int32_t node = lane < n ? A.path[s.row0 - warp + lane] : 0;
         const int32_t before = __shfl_up_sync(0xffffffffu, node, 1);

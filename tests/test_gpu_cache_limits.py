@@ -158,3 +158,17 @@ def test_append_reports_every_bad_sequence(sc, offs, max_gamma, rows, stored):
         assert call() == 0
         torch.cuda.synchronize()
         assert b.cache.status_bits() == BAD_OFFSETS
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_linear_compaction_of_long_chunks(sc, in_place):
+    """Linear drafts have no limit: a prompt's chunk is kept whole."""
+    chunks, past = [40, 300, 33, 32, 5], [10, 0, 30, 5, 6]
+    b = Batch(sc, chunks, past, 2, 2, 64, 8, poison=False)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k0 = b.k.clone()
+    now = b.cached if in_place else torch.zeros(5, **i32)
+    assert b.cache.compact(b.chunk, torch.tensor([39, 299, 33, 31, -1], **i32), None, now) == 0
+    torch.cuda.synchronize()
+    # the third accepts more than it drafted
+    assert now.tolist() == [50, 300, 30, 37, 6] and torch.equal(b.k, k0) and b.cache.status_bits() == BAD_OFFSETS
