@@ -21,8 +21,9 @@
  * calls are asynchronous on cuda_stream, allocate nothing, synchronise nothing, and can be captured into a
  * graph. Bad arguments return SV_ERR_INVALID_ARG (or SV_ERR_WORKSPACE) before anything is launched. Findings on
  * the device set bit (1u << code) of *device_status (nullable; the caller clears it):
- *   SV_ERR_BAD_OFFSETS  seq_offsets[0] != 0, T_b outside 1 .. max_gamma + 1, rows past `rows`, a parent
- *                       outside [0, j), a page id outside [0, pages), an accepted path that is none
+ *   SV_ERR_BAD_OFFSETS  seq_offsets[0] != 0, T_b outside 1 .. max_gamma + 1, rows past `rows`, parents or a path
+ *                       past seq_offsets[B], a parent outside [0, j), a page id outside [0, pages), an accepted
+ *                       path that is none
  *   SV_ERR_CAPACITY     cached[b] < 0, or slots cached[b] + T_b past the page table or the rotation table; or a
  *                       batch too long for one spec_cache_attend call (2^31 pieces of 128 slots, over all kv heads;
  *                       nothing is written then)

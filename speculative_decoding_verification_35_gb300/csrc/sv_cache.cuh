@@ -28,6 +28,7 @@ struct Chunk {
     const int32_t* offs;
     const int32_t* cached;
     const int32_t* parents;
+    const int32_t* end;  // the last offset, where an array of that many entries (parents, paths) is read; else nullptr
     int32_t B, rows, max_gamma;
 };
 
@@ -84,11 +85,13 @@ struct Seq {
 __device__ __forceinline__ Seq seq_of(const Chunk& c, int32_t capacity, int32_t b) {
     Seq s;
     const int64_t o0 = c.offs[b], o1 = c.offs[b + 1];
+    const int32_t end = c.end ? *c.end : 0x7fffffff;
     s.past = c.cached[b];
     s.row0 = (int32_t)(o0 + b);
     s.T = (int32_t)(o1 - o0 + 1);
     s.err = 0;
-    s.rows_ok = o0 >= 0 && o1 >= o0 && o1 - o0 <= c.max_gamma && o1 + b + 1 <= c.rows && (b > 0 || o0 == 0);
+    s.rows_ok = o0 >= 0 && o1 >= o0 && o1 - o0 <= c.max_gamma && o1 + b + 1 <= c.rows && o1 <= end &&
+                (b > 0 || o0 == 0);
     if (!s.rows_ok) s.err = 1u << SV_ERR_BAD_OFFSETS;
     else if (s.past < 0 || (int64_t)s.past + s.T > capacity) s.err = 1u << SV_ERR_CAPACITY;
     return s;

@@ -57,11 +57,13 @@ Pool pool_of(const sv_cache* c, int32_t layer) {
     return p;
 }
 
-Chunk chunk_of(const sv_chunk* c) {
+// path: the accepted path of spec_cache_compact, which reads no parents.
+Chunk chunk_of(const sv_chunk* c, const int32_t* path = nullptr) {
     Chunk r{};
     r.offs = c->seq_offsets;
     r.cached = c->cached;
     r.parents = c->max_gamma > 0 ? c->parents : nullptr;
+    r.end = r.parents || path ? c->seq_offsets + c->B : nullptr;
     r.B = c->B;
     r.rows = c->rows;
     r.max_gamma = std::min(c->max_gamma, std::max(c->rows, 1) - 1);  // as many as there can be
@@ -149,7 +151,7 @@ int spec_cache_compact(const sv_cache* cache, const sv_chunk* chunk, const int32
     if (!aligned(out_num_accepted, 4) || !aligned(out_cached, 4)) return SV_ERR_INVALID_ARG;
     CompactArgs A{};
     A.pool = pool_of(cache, 0);
-    A.chunk = chunk_of(chunk);
+    A.chunk = chunk_of(chunk, out_path);
     A.accepted = out_num_accepted;
     A.path = out_path;
     A.now = out_cached;

@@ -172,3 +172,37 @@ def test_linear_compaction_of_long_chunks(sc, in_place):
     torch.cuda.synchronize()
     # the third accepts more than it drafted
     assert now.tolist() == [50, 300, 30, 37, 6] and torch.equal(b.k, k0) and b.cache.status_bits() == BAD_OFFSETS
+
+
+def test_offsets_past_the_last_one(sc):
+    """Parents and paths end with the last sequence's: one that claims more, though its rows are there, fails."""
+    offs = [0, 3, 20, 8]
+    b = Batch(sc, [4, 4, 4], [20, 20, 20], 4, 2, 64, 8, poison=False)
+    for name in ("q", "kn", "vn"):
+        setattr(b, name, torch.randn((40, getattr(b, name).shape[1], 64), device="cuda").bfloat16())
+    b.table = torch.arange(24, dtype=torch.int32, device="cuda").view(3, 8)
+    b.k = torch.randn((1, 24, 8, 2, 64), device="cuda").bfloat16()
+    b.v = b.k.clone()
+    b.offs = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    b.parents = torch.zeros(64, dtype=torch.int32, device="cuda")  # more room than a batch's 8, so that any read is in it
+    b.make(31)
+    b.chunk.struct.rows = b.chunk.rows = 40
+    k0 = b.k.clone()
+    q_out = torch.full((40, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert b.cache.append(b.chunk, b.q, b.kn, b.vn, q_out) == 0
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == BAD_OFFSETS
+    diff = (b.k != k0)[0].flatten(2).any(2).nonzero().tolist()
+    assert diff == [[s // 8, s % 8] for s in range(20, 24)] and (q_out[4:] == 7).all()
+    out = torch.full_like(q_out, 7.0)
+    b.cache.status.zero_()
+    assert b.cache.attend(b.chunk, b.q, out) == 0
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == BAD_OFFSETS and (out[4:] == 7).all() and torch.isfinite(out[:4]).all()
+    k1, now = b.k.clone(), torch.zeros(3, dtype=torch.int32, device="cuda")
+    path = torch.tensor([3] + [-1] * 2 + [5] + [-1] * 60, dtype=torch.int32, device="cuda")
+    b.cache.status.zero_()
+    assert b.cache.compact(b.chunk, torch.tensor([1, 1, 0], dtype=torch.int32, device="cuda"), path, now) == 0
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == BAD_OFFSETS and now.tolist() == [22, 20, 20]
+    assert (b.k != k1)[0].flatten(2).any(2).nonzero().tolist() == [[2, 5]]
