@@ -24,7 +24,7 @@
  *   SV_ERR_BAD_OFFSETS  seq_offsets[0] != 0, T_b outside 1 .. max_gamma + 1, rows past `rows`, parents or a path
  *                       past seq_offsets[B], a parent outside [0, j), a page id outside [0, pages), an accepted
  *                       path that is none
- *   SV_ERR_CAPACITY     cached[b] < 0, or slots cached[b] + T_b past the page table or the rotation table; or a
+ *   SV_ERR_CAPACITY     cached[b] < 0, or slots cached[b] + T_b past the page table, the rotation table or 2^31 - 128; or a
  *                       batch too long for one spec_cache_attend call (2^31 pieces of 128 slots, over all kv heads;
  *                       nothing is written then)
  *   SV_ERR_TIMEOUT      a bounded wait inside the launch gave up (the outputs are then undefined)

@@ -97,9 +97,11 @@ __device__ __forceinline__ Seq seq_of(const Chunk& c, int32_t capacity, int32_t 
     return s;
 }
 
+// Slots a sequence may have. At most 2^31 - 128, so that the end of a tile of 128 slots is an int32 too: a table may name
+// a page many times, and so be that long on any pool.
 __device__ __forceinline__ int32_t capacity_of(const Pool& p) {
     const int64_t n = (int64_t)p.table_stride * p.page_size;
-    return n > 0x7fffffff ? 0x7fffffff : (int32_t)n;
+    return n > 0x7fffff80 ? 0x7fffff80 : (int32_t)n;
 }
 
 // The sequence of a row, by a whole warp: the last b with offs[b] + b <= row, 32 candidates a step. -1: the

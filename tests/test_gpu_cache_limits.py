@@ -206,3 +206,33 @@ def test_offsets_past_the_last_one(sc):
     torch.cuda.synchronize()
     assert b.cache.status_bits() == BAD_OFFSETS and now.tolist() == [22, 20, 20]
     assert (b.k != k1)[0].flatten(2).any(2).nonzero().tolist() == [[2, 5]]
+
+
+def test_lengths_next_to_32_bits(sc):
+    """A sequence's slots end 128 below 2^31, so that a tile's last one is an int32: past that it is out of capacity,
+    whatever the page table would hold."""
+    b = Batch(sc, [2, 2], [20, 20], 4, 2, 64, 8, poison=False)
+    k = torch.randn((1, 1, 65536, 2, 64), device="cuda").bfloat16()
+    b.k, b.v = k, k.clone()
+    b.table = torch.zeros((2, 32769), dtype=torch.int32, device="cuda")  # one page again and again
+    b.cached.copy_(torch.tensor([2 ** 31 - 129, 40]))
+    b.make()
+    k0 = b.k.clone()
+    q_out = torch.full((4, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert b.cache.append(b.chunk, b.q, b.kn, b.vn, q_out) == 0
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == CAPACITY and (q_out[:2] == 7).all()
+    assert (b.k != k0)[0].flatten(2).any(2).nonzero().tolist() == [[0, 40], [0, 41]]
+    b.cache.status.zero_()
+    lse = torch.zeros((4, 4), device="cuda")
+    assert b.cache.attend(b.chunk, b.q, q_out, lse) == 0
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == CAPACITY
+    assert not q_out[:2].any() and (lse[:2] == -float("inf")).all() and torch.isfinite(lse[2:]).all()
+    # the last slots that there are
+    b.cached[0] = 2 ** 31 - 130
+    b.cache.status.zero_()
+    assert b.cache.append(b.chunk, b.q, b.kn, b.vn, q_out) == 0
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == 0
+    assert torch.equal(b.k[0, 0, 65536 - 130], b.kn[0]) and torch.equal(b.k[0, 0, 65536 - 129], b.kn[1])
