@@ -113,7 +113,7 @@ typedef struct {
  * and may be q itself when q_stride is q_heads * head_dim. All 16-byte aligned, strides multiples of 8.
  */
 int spec_cache_append(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, const sv_rope* rope,
-                      sv_dtype dtype, int32_t q_heads, const void* q, int64_t q_stride, const void* k, const void* v,
+                      int32_t dtype, int32_t q_heads, const void* q, int64_t q_stride, const void* k, const void* v,
                       int64_t kv_stride, void* q_out, uint32_t* device_status, void* cuda_stream);
 
 /* Bytes of workspace spec_cache_attend needs on this cache (0 for an invalid one). */
@@ -135,7 +135,7 @@ size_t spec_cache_workspace_size(const sv_cache* cache);
  * written. workspace: spec_cache_workspace_size(cache) bytes aligned to 256, not shared by calls that may
  * overlap on the GPU; its contents need no preparation.
  */
-int spec_cache_attend(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, sv_dtype dtype, int32_t q_heads,
+int spec_cache_attend(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, int32_t dtype, int32_t q_heads,
                       const void* q, int64_t q_stride, float scale, int32_t window, void* out, float* lse,
                       uint32_t* device_status, void* workspace, size_t workspace_bytes, void* cuda_stream);
 

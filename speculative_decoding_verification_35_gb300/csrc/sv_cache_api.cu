@@ -77,7 +77,7 @@ int result(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
 extern "C" {
 
 int spec_cache_append(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, const sv_rope* rope,
-                      sv_dtype dtype, int32_t q_heads, const void* q, int64_t q_stride, const void* k, const void* v,
+                      int32_t dtype, int32_t q_heads, const void* q, int64_t q_stride, const void* k, const void* v,
                       int64_t kv_stride, void* q_out, uint32_t* device_status, void* cuda_stream) {
     if (!valid(cache) || !valid(chunk) || layer < 0 || layer >= cache->layers) return SV_ERR_INVALID_ARG;
     if (!valid_types(dtype, cache->dtype) || cache->head_dim % 8) return SV_ERR_INVALID_ARG;
@@ -115,7 +115,7 @@ size_t spec_cache_workspace_size(const sv_cache* cache) {
     return valid(cache) ? attend_workspace(cache->head_dim, cache->dtype) : 0;
 }
 
-int spec_cache_attend(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, sv_dtype dtype, int32_t q_heads,
+int spec_cache_attend(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, int32_t dtype, int32_t q_heads,
                       const void* q, int64_t q_stride, float scale, int32_t window, void* out, float* lse,
                       uint32_t* device_status, void* workspace, size_t workspace_bytes, void* cuda_stream) {
     if (!valid(cache) || !valid(chunk) || layer < 0 || layer >= cache->layers) return SV_ERR_INVALID_ARG;
