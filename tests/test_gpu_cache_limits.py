@@ -236,3 +236,54 @@ def test_lengths_next_to_32_bits(sc):
     torch.cuda.synchronize()
     assert b.cache.status_bits() == 0
     assert torch.equal(b.k[0, 0, 65536 - 130], b.kn[0]) and torch.equal(b.k[0, 0, 65536 - 129], b.kn[1])
+
+
+@pytest.mark.parametrize("kind,cache", [("bf16", "bf16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("wrong", [-1, 10 ** 6])
+def test_append_on_a_bad_and_a_good_page(sc, kind, cache, wrong):
+    """Tokens on a bad page are not stored; the chunk's others are, and every query is rotated."""
+    b = Batch(sc, [6, 3], [13, 4], 4, 2, 64, 8, kind, cache, poison=False, layers=2, layer=1)
+    good = [int(p) for p in b.table_h[0]]
+    b.table[0, 1] = wrong  # slots 8 to 15; the chunk has 13 to 18
+    tab = torch.randn((40, 64), device="cuda")
+    rope = sc.Rope(tab)
+    want = torch.empty((9, 4, 64), dtype=torch.bfloat16, device="cuda")
+    q_out = torch.full_like(want, 7.0)
+    k0, v0 = b.k.float().clone(), b.v.float().clone()
+    assert b.cache.append(b.chunk, b.q, b.kn, b.vn, q_out, rope, layer=1) == 0
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == BAD_OFFSETS
+    slots = sorted([good[s // 8], s % 8] for s in range(16, 19))
+    slots = sorted(slots + [[int(b.table_h[1][s // 8]), s % 8] for s in range(4, 7)])
+    for x, x0 in ((b.k, k0), (b.v, v0)):
+        assert torch.equal(x[0].float(), x0[0])
+        assert sorted((x.float() != x0)[1].flatten(2).any(2).nonzero().tolist()) == slots
+    # as on a table without the bad page
+    k1, v1 = b.k.float().clone(), b.v.float().clone()
+    b.table.copy_(torch.tensor(b.table_h))
+    b.cache.status.zero_()
+    assert b.cache.append(b.chunk, b.q, b.kn, b.vn, want, rope, layer=1) == 0
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == 0 and torch.equal(q_out, want)
+    for x, x1 in ((b.k, k1), (b.v, v1)):
+        diff = (x.float() != x1)[1].flatten(2).any(2).nonzero().tolist()
+        assert sorted(diff) == sorted([good[1], s % 8] for s in range(13, 16))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compact_findings_in_place(sc, in_place):
+    """Paths that are none keep their sequence's length and cache, also where the lengths are written over."""
+    chunks, past = [4, 4, 4, 4, 4], [10, 20, 30, 5, 6]
+    b = Batch(sc, chunks, past, 2, 2, 64, 8, poison=False)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k0 = b.k.clone()
+    b.table[3, 0] = -1
+    # a path that does not increase, a node past the chunk, more accepted than drafted, a bad page, a good one
+    path = torch.tensor([2, 1, -1, 4, -1, -1, 1, 2, 3, 2, 3, -1, 3, -1, -1], **i32)
+    now = b.cached if in_place else torch.zeros(5, **i32)
+    assert b.cache.compact(b.chunk, torch.tensor([2, 1, 4, 2, 1], **i32), path, now) == 0
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == BAD_OFFSETS
+    assert now.tolist() == [10, 20, 30, 8, 8]
+    diff = (b.k != k0)[0].flatten(2).any(2).nonzero().tolist()
+    assert diff == [[int(b.table_h[4][0]), 7]]
