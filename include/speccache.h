@@ -140,6 +140,17 @@ int spec_cache_attend(const sv_cache* cache, int32_t layer, const sv_chunk* chun
                       uint32_t* device_status, void* workspace, size_t workspace_bytes, void* cuda_stream);
 
 /*
+ * spec_cache_attend with the verify step's debug structure (NULL: none), of which spin_limit alone is read: polls after
+ * which a wait between the launch's warps gives up, 0 for the library's bound. A small value exists to exercise the
+ * time-out path in tests: the launch ends once its copies and products under way have, SV_ERR_TIMEOUT is set, and the
+ * outputs are undefined.
+ */
+int spec_cache_attend_ex(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, int32_t dtype, int32_t q_heads,
+                         const void* q, int64_t q_stride, float scale, int32_t window, void* out, float* lse,
+                         uint32_t* device_status, void* workspace, size_t workspace_bytes, const sv_debug* debug,
+                         void* cuda_stream);
+
+/*
  * After verification, in every layer: slot cached[b] + 1 + j gets the keys and values of slot
  * cached[b] + path[j], path[j] = out_path[seq_offsets[b] + j], for j < n_b = out_num_accepted[b] (as
  * spec_verify_tree wrote them: increasing nodes in 1 .. T_b - 1), and out_cached[b] = cached[b] + n_b + 1.

@@ -58,6 +58,7 @@ struct AttendArgs {
     float* lse;
     uint32_t* status;
     void* workspace;
+    uint32_t spin_limit;  // polls of a wait, 0: the kernels' own bound
 };
 
 struct CompactArgs {

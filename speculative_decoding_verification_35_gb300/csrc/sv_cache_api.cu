@@ -118,6 +118,14 @@ size_t spec_cache_workspace_size(const sv_cache* cache) {
 int spec_cache_attend(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, int32_t dtype, int32_t q_heads,
                       const void* q, int64_t q_stride, float scale, int32_t window, void* out, float* lse,
                       uint32_t* device_status, void* workspace, size_t workspace_bytes, void* cuda_stream) {
+    return spec_cache_attend_ex(cache, layer, chunk, dtype, q_heads, q, q_stride, scale, window, out, lse, device_status,
+                                workspace, workspace_bytes, nullptr, cuda_stream);
+}
+
+int spec_cache_attend_ex(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, int32_t dtype, int32_t q_heads,
+                         const void* q, int64_t q_stride, float scale, int32_t window, void* out, float* lse,
+                         uint32_t* device_status, void* workspace, size_t workspace_bytes, const sv_debug* debug,
+                         void* cuda_stream) {
     if (!valid(cache) || !valid(chunk) || layer < 0 || layer >= cache->layers) return SV_ERR_INVALID_ARG;
     if (!valid_types(dtype, cache->dtype)) return SV_ERR_INVALID_ARG;
     if (q_heads < 1 || q_heads % cache->heads || q_heads / cache->heads > 128) return SV_ERR_INVALID_ARG;
@@ -139,6 +147,7 @@ int spec_cache_attend(const sv_cache* cache, int32_t layer, const sv_chunk* chun
     A.lse = lse;
     A.status = device_status;
     A.workspace = workspace;
+    A.spin_limit = debug ? debug->spin_limit : 0;
     return result(launch_attend(A, dtype, cache->dtype, (cudaStream_t)cuda_stream));
 }
 

@@ -250,12 +250,12 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
                    pv_done = smem_u32(&sh.pv_done[stream]);
     const int32_t D = A.pool.dim;
     const bool tree = A.chunk.parents != nullptr;
-    volatile int* gave_up = &sh.gave_up;
+    const Limit limit{&sh.gave_up, P.polls};
     const int32_t tl = r / P.G, g = r - tl * P.G;
     uint32_t steps = 0;   // of this stream, over all items
     uint32_t tiles = 0;   // of the CTA, before this item
 
-    Items walk(sh);
+    Items walk(P, sh);
     Item it;
 #pragma unroll 1
     while (walk.next(it)) {
@@ -270,7 +270,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
             const uint32_t ring = (tiles + j) % kNotes;
             const bool whole = __all_sync(kAll, (k0 + kTile <= row.limit && row.low <= k0) || !row.real);
             const bool mixed = mixed_tile(it, k0);
-            if (!wait(s_full, steps & 1, gave_up)) return;
+            if (!wait(s_full, steps & 1, limit)) return;
             tc_after();
             if (K == kE4m3 && j == 0) row.sl = row_unit(row.sl, sh.q_down[walk.ring.i * sh.q_rows + stream * kTile + r]);
             uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
@@ -294,7 +294,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
                             const float f = !move || old == -INFINITY ? 1.f : exp2_fast((old - m) * row.sl);
                             l *= f;
                             if (__any_sync(kAll, move && old != -INFINITY)) {
-                                if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
+                                if (!wait(pv_done, (steps - 1) & 1, limit)) return;
                                 tc_after();
                                 rescale<DP>(o_col, f);
                             }
@@ -307,7 +307,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
             }
             if (rarely(mixed)) {  // before p_ready: the tile cannot be released, nor its barrier move on, until then
                 const uint32_t v = tiles + j;
-                if (!wait(smem_u32(&sh.value[v % P.v_slots]), (v / P.v_slots) & 1, gave_up)) return;
+                if (!wait(smem_u32(&sh.value[v % P.v_slots]), (v / P.v_slots) & 1, limit)) return;
             }
             tc_before();
             __syncwarp();
@@ -319,7 +319,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) any |= odd[i] = sh.odd[ring][i];
                 if (rarely(any && busy)) {
-                    if (!wait(pv_done, steps & 1, gave_up)) return;
+                    if (!wait(pv_done, steps & 1, limit)) return;
                     tc_after();
                     add_odd<K, DP>(A, it, o_col, k0, row.real ? odd : none, seen);
                     tc_wait_st();
@@ -330,7 +330,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
         tiles += it.n;
 
         // the item's end
-        if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
+        if (!wait(pv_done, (steps - 1) & 1, limit)) return;
         tc_after();
         const float ref = m == -INFINITY ? -INFINITY : m * row.sl - KT::kShift;
         const bool alone = it.begins && it.finishes;
@@ -419,16 +419,16 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
                    value = smem_u32(sh.value), s_full = smem_u32(&sh.s_full[st]), p_ready = smem_u32(&sh.p_ready[st]),
                    pv_done = smem_u32(&sh.pv_done[st]), q_empty = smem_u32(sh.q_empty), q_full = smem_u32(sh.q_full);
     const bool leader = elect();
-    volatile int* gave_up = &sh.gave_up;
+    const Limit limit{&sh.gave_up, P.polls};
     const uint32_t turn[2] = {smem_u32(&sh.turn[st]), smem_u32(&sh.turn[st ^ 1])};
     uint32_t p_parity = 0, turns = 0;
     Ring kr, vr, qr;
-    Items walk(sh);
+    Items walk(P, sh);
     Item it;
     bool ok = true;
 #pragma unroll 1
     while (ok && walk.next(it)) {
-        if (!(ok = wait(q_full + 8 * qr.i, qr.parity, gave_up))) break;
+        if (!(ok = wait(q_full + 8 * qr.i, qr.parity, limit))) break;
         tc_after();
         // the same in every lane; taken from one, so that the operands below live in uniform registers
         const int32_t n = __shfl_sync(kAll, it.n, 0);
@@ -436,13 +436,13 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
 #pragma unroll 1
         for (int32_t t = -1; t < n; ++t) {  // outputs of tile t, scores of the next
             const bool more = t + 1 < n;
-            if (t >= 0 && !(ok = wait(value + 8 * vr.i, vr.parity, gave_up))) break;
-            if (more && !(ok = wait(k_full + 8 * kr.i, kr.parity, gave_up))) break;
+            if (t >= 0 && !(ok = wait(value + 8 * vr.i, vr.parity, limit))) break;
+            if (more && !(ok = wait(k_full + 8 * kr.i, kr.parity, limit))) break;
             if (t >= 0) {
-                if (!(ok = wait(p_ready, p_parity, gave_up))) break;
+                if (!(ok = wait(p_ready, p_parity, limit))) break;
                 p_parity ^= 1u;
             }
-            if (!(ok = wait(turn[0], turns, gave_up))) break;
+            if (!(ok = wait(turn[0], turns, limit))) break;
             turns ^= 1u;
             tc_after();
             if (t >= 0) {
@@ -489,8 +489,7 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
     // products under way end before the tensor memory is given back
     if (leader) tc_commit(smem_u32(&sh.drain));
     __syncwarp();
-    int none = 0;
-    wait(smem_u32(&sh.drain), 0, &none);
+    drain(smem_u32(&sh.drain), 0);
 }
 
 template <int K, int DP>
@@ -746,6 +745,7 @@ cudaError_t launch_attend(const AttendArgs& A, int dtype, int cache_dtype, cudaS
     const int dp = part_dim(A.pool.dim, kind);
     Params P{};
     P.a = A;
+    P.polls = A.spin_limit ? A.spin_limit : kPolls;
     P.G = A.q_heads / A.pool.heads;
     P.box = kTile;
     while (A.pool.page_size % P.box) P.box /= 2;

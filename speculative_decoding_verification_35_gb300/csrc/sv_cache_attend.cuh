@@ -85,6 +85,7 @@ struct Params {
     int32_t ctas;       // of the launch
     int32_t part_rows;  // rows of a partial result
     int32_t lead;       // what an item's beginning and end cost, in tiles
+    uint32_t polls;     // of a wait, before it gives up
     float* part_o;      // [2 n][part_rows][64 or 128]
     float2* part_ml;    // [2 n][part_rows]
     Record* records;    // [n]
@@ -103,25 +104,35 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// True once the phase is over; may sleep for it, half a microsecond at most.
+// True once the phase is over; sleeps for it, 4 us at most (measured, with and without a hint of another time).
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "n"(500)
-        : "memory");
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
     return ok;
 }
-// A whole warp waits, a tenth of a second at least and a few seconds at most; false, and the CTA gives up, if that was
-// not enough. (Short, as it stands in some thirty places.)
-constexpr uint32_t kPolls = 1u << 22;
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+// A whole warp waits, a second at most; false, and the CTA gives up, if that was not enough. (Short, as it stands in some
+// thirty places: the limit is read only where the first look was in vain.)
+constexpr uint32_t kPolls = 1u << 18;
+struct Limit {
+    volatile int* gave_up;
+    uint32_t polls;  // kPolls, but for tests
+};
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Limit limit) {
+    uint32_t i = 0;
 #pragma unroll 1
-    for (uint32_t i = 0; i < kPolls; ++i)
+    do
         if (__all_sync(kAll, bar_try(bar, parity))) return true;
-    *gave_up = 1;
+    while (++i < limit.polls);
+    *limit.gave_up = 1;
     return false;
+}
+// What is under way in any case, copies and products, before the CTA ends: nothing is left to give up.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+    int none;
+    wait(bar, parity, Limit{&none, kPolls});
 }
 // Whether the phase is over, for a whole warp.
 __device__ __forceinline__ bool ready(uint32_t bar, uint32_t parity) {
@@ -527,16 +538,17 @@ __device__ __forceinline__ void plan(const Params& P, Common& sh) {
 // A role's view of the items. An item (and its tree) stays until the role asks for the next one.
 struct Items {
     Common& sh;
+    const uint32_t polls;
     Ring ring;
     bool held = false;
-    __device__ __forceinline__ Items(Common& s) : sh(s) {}
+    __device__ __forceinline__ Items(const Params& P, Common& s) : sh(s), polls(P.polls) {}
     __device__ __forceinline__ bool next(Item& it) {
         if (held) {
             __syncwarp();
             if ((threadIdx.x & 31) == 0) bar_arrive(smem_u32(&sh.item_empty[ring.i]));
             ring.step(kItems);
         }
-        if (!wait(smem_u32(&sh.item_full[ring.i]), ring.parity, &sh.gave_up)) return false;
+        if (!wait(smem_u32(&sh.item_full[ring.i]), ring.parity, Limit{&sh.gave_up, polls})) return false;
         it = sh.item[ring.i];
         held = true;
         return it.n > 0;
@@ -572,11 +584,11 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
     const int lane = threadIdx.x & 31;
     const int32_t box = P.box, boxes = P.boxes, ps = P.a.pool.page_size;
     const bool leader = elect();
-    volatile int* gave_up = &sh.gave_up;
+    const Limit limit{&sh.gave_up, P.polls};
     uint32_t tile = 0, issued[2] = {0, 0};
     Ring rings[2];
     bool ok = true;
-    Items walk(sh);
+    Items walk(P, sh);
     Item it;
 #pragma unroll 1
     while (ok && walk.next(it)) {
@@ -618,7 +630,7 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
                 if (kv) r = rings[1];
                 const uint32_t slots = kv ? P.v_slots : P.k_slots, full = smem_u32(kv ? sh.v_full : sh.k_full) + 8 * r.i,
                                empty = smem_u32(kv ? sh.v_empty : sh.k_empty) + 8 * r.i;
-                if (tile >= slots && !(ok = wait(empty, r.parity ^ 1, gave_up))) break;
+                if (tile >= slots && !(ok = wait(empty, r.parity ^ 1, limit))) break;
                 if (lane == 0) {
                     sh.bad[kv][tile % kNotes] = bad;
                     bar_expect(full, bytes);
@@ -651,10 +663,8 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
     for (int kv = first; kv <= last; ++kv) {
         const uint32_t slots = kv ? P.v_slots : P.k_slots, n = kv ? issued[1] : issued[0];
 #pragma unroll 1
-        for (uint32_t i = 0; i < slots && i < n; ++i) {
-            int none = 0;
-            wait(smem_u32(kv ? &sh.v_full[i] : &sh.k_full[i]), (n - 1 - i) / slots & 1, &none);
-        }
+        for (uint32_t i = 0; i < slots && i < n; ++i)
+            drain(smem_u32(kv ? &sh.v_full[i] : &sh.k_full[i]), (n - 1 - i) / slots & 1);
     }
 }
 
@@ -676,7 +686,7 @@ __device__ __forceinline__ bool copy_item_queries(const Params& P, Common& sh, c
     }
     __syncwarp();
     if (!rarely(flip)) return true;
-    if (!wait(bar, items & 1, &sh.gave_up)) return false;
+    if (!wait(bar, items & 1, Limit{&sh.gave_up, P.polls})) return false;
 #pragma unroll 1
     for (int i = lane; i < q_tiles * P.q_tile / 16; i += 32) {
         uint32_t u[4];
@@ -767,11 +777,11 @@ __device__ __forceinline__ void split_queries(const Params& P, Common& sh, const
 // Queries of e4m3 caches by warps of their own.
 __device__ __forceinline__ void query_role(const Params& P, Common& sh, uint32_t q_smem, int who, int of) {
     Ring qr;
-    Items walk(sh);
+    Items walk(P, sh);
     Item it;
 #pragma unroll 1
     for (uint32_t i = 0; walk.next(it); ++i, qr.step(P.q_bufs)) {
-        if (i >= (uint32_t)P.q_bufs && !wait(smem_u32(&sh.q_empty[qr.i]), qr.parity ^ 1, &sh.gave_up)) return;
+        if (i >= (uint32_t)P.q_bufs && !wait(smem_u32(&sh.q_empty[qr.i]), qr.parity ^ 1, Limit{&sh.gave_up, P.polls})) return;
         split_queries(P, sh, it, q_smem + qr.i * P.q_bytes, walk.ring.i, smem_u32(&sh.q_full[qr.i]), who, of);
     }
 }
@@ -852,6 +862,7 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
     const int lane = threadIdx.x & 31;
     const bool tree = P.a.chunk.parents != nullptr;
     const int32_t lead = sh.start.lead;
+    const Limit limit{&sh.gave_up, P.polls};
     int32_t b = sh.start.b, p = sh.start.p, h = sh.start.h, x = sh.start.x, left = sh.start.left;
     int32_t T = sh.start.T, past = sh.start.past, row0 = sh.start.row0;
     Ring ring;
@@ -904,7 +915,7 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
             left -= it.n;
             x = 0;
         }
-        if (i >= kItems && !wait(smem_u32(&sh.item_empty[ring.i]), ring.parity ^ 1, &sh.gave_up)) break;
+        if (i >= kItems && !wait(smem_u32(&sh.item_empty[ring.i]), ring.parity ^ 1, limit)) break;
         if (tree) {
             sh.tree[ring.i].above[lane] = above;
             sh.tree[ring.i].depth[lane] = depth;
@@ -925,7 +936,7 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
         }
         __syncwarp();
         if (it.n == 0) break;
-        if (i >= (uint32_t)P.q_bufs && !wait(smem_u32(&sh.q_empty[qr.i]), qr.parity ^ 1, &sh.gave_up)) break;
+        if (i >= (uint32_t)P.q_bufs && !wait(smem_u32(&sh.q_empty[qr.i]), qr.parity ^ 1, limit)) break;
         ++loads;
         const uint32_t at = q_smem + qr.i * P.q_bytes, q_full = smem_u32(&sh.q_full[qr.i]);
         if (K == kE4m3) split_queries(P, sh, it, at, ring.i, q_full, kSplitters - 1, kSplitters);
@@ -934,14 +945,13 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
     }
     if (lane == 0) record(P, sh);
     if (K != kE4m3 && loads > 0) {  // its copies land before the CTA ends, whoever gave up
-        int none = 0;
         bool flip;
         score_unit(P.a, 0, flip);
-        if (flip) wait(smem_u32(&sh.q_in), (loads - 1) & 1, &none);
+        if (flip) drain(smem_u32(&sh.q_in), (loads - 1) & 1);
         else
 #pragma unroll 1
             for (uint32_t k = loads > (uint32_t)P.q_bufs ? loads - P.q_bufs : 0; k < loads; ++k)
-                wait(smem_u32(&sh.q_full[k % P.q_bufs]), k / P.q_bufs & 1, &none);
+                drain(smem_u32(&sh.q_full[k % P.q_bufs]), k / P.q_bufs & 1);
     }
 }
 
@@ -951,16 +961,16 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
 template <int K>
 __device__ __forceinline__ void value_role(const Params& P, Common& sh, uint32_t v_smem) {
     const int lane = threadIdx.x & 31;
-    volatile int* gave_up = &sh.gave_up;
+    const Limit limit{&sh.gave_up, P.polls};
     uint32_t v = 0;
     Ring ring;
-    Items walk(sh);
+    Items walk(P, sh);
     Item it;
 #pragma unroll 1
     while (walk.next(it)) {
 #pragma unroll 1
         for (int32_t j = 0; j < it.n; ++j, ++v, ring.step(P.v_slots)) {
-            if (!wait(smem_u32(&sh.v_full[ring.i]), ring.parity, gave_up)) return;
+            if (!wait(smem_u32(&sh.v_full[ring.i]), ring.parity, limit)) return;
             const int32_t k0 = (it.tile + j) * kTile;
             const uint32_t bad = sh.bad[1][v % kNotes];
             const bool mixed = mixed_tile(it, k0);

@@ -87,13 +87,13 @@ struct alignas(16) Shared : Common {
 // A barrier of a group's warps; what lies between the two calls needs no one.
 struct Vote {
     uint32_t bar, parity;
-    volatile int* gave_up;
+    Limit limit;
     __device__ __forceinline__ void arrive() {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) bar_arrive(bar);
     }
     __device__ __forceinline__ bool pass() {
-        const bool ok = wait(bar, parity, gave_up);
+        const bool ok = wait(bar, parity, limit);
         parity ^= 1u;
         return ok;
     }
@@ -170,11 +170,11 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
     static_assert(sizeof(Notes<N>) <= Wt::kBytes, "the notes fit");
     constexpr int kParts = K == kE4m3 ? 2 : 1;
     const int32_t D = A.pool.dim;
-    volatile int* gave_up = &sh.gave_up;
-    Vote vote{smem_u32(&mine.vote), 0, gave_up};
+    const Limit limit{&sh.gave_up, P.polls};
+    Vote vote{smem_u32(&mine.vote), 0, limit};
     uint32_t steps = 0, tiles = 0, votes = 0;  // votes: on weights, modulo 3
     bool owed = false;  // a vote of the last item's end has been given and not passed: others may still read the notes
-    Items walk(sh);
+    Items walk(P, sh);
     Item it;
 #pragma unroll 1
     while (walk.next(it)) {
@@ -200,7 +200,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
 #pragma unroll 1
         for (int32_t j = 0; j < it.n; ++j, ++steps) {
             const uint32_t buf = steps & 1;
-            if (!wait(smem_u32(&sh.s_full[buf]), steps >> 1 & 1, gave_up)) return;
+            if (!wait(smem_u32(&sh.s_full[buf]), steps >> 1 & 1, limit)) return;
             tc_after();
             if (K == kE4m3 && j == 0)
 #pragma unroll
@@ -257,7 +257,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                     if (owed && !vote.pass()) return;
                     owed = false;
                     if (j > 0) {  // O is whole, and the notes' place free, once the last step's product has been
-                        if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
+                        if (!wait(pv_done, (steps - 1) & 1, limit)) return;
                         tc_after();
                     }
                     // the rows' maxima, by warp, then of all
@@ -345,7 +345,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                 }
             }
             // the weights' place is free once the last step's product has been
-            if (j > 0 && !wait(pv_done, (steps - 1) & 1, gave_up)) return;
+            if (j > 0 && !wait(pv_done, (steps - 1) & 1, limit)) return;
             constexpr int kWide = N * KT::kBytes / 16;  // 16 bytes of a part
 #pragma unroll
             for (int part = 0; part < kParts; ++part)
@@ -361,7 +361,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
             const bool mixed = mixed_tile(it, k0);
             if (rarely(mixed)) {  // before p_ready: the tile cannot be released, nor its barrier move on, until then
                 const uint32_t v = tiles + j;
-                if (!wait(smem_u32(&sh.value[v % P.v_slots]), (v / P.v_slots) & 1, gave_up)) return;
+                if (!wait(smem_u32(&sh.value[v % P.v_slots]), (v / P.v_slots) & 1, limit)) return;
             }
             fence_async();
             tc_before();
@@ -373,7 +373,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
 #pragma unroll
                 for (int i = 0; i < 4; ++i) any |= sh.odd[ring][i];
                 if (rarely(any)) {
-                    if (!wait(pv_done, steps & 1, gave_up)) return;
+                    if (!wait(pv_done, steps & 1, limit)) return;
                     tc_after();
 #pragma unroll 1
                     for (int i = 0; i < 4; ++i)
@@ -424,7 +424,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
 #pragma unroll
             for (int o = 4; o; o >>= 1) sum[q] += __shfl_xor_sync(kAll, sum[q], o);
         }
-        if (!wait(pv_done, (steps - 1) & 1, gave_up)) return;
+        if (!wait(pv_done, (steps - 1) & 1, limit)) return;
         tc_after();
         if (!(lane & 7))
 #pragma unroll
@@ -502,12 +502,12 @@ __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh,
                    pv_done = smem_u32(&sh.pv_done), q_full = smem_u32(sh.q_full), q_empty = smem_u32(sh.q_empty);
     const uint32_t q_part = (uint32_t)P.q_part >> 4, p = operand(p_smem, 16);
     const bool leader = elect();
-    volatile int* gave_up = &sh.gave_up;
+    const Limit limit{&sh.gave_up, P.polls};
     uint32_t ahead = 0, scores = 0, outputs = 0, polls = 0;
     uint32_t notes = 0;  // 16 bits a buffer: the first and last step of the outputs' depth, an item's first tile
     int32_t j = 0, n = 0;
     Ring kr, vr, qr;
-    Items walk(sh);
+    Items walk(P, sh);
     Item it;
     bool more = walk.next(it);
     n = __shfl_sync(kAll, it.n, 0);
@@ -564,15 +564,14 @@ __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh,
             --ahead;
             polls = 0;
         } else if ((++polls & 255u) == 0) {
-            if (polls >= kPolls) *gave_up = 1;
-            if (__any_sync(kAll, *gave_up)) break;
+            if (polls >> 4 >= limit.polls) *limit.gave_up = 1;  // these do not sleep: 0.1 us each, half a second in all
+            if (__any_sync(kAll, *limit.gave_up)) break;
         }
     }
     // products under way end before the tensor memory is given back
     if (leader) tc_commit(smem_u32(&sh.drain));
     __syncwarp();
-    int none = 0;
-    wait(smem_u32(&sh.drain), 0, &none);
+    drain(smem_u32(&sh.drain), 0);
 }
 
 template <int K, int NR, int G>

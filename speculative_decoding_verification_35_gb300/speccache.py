@@ -26,7 +26,8 @@ from .specverify import SV_BF16, _ptr, lib
 SV_F16, SV_E4M3 = 2, 3
 
 # every exported symbol of speccache.h, in header order
-EXPORTS = ("spec_cache_append", "spec_cache_workspace_size", "spec_cache_attend", "spec_cache_compact")
+EXPORTS = ("spec_cache_append", "spec_cache_workspace_size", "spec_cache_attend", "spec_cache_attend_ex",
+           "spec_cache_compact")
 
 
 class SvCache(ctypes.Structure):
@@ -58,6 +59,8 @@ def _bind():
     lib.spec_cache_attend.argtypes = [vp, i32, vp, ctypes.c_int, i32, vp, i64, ctypes.c_float, i32, vp, vp, vp, vp, sz,
                                       vp]
     lib.spec_cache_attend.restype = ctypes.c_int
+    lib.spec_cache_attend_ex.argtypes = lib.spec_cache_attend.argtypes[:-1] + [vp, vp]
+    lib.spec_cache_attend_ex.restype = ctypes.c_int
     lib.spec_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp]
     lib.spec_cache_compact.restype = ctypes.c_int
 
@@ -85,6 +88,13 @@ def spec_cache_attend(cache, layer, chunk, dtype, q_heads, q, q_stride, scale, w
     """Attention of a chunk over the cache. cache, chunk: SvCache, SvChunk or None; the rest addresses."""
     return lib.spec_cache_attend(_ref(cache), layer, _ref(chunk), dtype, q_heads, q, q_stride, scale, window, out, lse,
                                  device_status, workspace, workspace_bytes, cuda_stream)
+
+
+def spec_cache_attend_ex(cache, layer, chunk, dtype, q_heads, q, q_stride, scale, window, out, lse, device_status,
+                         workspace, workspace_bytes, debug, cuda_stream) -> int:
+    """spec_cache_attend with the debug structure (specverify.SvDebug or None; spin_limit alone is read)."""
+    return lib.spec_cache_attend_ex(_ref(cache), layer, _ref(chunk), dtype, q_heads, q, q_stride, scale, window, out,
+                                    lse, device_status, workspace, workspace_bytes, _ref(debug), cuda_stream)
 
 
 def spec_cache_compact(cache, chunk, out_num_accepted, out_path, out_cached, device_status, cuda_stream) -> int:
