@@ -179,6 +179,10 @@ __device__ __forceinline__ uint32_t from_float2<__half>(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
 // A launch whose CTAs may be brought in while the kernel before it in the stream ends: they wait for its end, and
 // its writes, with griddepcontrol.wait before they read anything.
 template <typename... Params, typename... Args>

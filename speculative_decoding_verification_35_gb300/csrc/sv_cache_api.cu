@@ -80,7 +80,7 @@ int spec_cache_append(const sv_cache* cache, int32_t layer, const sv_chunk* chun
                       int32_t dtype, int32_t q_heads, const void* q, int64_t q_stride, const void* k, const void* v,
                       int64_t kv_stride, void* q_out, uint32_t* device_status, void* cuda_stream) {
     if (!valid(cache) || !valid(chunk) || layer < 0 || layer >= cache->layers) return SV_ERR_INVALID_ARG;
-    if (!valid_types(dtype, cache->dtype) || cache->head_dim % 8) return SV_ERR_INVALID_ARG;
+    if (!valid_types(dtype, cache->dtype)) return SV_ERR_INVALID_ARG;
     if (rope && (!aligned(rope->table, 16) || rope->positions < 1 || rope->dim < 16 || rope->dim % 16 ||
                  rope->dim > cache->head_dim || rope->reserved != 0))
         return SV_ERR_INVALID_ARG;

@@ -33,10 +33,6 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
     *reinterpret_cast<uint4*>(p) = u;
 }
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
-
 // The division is the definition's own (x / scale, correctly rounded), so that the stored value is the nearest.
 __device__ __forceinline__ void store8_e4m3(char* p, const float (&x)[8], float scale) {
     uint2 u;

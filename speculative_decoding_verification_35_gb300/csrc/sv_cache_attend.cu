@@ -71,8 +71,6 @@ __device__ __forceinline__ Row row_of(const Params& P, const Item& it, const Ite
     return row;
 }
 
-__device__ __forceinline__ uint32_t prefix32(int32_t n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-
 // The 128 slots of a tile that a row sees.
 __device__ __forceinline__ void seen_of(const Row& row, const Item& it, int32_t k0, uint32_t bad, bool tree, uint32_t* seen) {
 #pragma unroll

@@ -221,6 +221,8 @@ __device__ __forceinline__ void mma_mixed(uint32_t d, uint32_t a, uint32_t b, ui
         asm volatile(SV_MMA_MIXED("f16") ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(add), "n"(kOperandHigh), "n"(kHigh)
                      : "memory");
 }
+// The lowest n bits.
+__device__ __forceinline__ uint32_t prefix32(int32_t n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 // One thread of a converged warp, always the same.
 __device__ __forceinline__ bool elect() {
     uint32_t p;
@@ -259,9 +261,6 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     F2 r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
-}
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 __device__ __forceinline__ __half2 half_pair(uint32_t e4m3) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)e4m3, __NV_E4M3);
