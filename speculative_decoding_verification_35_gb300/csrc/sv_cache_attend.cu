@@ -20,8 +20,9 @@
 //
 // Bound by the chain of a stream's tile: scores (512 cycles of the tensor cores at D = 128), softmax (some 1450), outputs
 // (512) and what lies between; two streams in turn keep the tensor cores busy 1024 of every 1560 cycles. Measured:
-// bfloat16, D = 128, 3 prompts of 700 to 2048 tokens over 1 to 8192 cached, 32 heads in 8 groups: 234 us, 1.27 PFLOP/s
-// of what the mask leaves (0.67 of a library product's 1.89), 3 us of them the merge.
+// bfloat16, D = 128, 3 prompts of 700 to 2048 tokens over 1 to 8192 cached, 32 heads in 8 groups: 235 us (231 to 238),
+// 1.26 PFLOP/s of what the mask leaves (0.67 of a library product's 1.89), 3 us of them the merge. The same prompts on an
+// e4m3 cache take 363 us; that kernel alone spills, 28 bytes a thread.
 #include "sv_cache_attend.cuh"
 
 #include <algorithm>
@@ -627,13 +628,13 @@ cudaError_t launch(Params P, int n, cudaStream_t st) {
     P.q_box = min(P.tokens, A.chunk.max_gamma + 1);
     P.q_part = kHalf;
     // measured on prompts of 700 to 2048 tokens: 235 us, with 1, 2, 4 and 5 272, 238, 238
-    // and 240. With an e4m3 cache the queries' parts take longer: 3, 6 and 10 make 476, 366 and 387 us of those prompts
-    // (and 54, 59 and 66 of 16 trees of 32 tokens).
+    // and 240. With an e4m3 cache the queries' parts take longer: 3, 6 and 10 make 476, 363 and 387 us of those prompts,
+    // and 54, 59 and 66 of 16 trees of 32 tokens, whose items have few rows each: 6 serves the prompts at the trees' cost.
     P.lead = K == kE4m3 ? 6 : 3;
     P.halves = NH;
     P.q_tile = (K == kE4m3 ? 2 : NH) * kHalf;
     P.q_bytes = 2 * P.q_tile;
-    P.q_bufs = K == kE4m3 ? 2 : 1;  // the next item's are split into parts, 256 rows by one warp, under this one's tiles
+    P.q_bufs = K == kE4m3 ? 2 : 1;  // the next item's are split into parts, 256 rows by three warps, under this one's tiles
     const int own = (int)(sizeof(Shared) + 15) / 16 * 16 + (A.chunk.parents ? kItems * (int)sizeof(Tree) : 0) +
                     (K == kE4m3 ? kItems * 2 * kTile * 4 : 0);
     const int slots = min(2 * kMaxSlots, (kSmem - own - P.q_bufs * P.q_bytes) / (NH * kHalf));

@@ -32,10 +32,14 @@ __device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, 0); 
 // type; kSlack: how far (log2) a weight may exceed the reference before the reference moves. A tile's 128 weights
 // sum to 2^(kShift + kSlack + 7) at most, within the type's range: bfloat16 has float's, and its reference hardly
 // ever moves after the first tile. (e4m3: every weight, 2^(kShift + kSlack) <= 448.)
+// Weights of 16-bit caches are rounded to the values' type, because a product's two operands share one. What that leaves
+// off could be a second operand, as it is for e4m3, but would cost half of the tensor cores' work again in the wide
+// kernel, which they bound together with the softmax, and in the other one of three tile slots (its weights' tile
+// would take 8 KB more where 16 bytes are free). Sums and lse have the weights unrounded.
 // kE4m3: the cache is 8 bits wide and the products are too. A bfloat16 query has 8 significant bits and an
-// e4m3 value 4, so q 2^k = hi + lo exactly, but for elements under 2^-11 of the row's largest (k brings it to
-// [128, 256)); a weight is hi + lo to about 2^-9 of itself. Each product then runs twice, at twice the 16-bit rate,
-// and no key or value is converted.
+// e4m3 value 4, so q 2^k = hi + lo exactly, but for elements under 2^-9 of the row's largest (k brings it to
+// [128, 256)), which are off by 2^-10 at most, e4m3's least half step; a weight is hi + lo to about 2^-9 of itself. Each
+// product then runs twice, at twice the 16-bit rate, and no key or value is converted.
 enum Kind { kBf16 = 0, kFp16 = 1, kE4m3 = 2 };
 template <int K>
 struct KindOf;

@@ -25,11 +25,11 @@
 //
 // Measured (one copy reads and writes 6.7 TB/s): bfloat16, D = 128, pages of 16, 8 key heads: 64 sequences of 6 tokens,
 // 500 to 8000 cached, 4 heads a group, 129 us (0.87 of the copy rate; with the rows on the lanes 133 to 141); 2
-// sequences of 8 tokens, 60000 to 131072 cached, 8 heads a group, 155 us (0.95; two CTAs an SM 213, rows on the lanes
-// 180). float16, D = 64, 16 heads of their own, 128 sequences of one token with a window of 1024: 60 us (0.44; rows on
-// the lanes 128), of which some 10 are the launches and the first tiles' way; its 128-byte pieces lie 2 KB apart, and
-// more than half of its items have one tile. e4m3, D = 128, 32 sequences of 4 tokens, 2000 to 16384 cached: 92 us (0.80;
-// rows on the lanes 150).
+// sequences of 8 tokens, 60000 to 131072 cached, 8 heads a group, 159 us (154 to 161, 0.92; two CTAs an SM 213, rows on
+// the lanes 180). float16, D = 64, 16 heads of their own, 128 sequences of one token with a window of 1024: 58 us (0.45;
+// rows on the lanes 128), of which some 10 are the launches and the first tiles' way; its 128-byte pieces lie 2 KB apart,
+// and more than half of its items have one tile. e4m3, D = 128, 32 sequences of 4 tokens, 2000 to 16384 cached: 93 us
+// (0.79; rows on the lanes 150). Of the nine kernels the one for e4m3 and 64 rows spills, 76 bytes a thread.
 #include "sv_cache_attend.cuh"
 
 #include <type_traits>
@@ -429,7 +429,9 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
         owed = true;
         const bool alone = it.begins && it.finishes;
         const size_t part = (size_t)(2 * blockIdx.x + (it.begins ? 1 : 0)) * P.part_rows + row0;
-        float f = 1.f;  // what a row's O is scaled by
+        // What a row's O is scaled by. Here and in lse the quotient and the logarithm are the short ones, 2 ulp and 2^-22 off:
+        // out is rounded to 2^-9 or 2^-12 next, and an exponential before them is 2^-22 off as well.
+        float f = 1.f;
         if (alone) f = total == 0.f ? 0.f : __fdividef(A.pool.v_scale ? A.pool.v_scale[it.h] : 1.f, total);
         if (k < rows && k < N) {
             if (alone) {
