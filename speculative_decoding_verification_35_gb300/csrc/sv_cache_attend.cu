@@ -22,7 +22,7 @@
 // (512) and what lies between; two streams in turn keep the tensor cores busy 1024 of every 1560 cycles. Measured:
 // bfloat16, D = 128, 3 prompts of 700 to 2048 tokens over 1 to 8192 cached, 32 heads in 8 groups: 235 us (231 to 238),
 // 1.26 PFLOP/s of what the mask leaves (0.67 of a library product's 1.89), 3 us of them the merge. The same prompts on an
-// e4m3 cache take 363 us; that kernel alone spills, 28 bytes a thread.
+// e4m3 cache take 356 us.
 #include "sv_cache_attend.cuh"
 
 #include <algorithm>
@@ -525,12 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&vm));
         if (K != kE4m3) asm volatile("prefetch.tensormap [%0];" ::"l"(&qm));
     }
-    if (w == 9) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
-        // else the SM's other CTA could not allocate before this one ends
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    begin<kThreads>(P, sh);
+    begin<kThreads, 512>(P, sh, w == 9);
     // 128 registers a thread at launch: 192 + 192 + 64 + 64 for the four warpgroups
     if (w < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
@@ -628,8 +623,8 @@ cudaError_t launch(Params P, int n, cudaStream_t st) {
     P.q_box = min(P.tokens, A.chunk.max_gamma + 1);
     P.q_part = kHalf;
     // measured on prompts of 700 to 2048 tokens: 235 us, with 1, 2, 4 and 5 272, 238, 238
-    // and 240. With an e4m3 cache the queries' parts take longer: 3, 6 and 10 make 476, 363 and 387 us of those prompts,
-    // and 54, 59 and 66 of 16 trees of 32 tokens, whose items have few rows each: 6 serves the prompts at the trees' cost.
+    // and 240. With an e4m3 cache the queries' parts take longer: 3, 6 and 10 make 476, 356 and 387 us of those prompts,
+    // and 54, 58 and 66 of 16 trees of 32 tokens, whose items have few rows each: 6 serves the prompts at the trees' cost.
     P.lead = K == kE4m3 ? 6 : 3;
     P.halves = NH;
     P.q_tile = (K == kE4m3 ? 2 : NH) * kHalf;

@@ -1030,14 +1030,23 @@ __device__ __forceinline__ void init_common(Common& sh, int streams, int readers
     sh.gave_up = 0;
 }
 
-// After the previous kernel's end: where the CTA begins, and the sequences that fail (their findings, and zeros in
-// their rows). All threads; the caller's barrier follows.
-template <int kThreads>
-__device__ __forceinline__ void begin(const Params& P, Common& sh) {
+// After the previous kernel's end: tensor memory, where the CTA begins, and the sequences that fail (their findings, and
+// zeros in their rows). All threads; the caller's barrier follows.
+// Tensor memory is taken after the wait, and the next kernel let in after that, by the warp that took it: a CTA that held
+// some while it waits for a kernel whose CTAs, on the same SM, are yet to take theirs would wait for ever, and so would
+// this one for the next kernel's.
+template <int kThreads, int kColumns>
+__device__ __forceinline__ void begin(const Params& P, Common& sh, bool allocates) {
     const int tid = threadIdx.x;
     // what is above may run while the stream's previous kernel ends
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
+    if (allocates) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "n"(kColumns)
+                     : "memory");
+        // else the SM's other CTA could not allocate before this one ends
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("griddepcontrol.launch_dependents;");
+    }
     plan<kThreads>(P, sh);
     if (blockIdx.x == 0 && tid == 0) {
         const int64_t end = (int64_t)P.a.chunk.offs[P.a.chunk.B] + P.a.chunk.B;

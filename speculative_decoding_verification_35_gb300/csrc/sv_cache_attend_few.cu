@@ -608,13 +608,7 @@ __global__ void __launch_bounds__(kThreads<G>, G == 1 ? 2 : 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&vm));
         if (K != kE4m3) asm volatile("prefetch.tensormap [%0];" ::"l"(&qm));
     }
-    if (role == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "n"(columns)
-                     : "memory");
-        // else the SM's other CTA could not allocate before this one ends
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    begin<kThreads<G>>(P, sh);
+    begin<kThreads<G>, columns>(P, sh, role == 1);
     // at launch 128 registers a thread for one group, 168 for two
     if (role < 0) {
         if (G == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");

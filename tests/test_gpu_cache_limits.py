@@ -287,3 +287,26 @@ def test_compact_findings_in_place(sc, in_place):
     assert now.tolist() == [10, 20, 30, 8, 8]
     diff = (b.k != k0)[0].flatten(2).any(2).nonzero().tolist()
     assert diff == [[int(b.table_h[4][0]), 7]]
+
+
+@pytest.mark.parametrize("chunks", [[1, 1, 1, 1], [6, 2, 5, 1], [130, 60, 9, 200]])
+def test_between_library_products(sc, chunks):
+    """Calls right after products of the library, which hold tensor memory as well, and beside those of another stream."""
+    b = Batch(sc, chunks, [2000, 700, 90, 300], 32, 8, 128, 16)
+    want, wl = b.attend()
+    x = torch.randn((512, 2048), device="cuda").bfloat16()
+    w = torch.randn((2048, 2048), device="cuda").bfloat16() * 2048 ** -0.5
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for i in range(40):
+        with torch.cuda.stream(side):
+            y = x[:8 << i % 7] @ w
+        z = x[:8 << i % 7] @ w
+        got.append(b.attend())
+        z = z @ w
+        got.append(b.attend())
+    torch.cuda.synchronize()
+    assert b.cache.status_bits() == 0 and torch.isfinite(y).all() and torch.isfinite(z).all()
+    for out, lse in got:
+        assert torch.equal(out, want) and torch.equal(lse, wl)
