@@ -20,8 +20,8 @@
 //
 // Bound by the chain of a stream's tile: scores (512 cycles of the tensor cores at D = 128), softmax (some 1450), outputs
 // (512) and what lies between; two streams in turn keep the tensor cores busy 1024 of every 1560 cycles. Measured:
-// bfloat16, D = 128, 3 prompts of 700 to 2048 tokens over 1 to 8192 cached, 32 heads in 8 groups: 235 us (231 to 238),
-// 1.26 PFLOP/s of what the mask leaves (0.67 of a library product's 1.89), 3 us of them the merge. The same prompts on an
+// bfloat16, D = 128, 3 prompts of 700 to 2048 tokens over 1 to 8192 cached, 32 heads in 8 groups: 233 us (230 to 238),
+// 1.27 PFLOP/s of what the mask leaves (0.67 of a library product's 1.89), 3 us of them the merge. The same prompts on an
 // e4m3 cache take 356 us.
 #include "sv_cache_attend.cuh"
 
