@@ -299,8 +299,8 @@ def prepare(case, seed):
     if own:  # the program's handles and the outputs' buffers
         ints = dict(dtype=torch.int32, device=DEV)
         if case["op"] in ("sample", "filter"):
-            from speculative_decoding_verification_35_gb300 import specverify as sv
-            s["filter"] = sv.Filter(s["temperature"], s["top_k"], s["top_p"], s["min_p"], s["request"])
+            from speculative_decoding_verification_35_gb300 import specsample as ss
+            s["filter"] = ss.Filter(s["temperature"], s["top_k"], s["top_p"], s["min_p"], s["request"])
             s["kept"] = torch.empty(case["rows"], **ints)
             if case["op"] == "sample":
                 s["tokens"] = torch.empty(case["rows"], **ints)
