@@ -163,6 +163,48 @@ int spec_cache_attend_ex(const sv_cache* cache, int32_t layer, const sv_chunk* c
 int spec_cache_compact(const sv_cache* cache, const sv_chunk* chunk, const int32_t* out_num_accepted,
                        const int32_t* out_path, int32_t* out_cached, uint32_t* device_status, void* cuda_stream);
 
+/*
+ * The pages of a cache's pool, dealt out on the device. Free pages wait in a ring: queue holds `pages` entries, of which
+ * the `count` from `head` on (around its end) are free page ids, state = {head, count}. Sequence b holds the first held[b]
+ * entries of its row of page_table. out_held and out_state may be held and state themselves; where they are not, the call
+ * leaves held and state as they were, and so can be made again. All int32, 4-byte aligned, contiguous; page_table has rows
+ * of table_stride entries. page_size: 1 to 65536 (the cache calls want a multiple of 8).
+ */
+typedef struct {
+    int32_t* page_table;
+    int32_t* queue;
+    const int32_t* held;
+    const int32_t* state;
+    int32_t* out_held;
+    int32_t* out_state;
+    int32_t table_stride;
+    int32_t page_size;
+    int32_t pages;
+    int32_t reserved; /* 0 */
+} sv_pages;
+
+/*
+ * Pages for what the sequences are to hold: need_b = ceil(n_b / page_size) pages, n_b = lengths[b] where lengths (int32[B]) is
+ * given, else the slots cached[b] + T_b of the chunk's tokens. One of chunk and lengths is given (neither for B = 0); with lengths, B sequences
+ * (0 in one gives all of its pages back: a sequence that has ended).
+ *   1. A sequence with held[b] > need_b gives back the entries need_b .. held[b] - 1 of its row, to the queue's end, in the
+ *      order of the sequences and of their entries (which stay in the table, unused).
+ *   2. The sequences with held[b] < need_b take what they lack from the queue's front, in order, into the entries
+ *      held[b] .. need_b - 1. The first one for which there are too few pages takes none, and no later one takes any.
+ * out_held[b] = need_b, or held[b] for a sequence that went without; out_state the queue's new head and count.
+ * slot_map (nullable, with a chunk only; int64[rows]): of every chunk token its place page_id * page_size + slot % page_size,
+ * or -1 where its sequence has a finding or went without, or the page id lies outside [0, pages). Rows outside every
+ * sequence are not written.
+ * Findings: SV_ERR_CAPACITY: too few pages, n_b < 0 or need_b above table_stride; SV_ERR_BAD_OFFSETS: rows as for the other
+ * calls, held[b] outside [0, table_stride], a page id outside [0, pages) taken or given back, head outside [0, pages), count
+ * below 0, or more free pages than `pages` after step 1. A sequence with a finding keeps its pages; with a bad state nothing is
+ * moved, every sequence keeps its pages and the slot map is -1. A bad page id is moved like any other (the cache calls
+ * refuse it in turn).
+ * At most 65536 sequences.
+ */
+int spec_cache_reserve(const sv_pages* pages, const sv_chunk* chunk, const int32_t* lengths, int32_t B, int64_t* slot_map,
+                       uint32_t* device_status, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -71,10 +71,27 @@ struct CompactArgs {
     int32_t esize;
 };
 
+struct ReserveArgs {
+    int32_t* table;
+    int32_t* queue;
+    const int32_t* held;
+    const int32_t* state;
+    int32_t* out_held;
+    int32_t* out_state;
+    int32_t table_stride, page_size, pages;
+    Chunk chunk;             // where there are no lengths
+    const int32_t* lengths;
+    int32_t B;
+    int64_t* slots;
+    uint32_t* status;
+};
+constexpr int32_t kMaxReserve = 1 << 16;  // sequences of a call
+
 size_t attend_workspace(int dim, int cache_dtype);  // bytes
 cudaError_t launch_append(const AppendArgs& A, int dtype, int cache_dtype, bool interleaved, cudaStream_t st);
 cudaError_t launch_attend(const AttendArgs& A, int dtype, int cache_dtype, cudaStream_t st);
 cudaError_t launch_compact(const CompactArgs& A, cudaStream_t st);
+cudaError_t launch_reserve(const ReserveArgs& A, cudaStream_t st);
 
 // One sequence's chunk. err: bits of the sequence's findings; rows_ok: its rows can be written.
 struct Seq {

@@ -169,4 +169,39 @@ int spec_cache_compact(const sv_cache* cache, const sv_chunk* chunk, const int32
     return result(launch_compact(A, (cudaStream_t)cuda_stream));
 }
 
+int spec_cache_reserve(const sv_pages* pages, const sv_chunk* chunk, const int32_t* lengths, int32_t B, int64_t* slot_map,
+                       uint32_t* device_status, void* cuda_stream) {
+    if (!pages || (chunk && lengths) || (!chunk && !lengths && B != 0)) return SV_ERR_INVALID_ARG;
+    if (chunk) {
+        if (!valid(chunk)) return SV_ERR_INVALID_ARG;
+        B = chunk->B;
+    }
+    if (B < 0 || B > kMaxReserve || pages->table_stride < 1 || pages->page_size < 1 || pages->page_size > 65536 || pages->pages < 1 ||
+        pages->reserved != 0)
+        return SV_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)pages->page_table, (const void*)pages->queue, (const void*)pages->held, (const void*)pages->state,
+                          (const void*)pages->out_held, (const void*)pages->out_state})
+        if (!aligned(p, 4)) return SV_ERR_INVALID_ARG;
+    if ((uintptr_t)lengths % 4 || (uintptr_t)slot_map % 8 || (uintptr_t)device_status % 4 || (slot_map && !chunk)) return SV_ERR_INVALID_ARG;
+    ReserveArgs A{};
+    A.table = pages->page_table;
+    A.queue = pages->queue;
+    A.held = pages->held;
+    A.state = pages->state;
+    A.out_held = pages->out_held;
+    A.out_state = pages->out_state;
+    A.table_stride = pages->table_stride;
+    A.page_size = pages->page_size;
+    A.pages = pages->pages;
+    if (chunk) {
+        A.chunk = chunk_of(chunk);
+        A.chunk.parents = A.chunk.end = nullptr;
+    }
+    A.lengths = lengths;
+    A.B = B;
+    A.slots = slot_map;
+    A.status = device_status;
+    return result(launch_reserve(A, (cudaStream_t)cuda_stream));
+}
+
 }  // extern "C"

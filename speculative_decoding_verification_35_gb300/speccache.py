@@ -27,7 +27,7 @@ SV_F16, SV_E4M3 = 2, 3
 
 # every exported symbol of speccache.h, in header order
 EXPORTS = ("spec_cache_append", "spec_cache_workspace_size", "spec_cache_attend", "spec_cache_attend_ex",
-           "spec_cache_compact")
+           "spec_cache_compact", "spec_cache_reserve")
 
 
 class SvCache(ctypes.Structure):
@@ -50,6 +50,13 @@ class SvRope(ctypes.Structure):
                 ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class SvPages(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("queue", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("state", ctypes.c_void_p), ("out_held", ctypes.c_void_p), ("out_state", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int32), ("page_size", ctypes.c_int32), ("pages", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 def _bind():
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     lib.spec_cache_append.argtypes = [vp, i32, vp, vp, ctypes.c_int, i32, vp, i64, vp, vp, i64, vp, vp, vp]
@@ -63,6 +70,8 @@ def _bind():
     lib.spec_cache_attend_ex.restype = ctypes.c_int
     lib.spec_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp]
     lib.spec_cache_compact.restype = ctypes.c_int
+    lib.spec_cache_reserve.argtypes = [vp, vp, vp, i32, vp, vp, vp]
+    lib.spec_cache_reserve.restype = ctypes.c_int
 
 
 _bind()
@@ -101,6 +110,11 @@ def spec_cache_compact(cache, chunk, out_num_accepted, out_path, out_cached, dev
     """Keep the accepted path of a verified chunk. cache, chunk: SvCache, SvChunk or None; the rest addresses."""
     return lib.spec_cache_compact(_ref(cache), _ref(chunk), out_num_accepted, out_path, out_cached, device_status,
                                   cuda_stream)
+
+
+def spec_cache_reserve(pages, chunk, lengths, B, slot_map, device_status, cuda_stream) -> int:
+    """Pages for a chunk or for given lengths. pages, chunk: SvPages, SvChunk or None; the rest addresses."""
+    return lib.spec_cache_reserve(_ref(pages), _ref(chunk), lengths, B, slot_map, device_status, cuda_stream)
 
 
 # ------------------------------------------------------------------------------------------------
@@ -293,6 +307,77 @@ class PagedCache:
             raise ValueError("out_num_accepted, out_path and out_cached must be contiguous")
         return lib.spec_cache_compact(self._at, chunk.at, out_num_accepted.data_ptr(), _ptr(out_path),
                                       out_cached.data_ptr(), self._status, self._stream(stream))
+
+    def status_bits(self) -> int:
+        return int(self.status.item()) & 0xFFFFFFFF
+
+
+class PagePool:
+    """The pages of a pool, dealt out to sequences on the device (see sv_pages).
+
+    page_table: int32 [sequences, pages per sequence], the table of the PagedCache that uses the pool. queue: int32 [pages],
+    the free ones among them; state: int32 [2], where in it they begin and how many they are; held: int32 [sequences].
+    PagePool.create makes them for a pool that is all free. The object holds the calls' status word.
+    """
+
+    def __init__(self, page_table, queue, held, state, page_size: int):
+        at = page_table.get_device()
+        _check(page_table, "page_table", (torch.int32,), (None, None))
+        _check(queue, "queue", (torch.int32,), (None,), at)
+        _check(held, "held", (torch.int32,), (page_table.shape[0],), at)
+        _check(state, "state", (torch.int32,), (2,), at)
+        for t, name in ((page_table, "page_table"), (queue, "queue"), (held, "held"), (state, "state")):
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        self.page_table, self.queue, self.held, self.state = page_table, queue, held, state
+        self.sequences, self.page_size, self._device = page_table.shape[0], page_size, at
+        self.struct = SvPages(_ptr(page_table), _ptr(queue), _ptr(held), _ptr(state), 0, 0, page_table.shape[1],
+                              _int32(page_size, "page_size"), queue.shape[0], 0)
+        self.status = torch.zeros(1, dtype=torch.int32, device=page_table.device)
+        self._at, self._status = ctypes.addressof(self.struct), _ptr(self.status)
+
+    @classmethod
+    def create(cls, sequences: int, width: int, pages: int, page_size: int, device="cuda"):
+        """A pool whose pages are all free, and a table of `width` pages a sequence that holds none."""
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.full((sequences, width), -1, **i32), torch.arange(pages, **i32), torch.zeros(sequences, **i32),
+                   torch.tensor([0, pages], **i32), page_size)
+
+    def reserve(self, chunk: Chunk | None = None, lengths=None, slot_map=None, out_held=None, out_state=None,
+                stream=None) -> int:
+        """Enqueue spec_cache_reserve: pages for the chunk's tokens, or for `lengths` (int32 [sequences]) to hold.
+        slot_map: int64 [rows], the chunk's places. out_held, out_state: held and state themselves by default."""
+        if (chunk is None) == (lengths is None):
+            raise ValueError("one of chunk and lengths is wanted")
+        if chunk is not None:
+            if chunk.B > self.sequences:
+                raise ValueError(f"page_table has {self.sequences} sequences, the chunk {chunk.B}")
+            if chunk.device != self._device:
+                raise ValueError(f"chunk must be on device {self._device}, got device {chunk.device}")
+            B, rows = chunk.B, chunk.rows
+        else:
+            _check(lengths, "lengths", (torch.int32,), (None,), self._device)
+            B, rows = lengths.shape[0], 0
+            if B > self.sequences:
+                raise ValueError(f"page_table has {self.sequences} sequences, lengths {B}")
+            if slot_map is not None:
+                raise ValueError("slot_map needs a chunk")
+        if slot_map is not None:
+            _check(slot_map, "slot_map", (torch.int64,), (None,), self._device)
+            if slot_map.shape[0] < rows:
+                raise ValueError(f"slot_map must have {rows} rows, got {slot_map.shape[0]}")
+        out_held = self.held if out_held is None else out_held
+        out_state = self.state if out_state is None else out_state
+        _check(out_held, "out_held", (torch.int32,), (None,), self._device)
+        _check(out_state, "out_state", (torch.int32,), (2,), self._device)
+        if out_held.shape[0] < B:
+            raise ValueError(f"out_held must have {B} entries, got {out_held.shape[0]}")
+        for t, name in ((lengths, "lengths"), (slot_map, "slot_map"), (out_held, "out_held"), (out_state, "out_state")):
+            if t is not None and not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        self.struct.out_held, self.struct.out_state = out_held.data_ptr(), out_state.data_ptr()
+        return lib.spec_cache_reserve(self._at, None if chunk is None else chunk.at, _ptr(lengths), B, _ptr(slot_map), self._status,
+                                      stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._device))
 
     def status_bits(self) -> int:
         return int(self.status.item()) & 0xFFFFFFFF
