@@ -154,6 +154,30 @@ int spec_cache_attend_ex(const sv_cache* cache, int32_t layer, const sv_chunk* c
                          void* cuda_stream);
 
 /*
+ * What a model does to its scores before the softmax, and which slots a prompt's tokens see beside those before them.
+ * With z = scale q . k of a token at position p and a slot at position p' (a tree's tokens lie at their depths),
+ *   z <- cap tanh(z / cap)             where cap > 0: 0, or 0.001 to 1000000
+ *   z <- z - slopes[head] |p - p'|     where slopes are given: float[q_heads], a bias that grows with the distance
+ * and with prefix (int32[B], chains only) every token of sequence b sees the slots before min(prefix[b], cached[b] + T_b),
+ * its own chunk's later tokens among them, as far as the window reaches back. Each NULL or 0 changes nothing.
+ */
+typedef struct {
+    const float* slopes;
+    const int32_t* prefix;
+    float cap;
+    int32_t reserved; /* 0 */
+} sv_scores;
+
+/*
+ * spec_cache_attend_ex on such scores (NULL: plain ones); lse is of the scores as they are then. The cap's tanh is within
+ * 2e-7 of itself.
+ */
+int spec_cache_attend_scored(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, int32_t dtype, int32_t q_heads,
+                             const void* q, int64_t q_stride, float scale, int32_t window, const sv_scores* scores,
+                             void* out, float* lse, uint32_t* device_status, void* workspace, size_t workspace_bytes,
+                             const sv_debug* debug, void* cuda_stream);
+
+/*
  * After verification, in every layer: slot cached[b] + 1 + j gets the keys and values of slot
  * cached[b] + path[j], path[j] = out_path[seq_offsets[b] + j], for j < n_b = out_num_accepted[b] (as
  * spec_verify_tree wrote them: increasing nodes in 1 .. T_b - 1), and out_cached[b] = cached[b] + n_b + 1.

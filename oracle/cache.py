@@ -166,3 +166,57 @@ def reserve(table, queue, held, state, want, page_size):
                 head, count = (head + 1) % pages, count - 1
         now[b] = n
     return table, queue, now, np.array([head, count]), without
+
+
+def attend_scored(q, k_pages, v_pages, table, seq_offsets, parents, cached, scale, window=0, cap=0.0, slopes=None,
+                  prefix=None):
+    """attend on scores capped by a tanh, less slopes[head] |distance|, slots before prefix[b] seen by every token.
+
+    (out, lse, mean |v|, score magnitude before the cap, weight floor, largest bias of a slot whose weight is not below
+    2^-30 of the row's largest).
+    """
+    q = np.asarray(q, dtype=np.float64)
+    R, hq, D = q.shape
+    pages, ps, hkv, _ = k_pages.shape
+    G = hq // hkv
+    out, mean, floor = (np.zeros((R, hq, D)) for _ in range(3))
+    lse, big, bias = np.full((R, hq), -np.inf), np.zeros((R, hq)), np.zeros((R, hq))
+    for b in range(len(cached)):
+        r, T = rows_of(seq_offsets, b)
+        past = int(cached[b])
+        par = _parents(parents, seq_offsets, b, T)
+        slot = np.arange(past + T)
+        pos = np.concatenate([slot[:past], past + depths(par)])
+        seen = np.concatenate([np.ones((T, past), dtype=bool), lineage(par)], axis=1)
+        if prefix is not None:
+            seen |= slot < int(prefix[b])
+        apart = pos[past:, None] - pos
+        if window:
+            seen &= apart < window
+        page = table[b][slot // ps].astype(np.int64)
+        seen &= (page >= 0) & (page < pages)
+        need = seen.any(axis=0)
+        s, seen, apart = slot[need], seen[:, need], np.abs(apart[:, need]).astype(np.float64)
+        for h in range(hkv):
+            K = np.asarray(k_pages[page[need], s % ps, h], dtype=np.float64)
+            V = np.asarray(v_pages[page[need], s % ps, h], dtype=np.float64)
+            for g in range(h * G, h * G + G):
+                z = scale * (q[r:r + T, g] @ K.T)
+                mag = abs(scale) * (np.abs(q[r:r + T, g]) @ np.abs(K).T)
+                if cap:
+                    z = cap * np.tanh(z / cap)
+                d = np.zeros_like(apart) if slopes is None else float(slopes[g]) * apart
+                z = np.where(seen, z - d, -np.inf)
+                for j in range(T):
+                    if not seen[j].any():
+                        continue
+                    top = z[j].max()
+                    e = np.exp(z[j] - top)
+                    m = seen[j]
+                    out[r + j, g] = e[m] @ V[m] / e.sum()
+                    mean[r + j, g] = e[m] @ np.abs(V[m]) / e.sum()
+                    floor[r + j, g] = np.abs(V[m]).sum(axis=0) / e.sum()
+                    lse[r + j, g] = top + np.log(e.sum())
+                    big[r + j, g] = mag[j, m].max()
+                    bias[r + j, g] = np.abs(d[j, e > 2.0 ** -30]).max()
+    return out, lse, mean, big, floor, bias

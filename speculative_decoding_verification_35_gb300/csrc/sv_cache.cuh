@@ -59,6 +59,10 @@ struct AttendArgs {
     uint32_t* status;
     void* workspace;
     uint32_t spin_limit;  // polls of a wait, 0: the kernels' own bound
+    bool scored;          // one of these is given
+    float cap;            // 0: none
+    const float* slopes;  // [q_heads] or nullptr
+    const int32_t* prefix;  // [B] or nullptr
 };
 
 struct CompactArgs {

@@ -72,6 +72,47 @@ Chunk chunk_of(const sv_chunk* c, const int32_t* path = nullptr) {
 
 int result(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
 
+// Caps of scores: no cap or its reciprocal leaves float's range, whatever the scores.
+constexpr float kLeastCap = 1e-3f, kMostCap = 1e6f;
+
+int attend(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, int32_t dtype, int32_t q_heads, const void* q, int64_t q_stride,
+           float scale, int32_t window, const sv_scores* scores, void* out, float* lse, uint32_t* device_status, void* workspace,
+           size_t workspace_bytes, const sv_debug* debug, void* cuda_stream) {
+    if (!valid(cache) || !valid(chunk) || layer < 0 || layer >= cache->layers) return SV_ERR_INVALID_ARG;
+    if (!valid_types(dtype, cache->dtype)) return SV_ERR_INVALID_ARG;
+    if (q_heads < 1 || q_heads % cache->heads || q_heads / cache->heads > 128) return SV_ERR_INVALID_ARG;
+    if (q_stride < (int64_t)q_heads * cache->head_dim || q_stride % 8) return SV_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || window < 0) return SV_ERR_INVALID_ARG;
+    if (scores) {
+        if (scores->reserved != 0 || !(scores->cap == 0.f || (scores->cap >= kLeastCap && scores->cap <= kMostCap))) return SV_ERR_INVALID_ARG;
+        if ((uintptr_t)scores->slopes % 4 || (uintptr_t)scores->prefix % 4 || (scores->prefix && chunk->parents)) return SV_ERR_INVALID_ARG;
+    }
+    if ((uintptr_t)lse % 4 || (uintptr_t)device_status % 4) return SV_ERR_INVALID_ARG;
+    if (chunk->B == 0 || chunk->rows == 0) return SV_OK;
+    if (!aligned(q, 16) || !aligned(out, 16)) return SV_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256) || workspace_bytes < spec_cache_workspace_size(cache)) return SV_ERR_WORKSPACE;
+    AttendArgs A{};
+    A.pool = pool_of(cache, layer);
+    A.chunk = chunk_of(chunk);
+    A.q_heads = q_heads;
+    A.q = q;
+    A.q_stride = q_stride;
+    A.scale = scale;
+    A.window = window;
+    A.out = out;
+    A.lse = lse;
+    A.status = device_status;
+    A.workspace = workspace;
+    if (scores) {
+        A.cap = scores->cap;
+        A.slopes = scores->slopes;
+        A.prefix = scores->prefix;
+        A.scored = A.cap > 0.f || A.slopes || A.prefix;
+    }
+    A.spin_limit = debug ? debug->spin_limit : 0;
+    return result(launch_attend(A, dtype, cache->dtype, (cudaStream_t)cuda_stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -126,29 +167,16 @@ int spec_cache_attend_ex(const sv_cache* cache, int32_t layer, const sv_chunk* c
                          const void* q, int64_t q_stride, float scale, int32_t window, void* out, float* lse,
                          uint32_t* device_status, void* workspace, size_t workspace_bytes, const sv_debug* debug,
                          void* cuda_stream) {
-    if (!valid(cache) || !valid(chunk) || layer < 0 || layer >= cache->layers) return SV_ERR_INVALID_ARG;
-    if (!valid_types(dtype, cache->dtype)) return SV_ERR_INVALID_ARG;
-    if (q_heads < 1 || q_heads % cache->heads || q_heads / cache->heads > 128) return SV_ERR_INVALID_ARG;
-    if (q_stride < (int64_t)q_heads * cache->head_dim || q_stride % 8) return SV_ERR_INVALID_ARG;
-    if (!std::isfinite(scale) || window < 0) return SV_ERR_INVALID_ARG;
-    if ((uintptr_t)lse % 4 || (uintptr_t)device_status % 4) return SV_ERR_INVALID_ARG;
-    if (chunk->B == 0 || chunk->rows == 0) return SV_OK;
-    if (!aligned(q, 16) || !aligned(out, 16)) return SV_ERR_INVALID_ARG;
-    if (!aligned(workspace, 256) || workspace_bytes < spec_cache_workspace_size(cache)) return SV_ERR_WORKSPACE;
-    AttendArgs A{};
-    A.pool = pool_of(cache, layer);
-    A.chunk = chunk_of(chunk);
-    A.q_heads = q_heads;
-    A.q = q;
-    A.q_stride = q_stride;
-    A.scale = scale;
-    A.window = window;
-    A.out = out;
-    A.lse = lse;
-    A.status = device_status;
-    A.workspace = workspace;
-    A.spin_limit = debug ? debug->spin_limit : 0;
-    return result(launch_attend(A, dtype, cache->dtype, (cudaStream_t)cuda_stream));
+    return attend(cache, layer, chunk, dtype, q_heads, q, q_stride, scale, window, nullptr, out, lse, device_status, workspace,
+                  workspace_bytes, debug, cuda_stream);
+}
+
+int spec_cache_attend_scored(const sv_cache* cache, int32_t layer, const sv_chunk* chunk, int32_t dtype, int32_t q_heads,
+                             const void* q, int64_t q_stride, float scale, int32_t window, const sv_scores* scores, void* out,
+                             float* lse, uint32_t* device_status, void* workspace, size_t workspace_bytes, const sv_debug* debug,
+                             void* cuda_stream) {
+    return attend(cache, layer, chunk, dtype, q_heads, q, q_stride, scale, window, scores, out, lse, device_status, workspace,
+                  workspace_bytes, debug, cuda_stream);
 }
 
 int spec_cache_compact(const sv_cache* cache, const sv_chunk* chunk, const int32_t* out_num_accepted,

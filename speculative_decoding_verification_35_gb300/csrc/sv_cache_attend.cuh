@@ -1,5 +1,5 @@
-// Shared by the attention kernels of spec_cache_attend (sv_cache_attend.cu: up to 256 rows a work item,
-// sv_cache_attend_few.cu: up to 64): how the work is numbered and shared out, the warps that load and clean, and
+// Shared by the attention kernels of spec_cache_attend (sv_cache_attend_wide.cuh: up to 256 rows a work item,
+// sv_cache_attend_few.cuh: up to 64): how the work is numbered and shared out, the warps that load and clean, and
 // the PTX beneath. The heads of the two files say why they are made as they are.
 #pragma once
 #include <cuda.h>
@@ -248,6 +248,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // Two floats in one register pair, for the packed multiply-add and add.
 using F2 = unsigned long long;
 __device__ __forceinline__ F2 pack2(float a, float b) {
@@ -264,6 +269,11 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     F2 r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ __half2 half_pair(uint32_t e4m3) {
@@ -291,16 +301,22 @@ struct alignas(16) Item {
     int32_t tile, n;              // the CTA's tiles: the first (absolute), how many; 0: no more items
     int32_t mixed_lo, mixed_hi;   // slots below mixed_lo and from mixed_hi on are seen by some of its rows only
     int32_t begins, finishes;     // its first and last tiles are among the CTA's
-    int32_t pad;
+    int32_t reach;                // kScored: the slots before it are seen by every token
 };
 
-__device__ __forceinline__ void span(const Params& P, int32_t T, int32_t past, int32_t p, Item& it, int32_t& first,
+template <bool kScored>
+__device__ __forceinline__ void span(const Params& P, int32_t b, int32_t T, int32_t past, int32_t p, Item& it, int32_t& first,
                                      int32_t& count) {
     it.t0 = p * P.block;
     it.nt = min(P.block, T - it.t0);
     it.split = P.tokens == P.block ? it.nt : it.nt > P.tokens ? P.tokens : (it.nt + 1) / 2;
     it.past = past;
     it.end = past + it.t0 + it.nt;
+    it.reach = 0;
+    if (kScored && P.a.prefix) {
+        it.reach = max(0, min(P.a.prefix[b], past + T));
+        it.end = max(it.end, it.reach);
+    }
     it.lo = 0;
     if (P.a.window > 0) {  // the least position of its rows: the root's in a tree
         const int32_t t = P.a.chunk.parents ? 0 : it.t0;
@@ -326,14 +342,15 @@ __device__ __forceinline__ Seq checked_seq(const Params& P, int32_t b) {
 }
 
 // Tiles and items of a sequence, for one key head.
-__device__ __forceinline__ void size_of(const Params& P, const Seq& s, uint32_t& tiles, uint32_t& blocks) {
+template <bool kScored>
+__device__ __forceinline__ void size_of(const Params& P, int32_t b, const Seq& s, uint32_t& tiles, uint32_t& blocks) {
     tiles = blocks = 0;
     if (s.err) return;
 #pragma unroll 1
     for (int32_t p = 0; p * P.block < s.T; ++p) {
         Item it;
         int32_t first, count;
-        span(P, s.T, s.past, p, it, first, count);
+        span<kScored>(P, b, s.T, s.past, p, it, first, count);
         if (tiles >> 31 == 0) tiles += count;  // more are refused, so they need not be counted
         ++blocks;
     }
@@ -376,6 +393,7 @@ __device__ __forceinline__ uint32_t share(uint32_t a, uint32_t b, uint32_t c) { 
 
 // Where the CTA begins: by all threads, in the end by one,
 // whose sequence b it is, `rest` units into it.
+template <bool kScored>
 __device__ __forceinline__ void begin_at(const Params& P, Common& sh, const Seq& s, int32_t b, uint32_t rest, uint32_t lead,
                                          uint32_t W, uint32_t n, uint32_t u0, uint32_t u1) {
     const uint32_t heads = P.a.pool.heads;
@@ -383,7 +401,7 @@ __device__ __forceinline__ void begin_at(const Params& P, Common& sh, const Seq&
     int32_t first, count, p = 0;
 #pragma unroll 1
     for (;; ++p) {
-        span(P, s.T, s.past, p, it, first, count);
+        span<kScored>(P, b, s.T, s.past, p, it, first, count);
         const uint32_t all = (count + lead) * heads;
         if (rest < all) break;
         rest -= all;
@@ -398,13 +416,14 @@ __device__ __forceinline__ void begin_at(const Params& P, Common& sh, const Seq&
 
 // The record of the item that the CTA begins in, if it is the second one to work on it. Late, by one thread: only the
 // merge needs it.
+template <bool kScored>
 __device__ __forceinline__ void record(const Params& P, const Common& sh) {
     const Start& s = sh.start;
     const uint32_t c = blockIdx.x;
     if (s.left == 0 || s.x <= s.lead) return;
     Item it;
     int32_t first, count;
-    span(P, s.T, s.past, s.p, it, first, count);
+    span<kScored>(P, s.b, s.T, s.past, s.p, it, first, count);
     // the item's first tile is unit `from`; if the CTA before this one had it, this one records the item
     const uint32_t from = s.u0 - s.x + s.lead;
     if (from < share(s.W, c - 1, s.n)) return;
@@ -424,7 +443,7 @@ __device__ __forceinline__ void record(const Params& P, const Common& sh) {
     P.records[c] = r;
 }
 
-template <int kThreads>
+template <int kThreads, bool kScored>
 __device__ __forceinline__ void plan(const Params& P, Common& sh) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int32_t B = P.a.chunk.B, c = (int32_t)blockIdx.x;
@@ -467,7 +486,7 @@ __device__ __forceinline__ void plan(const Params& P, Common& sh) {
                 if (b < B) {
                     mine = seq_of(P.a.chunk, capacity_of(P.a.pool), b);
                     if (!mine.err && P.a.chunk.parents && (wrong[tid >> 5] >> (tid & 31) & 1u)) mine.err = 1u << SV_ERR_BAD_OFFSETS;
-                    size_of(P, mine, my_tiles, my_blocks);
+                    size_of<kScored>(P, b, mine, my_tiles, my_blocks);
                 }
             }
             if (round == 0) {
@@ -500,7 +519,7 @@ __device__ __forceinline__ void plan(const Params& P, Common& sh) {
                 total += x;
             }
             const uint32_t first_unit = before + incl - u;
-            if (u > 0 && u0 >= first_unit && u0 < first_unit + u) begin_at(P, sh, mine, b, u0 - first_unit, lead, W, n, u0, u1);
+            if (u > 0 && u0 >= first_unit && u0 < first_unit + u) begin_at<kScored>(P, sh, mine, b, u0 - first_unit, lead, W, n, u0, u1);
             base += total;
         }
         if (round > 0) break;
@@ -570,6 +589,34 @@ __device__ __forceinline__ float score_unit(const AttendArgs& A, int32_t h, bool
 // The same for a row whose queries were brought up by a power of two (e4m3): 2^-120 for a row of zeros, so that this
 // product, too, is kept above zero.
 __device__ __forceinline__ float row_unit(float unit, float down) { return at_least(unit * down, 1e-37f); }
+
+// Capped scores, cap tanh(z / cap), from scores to log2 of the weights (cap log2e tanh(..)). With x = z / cap up to 1, where a
+// model keeps most of them, tanh x = x q(x^2), q of degree 6 with q(0) = 1 fitted for the least relative error on [0, 1]
+// (5.5e-8; 1.6e-7 with the roundings): nine packed operations for two scores and none of the special-function unit, which
+// the weights keep busy. Past 1, 1 - 2 / (1 + 2^(2 x log2 e)): its error, some 2^-22 of one, is as small a part there.
+struct Cap {
+    F2 c[7];   // times cap log2e, the highest first
+    float by;  // x = s by, for scores of unit 1
+    float most;  // cap log2e
+    __device__ __forceinline__ explicit Cap(float cap) {
+        most = cap * kLog2e;
+        by = kLn2 / cap;
+        const float q[7] = {0.00105826119f, -0.00625932904f, 0.0203597479f, -0.0534987018f, 0.133264087f, -0.333329868f, 1.f};
+#pragma unroll
+        for (int i = 0; i < 7; ++i) c[i] = pack2(q[i] * most, q[i] * most);
+    }
+    // x up to 1
+    __device__ __forceinline__ F2 near(F2 x) const {
+        const F2 y = mul2(x, x);
+        F2 p = c[0];
+#pragma unroll
+        for (int i = 1; i < 7; ++i) p = fma2(p, y, c[i]);
+        return mul2(p, x);
+    }
+    __device__ __forceinline__ float far(float x) const {
+        return fmaf(-2.f * most, rcp_fast(1.f + exp2_fast(x * (2.f * kLog2e))), most);
+    }
+};
 
 // Only among slots that some rows of the item see and others do not can a value meet a weight of zero, and a NaN
 // or infinity be carried into a row that does not see it.
@@ -860,7 +907,7 @@ __device__ __forceinline__ void scan_rows(int halves, uint32_t at, int32_t lo, i
 
 // The CTA's items, one after the other, by one warp, and their queries (e4m3: a part of them, where kSplitters warps do
 // that); a last one of no tiles ends them.
-template <int K, int kSplitters>
+template <int K, int kSplitters, bool kScored>
 __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t q_smem, const CUtensorMap* qm) {
     const int lane = threadIdx.x & 31;
     const bool tree = P.a.chunk.parents != nullptr;
@@ -904,7 +951,7 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
         }
         if (left > 0 && T > 0) {
             int32_t first, count;
-            span(P, T, past, p, it, first, count);
+            span<kScored>(P, b, T, past, p, it, first, count);
             const int32_t j = max(0, x - lead);
             it.b = b;
             it.h = h;
@@ -914,6 +961,7 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
             it.n = min(count - j, left);
             it.finishes = j + it.n == count;
             it.mixed_hi = past + (tree ? 0 : it.t0 + 1);
+            if (kScored) it.mixed_hi = max(it.mixed_hi, it.reach);
             it.mixed_lo = P.a.window > 0 && (tree || it.nt > 1) ? it.lo + it.nt + (tree ? it.t0 : 0) : 0;
             left -= it.n;
             x = 0;
@@ -946,7 +994,7 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
         else if (!copy_item_queries(P, sh, it, at, qm, i, q_full)) break;
         qr.step(P.q_bufs);
     }
-    if (lane == 0) record(P, sh);
+    if (lane == 0) record<kScored>(P, sh);
     if (K != kE4m3 && loads > 0) {  // its copies land before the CTA ends, whoever gave up
         bool flip;
         score_unit(P.a, 0, flip);
@@ -1035,7 +1083,7 @@ __device__ __forceinline__ void init_common(Common& sh, int streams, int readers
 // Tensor memory is taken after the wait, and the next kernel let in after that, by the warp that took it: a CTA that held
 // some while it waits for a kernel whose CTAs, on the same SM, are yet to take theirs would wait for ever, and so would
 // this one for the next kernel's.
-template <int kThreads, int kColumns>
+template <int kThreads, int kColumns, bool kScored>
 __device__ __forceinline__ void begin(const Params& P, Common& sh, bool allocates) {
     const int tid = threadIdx.x;
     // what is above may run while the stream's previous kernel ends
@@ -1047,7 +1095,7 @@ __device__ __forceinline__ void begin(const Params& P, Common& sh, bool allocate
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         asm volatile("griddepcontrol.launch_dependents;");
     }
-    plan<kThreads>(P, sh);
+    plan<kThreads, kScored>(P, sh);
     if (blockIdx.x == 0 && tid == 0) {
         const int64_t end = (int64_t)P.a.chunk.offs[P.a.chunk.B] + P.a.chunk.B;
         if (end > P.a.chunk.rows || P.a.chunk.offs[0] != 0) report(P.a.status, 1u << SV_ERR_BAD_OFFSETS);
@@ -1078,8 +1126,11 @@ cudaError_t launch_early(const void* kernel, std::atomic<unsigned long long>* al
                          void** args);
 bool encode_pool(CUtensorMap* m, const Pool& p, char* base, int esize, int kind, int box);
 bool encode_queries(CUtensorMap* m, const AttendArgs& A, int kind, int G, int q_box);
-constexpr int kFewRows = 64;  // rows of a chunk up to which sv_cache_attend_few.cu serves it
+constexpr int kFewRows = 64;  // rows of a chunk up to which sv_cache_attend_few.cuh serves it
+template <bool kScored>
 cudaError_t launch_few(Params& P, int kind, int rows, int sms, cudaStream_t st);  // sets P.part_rows and P.ctas
+template <bool kScored>
+cudaError_t launch_wide(const Params& P, int kind, int dp, int n, cudaStream_t st);
 
 }  // namespace cache
 }  // namespace sv

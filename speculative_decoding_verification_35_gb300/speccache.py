@@ -27,7 +27,7 @@ SV_F16, SV_E4M3 = 2, 3
 
 # every exported symbol of speccache.h, in header order
 EXPORTS = ("spec_cache_append", "spec_cache_workspace_size", "spec_cache_attend", "spec_cache_attend_ex",
-           "spec_cache_compact", "spec_cache_reserve")
+           "spec_cache_attend_scored", "spec_cache_compact", "spec_cache_reserve")
 
 
 class SvCache(ctypes.Structure):
@@ -50,6 +50,10 @@ class SvRope(ctypes.Structure):
                 ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class SvScores(ctypes.Structure):
+    _fields_ = [("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p), ("cap", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 class SvPages(ctypes.Structure):
     _fields_ = [("page_table", ctypes.c_void_p), ("queue", ctypes.c_void_p), ("held", ctypes.c_void_p),
                 ("state", ctypes.c_void_p), ("out_held", ctypes.c_void_p), ("out_state", ctypes.c_void_p),
@@ -68,6 +72,8 @@ def _bind():
     lib.spec_cache_attend.restype = ctypes.c_int
     lib.spec_cache_attend_ex.argtypes = lib.spec_cache_attend.argtypes[:-1] + [vp, vp]
     lib.spec_cache_attend_ex.restype = ctypes.c_int
+    lib.spec_cache_attend_scored.argtypes = lib.spec_cache_attend.argtypes[:9] + [vp] + lib.spec_cache_attend_ex.argtypes[9:]
+    lib.spec_cache_attend_scored.restype = ctypes.c_int
     lib.spec_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp]
     lib.spec_cache_compact.restype = ctypes.c_int
     lib.spec_cache_reserve.argtypes = [vp, vp, vp, i32, vp, vp, vp]
@@ -104,6 +110,14 @@ def spec_cache_attend_ex(cache, layer, chunk, dtype, q_heads, q, q_stride, scale
     """spec_cache_attend with the debug structure (specverify.SvDebug or None; spin_limit alone is read)."""
     return lib.spec_cache_attend_ex(_ref(cache), layer, _ref(chunk), dtype, q_heads, q, q_stride, scale, window, out,
                                     lse, device_status, workspace, workspace_bytes, _ref(debug), cuda_stream)
+
+
+def spec_cache_attend_scored(cache, layer, chunk, dtype, q_heads, q, q_stride, scale, window, scores, out, lse,
+                             device_status, workspace, workspace_bytes, debug, cuda_stream) -> int:
+    """spec_cache_attend_ex on capped, biased or prefixed scores (SvScores or None)."""
+    return lib.spec_cache_attend_scored(_ref(cache), layer, _ref(chunk), dtype, q_heads, q, q_stride, scale, window,
+                                        _ref(scores), out, lse, device_status, workspace, workspace_bytes, _ref(debug),
+                                        cuda_stream)
 
 
 def spec_cache_compact(cache, chunk, out_num_accepted, out_path, out_cached, device_status, cuda_stream) -> int:
@@ -269,9 +283,11 @@ class PagedCache:
                                      self._stream(stream))
 
     def attend(self, chunk: Chunk, q, out, lse=None, scale: float | None = None, window: int = 0, layer: int = 0,
-               stream=None) -> int:
+               stream=None, cap: float = 0.0, slopes=None, prefix=None) -> int:
         """Enqueue spec_cache_attend: attention of the chunk's rotated queries into out (and lse, float32
-        [rows, q_heads]). scale: 1 / sqrt(head_dim) by default; window: 0 for none, as any past every length is."""
+        [rows, q_heads]). scale: 1 / sqrt(head_dim) by default; window: 0 for none, as any past every length is.
+        cap (scores become cap tanh(score / cap)), slopes (float32 [q_heads], less for each step of distance) and prefix
+        (int32 [sequences], slots that every token sees): spec_cache_attend_scored."""
         if chunk.B > self.sequences or chunk.device != self._device or not -2 ** 31 <= layer < 2 ** 31:
             self._refuse(chunk, layer)
         rows, kind = chunk.rows, q.dtype
@@ -289,6 +305,20 @@ class PagedCache:
             scale = self.head_dim ** -0.5
         if not -2 ** 31 <= window < 2 ** 31:
             window = max(-2 ** 31, min(window, 2 ** 31 - 1))
+        if cap or slopes is not None or prefix is not None:
+            if slopes is not None:
+                _check(slopes, "slopes", (torch.float32,), (qh,), self._device)
+            if prefix is not None:
+                _check(prefix, "prefix", (torch.int32,), (chunk.B,), self._device)
+                if chunk.parents is not None:
+                    raise ValueError("a chunk of trees has no prefix")
+            for t in (slopes, prefix):
+                if t is not None and not t.is_contiguous():
+                    raise ValueError("slopes and prefix must be contiguous")
+            scores = SvScores(_ptr(slopes), _ptr(prefix), cap, 0)
+            return lib.spec_cache_attend_scored(self._at, layer, chunk.at, code, qh, q.data_ptr(), qs, scale, window,
+                                                ctypes.addressof(scores), out.data_ptr(), _ptr(lse), self._status, self._ws,
+                                                self.ws_bytes, None, self._stream(stream))
         return lib.spec_cache_attend(self._at, layer, chunk.at, code, qh, q.data_ptr(), qs, scale, window,
                                      out.data_ptr(), _ptr(lse), self._status, self._ws, self.ws_bytes,
                                      self._stream(stream))
