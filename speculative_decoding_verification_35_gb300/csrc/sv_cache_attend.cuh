@@ -192,6 +192,15 @@ __device__ __forceinline__ void tc_st16(uint32_t col, const uint32_t* r) {
         SV_W8(r, 0), SV_W8(r, 8)
         : "memory");
 }
+__device__ __forceinline__ void tc_ld4(uint32_t col, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(col));
+}
+__device__ __forceinline__ void tc_st4(uint32_t col, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(col), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
 // Shared-memory operand of 128-byte rows under the 128-byte swizzle, eight rows 1024 bytes apart: the low word
 // of its descriptor (address, and the bytes between column halves of an operand whose rows run along the depth),
 // and the high word, which all share.
@@ -339,6 +348,13 @@ __device__ __forceinline__ Seq checked_seq(const Params& P, int32_t b) {
     Seq s = seq_of(P.a.chunk, capacity_of(P.a.pool), b);
     if (!s.err && P.a.chunk.parents && !tree_ok(P.a.chunk, b, s.T)) s.err = 1u << SV_ERR_BAD_OFFSETS;
     return s;
+}
+
+// The CTA's j-th tile of an item. Where scores fall with the distance the last tiles come first: from the first to the last a
+// row's reference would move at every tile (measured, 32 rows of 4001 slots: 159 us, and 75 backwards).
+template <bool kScored>
+__device__ __forceinline__ int32_t tile_at(const Params& P, const Item& it, int32_t j) {
+    return kScored && P.a.slopes ? it.tile + it.n - 1 - j : it.tile + j;
 }
 
 // Tiles and items of a sequence, for one key head.
@@ -605,16 +621,19 @@ struct Cap {
 #pragma unroll
         for (int i = 0; i < 7; ++i) c[i] = pack2(q[i] * most, q[i] * most);
     }
-    // x up to 1
-    __device__ __forceinline__ F2 near(F2 x) const {
+    // x up to 1; and what is added to the score
+    __device__ __forceinline__ F2 near(F2 x, F2 o) const {
         const F2 y = mul2(x, x);
         F2 p = c[0];
 #pragma unroll
         for (int i = 1; i < 7; ++i) p = fma2(p, y, c[i]);
-        return mul2(p, x);
+        return fma2(p, x, o);
     }
-    __device__ __forceinline__ float far(float x) const {
-        return fmaf(-2.f * most, rcp_fast(1.f + exp2_fast(x * (2.f * kLog2e))), most);
+    // any x
+    __device__ __forceinline__ float of(float x) const {
+        float n, none;
+        unpack2(near(pack2(x, x), 0), n, none);
+        return fabsf(x) > 1.f ? fmaf(-2.f * most, rcp_fast(1.f + exp2_fast(x * (2.f * kLog2e))), most) : n;
     }
 };
 
@@ -629,6 +648,7 @@ __device__ __forceinline__ bool mixed_tile(const Item& it, int32_t k0) {
 // ---------------------------------------------------------------------------------------------------------
 // Tiles of keys (first 0) and values (last 1), or of one of them. P.halves: column halves of 128 bytes a row, one
 // after the other in a slot.
+template <bool kScored>
 __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t k_smem, uint32_t v_smem, const CUtensorMap* km,
                                           const CUtensorMap* vm, int first, int last) {
     const int lane = threadIdx.x & 31;
@@ -645,7 +665,7 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
         const int32_t* table = P.a.pool.table + (int64_t)it.b * P.a.pool.table_stride;
         const int32_t head = __shfl_sync(kAll, it.h, 0), n = __shfl_sync(kAll, it.n, 0);
         // where a lane's box of a tile lies; its page's id is read a tile ahead
-        int32_t slot = it.tile * kTile + lane * box, i = slot / ps, in = slot - i * ps;
+        int32_t slot = tile_at<kScored>(P, it, 0) * kTile + lane * box, i = slot / ps, in = slot - i * ps;
         bool next_need = false;
         int32_t next_page = -1, next_at = 0;
 #pragma unroll 1
@@ -655,12 +675,22 @@ __device__ __forceinline__ void load_role(const Params& P, Common& sh, uint32_t 
             next_need = j + 1 < n && lane < boxes && slot < it.end && slot + box > it.lo;
             next_at = in;
             next_page = next_need ? table[i] : -1;
-            slot += kTile;
-            i += P.tile_pages;
-            in += P.tile_rest;
-            if (in >= ps) {
-                in -= ps;
-                ++i;
+            if (kScored && P.a.slopes) {
+                slot -= kTile;
+                i -= P.tile_pages;
+                in -= P.tile_rest;
+                if (in < 0) {
+                    in += ps;
+                    --i;
+                }
+            } else {
+                slot += kTile;
+                i += P.tile_pages;
+                in += P.tile_rest;
+                if (in >= ps) {
+                    in -= ps;
+                    ++i;
+                }
             }
             if (j < 0) continue;
             const bool miss = need && (page < 0 || page >= P.a.pool.pages);
@@ -1009,7 +1039,7 @@ __device__ __forceinline__ void item_role(const Params& P, Common& sh, uint32_t 
 // Value tiles before they are multiplied: rows of slots that no row of the item sees are cleared
 // (they may hold anything, and a weight of zero times NaN is NaN), and so are single non-finite values that only
 // some rows see; those are noted for the rows that do.
-template <int K>
+template <int K, bool kScored>
 __device__ __forceinline__ void value_role(const Params& P, Common& sh, uint32_t v_smem) {
     const int lane = threadIdx.x & 31;
     const Limit limit{&sh.gave_up, P.polls};
@@ -1022,7 +1052,7 @@ __device__ __forceinline__ void value_role(const Params& P, Common& sh, uint32_t
 #pragma unroll 1
         for (int32_t j = 0; j < it.n; ++j, ++v, ring.step(P.v_slots)) {
             if (!wait(smem_u32(&sh.v_full[ring.i]), ring.parity, limit)) return;
-            const int32_t k0 = (it.tile + j) * kTile;
+            const int32_t k0 = tile_at<kScored>(P, it, j) * kTile;
             const uint32_t bad = sh.bad[1][v % kNotes];
             const bool mixed = mixed_tile(it, k0);
             if (rarely(bad || k0 < it.lo || k0 + kTile > it.end || mixed)) {

@@ -84,6 +84,11 @@ struct alignas(16) Shared : Common {
     uint64_t s_full[2], p_ready, pv_done;
     Group<NR / G, G> group[G];
 };
+// kScored: of the rows, a copy for every softmax warp.
+template <int N>
+struct alignas(16) Bias {
+    float slope[N], pos[N];
+};
 
 // A barrier of a group's warps; what lies between the two calls needs no one.
 struct Vote {
@@ -116,11 +121,6 @@ __device__ __forceinline__ void tc_ld1(uint32_t col, uint32_t& r) {
 __device__ __forceinline__ void tc_st1(uint32_t col, uint32_t r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(col), "r"(r) : "memory");
 }
-__device__ __forceinline__ void tc_ld4(uint32_t col, uint32_t* r) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(col));
-}
 // e4m3 weights in pairs: what rounding gives, and 2^kLow of what it leaves
 template <int kLow>
 __device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -148,52 +148,37 @@ __device__ __forceinline__ uint32_t rows_seeing(const Params& P, const Item& it,
     return m;
 }
 
-// kScored: a slot's scores of the rows become log2 of the weights, capped and biased. slope, from: a lane's, of the row of its
-// number; at: the slot's position, both counted from the first chunk token.
+// kScored, capped: the rows' scores of a slot, in place. False, for the whole warp, where some lie past the cap.
 template <int K, int N>
-__device__ __forceinline__ void score(const AttendArgs& A, uint32_t* s, const float* u, int32_t rows, float slope, float from, float at) {
-    const Cap cap(A.cap > 0.f ? A.cap : 1.f);
+__device__ __forceinline__ bool near(const Cap& cap, uint32_t* s, const float* u, int32_t rows) {
     float big = 0.f;
-    const float by = A.cap > 0.f ? cap.by : 1.f;
 #pragma unroll
     for (int r = 0; r < N; r += 4) {
         if (r >= rows) break;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float x = __uint_as_float(s[r + e]) * (u[K == kE4m3 ? r + e : 0] * by);
+            const float x = __uint_as_float(s[r + e]) * (u[K == kE4m3 ? r + e : 0] * cap.by);
             big = fmaxf(big, fabsf(x));
             s[r + e] = __float_as_uint(x);
         }
     }
-    const bool far = A.cap > 0.f && __any_sync(kAll, big > 1.f);
+    if (rarely(__any_sync(kAll, big > 1.f))) return false;
 #pragma unroll
     for (int r = 0; r < N; r += 4) {
         if (r >= rows) break;
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-            float a = __uint_as_float(s[r + e]), b = __uint_as_float(s[r + e + 1]);
-            if (A.cap > 0.f) {
-                float x, y;
-                unpack2(cap.near(pack2(a, b)), x, y);
-                if (rarely(far)) {
-                    x = fabsf(a) > 1.f ? cap.far(a) : x;
-                    y = fabsf(b) > 1.f ? cap.far(b) : y;
-                }
-                a = x;
-                b = y;
-            }
-            if (A.slopes) {
-                a = fmaf(-__shfl_sync(kAll, slope, r + e), fabsf(__shfl_sync(kAll, from, r + e) - at), a);
-                b = fmaf(-__shfl_sync(kAll, slope, r + e + 1), fabsf(__shfl_sync(kAll, from, r + e + 1) - at), b);
-            }
+            float a, b;
+            unpack2(cap.near(pack2(__uint_as_float(s[r + e]), __uint_as_float(s[r + e + 1])), 0), a, b);
             s[r + e] = __float_as_uint(a);
             s[r + e + 1] = __float_as_uint(b);
         }
     }
+    return true;
 }
 
 template <int K, int NR, int G, bool kScored>
-__device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh, char* weights) {
+__device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh, char* weights, Bias<NR / G>* biases) {
     using KT = KindOf<K>;
     using T = typename KT::T;
     using Wt = Weights<K, NR>;
@@ -209,6 +194,8 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
     constexpr int kParts = K == kE4m3 ? 2 : 1;
     const int32_t D = A.pool.dim;
     const Limit limit{&sh.gave_up, P.polls};
+    const Cap cap(kScored && A.cap > 0.f ? A.cap : 1.f);
+    const bool scored = kScored && (A.cap > 0.f || A.slopes);
     Vote vote{smem_u32(&mine.vote), 0, limit};
     uint32_t steps = 0, tiles = 0, votes = 0;  // votes: on weights, modulo 3
     bool owed = false;  // a vote of the last item's end has been given and not passed: others may still read the notes
@@ -223,6 +210,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
         const float unit = score_unit(A, it.h, flip);
         float l[N], off[N], u[K == kE4m3 ? N : 1];  // weights are 2^(u s + off)
         u[0] = unit;
+        const float last = scored ? 1.f : unit;  // kScored: what is left to multiply
         // The loops below take four rows at a time. Those past the item's last have another sequence's queries, or what
         // an earlier item left (e4m3: and an unset factor): their weights are zero, or nothing would keep their scores
         // from voting on the references, and so from changing the roundings of the item's own rows.
@@ -234,11 +222,22 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
         // every warp settles the references by itself, from the same notes: a lane has a row's (off again, and whether
         // there is a reference at all)
         float own_off = Wt::kShift;
-        float own_slope = 0.f, own_pos = 0.f;  // kScored: log2 of the weight that a step of distance costs, and where it counts from
-        if (kScored && lane < rows) {
-            const int32_t t = (row0 + lane) / P.G;
-            if (A.slopes) own_slope = A.slopes[it.h * P.G + row0 + lane - t * P.G] * kLog2e;
-            own_pos = (float)(tree ? tree->depth[t] : t);
+        Bias<N>& bias = biases[threadIdx.x >> 5];
+        if (kScored && A.slopes) {
+            float slope = 0.f, pos = 0.f;
+            if (lane < rows) {
+                const int32_t t = (row0 + lane) / P.G;
+                slope = A.slopes[it.h * P.G + row0 + lane - t * P.G] * kLog2e;
+                pos = (float)(tree ? tree->depth[t] : t);
+            }
+            __syncwarp();
+            if (lane < N) {
+                bias.slope[lane] = slope;
+                bias.pos[lane] = pos;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < N; ++r) off[r] = fmaf(-bias.slope[r], bias.pos[r], off[r]);
         }
         bool own = false, unset = true;
 #pragma unroll 1
@@ -255,7 +254,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                         u[r + e] = row_unit(unit, sh.q_down[walk.ring.i * sh.q_rows + row0 + r + e]);
                 }
             const uint32_t s_col = tmem + buf * NR;
-            const int32_t k0 = (it.tile + j) * kTile;
+            const int32_t k0 = tile_at<kScored>(P, it, j) * kTile;
             const uint32_t ring = (tiles + j) % kNotes;
             const uint32_t bad = sh.bad[0][ring];
             const bool cut = k0 < max(it.lo, it.mixed_lo) || k0 + kTile > min(it.mixed_hi, it.end) || bad;
@@ -263,7 +262,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
             if (rarely(cut)) seen = rows_seeing<kScored>(P, it, tree, k0 + k, bad, row0);
             uint32_t s[N];
             // Once, mostly: while the votes come in that no weight is too large, the weights are taken as if none were.
-            bool fresh = unset;
+            bool fresh = unset, done = false;  // done: kScored, the scores lie capped in their place
 #pragma unroll 1
             for (;;) {
 #pragma unroll
@@ -275,7 +274,47 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                 if (kScored) {
                     int32_t i = k0 + k - it.past;  // a chunk token of a tree lies at another position than its slot
                     if (rarely(tree && i >= 0 && i < it.nt)) i = tree->depth[i];
-                    score<K, N>(A, s, u, rows, own_slope, own_pos, (float)i);
+                    if (A.cap > 0.f && !done && !near<K, N>(cap, s, u, rows)) {
+                        // some score lies past the cap: all of them in their place, and again
+#pragma unroll 1
+                        for (int r = 0; r < rows; r += 4) {
+                            uint32_t x[4];
+                            tc_ld4(s_col + r, x);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float f = K == kE4m3 ? row_unit(unit, sh.q_down[walk.ring.i * sh.q_rows + row0 + r + e]) : unit;
+                                x[e] = __float_as_uint(cap.of(__uint_as_float(x[e]) * (f * cap.by)));
+                            }
+                            tc_st4(s_col + r, x);
+                        }
+                        tc_wait_st();
+                        done = true;
+                        continue;
+                    }
+                    if (A.slopes) {
+                        const float at = (float)i;
+                        const bool behind = A.prefix && i > 0;  // some rows lie before the slot: the distance is at - pos, not pos - at
+#pragma unroll
+                        for (int r = 0; r < N; r += 4) {
+                            if (r >= rows) break;
+                            const float4 k = *reinterpret_cast<const float4*>(bias.slope + r);
+                            float x[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                x[e] = __uint_as_float(s[r + e]);
+                                if (!(A.cap > 0.f)) x[e] *= u[K == kE4m3 ? r + e : 0];
+                            }
+                            x[0] = fmaf(k.x, at, x[0]), x[1] = fmaf(k.y, at, x[1]), x[2] = fmaf(k.z, at, x[2]), x[3] = fmaf(k.w, at, x[3]);
+                            if (rarely(behind)) {
+                                const float4 p = *reinterpret_cast<const float4*>(bias.pos + r);
+                                x[0] = fmaf(k.x, fminf(0.f, p.x - at) * 2.f, x[0]), x[1] = fmaf(k.y, fminf(0.f, p.y - at) * 2.f, x[1]);
+                                x[2] = fmaf(k.z, fminf(0.f, p.z - at) * 2.f, x[2]), x[3] = fmaf(k.w, fminf(0.f, p.w - at) * 2.f, x[3]);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[r + e] = __float_as_uint(x[e]);
+                        }
+                    }
                 }
                 if (rarely(cut))
 #pragma unroll
@@ -292,7 +331,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
                     if (r >= rows) break;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float y = kScored ? __uint_as_float(s[r + e]) + off[r + e] : fmaf(__uint_as_float(s[r + e]), u[K == kE4m3 ? r + e : 0], off[r + e]);
+                        const float y = fmaf(__uint_as_float(s[r + e]), kScored && K == kE4m3 ? (scored ? 1.f : u[r + e]) : kScored ? last : u[K == kE4m3 ? r + e : 0], off[r + e]);
                         s[r + e] = __float_as_uint(y);
                         top = fmaxf(top, y);
                     }
@@ -534,7 +573,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared<NR, G>& sh,
 // The products, by one thread, in the order in which they become possible: a tile's scores, into one of two buffers, once
 // its keys are in (an item's first: its queries too); its outputs, once its weights and values are. Scores run up to two
 // tiles ahead, also into the next item.
-template <int K, int NR, int G>
+template <int K, int NR, int G, bool kScored>
 __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh, uint32_t q_smem, uint32_t p_smem, uint32_t k_smem,
                                              uint32_t v_smem) {
     constexpr bool k8 = K == kE4m3;
@@ -582,7 +621,7 @@ __device__ __forceinline__ void product_role(const Params& P, Shared<NR, G>& sh,
             }
             __syncwarp();
             int32_t lo, hi;
-            steps_of<K>(it, (it.tile + j) * kTile, lo, hi);
+            steps_of<K>(it, tile_at<kScored>(P, it, j) * kTile, lo, hi);
             notes = (notes & ~(0xffffu << 16 * buf)) | (uint32_t)(lo | hi << 4 | (j == 0) << 8) << 16 * buf;
             kr.step(P.k_slots);
             ++scores;
@@ -670,12 +709,13 @@ __global__ void __launch_bounds__(kThreads<G>, G == 1 ? 2 : 1)
     if (role < 0) {
         if (G == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        softmax_role<K, NR, G, kScored>(P, sh, raw + P.q_bufs * P.q_bytes);
+        softmax_role<K, NR, G, kScored>(P, sh, raw + P.q_bufs * P.q_bytes,
+                                        reinterpret_cast<Bias<NR / G>*>(sh.q_down + (K == kE4m3 ? kItems * NR : 0)));
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (role == 0) load_role(P, sh, k_smem, v_smem, &km, &vm, 0, 1);
-        else if (role == 1) product_role<K, NR, G>(P, sh, q_smem, p_smem, k_smem, v_smem);
-        else if (role == 2) value_role<K>(P, sh, v_smem);
+        if (role == 0) load_role<kScored>(P, sh, k_smem, v_smem, &km, &vm, 0, 1);
+        else if (role == 1) product_role<K, NR, G, kScored>(P, sh, q_smem, p_smem, k_smem, v_smem);
+        else if (role == 2) value_role<K, kScored>(P, sh, v_smem);
         else item_role<K, 1, kScored>(P, sh, q_smem, &qm);
     }
     tc_before();
@@ -698,7 +738,7 @@ cudaError_t launch(Params& P, int sms, cudaStream_t st) {
     P.lead = halves == 2 ? 1 : 2;  // measured on the cases above: others of 0 to 4 are 1 to 30 % slower
     P.q_tile = (K == kE4m3 ? 2 : halves) * P.q_part;
     const int own = (int)(sizeof(Shared<NR, G>) + 15) / 16 * 16 + (A.chunk.parents ? kItems * (int)sizeof(Tree) : 0) +
-                    (K == kE4m3 ? kItems * NR * 4 : 0);
+                    (K == kE4m3 ? kItems * NR * 4 : 0) + (kScored && A.slopes ? 4 * G * (int)sizeof(Bias<NR / G>) : 0);
     P.q_bytes = P.q_tile;
     auto slots_of = [&](int bufs) {
         const int rest = (G == 1 ? kHalfSm : kSmem) - bufs * P.q_bytes - Weights<K, NR>::kBytes - own;

@@ -81,7 +81,7 @@ __device__ __forceinline__ Row row_of(const Params& P, const Item& it, const Ite
         row.pos = pos;
         row.slope = A.slopes && row.real ? A.slopes[it.h * P.G + g] * kLog2e : 0.f;
         row.raw = row.sl;
-        row.sl = 1.f;
+        if (A.cap > 0.f || A.slopes) row.sl = 1.f;
     }
     return row;
 }
@@ -171,63 +171,64 @@ __device__ __forceinline__ void hide_tile(uint32_t s_col, const uint32_t* seen) 
     }
     tc_wait_st();
 }
-// kScored: scores become log2 of the weights, capped and biased, in their place. A pass of its own over the tile, 32 columns
-// at a time.
-__device__ __forceinline__ void score_tile(const AttendArgs& A, const Row& row, const Item& it, const Items& items, uint32_t s_col, int32_t k0) {
-    const Cap cap(A.cap > 0.f ? A.cap : 1.f);
-    const float by = A.cap > 0.f ? row.raw * cap.by : row.raw;
-    const F2 by2 = pack2(by, by), down = pack2(-row.slope, -row.slope);
-    const bool tree = A.chunk.parents != nullptr;
+// kScored: what becomes of the scores.
+struct Scoring {
+    Cap cap;
+    bool capped, biased;
+    float by;
+    __device__ __forceinline__ explicit Scoring(const AttendArgs& A)
+        : cap(A.cap > 0.f ? A.cap : 1.f), capped(A.cap > 0.f), biased(A.slopes != nullptr), by(capped ? cap.by : 1.f) {}
+    // 32 scores of a row, times f, capped, in place; col: where they lie in tensor memory, which is free to be written.
+    __device__ __forceinline__ void cap32(uint32_t* s, float f, uint32_t col) const {
+        const F2 f2 = pack2(f, f);
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) big = fmaxf(big, fmaxf(fabsf(__uint_as_float(s[i])), fabsf(__uint_as_float(s[i + 1]))));
+        if (rarely(__any_sync(kAll, big * f > 1.f))) {  // some lie past the cap: in a few instructions
+#pragma unroll 1
+            for (int c = 0; c < 32; c += 4) {
+                uint32_t x[4];
+                tc_ld4(col + c, x);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = __float_as_uint(cap.of(__uint_as_float(x[i]) * f));
+                tc_st4(col + c, x);
+            }
+            tc_wait_st();
+            tc_ld32(col, s);
+            tc_wait_ld();
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            float a, b;
+            unpack2(cap.near(mul2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), f2), 0), a, b);
+            s[i] = __float_as_uint(a);
+            s[i + 1] = __float_as_uint(b);
+        }
+    }
+};
+// A tile's scores become logarithms of the weights, in their place: a pass of its own.
+__device__ __forceinline__ void score_tile(const Scoring& sc, bool tree, const Row& row, const Item& it, const Items& items, uint32_t s_col,
+                                        int32_t k0) {
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
         uint32_t s[32];
-        F2 x[16];
         tc_ld32(s_col + 32 * q, s);
         tc_wait_ld();
-        float big = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            big = fmaxf(big, fmaxf(fabsf(__uint_as_float(s[2 * i])), fabsf(__uint_as_float(s[2 * i + 1]))));
-            x[i] = mul2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), by2);
-        }
-        if (A.cap > 0.f) {
-            if (rarely(__any_sync(kAll, big * by > 1.f))) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float a, b;
-                    unpack2(x[i], a, b);
-                    const F2 n = cap.near(x[i]);
-                    float na, nb;
-                    unpack2(n, na, nb);
-                    x[i] = pack2(fabsf(a) > 1.f ? cap.far(a) : na, fabsf(b) > 1.f ? cap.far(b) : nb);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = cap.near(x[i]);
-            }
-        }
-        if (A.slopes) {
+        if (sc.capped) sc.cap32(s, row.raw * sc.by, s_col + 32 * q);
+        if (sc.biased) {
+            const float unit = sc.capped ? 1.f : row.raw;
             const int32_t at = k0 + 32 * q;
             const float far = (float)(row.pos - at);
             const bool nodes = tree && at + 32 > it.past;  // chunk tokens of a tree lie at other positions than their slots
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float d[2] = {far - (float)(2 * i), far - (float)(2 * i + 1)};
-                if (rarely(nodes))
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int32_t t = at + 2 * i + e - it.past;
-                        if (t >= 0 && t < it.nt) d[e] = (float)(row.pos - it.past - items.tree().depth[t]);
-                    }
-                x[i] = fma2(pack2(fabsf(d[0]), fabsf(d[1])), down, x[i]);
+            for (int i = 0; i < 32; ++i) {
+                float d = far - (float)i;
+                const int32_t t = at + i - it.past;
+                if (rarely(nodes) && t >= 0 && t < it.nt) d = (float)(row.pos - it.past - items.tree().depth[t]);
+                s[i] = __float_as_uint(fmaf(-row.slope, fabsf(d), __uint_as_float(s[i]) * unit));
             }
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float a, b;
-            unpack2(x[i], a, b);
-            s[2 * i] = __float_as_uint(a);
-            s[2 * i + 1] = __float_as_uint(b);
         }
         tc_st32(s_col + 32 * q, s);
     }
@@ -329,6 +330,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
     const int32_t tl = r / P.G, g = r - tl * P.G;
     uint32_t steps = 0;   // of this stream, over all items
     uint32_t tiles = 0;   // of the CTA, before this item
+    const Scoring scoring(A);  // kScored
 
     Items walk(P, sh);
     Item it;
@@ -341,25 +343,25 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
 #pragma unroll 1
         for (int32_t j = 0; j < it.n; ++j, ++steps) {
             // what needs no scores, before them
-            const int32_t k0 = (it.tile + j) * kTile;
+            const int32_t k0 = tile_at<kScored>(P, it, j) * kTile;
             const uint32_t ring = (tiles + j) % kNotes;
             const bool whole = __all_sync(kAll, (k0 + kTile <= row.limit && row.low <= k0) || !row.real);
             const bool mixed = mixed_tile(it, k0);
             if (!wait(s_full, steps & 1, limit)) return;
             tc_after();
             if (K == kE4m3 && j == 0) {
-                float& unit = kScored ? row.raw : row.sl;
+                float& unit = kScored && (scoring.capped || scoring.biased) ? row.raw : row.sl;
                 unit = row_unit(unit, sh.q_down[walk.ring.i * sh.q_rows + stream * kTile + r]);
             }
             uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
             if (busy) {
-                if (kScored) score_tile(A, row, it, walk, s_col, k0);
                 const uint32_t bad = sh.bad[0][ring];
+                float sum;
+                if (kScored && (scoring.capped || scoring.biased)) score_tile(scoring, tree, row, it, walk, s_col, k0);
                 if (!whole || bad) {
                     seen_of(row, it, k0, bad, tree, seen);
                     hide_tile(s_col, seen);
                 }
-                float sum;
                 bool first = K == kE4m3 || unset;
 #pragma unroll 1
                 for (;; first = true) {
@@ -477,7 +479,7 @@ __device__ __forceinline__ void softmax_role(const Params& P, Shared& sh) {
 // A stream's products, by one thread: S = Q K^T of its next tile follows O += P V of this one, whose P lies where that
 // S will. The streams take turns, each turn both products: left to themselves they fall into step, both at their
 // products and then both at their exponentials (measured: 4200 cycles a tile of 256 rows, 3050 in turns).
-template <int K, int NH>
+template <int K, int NH, bool kScored>
 __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem,
                                              const uint32_t st) {
     constexpr bool k8 = K == kE4m3;
@@ -528,7 +530,7 @@ __device__ __forceinline__ void product_role(const Params& P, Shared& sh, uint32
                 const uint32_t b = operand(v_smem + vr.i * slot_bytes, kHalf);
                 const uint32_t add = t > 0;
                 int32_t lo, hi;
-                steps_of<K>(it, (it.tile + t) * kTile, lo, hi);
+                steps_of<K>(it, tile_at<kScored>(P, it, t) * kTile, lo, hi);
                 if (leader) {
 #pragma unroll
                     for (int i = 0; i < kTile / KindOf<K>::kStep; ++i)
@@ -612,9 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         softmax_role<K, DP, kScored>(P, sh);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (w == 8 || w == 10) load_role(P, sh, k_smem, v_smem, &km, &vm, w == 10, w == 10);
-        else if (w == 9 || w == 13) product_role<K, NH>(P, sh, q_smem, k_smem, v_smem, w == 13);
-        else if (w == 11) value_role<K>(P, sh, v_smem);
+        if (w == 8 || w == 10) load_role<kScored>(P, sh, k_smem, v_smem, &km, &vm, w == 10, w == 10);
+        else if (w == 9 || w == 13) product_role<K, NH, kScored>(P, sh, q_smem, k_smem, v_smem, w == 13);
+        else if (w == 11) value_role<K, kScored>(P, sh, v_smem);
         else if (w == 12) item_role<K, kSplitters, kScored>(P, sh, q_smem, &qm);
         else if (K == kE4m3 && w >= 14) query_role(P, sh, q_smem, w - 14, kSplitters);
     }
