@@ -88,6 +88,8 @@ struct ReserveArgs {
     int32_t B;
     int64_t* slots;
     uint32_t* status;
+    uint32_t page_recip;  // set by the launch: a division by page_size is a product and a shift
+    int32_t page_bits;
 };
 constexpr int32_t kMaxReserve = 1 << 16;  // sequences of a call
 

@@ -12,6 +12,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "sv_cache.cuh"
 
@@ -21,15 +22,17 @@ namespace sv {
 namespace cache {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCtas = 8;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCtas = 16;
+constexpr int kAtOnce = 4, kSmall = 1024;
 constexpr unsigned kAll = 0xffffffffu;
 typedef unsigned long long u64;
 
-// A block of sequences, one a thread.
+// A block of sequences, one a thread. The sums are those before each sequence, and of all. They are kept to 2^32 - 1, which
+// only sums that are refused exceed, and rows that several sequences claim.
 struct Block {
     int32_t held[kThreads], need[kThreads], past[kThreads], row0[kThreads];
-    bool fine[kThreads];                                              // has no finding and got what it needs
-    u64 give[kThreads + 1], take[kThreads + 1], rows[kThreads + 1];  // sums before each
+    bool fine[kThreads];  // has no finding and got what it needs
+    uint32_t give[kThreads + 1], take[kThreads + 1], rows[kThreads + 1];
     u64 scan[3][kWarps];
     u64 served;  // pages that the block's sequences take
 };
@@ -55,76 +58,99 @@ __device__ __forceinline__ u64 inscan(u64 v) {
     return v;
 }
 // The entry of `sums` (kThreads + 1 of them) in which i lies.
-__device__ __forceinline__ int find(const u64* sums, u64 i) {
+__device__ __forceinline__ int find(const uint32_t* sums, uint32_t i) {
     int lo = 0;
 #pragma unroll
     for (int o = kThreads / 2; o; o >>= 1)
         if (sums[lo + o] <= i) lo += o;
     return lo;
 }
-
-// The queue's entry i behind its head; i < pages.
-__device__ __forceinline__ int32_t* queue_at(const ReserveArgs& A, int64_t head, u64 i) {
-    const u64 at = (u64)head + i;
-    return A.queue + (at < (u64)A.pages ? at : at - (u64)A.pages);
+// The queue's entry i behind its head; both below `pages`.
+__device__ __forceinline__ int32_t* queue_at(const ReserveArgs& A, uint32_t head, uint32_t i) {
+    const uint32_t at = head + i;
+    return A.queue + (at < (uint32_t)A.pages ? at : at - (uint32_t)A.pages);
+}
+// n / page_size for 0 <= n < 2^31: page_recip is 2^(31 + L) / page_size, rounded up, L = page_bits the least with 2^L >= page_size
+// (the rounding adds less than 2^L to page_recip page_size, and so less than 1 / page_size to the quotient).
+__device__ __forceinline__ int32_t page_of(const ReserveArgs& A, int32_t n) {
+    return (int32_t)(((u64)(uint32_t)n * A.page_recip) >> (31 + A.page_bits));
 }
 
-// The block of the sequences from b0 on: what they need, and the sums. before: pages that earlier blocks would take;
-// count: free pages, with those given back. All threads; ends with a barrier. Returns the thread's finding.
-__device__ __forceinline__ uint32_t read_block(const ReserveArgs& A, Block& s, int32_t b0, u64 before, u64 count, bool bad) {
+// A thread's sequence, and what it gives back, takes and has of rows, by itself and with those before it.
+struct Mine {
+    int32_t b, held, need;
+    uint32_t err;
+    u64 gives, takes, takes_upto;
+};
+
+// The block of the sequences from b0 on, with its sums. All threads; ends with a barrier. Returns what the block gives back.
+__device__ __forceinline__ u64 read_block(const ReserveArgs& A, Block& s, int32_t b0, Mine& me, u64& takes) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int32_t b = b0 + tid;
-    uint32_t err = 0;
-    int32_t held = 0, need = 0;
+    me = Mine{};
+    me.b = b0 + tid;
     u64 v[3] = {0, 0, 0};  // gives, takes, rows
-    if (b < A.B) {
-        held = A.held[b];
+    if (me.b < A.B) {
+        me.held = A.held[me.b];
         int64_t n;
         if (A.lengths) {
-            n = A.lengths[b];
+            n = A.lengths[me.b];
         } else {
-            const Seq q = seq_of(A.chunk, 0x7fffffff, b);
-            err = q.err;
-            n = (int64_t)q.past + q.T;
-            if (q.past < 0) n = -1;
+            const Seq q = seq_of(A.chunk, 0x7fffffff, me.b);
+            me.err = q.err;
+            n = q.past < 0 ? -1 : (int64_t)q.past + q.T;
             if (q.rows_ok) v[2] = (u64)q.T;
             s.past[tid] = q.past;
             s.row0[tid] = q.row0;
         }
-        if (held < 0 || held > A.table_stride) err |= 1u << SV_ERR_BAD_OFFSETS;
+        if (me.held < 0 || me.held > A.table_stride) me.err |= 1u << SV_ERR_BAD_OFFSETS;
         const int64_t pages = (n + A.page_size - 1) / A.page_size;
-        if (n < 0 || pages > A.table_stride) err |= 1u << SV_ERR_CAPACITY;
-        need = err || bad ? held : (int32_t)pages;
-        if (!err && !bad) {
-            if (need < held) v[0] = (u64)(held - need);
-            else v[1] = (u64)(need - held);
+        if (n < 0 || pages > A.table_stride) me.err |= 1u << SV_ERR_CAPACITY;
+        me.need = me.err ? me.held : (int32_t)pages;
+        if (!me.err) {
+            if (me.need < me.held) v[0] = (u64)(me.held - me.need);
+            else v[1] = (u64)(me.need - me.held);
         }
     }
-    u64 upto[3];
+    u64 upto[3], all[3] = {0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         upto[i] = inscan(v[i]);
         if (lane == 31) s.scan[i][warp] = upto[i];
     }
-    if (tid == 0) s.served = 0;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        u64 x = upto[i];
-        for (int w = 0; w < warp; ++w) x += s.scan[i][w];
-        u64* sums = i == 0 ? s.give : i == 1 ? s.take : s.rows;
-        sums[tid] = x - v[i];
-        if (tid == kThreads - 1) sums[kThreads] = x;
-        upto[i] = x;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const u64 x = s.scan[i][w];
+            if (w < warp) upto[i] += x;
+            all[i] += x;
+        }
+        uint32_t* sums = i == 0 ? s.give : i == 1 ? s.take : s.rows;
+        sums[tid] = (uint32_t)min(upto[i] - v[i], 0xffffffffull);
+        if (tid == 0) sums[kThreads] = (uint32_t)min(all[i], 0xffffffffull);
     }
-    const bool served = before + upto[1] <= count;
-    if (!served && v[1]) err |= 1u << SV_ERR_CAPACITY;
-    if (served && v[1]) atomicMax(&s.served, upto[1]);
-    s.held[tid] = held;
-    s.need[tid] = served || !v[1] ? need : held;
-    s.fine[tid] = b < A.B && !err && !bad;
+    s.held[tid] = me.held;
+    s.need[tid] = me.need;
+    if (tid == 0) s.served = 0;
+    me.gives = v[0];
+    me.takes = v[1];
+    me.takes_upto = upto[1];
+    takes = all[1];
     __syncthreads();
-    return err;
+    return all[0];
+}
+// Who gets what it lacks, of `free` pages, after the blocks before took (or would have) `before`. All threads; ends with a barrier.
+__device__ __forceinline__ void serve(Block& s, Mine& me, u64 before, u64 free, bool bad, int32_t B) {
+    const int tid = threadIdx.x;
+    const bool served = !bad && before + me.takes_upto <= free;
+    if (bad || (!served && me.takes)) me.need = me.held;
+    if (!bad && !served && me.takes) me.err |= 1u << SV_ERR_CAPACITY;
+    const unsigned who = __ballot_sync(kAll, served && me.takes);
+    if (who && (tid & 31) == 31 - __clz(who)) atomicMax(&s.served, me.takes_upto);
+    s.need[tid] = me.need;
+    s.fine[tid] = me.b < B && !me.err && !bad;
+    __syncthreads();
 }
 
 __global__ void __launch_bounds__(kThreads) k_cache_reserve(const __grid_constant__ ReserveArgs A) {
@@ -134,74 +160,91 @@ __global__ void __launch_bounds__(kThreads) k_cache_reserve(const __grid_constan
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Team team{(int)blockIdx.x, (int)gridDim.x};
     const int tid = threadIdx.x;
-    const u64 me = (u64)team.rank * kThreads + tid, step = (u64)team.size * kThreads;
+    const uint32_t first = (uint32_t)(team.rank * kThreads + tid), step = (uint32_t)(team.size * kThreads);
     const bool once = A.B <= kThreads;
-    const int64_t head = A.state[0];
-    int64_t count = A.state[1];
-    const u64 pages = (u64)A.pages;
+    const int32_t head = A.state[0], count = A.state[1];
     bool bad = head < 0 || head >= A.pages || count < 0;
     uint32_t err = 0;
+    Mine me{};
+    u64 takes = 0;
 
     // what is given back in all
     u64 gives = 0;
 #pragma unroll 1
     for (int32_t b0 = 0; b0 < A.B; b0 += kThreads) {
         if (b0 > 0) __syncthreads();
-        read_block(A, s, b0, 0, 0, false);
-        gives += s.give[kThreads];
+        gives += read_block(A, s, b0, me, takes);
     }
-    if (bad || (u64)count + gives > pages) bad = true;
-    if (bad) gives = 0;
+    bad = bad || (u64)count + gives > (u64)A.pages;
     // into the queue, behind its last
-    u64 base = 0;
+    uint32_t given = 0;
 #pragma unroll 1
-    for (int32_t b0 = 0; b0 < A.B && gives > 0; b0 += kThreads) {
+    for (int32_t b0 = 0; b0 < A.B && gives > 0 && !bad; b0 += kThreads) {
         if (!once) {
             __syncthreads();
-            read_block(A, s, b0, 0, 0, false);
+            read_block(A, s, b0, me, takes);
         }
-        for (u64 i = me; i < s.give[kThreads]; i += step) {
+        for (uint32_t i = first; i < s.give[kThreads]; i += step) {
             const int t = find(s.give, i);
-            const int32_t id = A.table[(int64_t)(b0 + t) * A.table_stride + s.need[t] + (int64_t)(i - s.give[t])];
+            const int32_t id = A.table[(int64_t)(b0 + t) * A.table_stride + (s.need[t] + (int32_t)(i - s.give[t]))];
             if (id < 0 || id >= A.pages) report(A.status, 1u << SV_ERR_BAD_OFFSETS);
-            *queue_at(A, head, (u64)count + base + i) = id;
+            *queue_at(A, head, (uint32_t)count + given + i) = id;
         }
-        base += s.give[kThreads];
+        given += s.give[kThreads];
     }
     team.sync();
     const u64 free = bad ? 0 : (u64)count + gives;
     // out of it, from the front; and the slots
-    base = 0;
-    u64 taken = 0;
+    u64 base = 0, taken = 0;
 #pragma unroll 1
     for (int32_t b0 = 0; b0 < A.B; b0 += kThreads) {
-        if (b0 > 0) __syncthreads();
-        err |= read_block(A, s, b0, base, free, bad);
-        if (tid == 0) block_base[b0 / kThreads] = base;
-        const u64 served = s.served;
-        for (u64 i = me; i < served; i += step) {
-            const int t = find(s.take, i);
-            const int32_t id = __ldcg(queue_at(A, head, base + i));
-            if (id < 0 || id >= A.pages) report(A.status, 1u << SV_ERR_BAD_OFFSETS);
-            A.table[(int64_t)(b0 + t) * A.table_stride + s.held[t] + (int64_t)(i - s.take[t])] = id;
+        if (!once) {
+            __syncthreads();
+            read_block(A, s, b0, me, takes);
         }
-        if (A.slots)
-            for (u64 i = me; i < s.rows[kThreads]; i += step) {
-                const int t = find(s.rows, i);
-                const int32_t j = (int32_t)(i - s.rows[t]);
-                int64_t at = -1;
-                if (s.fine[t]) {
-                    const int32_t slot = s.past[t] + j, k = slot / A.page_size;
-                    const int32_t id = k < s.held[t] ? A.table[(int64_t)(b0 + t) * A.table_stride + k]
-                                                     : __ldcg(queue_at(A, head, base + s.take[t] + (u64)(k - s.held[t])));
-                    if (id >= 0 && id < A.pages) at = (int64_t)id * A.page_size + (slot - k * A.page_size);
-                    else report(A.status, 1u << SV_ERR_BAD_OFFSETS);
+        serve(s, me, base, free, bad, A.B);
+        err |= me.err;
+        if (tid == 0) block_base[b0 / kThreads] = base;
+        const uint32_t served = (uint32_t)s.served, from = (uint32_t)base;  // both below `pages` where pages are taken
+        for (uint32_t i = first; i < served; i += step) {
+            const int t = find(s.take, i);
+            const int32_t id = __ldcg(queue_at(A, head, from + i));
+            if (id < 0 || id >= A.pages) report(A.status, 1u << SV_ERR_BAD_OFFSETS);
+            A.table[(int64_t)(b0 + t) * A.table_stride + (s.held[t] + (int32_t)(i - s.take[t]))] = id;
+        }
+        if (A.slots) {
+            // a warp takes a run of slots, several a lane at once where there are many: the sequence of the run's first is
+            // searched for once, and is that of most others in a prompt
+            const uint32_t all = s.rows[kThreads], lane = tid & 31, per = all > 2 * step ? kAtOnce : 1;
+            for (uint64_t r0 = (uint64_t)(first - lane) * per; r0 < all; r0 += (uint64_t)step * per) {
+                int32_t row[kAtOnce], id[kAtOnce], in[kAtOnce];
+                const int t0 = find(s.rows, (uint32_t)r0);
+                const uint32_t t0_end = s.rows[t0 + 1];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const uint64_t i64 = r0 + 32 * k + lane;
+                    row[k] = id[k] = -1;
+                    if (k >= (int)per || i64 >= all) continue;
+                    const uint32_t i = (uint32_t)i64;
+                    const int t = i < t0_end ? t0 : find(s.rows, i);
+                    const int32_t j = (int32_t)(i - s.rows[t]), slot = s.past[t] + j, page = page_of(A, slot);
+                    row[k] = s.row0[t] + j;
+                    if (!s.fine[t]) continue;
+                    in[k] = slot - page * A.page_size;
+                    id[k] = page < s.held[t] ? A.table[(int64_t)(b0 + t) * A.table_stride + page]
+                                             : __ldcg(queue_at(A, head, from + s.take[t] + (uint32_t)(page - s.held[t])));
+                    if (id[k] < 0 || id[k] >= A.pages) {
+                        report(A.status, 1u << SV_ERR_BAD_OFFSETS);
+                        id[k] = -1;
+                    }
                 }
-                A.slots[s.row0[t] + j] = at;
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+                    if (row[k] >= 0) A.slots[row[k]] = id[k] < 0 ? -1 : (int64_t)id[k] * A.page_size + in[k];
             }
+        }
         if (served) taken = base + served;
-        base += s.take[kThreads];
-        if (once) break;
+        base += takes;
     }
     team.sync();  // no other CTA reads held any more
 #pragma unroll 1
@@ -209,17 +252,18 @@ __global__ void __launch_bounds__(kThreads) k_cache_reserve(const __grid_constan
         if (b0 / kThreads % team.size != team.rank) continue;
         if (!once) {
             __syncthreads();
-            read_block(A, s, b0, block_base[b0 / kThreads], free, bad);
+            read_block(A, s, b0, me, takes);
+            serve(s, me, block_base[b0 / kThreads], free, bad, A.B);
         }
-        if (b0 + tid < A.B) A.out_held[b0 + tid] = s.need[tid];
+        if (me.b < A.B) A.out_held[me.b] = me.need;
     }
     if (team.rank == 0) {
         if (bad) err |= 1u << SV_ERR_BAD_OFFSETS;
         err = __reduce_or_sync(kAll, err);
         if ((tid & 31) == 0) report(A.status, err);
         if (tid == 0) {
-            A.out_state[0] = bad ? (int32_t)head : (int32_t)(((u64)head + taken) % pages);
-            A.out_state[1] = bad ? (int32_t)count : (int32_t)(free - taken);
+            A.out_state[0] = bad ? head : (int32_t)(((u64)head + taken) % (u64)A.pages);
+            A.out_state[1] = bad ? count : (int32_t)(free - taken);
             if (!A.lengths && A.B > 0) {
                 const int64_t end = (int64_t)A.chunk.offs[A.B] + A.B;
                 if (end > A.chunk.rows || A.chunk.offs[0] != 0) report(A.status, 1u << SV_ERR_BAD_OFFSETS);
@@ -231,7 +275,24 @@ __global__ void __launch_bounds__(kThreads) k_cache_reserve(const __grid_constan
 }  // namespace
 
 cudaError_t launch_reserve(const ReserveArgs& A, cudaStream_t st) {
-    const int ctas = 1;
+    // slots and pages that there may be; a cluster costs a small call what its barriers do
+    const int64_t most = A.lengths ? std::min((int64_t)A.B * A.table_stride, (int64_t)A.pages) : (int64_t)A.chunk.rows + A.B;
+    const int ctas = most > kSmall ? kMaxCtas : 1;
+    ReserveArgs a = A;
+    a.page_bits = 0;
+    while ((1u << a.page_bits) < (uint32_t)A.page_size) ++a.page_bits;
+    a.page_recip = (uint32_t)((((u64)1 << (31 + a.page_bits)) + (uint32_t)A.page_size - 1) / (uint32_t)A.page_size);
+    if (ctas > 8) {  // a cluster of that size asks for it, once a device; setting it twice does no harm
+        int dev;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        static std::atomic<unsigned long long> allowed{0};
+        if (dev >= 64 || !(allowed.load() >> dev & 1u)) {
+            e = cudaFuncSetAttribute(k_cache_reserve, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            if (dev < 64) allowed.fetch_or(1ull << dev);
+        }
+    }
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -244,7 +305,7 @@ cudaError_t launch_reserve(const ReserveArgs& A, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_cache_reserve, A);
+    return cudaLaunchKernelEx(&cfg, k_cache_reserve, a);
 }
 
 }  // namespace cache
