@@ -70,27 +70,36 @@ typedef unsigned long long u64;
 
 struct RowPar {
     ExpConst E;
-    float T, p, u;
+    float T, p, u, mp;
     int32_t k;      // 0: none
     u64 least;      // of a kept weight, 0: none
     uint32_t err;
 };
 
 struct Result {
-    float thr;      // logits above it are kept
-    uint32_t r;     // and so many equal to it, in index order
-    int32_t partial;  // these are not all of them (or may not be)
-    int32_t n;      // kept, -1: not known yet
-    float m;        // the largest logit
+    float thr;        // logits above it are kept; and those equal to it, all or (partial) the first r by index
+    uint32_t r;
+    int32_t partial;
+    int32_t n;        // kept, -1: not known yet
+    float m;          // the largest logit
     uint32_t err;
-    int32_t slow;   // the quick way could not tell
+    int32_t slow;     // the quick way could not tell
+    int32_t at;       // quick: the threshold's place among the bins
+    uint32_t ties;    // quick: logits equal to it
+    u64 mass;         // quick: of those above the threshold (and equal to it, where all are kept)
 };
 
 struct Found {  // a level of the slow way
     int32_t bin;    // -1: the target lies past all bins
     u64 rest;       // what is left of the target within the bin, or past all
     u64 value;      // of the bin
-    u64 total;      // of the first level
+};
+
+// What a CTA, or a warp, has: the weights and the number of its logits above the threshold (or at it, where all of those are
+// kept), and how many are at it, where some are.
+struct Part {
+    u64 mass;
+    uint32_t above, ties;
 };
 
 struct alignas(16) Shared {
@@ -99,20 +108,21 @@ struct alignas(16) Shared {
     u64 group_mass[kGroups + 1];
     uint32_t group_count[kGroups + 1];
     u64 scan[kWarps];
-    u64 warp_mass[kWarps];
-    uint32_t warp_ties[kWarps], warp_above[kWarps];
-    uint32_t warp_max[kWarps];
+    Part warp_part[kWarps], part;  // part: the CTA's
+    uint32_t warp_max[kWarps], warp_min[kWarps];
+    uint32_t max_key, min_key;  // the CTA's largest logit, and the least of its threads' largest
     uint32_t flags;
-    uint32_t max_key;
     float floor;
     RowPar par;
     Result res;
     Found found;
-    // of this CTA's warps, after all have counted
-    int32_t ties_kept[kWarps];
-    int32_t hit_warp;  // the warp (of the cluster) that holds the drawn token
+    int32_t hit;      // the CTA, then the warp of the cluster, that holds the drawn token
     u64 hit_rest, total;
-    uint32_t above;
+    uint32_t keeps;   // of the ties of the CTA (filter) or of the CTA that holds the draw
+    int32_t warp_keeps[kWarps], n;
+    int32_t token;
+    float logit;
+    double log_total;
 };
 
 enum : uint32_t { kNonfinite = 1, kOutside = 2 };
@@ -229,13 +239,41 @@ struct Team {
     }
 };
 
-// A warp's segment of the row: chunks of 16 bytes, as memory is aligned, numbered from the one that holds the row's first
-// element. Elements of a chunk that are not the row's are held as -inf.
+// Chunks of 16 bytes of the row, as memory is aligned, numbered from the one that holds the row's first element. Elements of
+// a chunk that are not the row's are held as -inf. (Of a warp's own slice, or in another CTA.)
 struct Segment {
     const uint4* data;  // chunk c at data[c]
     int32_t c0, c1;
-    int32_t off;  // elements before the row's first in chunk 0
 };
+
+// ceil(f x) or floor(f x) for f in [0, 1), exactly: f is 24 bits and an exponent.
+__device__ __forceinline__ u64 scaled(u64 x, float f, bool up) {
+    if (!(f > 0.f)) return 0;
+    const uint32_t b = __float_as_uint(f), e = b >> 23;
+    const u64 m = e ? (b & 0x7fffffu) | 0x800000u : b;
+    const int shift = 150 - (int)max(e, 1u);  // f = m 2^-shift, shift >= 24
+    const u64 hi = __umul64hi(x, m), lo = x * m;
+    u64 q, rest;
+    if (shift < 64) {
+        q = hi << (64 - shift) | lo >> shift;
+        rest = lo & (((u64)1 << shift) - 1);
+    } else {
+        q = shift < 128 ? hi >> (shift - 64) : 0;
+        rest = 1;  // of no matter below 1, and never exactly none: x m < 2^86
+        if (shift < 128) rest = lo | (hi & (((u64)1 << (shift - 64)) - 1));
+        else rest = x;
+    }
+    return q + (up && rest);
+}
+// ceil(a / b) where it is at most 2^18 (or so): the quotient in float is off by less than one.
+__device__ __forceinline__ uint32_t div_up(u64 a, u64 b) {
+    if (b == 0) return 1;
+    uint32_t q = (uint32_t)__fdividef((float)a, (float)b);
+    if (q > 0) --q;
+#pragma unroll 1
+    while (q * b < a) ++q;
+    return q;
+}
 
 template <typename T>
 struct Work {
@@ -243,8 +281,89 @@ struct Work {
     const Args& A;
     Shared& sh;
     const Team& team;
-    Segment s;
+    Segment s;    // the warp's
+    int32_t off;  // elements before the row's first in chunk 0
     int lane, warp;
+
+    // ------------------------------------------------------------------------------------------------
+    // the largest, and what lies too low to matter
+    // ------------------------------------------------------------------------------------------------
+    // Keys of a thread's largest and whether it met a NaN or +inf.
+    __device__ __forceinline__ uint32_t largest(uint32_t& flags) {
+        flags = 0;
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t none = 0xff80ff80u;
+            uint32_t top = none, high = 0x80008000u, wide = 0;  // as floats, signed and unsigned
+#pragma unroll 2
+            for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
+                const uint4 q = s.data[c];
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    asm("max.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(w[i]));
+                    high = __vmaxs2(high, w[i]);
+                    wide = __vmaxu2(wide, w[i]);
+                }
+            }
+            if ((int16_t)high >= 0x7f80 || (int32_t)high >> 16 >= 0x7f80 || (wide & 0xffffu) > 0xff80u || wide >> 16 > 0xff80u)
+                flags = kNonfinite;
+            return key_of(fmaxf(bf16lo_to_f32(top), bf16hi_to_f32(top)));
+        } else {
+            uint32_t top = kKeyMinusInf;
+#pragma unroll 2
+            for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
+                float x[E::N];
+                E::unpack(s.data[c], x);
+#pragma unroll
+                for (int e = 0; e < E::N; ++e) {
+                    const uint32_t k = key_of(x[e]);
+                    if (k >= kKeyInf || k < kKeyMinusInf) flags = kNonfinite;
+                    else top = max(top, k);
+                }
+            }
+            return top;
+        }
+    }
+    // The CTA's largest, and the least of its threads': with a block barrier at the end.
+    __device__ __forceinline__ void survey() {
+        uint32_t flags;
+        const uint32_t top = largest(flags);
+        flags = __reduce_or_sync(kAll, flags);
+        const uint32_t hi = __reduce_max_sync(kAll, top), lo = __reduce_min_sync(kAll, top);
+        if (lane == 0) {
+            sh.warp_max[warp] = hi;
+            sh.warp_min[warp] = lo;
+            if (flags) atomicOr(&sh.flags, flags);
+        }
+        __syncthreads();
+        const uint32_t h = __reduce_max_sync(kAll, sh.warp_max[lane % kWarps]), l = __reduce_min_sync(kAll, sh.warp_min[lane % kWarps]);
+        if (threadIdx.x == 0) {
+            sh.max_key = h;
+            sh.min_key = l;
+        }
+        __syncthreads();
+    }
+    // Logits below this decide nothing. With top-k, k up to the threads of a CTA: each of them has a logit of at least
+    // min_key, so k have, and what is not among the first k of the ranking does not matter (of 32 K logits a tenth is left).
+    // With min-p alone: those whose weight is clearly too small.
+    __device__ __forceinline__ float lowest() const {
+        const RowPar& R = sh.par;
+        const float top = float_of(sh.max_key);
+        if (R.T == 0.f) return top;
+        if (R.k > 0 && R.k <= kThreads) return float_of(sh.min_key);
+        if (R.least && !(R.p < 1.f)) return top + 1.0001f * R.T * __logf(fminf(R.mp, 1.f)) - 1e-5f * (fabsf(top) + R.T);
+        return -INFINITY;
+    }
+    __device__ __forceinline__ uint32_t cluster_max() const {
+        uint32_t k = 0;
+        if (lane < team.size) k = *team.of(&sh.max_key, lane);
+        return __reduce_max_sync(kAll, k);
+    }
+    __device__ __forceinline__ uint32_t cluster_flags() const {
+        uint32_t f = 0;
+        if (lane < team.size) f = *team.of(&sh.flags, lane);
+        return __reduce_or_sync(kAll, f);
+    }
 
     // ------------------------------------------------------------------------------------------------
     // the quick way (bfloat16)
@@ -257,11 +376,11 @@ struct Work {
         }
         const uint32_t a = bits & 0x7fffu;
         if (a == 0) atomicAdd(&sh.hist[kMid], 1u);
-        else if ((bits & 0xffffu) == 0xff80u) return;  // -inf: not ranked
-        else flags |= a >= 0x7f80u ? kNonfinite : kOutside;
+        else if ((bits & 0xffffu) != 0xff80u) flags |= kOutside;  // -inf is not ranked
     }
-    __device__ __forceinline__ void count_values() {
+    __device__ __forceinline__ void count_values(float low) {
         uint32_t flags = 0;
+        const __nv_bfloat162 low2 = __bfloat162bfloat162(__float2bfloat16_rd(low));
 #pragma unroll 2
         for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
             const uint4 q = s.data[c];
@@ -269,9 +388,10 @@ struct Work {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 constexpr uint32_t lo = (kCodeLo - 1) * 0x10001u, hi = (kCodeHi + 1) * 0x10001u;
+                const uint32_t in = __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), low2);
                 const uint32_t o = __vminu2(__vmaxu2(w[i] & 0x7fff7fffu, lo), hi) - lo;
-                count_one(w[i], o & 0xffffu, flags);
-                count_one(w[i] >> 16, o >> 16, flags);
+                if (in & 1u) count_one(w[i], o & 0xffffu, flags);
+                if (in >> 16) count_one(w[i] >> 16, o >> 16, flags);
             }
         }
         flags = __reduce_or_sync(kAll, flags);
@@ -283,213 +403,210 @@ struct Work {
         const uint32_t a = (uint32_t)(o < 0 ? -o : o);
         return __uint_as_float(a == 0 ? 0u : (o < 0 ? 0x80000000u : 0u) | (kCodeLo - 1 + a) << 16);
     }
-    // Of group g of 64 bins, a lane's two: counts and weights.
-    __device__ __forceinline__ void pair_at(int g, float m, uint32_t* c, u64* w) {
+    // Of group g of 64 bins, a lane's two: counts and weights. False, for the warp, if there is nothing.
+    __device__ __forceinline__ bool pair_at(int g, float m, uint32_t* c, u64* w) const {
         const int d = g * kGroupBins + 2 * lane;
         c[0] = d < kBins ? sh.hist[kBins - 1 - d] : 0u;
         c[1] = d + 1 < kBins ? sh.hist[kBins - 2 - d] : 0u;
         w[0] = w[1] = 0;
-        if (c[0] | c[1]) {
-            const Fixed2 f = weights2(value_at(d), value_at(d + 1), m, sh.par.E, sh.tab);
-            w[0] = join(f.ax, f.bx);
-            w[1] = join(f.ay, f.by);
-        }
-    }
-    struct Crossing {
-        uint32_t n, r, ties;  // tokens up to it, of them in its bin, and the bin's
-        u64 sum;              // of the weights up to it
-        float thr;
-    };
-    // The bin in which the count or the sum of the ranking's weights reaches a target that it does reach. Warp 0; `before`:
-    // count and sum before the lane's five groups, which hold cl and ml.
-    template <bool kMass>
-    __device__ __forceinline__ Crossing cross(u64 target, float m, uint32_t c_before, u64 m_before, uint32_t cl, u64 ml) {
-        const bool mine = kMass ? m_before < target && target <= m_before + ml : c_before < target && target <= c_before + cl;
-        int g = 5 * lane;
-        uint32_t pc = c_before;
-        u64 pm = m_before;
-        if (mine)
-#pragma unroll 1
-            for (; g < 5 * lane + 4 && (kMass ? pm + sh.group_mass[g] : pc + sh.group_count[g]) < target; ++g) {
-                pm += sh.group_mass[g];
-                pc += sh.group_count[g];
-            }
-        const int src = __ffs(__ballot_sync(kAll, mine)) - 1;
-        g = __shfl_sync(kAll, g, src);
-        pc = __shfl_sync(kAll, pc, src);
-        pm = __shfl_sync(kAll, pm, src);
-        uint32_t c[2];
-        u64 w[2];
-        pair_at(g, m, c, w);
-        const u64 mass = c[0] * w[0] + c[1] * w[1];
-        uint32_t cc = c[0] + c[1];
-        const u64 upto = warp_inscan(mass, lane);
-        const uint32_t c_upto = (uint32_t)warp_inscan(cc, lane);
-        pc += c_upto - cc;
-        pm += upto - mass;
-        const bool here = kMass ? pm < target && target <= pm + mass : pc < target && target <= pc + cc;
-        int i = 0;
-        if (kMass ? pm + c[0] * w[0] < target : pc + c[0] < target) {
-            i = 1;
-            pm += c[0] * w[0];
-            pc += c[0];
-        }
-        const uint32_t ties = i ? c[1] : c[0];
-        const u64 wt = i ? w[1] : w[0];
-        Crossing x;
-        x.r = kMass ? (uint32_t)((target - pm + wt - 1) / (wt ? wt : 1)) : (uint32_t)(target - pc);
-        x.ties = ties;
-        x.n = pc + x.r;
-        x.sum = pm + x.r * wt;
-        x.thr = value_at(g * kGroupBins + 2 * lane + i);
-        const int at = __ffs(__ballot_sync(kAll, here)) - 1;
-        x.r = __shfl_sync(kAll, x.r, at);
-        x.ties = __shfl_sync(kAll, x.ties, at);
-        x.n = __shfl_sync(kAll, x.n, at);
-        x.sum = __shfl_sync(kAll, x.sum, at);
-        x.thr = __shfl_sync(kAll, x.thr, at);
-        return x;
+        if (!__any_sync(kAll, c[0] | c[1])) return false;
+        const Fixed2 f = weights2(value_at(d), value_at(d + 1), m, sh.par.E, sh.tab);
+        w[0] = join(f.ax, f.bx);
+        w[1] = join(f.ay, f.by);
+        return true;
     }
     // By the first CTA, whose histogram is the row's.
-    __device__ __forceinline__ void choose(uint32_t flags) {
-        // the largest
-        int d_max = kBins;
-        for (int d = threadIdx.x; d < kBins; d += kThreads)
-            if (sh.hist[kBins - 1 - d]) {
-                d_max = d;
-                break;
-            }
-        d_max = __reduce_min_sync(kAll, d_max);
-        if (lane == 0) sh.warp_max[warp] = (uint32_t)d_max;
-        __syncthreads();
-        d_max = (int)__reduce_min_sync(kAll, sh.warp_max[lane % kWarps]);
-        const bool any = d_max < kBins;
-        const float m = any ? value_at(d_max) : 0.f;
-        // groups; and the weights of at least par.least, which are the ranking's first
-        const u64 least = sh.par.least;
-        uint32_t many = 0;
+    __device__ __forceinline__ void choose() {
+        const uint32_t flags = cluster_flags(), top = cluster_max();
+        const RowPar& R = sh.par;
+        const float m = float_of(top);
+        const u64 least = R.least;
+        uint32_t many = 0;  // of weights of at least `least`, which are the ranking's first
+        u64 heavy = 0;
         int last = -1;
 #pragma unroll 1
         for (int g = warp; g < kGroups; g += kWarps) {
-            uint32_t c[2];
-            u64 w[2];
-            pair_at(g, m, c, w);
-            uint32_t cc = c[0] + c[1];
-            u64 mass = 0;
-            if (__any_sync(kAll, cc)) {
-                mass = warp_sum(c[0] * w[0] + c[1] * w[1]);
-                if (least) {
-                    const int d = g * kGroupBins + 2 * lane;
-                    if (c[0] && w[0] >= least) many += c[0], last = d;
-                    if (c[1] && w[1] >= least) many += c[1], last = d + 1;
-                }
-                cc = __reduce_add_sync(kAll, cc);
+            uint32_t c[2], cc = 0;
+            u64 w[2], mass = 0;
+            if (pair_at(g, m, c, w)) {
+                mass = c[0] * w[0] + c[1] * w[1];
+                const int d = g * kGroupBins + 2 * lane;
+                if (least && c[0] && w[0] >= least) many += c[0], heavy += c[0] * w[0], last = d;
+                if (least && c[1] && w[1] >= least) many += c[1], heavy += c[1] * w[1], last = d + 1;
+                mass = warp_sum(mass);
+                cc = __reduce_add_sync(kAll, c[0] + c[1]);
             }
             if (lane == 0) {
                 sh.group_count[g] = cc;
                 sh.group_mass[g] = mass;
             }
         }
-        if (least) {
-            many = __reduce_add_sync(kAll, many);
-            last = __reduce_max_sync(kAll, last);
-        }
+        many = __reduce_add_sync(kAll, many);
+        last = __reduce_max_sync(kAll, last);
+        heavy = warp_sum(heavy);
         if (lane == 0) {
-            sh.warp_above[warp] = many;
-            sh.warp_ties[warp] = (uint32_t)(last + 1);
+            sh.warp_part[warp] = Part{heavy, many, (uint32_t)(last + 1)};
         }
         __syncthreads();
         if (warp > 0) return;
         uint32_t cl = 0;
         u64 ml = 0;
+#pragma unroll 1
         for (int g = 5 * lane; g < 5 * lane + 5 && g < kGroups; ++g) {
             cl += sh.group_count[g];
             ml += sh.group_mass[g];
         }
-        const uint32_t c_upto = (uint32_t)warp_inscan(cl, lane), all = __shfl_sync(kAll, c_upto, 31);
-        const u64 m_upto = warp_inscan(ml, lane);
+        const u64 c_upto = warp_inscan(cl, lane), m_upto = warp_inscan(ml, lane);
+        const uint32_t all = (uint32_t)__shfl_sync(kAll, c_upto, 31);
         u64 sum = __shfl_sync(kAll, m_upto, 31);
-        const RowPar& R = sh.par;
         Result res{};
         res.m = m;
         res.n = (int32_t)all;
         res.thr = kLowest;  // all that are ranked, unless something says otherwise
-        if (R.k > 0 && (uint32_t)R.k < all) {
-            const Crossing x = cross<false>((u64)R.k, m, c_upto - cl, m_upto - ml, cl, ml);
-            res.thr = x.thr;
-            res.r = x.r;
-            res.partial = x.r < x.ties;
-            res.n = (int32_t)x.n;
-            sum = x.sum;
-        }
-        if (R.p < 1.f && any) {
-            const u64 target = max((u64)ceil((double)R.p * (double)sum), (u64)1);
-            const Crossing x = cross<true>(min(target, sum), m, c_upto - cl, m_upto - ml, cl, ml);
-            if ((int32_t)x.n < res.n) {
-                res.thr = x.thr;
-                res.r = x.r;
-                res.partial = x.r < x.ties;
-                res.n = (int32_t)x.n;
+        res.at = kBins - 1;
+        res.mass = sum;
+        const bool found = top > kKeyMinusInf && R.T > 0.f;
+#pragma unroll 1
+        for (int step = 0; step < 2 && found; ++step) {  // the first k, then as many as sum to top_p of their weights
+            u64 target = (u64)R.k;
+            if (step == 0 && (R.k <= 0 || (uint32_t)R.k > all)) continue;
+            if (step == 1) {
+                if (!(R.p < 1.f)) continue;
+                target = max(scaled(sum, R.p, true), (u64)1);
+            }
+            // the lane, the group and the bin in which the counts or weights reach the target
+            const u64 before = step ? m_upto - ml : c_upto - cl, own = step ? ml : cl;
+            const bool mine = before < target && target <= before + own;
+            int g = 5 * lane;
+            u64 pc = c_upto - cl, pm = m_upto - ml;
+            if (mine)
+#pragma unroll 1
+                for (; (step ? pm + sh.group_mass[g] : pc + sh.group_count[g]) < target; ++g) {
+                    pm += sh.group_mass[g];
+                    pc += sh.group_count[g];
+                }
+            const int src = __ffs(__ballot_sync(kAll, mine)) - 1;
+            g = __shfl_sync(kAll, g, src);
+            pc = __shfl_sync(kAll, pc, src);
+            pm = __shfl_sync(kAll, pm, src);
+            uint32_t c[2];
+            u64 w[2];
+            pair_at(g, m, c, w);
+            const u64 mass = c[0] * w[0] + c[1] * w[1], cc = c[0] + c[1];
+            pm += warp_inscan(mass, lane) - mass;
+            pc += warp_inscan(cc, lane) - cc;
+            const bool here = step ? pm < target && target <= pm + mass : pc < target && target <= pc + cc;
+            int i = 0;
+            if ((step ? pm + c[0] * w[0] : pc + c[0]) < target) {
+                i = 1;
+                pm += c[0] * w[0];
+                pc += c[0];
+            }
+            const uint32_t ties = i ? c[1] : c[0];
+            const u64 wt = i ? w[1] : w[0];
+            uint32_t r = 0;
+            if (here) r = step ? div_up(target - pm, wt) : (uint32_t)(target - pc);
+            const int at = __ffs(__ballot_sync(kAll, here)) - 1;
+            const uint32_t n = (uint32_t)__shfl_sync(kAll, pc + r, at);
+            if (step == 0) sum = __shfl_sync(kAll, pm + r * wt, at);
+            if ((int32_t)n <= res.n) {  // (equal, too: logits that were too low to count are not kept)
+                res.n = (int32_t)n;
+                res.r = __shfl_sync(kAll, r, at);
+                res.ties = __shfl_sync(kAll, ties, at);
+                res.partial = res.r < res.ties;
+                res.at = __shfl_sync(kAll, g * kGroupBins + 2 * lane + i, at);
+                res.mass = __shfl_sync(kAll, pm + (r < ties ? 0 : r * wt), at);
             }
         }
-        if (least) {
-            many = __reduce_add_sync(kAll, lane < kWarps ? sh.warp_above[lane] : 0u);
-            last = (int)__reduce_max_sync(kAll, lane < kWarps ? sh.warp_ties[lane] : 0u) - 1;
-            if ((int32_t)many < res.n) {
-                res.thr = value_at(last);
-                res.partial = 0;
+        if (least && found) {
+            const Part x = lane < kWarps ? sh.warp_part[lane] : Part{0, 0, 0};
+            many = __reduce_add_sync(kAll, x.above);
+            last = (int)__reduce_max_sync(kAll, x.ties) - 1;
+            heavy = warp_sum(x.mass);
+            if ((int32_t)many <= res.n) {
                 res.n = (int32_t)many;
+                res.partial = 0;
+                res.at = last;
+                res.mass = heavy;
             }
         }
-        if (R.T == 0.f) {
-            res.thr = m;
+        if (R.T == 0.f && top > kKeyMinusInf) {  // the bins hold what equals the largest of a CTA, the first of them that of all
+            const uint32_t a = __float_as_uint(m) >> 16;
+            const int o = max(0, (int)(a & 0x7fffu) - (int)(kCodeLo - 1));
+            res.at = min(max(kMid - (a & 0x8000u ? -o : o), 0), kBins - 1);
+            res.ties = sh.hist[kBins - 1 - res.at];
             res.r = 1;
-            res.partial = sh.hist[kBins - 1 - min(d_max, kBins - 1)] > 1;
+            res.partial = res.ties > 1;
             res.n = 1;
+            res.mass = res.partial ? 0 : (u64)1 << kBits;
         }
+        if (res.at < kBins - 1) res.thr = value_at(res.at);
         res.err = R.err | (flags & kNonfinite ? 1u << SV_ERR_NONFINITE : 0u);
-        res.slow = (flags & kOutside) != 0;
-        if (!any && !res.slow && !(flags & kNonfinite)) res.err |= 1u << SV_ERR_EMPTY_ROW;
+        if (!(flags & kNonfinite) && top <= kKeyMinusInf) res.err |= 1u << SV_ERR_EMPTY_ROW;
+        res.slow = !res.err && (flags & kOutside);
         if (lane == 0) sh.res = res;
     }
     // Histograms of the cluster, summed into the first CTA's, a share of the bins by each.
     __device__ __forceinline__ void merge_counts() {
         if (team.size == 1) return;
         const int per = (kHist / 4 + team.size - 1) / team.size, v0 = team.rank * per, v1 = min(v0 + per, kHist / 4);
+#pragma unroll 1
         for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
-            uint4 t = make_uint4(0, 0, 0, 0);
-            for (int q = 0; q < team.size; ++q) {
-                const uint4 x = reinterpret_cast<const uint4*>(team.of(sh.hist, q))[v];
-                t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+            uint4 x[kMaxCtas];
+#pragma unroll
+            for (int q = 0; q < kMaxCtas; ++q) {
+                x[q] = make_uint4(0, 0, 0, 0);
+                if (q < team.size) x[q] = reinterpret_cast<const uint4*>(team.of(sh.hist, q))[v];
             }
+            uint4 t = x[0];
+#pragma unroll
+            for (int q = 1; q < kMaxCtas; ++q) t.x += x[q].x, t.y += x[q].y, t.z += x[q].z, t.w += x[q].w;
             reinterpret_cast<uint4*>(team.of(sh.hist, 0))[v] = t;
         }
         team.sync();
     }
     __device__ __forceinline__ void zero_hist() {
+#pragma unroll 1
         for (int i = threadIdx.x; i < kHist / 4; i += kThreads) reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0, 0, 0, 0);
+    }
+    // What a CTA has of the kept, from its histogram. (The first one's is the row's by now: it has what the others have not.)
+    __device__ __forceinline__ void part_of_counts(const Result& res) {
+        const int end = res.partial ? res.at : res.at + 1;
+        u64 mass = 0;
+        uint32_t ties = 0, above = 0;
+#pragma unroll 1
+        for (int g = warp; g * kGroupBins <= res.at && team.rank > 0; g += kWarps) {
+            uint32_t c[2];
+            u64 w[2];
+            if (!pair_at(g, res.m, c, w)) continue;
+            const int d = g * kGroupBins + 2 * lane;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (d + i < end) mass += c[i] * w[i], above += c[i];
+                else if (d + i == res.at) ties += c[i];
+            }
+        }
+        sum_up(mass, above, ties);
+    }
+    // The CTA's part, from its warps'.
+    __device__ __forceinline__ void sum_up(u64 mass, uint32_t above, uint32_t ties) {
+        mass = warp_sum(mass);
+        above = __reduce_add_sync(kAll, above);
+        ties = __reduce_add_sync(kAll, ties);
+        if (lane == 0) sh.warp_part[warp] = Part{mass, above, ties};
+        __syncthreads();
+        if (warp == 0) {
+            const Part x = lane < kWarps ? sh.warp_part[lane] : Part{0, 0, 0};
+            mass = warp_sum(x.mass);
+            above = __reduce_add_sync(kAll, x.above);
+            ties = __reduce_add_sync(kAll, x.ties);
+            if (lane == 0) sh.part = Part{mass, above, ties};
+        }
     }
 
     // ------------------------------------------------------------------------------------------------
     // the slow way
     // ------------------------------------------------------------------------------------------------
-    __device__ __forceinline__ uint32_t largest(uint32_t& flags) {
-        uint32_t top = 0;
-        flags = 0;
-#pragma unroll 2
-        for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
-            float x[E::N];
-            E::unpack(s.data[c], x);
-#pragma unroll
-            for (int e = 0; e < E::N; ++e) {
-                const uint32_t k = key_of(x[e]);
-                if (k >= kKeyInf || k < kKeyMinusInf) flags = kNonfinite;
-                else top = max(top, k);
-            }
-        }
-        flags = __reduce_or_sync(kAll, flags);
-        return __reduce_max_sync(kAll, top);
-    }
     // One level: the elements whose keys lie in [lo, lo + (bins << shift)), above `floor` and above -inf's, by digit, and
     // the digit at which their counts (or weights, in the ranking's order) reach the target. first: the target is top_p
     // of all weights and `extra`.
@@ -562,9 +679,9 @@ struct Work {
             }
             if (first && kMass) {
                 const u64 sum = total + extra;
-                target = min(max((u64)ceil((double)sh.par.p * (double)sum), (u64)1), sum);
+                target = max(scaled(sum, sh.par.p, true), (u64)1);
             }
-            if (threadIdx.x == 0 && target > total) sh.found = {-1, target - total, 0, total};
+            if (threadIdx.x == 0 && target > total) sh.found = {-1, target - total, 0};
             if (before < target && target <= before + mine) {
                 int b = bins - 1 - per * (int)threadIdx.x;
                 u64 v;
@@ -573,7 +690,7 @@ struct Work {
                     if (target <= before + v) break;
                     before += v;
                 }
-                sh.found = {b, target - before, v, total};
+                sh.found = {b, target - before, v};
             }
         }
         team.sync();
@@ -597,20 +714,7 @@ struct Work {
     }
     __device__ __forceinline__ Result choose_slow() {
         const RowPar& R = sh.par;
-        uint32_t flags, top = largest(flags);
-        __syncthreads();
-        if (threadIdx.x == 0) sh.flags = 0, sh.max_key = 0;
-        __syncthreads();
-        if (lane == 0) {
-            if (flags) atomicOr(&sh.flags, flags);
-            atomicMax(&sh.max_key, top);
-        }
-        team.sync();
-        flags = top = 0;
-        for (int q = 0; q < team.size; ++q) {
-            flags |= *team.of(&sh.flags, q);
-            top = max(top, *team.of(&sh.max_key, q));
-        }
+        const uint32_t flags = cluster_flags() & kNonfinite, top = cluster_max();
         Result res{};
         res.err = R.err | (flags ? 1u << SV_ERR_NONFINITE : 0u);
         if (!flags && top <= kKeyMinusInf) res.err |= 1u << SV_ERR_EMPTY_ROW;
@@ -636,10 +740,10 @@ struct Work {
             if (seek<true>(floor, m, 0, r * w, key, rest, value)) {
                 const u64 wk = weight(float_of(key), m, R.E, sh.tab);
                 floor = key;
-                r = (rest + wk - 1) / wk;
-                ties = value / wk;
+                r = div_up(rest, wk);
+                ties = div_up(value, wk);
             } else {
-                r = (rest + w - 1) / w;
+                r = div_up(rest, w);
             }
         }
         if (r) {
@@ -673,19 +777,16 @@ struct Work {
     // ------------------------------------------------------------------------------------------------
     // with the threshold
     // ------------------------------------------------------------------------------------------------
-    // What a warp has of kept tokens: those above the threshold (or at it, where all of these are kept), their weights, and
-    // how many are at it.
+    // What a segment has of the kept.
     template <bool kMass>
-    __device__ __forceinline__ void tally(const Result& res) {
-        uint32_t above = 0, ties = 0;
-        u64 mass = 0;
+    __device__ __forceinline__ void tally(const Result& res, const Segment& g, u64& mass, uint32_t& above, uint32_t& ties) const {
+        above = ties = 0;
         int32_t sa = 0, sb = 0;  // of at most 192 weights
-        const ExpConst C = sh.par.E;
         const bool whole = !res.partial;
 #pragma unroll 1
-        for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
+        for (int32_t c = g.c0 + lane; c < g.c1; c += 32) {
             float x[E::N];
-            E::unpack(s.data[c], x);
+            E::unpack(g.data[c], x);
 #pragma unroll
             for (int e = 0; e < E::N; e += 2) {
                 const bool in0 = x[e] > res.thr || (whole && x[e] == res.thr), in1 = x[e + 1] > res.thr || (whole && x[e + 1] == res.thr);
@@ -693,86 +794,52 @@ struct Work {
                 if (!(in0 || in1)) continue;
                 above += in0 + in1;
                 if (!kMass) continue;
-                const Fixed2 f = weights2(x[e], x[e + 1], res.m, C, sh.tab);
+                const Fixed2 f = weights2(x[e], x[e + 1], res.m, sh.par.E, sh.tab);
                 sa += (in0 ? f.ax : 0) + (in1 ? f.ay : 0);
                 sb += (in0 ? f.bx : 0) + (in1 ? f.by : 0);
             }
         }
-        if (kMass) mass = warp_sum(join(sa, sb));
-        above = __reduce_add_sync(kAll, above);
-        ties = __reduce_add_sync(kAll, ties);
-        if (lane == 0) {
-            sh.warp_above[warp] = above;
-            sh.warp_ties[warp] = ties;
-            sh.warp_mass[warp] = mass;
-        }
+        mass = kMass ? join(sa, sb) : 0;
     }
-    // The cluster's tallies in index order, by the first warp of each CTA: how many ties each of its own warps keeps, the
-    // count, and the warp that holds the draw.
-    template <bool kMass>
-    __device__ __forceinline__ void settle(const Result& res) {
-        if (warp > 0) return;
-        const int all = team.size * kWarps;
-        const u64 w = kMass && res.partial && sh.par.T > 0.f ? weight(res.thr, res.m, sh.par.E, sh.tab) : (u64)1 << kBits;
-        uint32_t tie_base = 0, above_base = 0;
-        u64 mass_base = 0;
-        u64 upto[kMaxCtas * kWarps / 32], own[kMaxCtas * kWarps / 32];
-#pragma unroll
-        for (int i = 0; i < kMaxCtas * kWarps / 32; ++i) {
-            const int g = 32 * i + lane;
-            if (32 * i >= all) break;
-            uint32_t ties = 0, above = 0;
-            u64 mass = 0;
-            if (g < all) {
-                const Shared* o = team.of(&sh, g / kWarps);
-                ties = o->warp_ties[g % kWarps];
-                above = o->warp_above[g % kWarps];
-                if (kMass) mass = o->warp_mass[g % kWarps];
-            }
-            const uint32_t t = (uint32_t)warp_inscan(ties, lane);
-            const int64_t left = (int64_t)res.r - (tie_base + t - ties);
-            const uint32_t keeps = !res.partial || left <= 0 ? 0u : (uint32_t)min((int64_t)ties, left);
-            if (g < all && g / kWarps == team.rank) sh.ties_kept[g % kWarps] = (int32_t)keeps;
-            tie_base += __shfl_sync(kAll, t, 31);
-            above_base += __reduce_add_sync(kAll, above + keeps);
-            if (kMass) {
-                own[i] = mass + keeps * w;
-                upto[i] = mass_base + warp_inscan(own[i], lane);
-                mass_base = __shfl_sync(kAll, upto[i], 31);
+    // Every CTA's part, by the first warp: lane q has CTA q's, and the ties that it keeps. known: the first CTA's is what the
+    // others leave of the row's.
+    __device__ __forceinline__ Part parts(const Result& res, bool known, uint32_t& keeps) const {
+        Part p{0, 0, 0};
+        if (lane < team.size) p = *team.of(&sh.part, lane);
+        if (known) {
+            const u64 mass = warp_sum(p.mass);
+            const uint32_t ties = __reduce_add_sync(kAll, p.ties), above = __reduce_add_sync(kAll, p.above);
+            if (lane == 0) {
+                p.mass = res.mass - mass;
+                p.ties = res.partial ? res.ties - ties : 0;
+                p.above = (uint32_t)res.n - (res.partial ? res.r : 0) - above;
             }
         }
-        if (lane == 0) {
-            sh.above = above_base;
-            sh.total = mass_base;
-        }
-        if (!kMass) return;
-        const u64 target = (u64)((double)sh.par.u * (double)mass_base);  // the running weight must exceed it
-#pragma unroll
-        for (int i = 0; i < kMaxCtas * kWarps / 32; ++i) {
-            if (32 * i >= all) break;
-            if (target < upto[i] && target >= upto[i] - own[i]) {
-                sh.hit_warp = 32 * i + lane;
-                sh.hit_rest = target - (upto[i] - own[i]);
-            }
-        }
+        const uint32_t upto = (uint32_t)warp_inscan(p.ties, lane);
+        keeps = res.partial ? min(p.ties, res.r - min(res.r, upto - p.ties)) : 0;
+        return p;
     }
-    // The index of the n-th tie of the segment (n >= 1).
-    __device__ __forceinline__ int32_t nth_tie(float thr, int32_t n) {
+    __device__ __forceinline__ u64 tie_weight(const Result& res) const {
+        return res.partial ? weight(res.thr, res.m, sh.par.E, sh.tab) : 0;
+    }
+    // The index of the n-th tie of a segment (n >= 1).
+    __device__ __forceinline__ int32_t nth_tie(float thr, const Segment& g, int32_t n) const {
 #pragma unroll 1
-        for (int32_t c0 = s.c0; c0 < s.c1; c0 += 32) {
+        for (int32_t c0 = g.c0; c0 < g.c1; c0 += 32) {
             const int32_t c = c0 + lane;
             uint32_t eq = 0;
-            if (c < s.c1) {
+            if (c < g.c1) {
                 float x[E::N];
-                E::unpack(s.data[c], x);
+                E::unpack(g.data[c], x);
 #pragma unroll
                 for (int e = 0; e < E::N; ++e) eq |= (uint32_t)(x[e] == thr) << e;
             }
             const int32_t upto = (int32_t)warp_inscan((u64)__popc(eq), lane);
             int32_t at = -1;
             if (upto >= n && upto - __popc(eq) < n) {
+#pragma unroll 1
                 for (int32_t i = n - (upto - __popc(eq)); i > 1; --i) eq &= eq - 1;
-                at = c * E::N + __ffs(eq) - 1 - s.off;
+                at = c * E::N + __ffs(eq) - 1 - off;
             }
             at = __reduce_max_sync(kAll, at);
             if (at >= 0) return at;
@@ -780,39 +847,116 @@ struct Work {
         }
         return A.V;
     }
-    // Ties up to this index are kept.
-    __device__ __forceinline__ int32_t cut_of(const Result& res) {
-        if (!res.partial) return 0x7fffffff;
-        const int32_t keeps = sh.ties_kept[warp], ties = (int32_t)sh.warp_ties[warp];
-        if (keeps == ties) return 0x7fffffff;
-        return keeps == 0 ? -1 : nth_tie(res.thr, keeps);
+    // Ties up to this index are kept, in a segment that has `ties` and keeps `keeps` of them.
+    __device__ __forceinline__ int32_t cut_of(const Result& res, const Segment& g, uint32_t ties, uint32_t keeps) const {
+        if (!res.partial || keeps == ties) return 0x7fffffff;
+        return keeps == 0 ? -1 : nth_tie(res.thr, g, (int32_t)keeps);
     }
-    __device__ __forceinline__ uint32_t kept_of(const float* x, int32_t i0, const Result& res, int32_t cut) {
+    __device__ __forceinline__ uint32_t kept_of(const float* x, int32_t i0, const Result& res, int32_t cut) const {
         uint32_t k = 0;
 #pragma unroll
         for (int e = 0; e < E::N; ++e) k |= (uint32_t)(x[e] > res.thr || (x[e] == res.thr && i0 + e <= cut)) << e;
         return k;
     }
-    // The draw, by the warp that holds it: the first kept token whose running weight exceeds `target`.
-    __device__ __forceinline__ void pick(const Result& res, int32_t row, u64 target) {
-        const int32_t cut = cut_of(res);
+
+    // ------------------------------------------------------------------------------------------------
+    // the draw
+    // ------------------------------------------------------------------------------------------------
+    // The CTA that holds it, from the CTAs' parts; then all warps of the cluster share out that CTA's slice, and the warp
+    // whose share holds it finds it. `slices`: the first chunk of a CTA's slice.
+    template <typename F>
+    __device__ __forceinline__ void draw(const Result& res, bool known, int32_t row, F&& slices) {
         const RowPar& R = sh.par;
+        const u64 w = tie_weight(res);
+        if (warp == 0) {
+            uint32_t keeps;
+            const Part p = parts(res, known, keeps);
+            const u64 own = p.mass + keeps * w, upto = warp_inscan(own, lane), all = __shfl_sync(kAll, upto, 31);
+            const u64 target = scaled(all, R.u, false);  // the running weight must exceed it
+            const uint32_t n = __reduce_add_sync(kAll, p.above + keeps);
+            if (target < upto && target >= upto - own) {
+                sh.hit = lane;
+                sh.hit_rest = target - (upto - own);
+                sh.keeps = keeps;
+                sh.total = all;
+                sh.n = (int32_t)n;
+            }
+        }
+        __syncthreads();
+        const int hit = sh.hit;
+        // the shares
+        const int32_t h0 = slices(hit), h1 = slices(hit + 1), n = team.size * kWarps, me = team.rank * kWarps + warp;
+        auto share = [&](int i) { return h0 + (int32_t)((int64_t)(h1 - h0) * i / n); };
+        Segment g{team.of(const_cast<uint4*>(reinterpret_cast<const uint4*>(&sh + 1)), hit) - h0, share(me), share(me + 1)};
+        u64 mass;
+        uint32_t above, ties;
+        tally<true>(res, g, mass, above, ties);
+        mass = warp_sum(mass);
+        ties = __reduce_add_sync(kAll, ties);
+        if (lane == 0) sh.warp_part[warp] = Part{mass, 0, ties};
+        team.sync();
+        // lane i has shares 4 i .. 4 i + 3
+        if (warp == 0) {
+            Part p[4];
+            uint32_t tl = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = 4 * lane + i;
+                p[i] = Part{0, 0, 0};
+                if (at < n) p[i] = team.of(&sh, at / kWarps)->warp_part[at % kWarps];
+                tl += p[i].ties;
+            }
+            uint32_t left = sh.keeps - min(sh.keeps, (uint32_t)warp_inscan(tl, lane) - tl);  // ties that the lane's shares may keep
+            u64 ml = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t k = min(left, p[i].ties);
+                left -= k;
+                p[i].above = k;
+                p[i].mass += k * w;
+                ml += p[i].mass;
+            }
+            u64 at = warp_inscan(ml, lane) - ml;
+            const u64 target = sh.hit_rest;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (target >= at && target < at + p[i].mass) {
+                    sh.hit = 4 * lane + i;
+                    sh.hit_rest = target - at;
+                    sh.warp_keeps[0] = (int32_t)p[i].above;
+                }
+                at += p[i].mass;
+            }
+        }
+        __syncthreads();
+        if (sh.hit / kWarps == team.rank) {
+            const int who = sh.hit % kWarps;
+            if (warp == who) pick(res, g, cut_of(res, g, ties, (uint32_t)sh.warp_keeps[0]), sh.hit_rest);
+            else if (warp == (who ^ 1) && lane == 0) sh.log_total = log((double)sh.total) - kBits * 0.6931471805599453;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                A.tokens[row] = sh.token;
+                if (A.logprob) A.logprob[row] = R.T > 0.f ? (float)(((double)sh.logit - res.m) / R.T - sh.log_total) : 0.f;
+            }
+        }
+    }
+    // The first kept token of a segment whose running weight exceeds `target`.
+    __device__ __forceinline__ void pick(const Result& res, const Segment& g, int32_t cut, u64 target) {
         u64 base = 0;
 #pragma unroll 1
-        for (int32_t c0 = s.c0; c0 < s.c1; c0 += 32) {
+        for (int32_t c0 = g.c0; c0 < g.c1; c0 += 32) {
             const int32_t c = c0 + lane;
             u64 w[E::N], sum = 0;
             float x[E::N];
 #pragma unroll
             for (int e = 0; e < E::N; ++e) w[e] = 0;
-            if (c < s.c1) {
-                E::unpack(s.data[c], x);
-                const uint32_t k = kept_of(x, c * E::N - s.off, res, cut);
+            if (c < g.c1) {
+                E::unpack(g.data[c], x);
+                const uint32_t k = kept_of(x, c * E::N - off, res, cut);
 #pragma unroll
                 for (int e = 0; e < E::N; e += 2)
                     if (k >> e & 3u) {
-                        Fixed2 f{1 << 22, 1 << 22, 0, 0};
-                        if (R.T > 0.f) f = weights2(x[e], x[e + 1], res.m, R.E, sh.tab);
+                        const Fixed2 f = weights2(x[e], x[e + 1], res.m, sh.par.E, sh.tab);
                         w[e] = k >> e & 1u ? join(f.ax, f.bx) : 0;
                         w[e + 1] = k >> e & 2u ? join(f.ay, f.by) : 0;
                     }
@@ -823,36 +967,63 @@ struct Work {
             if (target < upto && target >= upto - sum) {
                 u64 run = upto - sum;
                 int at = -1;
+                float l = 0.f;
 #pragma unroll
                 for (int e = 0; e < E::N; ++e) {
                     run += w[e];
-                    if (at < 0 && run > target) at = e;
+                    if (at < 0 && run > target) {
+                        at = e;
+                        l = x[e];
+                    }
                 }
-                float l = x[0];
-#pragma unroll
-                for (int e = 1; e < E::N; ++e) l = e == at ? x[e] : l;
-                A.tokens[row] = c * E::N + at - s.off;
-                // l - m in float is exact or far below the result's rounding
-                if (A.logprob)
-                    A.logprob[row] = R.T > 0.f ? (float)(((double)l - res.m) / R.T - (log((double)sh.total) - kBits * 0.6931471805599453)) : 0.f;
+                sh.token = c * E::N + at - off;
+                sh.logit = l;
             }
             base = __shfl_sync(kAll, upto, 31);
             if (target < base) return;
         }
     }
+
+    // ------------------------------------------------------------------------------------------------
+    // the filtered row
+    // ------------------------------------------------------------------------------------------------
+    // The ties that this CTA's warps keep, where they are not all kept; and the row's count where it is not known.
+    __device__ __forceinline__ int32_t cut_here(const Result& res, bool known) {
+        u64 none;
+        uint32_t above, ties = 0;
+        if (warp == 0) {
+            uint32_t keeps;
+            const Part p = parts(res, known, keeps);
+            const uint32_t n = __reduce_add_sync(kAll, p.above + keeps);
+            if (lane == team.rank) {
+                sh.keeps = keeps;
+                sh.total = p.ties;
+                sh.n = (int32_t)n;
+            }
+        }
+        __syncthreads();
+        if (!res.partial || sh.keeps == (uint32_t)sh.total) return 0x7fffffff;
+        if (sh.keeps == 0) return -1;
+        tally<false>(res, s, none, above, ties);
+        ties = __reduce_add_sync(kAll, ties);
+        if (lane == 0) sh.warp_keeps[warp] = (int32_t)ties;
+        __syncthreads();
+        const uint32_t mine = lane < kWarps ? (uint32_t)sh.warp_keeps[lane] : 0u;
+        const uint32_t before = (uint32_t)__shfl_sync(kAll, warp_inscan(mine, lane) - mine, warp);
+        return cut_of(res, s, ties, min(ties, sh.keeps - min(sh.keeps, before)));
+    }
     // The segment with -inf where a token is not kept (copy: as it is).
-    __device__ __forceinline__ void write(const Result& res, int32_t row, bool copy) {
+    __device__ __forceinline__ void write(const Result& res, int32_t row, bool copy, int32_t cut) const {
         typedef typename E::Bits Bits;
-        const int32_t cut = copy ? 0 : cut_of(res);
         Bits* out = (Bits*)A.out + (int64_t)row * A.out_stride;
         const int32_t o_off = (int32_t)((uintptr_t)out % 16 / sizeof(Bits));
-        if (o_off == s.off) {
+        if (o_off == off) {
 #pragma unroll 2
             for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
                 const uint4 q = s.data[c];
                 float x[E::N];
                 E::unpack(q, x);
-                const int32_t i0 = c * E::N - s.off;
+                const int32_t i0 = c * E::N - off;
                 const uint32_t k = copy ? ~0u : kept_of(x, i0, res, cut);
                 const uint4 y = E::masked(q, k);
                 if (i0 >= 0 && i0 + E::N <= A.V) {
@@ -867,8 +1038,8 @@ struct Work {
             return;
         }
         // chunks of the output, which begin elsewhere
-        const Bits* in = reinterpret_cast<const Bits*>(s.data) + s.off;  // element i at in[i]
-        const int32_t e0 = max(0, s.c0 * E::N - s.off), e1 = min(A.V, s.c1 * E::N - s.off);
+        const Bits* in = reinterpret_cast<const Bits*>(s.data) + off;  // element i at in[i]
+        const int32_t e0 = max(0, s.c0 * E::N - off), e1 = min(A.V, s.c1 * E::N - off);
 #pragma unroll 1
         for (int32_t c = (e0 + o_off) / E::N + lane; c * E::N - o_off < e1; c += 32) {
             const int32_t i0 = c * E::N - o_off;
@@ -907,7 +1078,7 @@ __device__ __forceinline__ void read_par(const Args& A, RowPar& R, int32_t row, 
         if (A.temperature) R.T = A.temperature[q];
         if (A.top_k) R.k = max(A.top_k[q], 0);
         if (A.top_p) R.p = A.top_p[q];
-        float mp = A.min_p ? A.min_p[q] : 0.f;
+        const float mp = R.mp = A.min_p ? A.min_p[q] : 0.f;
         if (draws) R.u = A.uniforms[row];
         ok = R.T >= 0.f && R.T < INFINITY && R.p == R.p && mp == mp && R.u >= 0.f && R.u < 1.f;
         if (mp > 0.f) R.least = max((u64)ceil((double)fminf(mp, 1.f) * (double)((u64)1 << kBits)), (u64)1);
@@ -935,18 +1106,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ Ar
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // the segment on its way
+    // the slice on its way
     const T* base = (const T*)A.logits + (int64_t)row * A.stride;
-    Segment s;
-    s.off = (int32_t)((uintptr_t)base % 16 / sizeof(T));
-    const int32_t chunks = (s.off + A.V + E::N - 1) / E::N;
+    const int32_t off = (int32_t)((uintptr_t)base % 16 / sizeof(T));
+    const int32_t chunks = (off + A.V + E::N - 1) / E::N;
     const int parts = C * kWarps, part = team.rank * kWarps + warp;
-    s.c0 = (int32_t)((int64_t)chunks * part / parts);
-    s.c1 = (int32_t)((int64_t)chunks * (part + 1) / parts);
-    const int32_t first = (int32_t)((int64_t)chunks * (team.rank * kWarps) / parts);  // of the CTA
-    s.data = held - first;
+    auto begin = [&](int i) { return (int32_t)((int64_t)chunks * i / parts); };
+    const int32_t first = begin(team.rank * kWarps);
+    const Segment s{held - first, begin(part), begin(part + 1)};
     for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
-        const int32_t i0 = c * E::N - s.off;
+        const int32_t i0 = c * E::N - off;
         if (i0 >= 0 && i0 + E::N <= A.V) {
             cp_async16(held + (c - first), base + i0);
         } else {
@@ -964,50 +1133,52 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ Ar
     }
     if (tid == kThreads - 1) {
         sh.flags = 0;
-        sh.hit_warp = -1;
         read_par(A, sh.par, row, kDraws);
     }
-    Work<T> work{A, sh, team, s, lane, warp};
+    Work<T> work{A, sh, team, s, off, lane, warp};
     constexpr bool kQuick = sizeof(T) == 2;
     if (kQuick) work.zero_hist();
     __syncthreads();
     cp_async_wait<0>();
     __syncwarp();
 
+    work.survey();
     Result res{};
     res.slow = 1;
     if (kQuick) {
-        work.count_values();
+        work.count_values(work.lowest());
         team.sync();
         work.merge_counts();
-        if (team.rank == 0) {
-            uint32_t flags = 0;
-            for (int q = 0; q < C; ++q) flags |= *team.of(&sh.flags, q);
-            work.choose(flags);
-        }
+        if (team.rank == 0) work.choose();
         team.sync();
         res = *team.of(&sh.res, 0);
+    } else {
+        team.sync();
     }
+    const bool known = !res.slow;
     if (res.slow) res = work.choose_slow();
 
     const bool ok = !res.err;
-    bool told = false;  // the row's count is known
-    if (ok && (kDraws || res.partial || res.n < 0)) {
-        __syncthreads();
-        work.template tally<kDraws>(res);
+    int32_t n = ok ? res.n : -1, cut = 0x7fffffff;
+    if (ok && (kDraws || res.partial || !known)) {
+        if (known) {
+            work.part_of_counts(res);
+        } else {
+            u64 mass;
+            uint32_t above, ties;
+            work.template tally<kDraws>(res, s, mass, above, ties);
+            __syncthreads();
+            work.sum_up(mass, above, ties);
+        }
         team.sync();
-        work.template settle<kDraws>(res);
-        told = true;
-        __syncthreads();
+        if (kDraws) work.draw(res, known, row, [&](int q) { return begin(q * kWarps); });
+        else cut = work.cut_here(res, known);
+        n = sh.n;
     }
     if (C > 1) team.arrive();  // nothing of another CTA is read from here on
-    if (ok && kDraws) {
-        if (sh.hit_warp == part) work.pick(res, row, sh.hit_rest);
-    } else if (!kDraws) {
-        work.write(res, row, !ok);
-    }
+    if (!kDraws) work.write(res, row, !ok, cut);
     if (team.rank == 0 && tid == 0) {
-        if (A.kept) A.kept[row] = !ok ? -1 : told ? (int32_t)sh.above : res.n;
+        if (A.kept) A.kept[row] = n;
         if (!ok) {
             if (kDraws) {
                 A.tokens[row] = -1;
