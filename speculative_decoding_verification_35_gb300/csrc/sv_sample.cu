@@ -55,11 +55,12 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kBits = 44;  // of a weight's fraction; 2^18 weights of 1 sum to 2^62
 constexpr float kLowest = -3.402823466e38f;
 
-// The bins of the quick way, one for each bfloat16 magnitude code in [kCodeLo, kCodeHi] of either sign, one in the middle for
-// zero, and one at either end that stays empty.
+// The bins of the quick way, in the ranking's order: one for each bfloat16 magnitude code in [kCodeLo, kCodeHi] of either sign, one
+// in the middle for zero, and one at either end that counts for nothing (the last has -inf). Their words lie in the order
+// of the magnitudes: zero and the positive ones, from kNegative on zero (-0.0) and the negative ones.
 constexpr uint32_t kCodeLo = 0x3280u, kCodeHi = 0x447fu;  // 2^-26, 1020
 constexpr uint32_t kCodes = kCodeHi - kCodeLo + 1;
-constexpr int kMid = kCodes + 1, kBins = 2 * kMid + 1;
+constexpr int kMid = kCodes + 1, kBins = 2 * kMid + 1, kNegative = kMid + 1;
 constexpr int kGroupBins = 64, kGroups = (kBins + kGroupBins - 1) / kGroupBins;
 constexpr int kHist = kGroups * kGroupBins;  // words
 constexpr int kDigits = 4096;                // bins of the other way: two words each
@@ -67,6 +68,7 @@ static_assert(2 * kDigits <= kHist, "the histogram's words serve both ways");
 static_assert(kGroups <= 160, "five groups a lane");
 
 typedef unsigned long long u64;
+constexpr int kList = kThreads;  // candidates that the first CTA ranks, a thread each
 
 struct RowPar {
     ExpConst E;
@@ -84,9 +86,17 @@ struct Result {
     float m;          // the largest logit
     uint32_t err;
     int32_t slow;     // the quick way could not tell
+    int32_t listed;   // ranked from a list: a tie is kept up to index `cut`
+    int32_t cut;
     int32_t at;       // quick: the threshold's place among the bins
     uint32_t ties;    // quick: logits equal to it
     u64 mass;         // quick: of those above the threshold (and equal to it, where all are kept)
+};
+
+// A row whose kept tokens lie among few: those candidates, in the first CTA's shared memory (the histogram's place).
+struct List {
+    u64 order[kList];      // key << 32 | ~index: larger is earlier in the ranking
+    u64 trade[2][kList];   // for the sort
 };
 
 struct Found {  // a level of the slow way
@@ -109,8 +119,9 @@ struct alignas(16) Shared {
     uint32_t group_count[kGroups + 1];
     u64 scan[kWarps];
     Part warp_part[kWarps], part;  // part: the CTA's
-    uint32_t warp_max[kWarps], warp_min[kWarps];
-    uint32_t max_key, min_key;  // the CTA's largest logit, and the least of its threads' largest
+    uint32_t tops[kThreads], warp_max[kWarps], warp_min[kWarps];  // keys of the threads' largest
+    uint32_t max_key, low_key, share_key;  // the CTA's largest logit, the least that it counts, and the least of its share of k
+    uint32_t listed;                       // candidates
     uint32_t flags;
     float floor;
     RowPar par;
@@ -135,7 +146,7 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float float_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
-constexpr uint32_t kKeyMinusInf = 0x007fffffu, kKeyInf = 0xff800000u;
+constexpr uint32_t kKeyMinusInf = 0x007fffffu;
 
 // Fixed-point parts of two weights: W = (a << 22) + b. The first rounds to 2^-22 (the unit in the last place of 3 + w), the
 // second what that leaves, and the low part of the weight, to 2^-44.
@@ -186,10 +197,25 @@ struct Elem<float> {
         x[2] = __uint_as_float(q.z);
         x[3] = __uint_as_float(q.w);
     }
-    // a chunk with the elements of `mask` as they are and the others -inf
-    static __device__ __forceinline__ uint4 masked(const uint4& q, uint32_t mask) {
-        return make_uint4(mask & 1 ? q.x : kMinusInf, mask & 2 ? q.y : kMinusInf, mask & 4 ? q.z : kMinusInf, mask & 8 ? q.w : kMinusInf);
+    // a chunk with the elements from `least` on as they are and the others -inf
+    static __device__ __forceinline__ uint4 keep(const uint4& q, float least) {
+        return make_uint4(__uint_as_float(q.x) >= least ? q.x : kMinusInf, __uint_as_float(q.y) >= least ? q.y : kMinusInf,
+                          __uint_as_float(q.z) >= least ? q.z : kMinusInf, __uint_as_float(q.w) >= least ? q.w : kMinusInf);
     }
+    // which of them are from `least` on
+    static __device__ __forceinline__ uint32_t from(const uint4& q, float least) {
+        return (uint32_t)(__uint_as_float(q.x) >= least) | (uint32_t)(__uint_as_float(q.y) >= least) << 1 |
+               (uint32_t)(__uint_as_float(q.z) >= least) << 2 | (uint32_t)(__uint_as_float(q.w) >= least) << 3;
+    }
+    static __device__ __forceinline__ float next(float x) { return float_of(key_of(x) + 1u); }
+    // the largest so far, NaN from the first NaN on
+    static __device__ __forceinline__ void larger(uint32_t& top, const uint4& q) {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+r"(top) : "r"(w[i]));
+    }
+    static __device__ __forceinline__ float largest(uint32_t top) { return __uint_as_float(top); }
+    static constexpr uint32_t kNone = kMinusInf;
     static constexpr uint32_t bits_minus_inf = kMinusInf;
     typedef uint32_t Bits;
     static __device__ __forceinline__ float value(Bits b) { return __uint_as_float(b); }
@@ -205,15 +231,39 @@ struct Elem<__nv_bfloat16> {
             x[2 * i + 1] = bf16hi_to_f32(w[i]);
         }
     }
-    static __device__ __forceinline__ uint4 masked(const uint4& q, uint32_t mask) {
+    static __device__ __forceinline__ uint32_t from2(uint32_t w, __nv_bfloat162 least) {
+        return __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w), least);
+    }
+    static __device__ __forceinline__ uint4 keep(const uint4& q, float least) {
+        const __nv_bfloat162 l = __float2bfloat162_rn(least);
         uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (!(mask >> (2 * i) & 1u)) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
-            if (!(mask >> (2 * i + 1) & 1u)) w[i] = (w[i] & 0xffffu) | 0xff800000u;
+            const uint32_t m = from2(w[i], l);
+            w[i] = (w[i] & m) | (0xff80ff80u & ~m);
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
+    static __device__ __forceinline__ uint32_t from(const uint4& q, float least) {
+        const __nv_bfloat162 l = __float2bfloat162_rn(least);
+        const uint32_t m[4] = {from2(q.x, l), from2(q.y, l), from2(q.z, l), from2(q.w, l)};
+        if (!(m[0] | m[1] | m[2] | m[3])) return 0;
+        uint32_t k = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k |= ((m[i] & 1u) | (m[i] >> 15 & 2u)) << 2 * i;
+        return k;
+    }
+    static __device__ __forceinline__ float next(float x) { return float_of(key_of(x) + 0x10000u); }
+    static __device__ __forceinline__ void larger(uint32_t& top, const uint4& q) {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(w[i]));
+    }
+    static __device__ __forceinline__ float largest(uint32_t top) {
+        const float a = bf16lo_to_f32(top), b = bf16hi_to_f32(top);
+        return a != a ? a : b != b ? b : fmaxf(a, b);
+    }
+    static constexpr uint32_t kNone = 0xff80ff80u;
     static constexpr uint16_t bits_minus_inf = 0xff80u;
     typedef uint16_t Bits;
     static __device__ __forceinline__ float value(Bits b) { return __uint_as_float((uint32_t)b << 16); }
@@ -284,75 +334,88 @@ struct Work {
     Segment s;    // the warp's
     int32_t off;  // elements before the row's first in chunk 0
     int lane, warp;
+    float low;    // logits below it decide nothing
 
     // ------------------------------------------------------------------------------------------------
     // the largest, and what lies too low to matter
     // ------------------------------------------------------------------------------------------------
-    // Keys of a thread's largest and whether it met a NaN or +inf.
-    __device__ __forceinline__ uint32_t largest(uint32_t& flags) {
-        flags = 0;
-        if constexpr (sizeof(T) == 2) {
-            const uint32_t none = 0xff80ff80u;
-            uint32_t top = none, high = 0x80008000u, wide = 0;  // as floats, signed and unsigned
-#pragma unroll 2
-            for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
-                const uint4 q = s.data[c];
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    asm("max.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(w[i]));
-                    high = __vmaxs2(high, w[i]);
-                    wide = __vmaxu2(wide, w[i]);
-                }
-            }
-            if ((int16_t)high >= 0x7f80 || (int32_t)high >> 16 >= 0x7f80 || (wide & 0xffffu) > 0xff80u || wide >> 16 > 0xff80u)
-                flags = kNonfinite;
-            return key_of(fmaxf(bf16lo_to_f32(top), bf16hi_to_f32(top)));
-        } else {
-            uint32_t top = kKeyMinusInf;
-#pragma unroll 2
-            for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
-                float x[E::N];
-                E::unpack(s.data[c], x);
-#pragma unroll
-                for (int e = 0; e < E::N; ++e) {
-                    const uint32_t k = key_of(x[e]);
-                    if (k >= kKeyInf || k < kKeyMinusInf) flags = kNonfinite;
-                    else top = max(top, k);
-                }
-            }
-            return top;
-        }
+    // The key of a thread's largest, and whether it met a NaN or +inf.
+    __device__ __forceinline__ uint32_t largest(uint32_t& flags) const {
+        uint32_t top = E::kNone;
+#pragma unroll 4
+        for (int32_t c = s.c0 + lane; c < s.c1; c += 32) E::larger(top, s.data[c]);
+        const float x = E::largest(top);
+        flags = x < INFINITY ? 0u : (uint32_t)kNonfinite;
+        return x < INFINITY ? key_of(x) : kKeyMinusInf;
     }
-    // The CTA's largest, and the least of its threads': with a block barrier at the end.
+    // Of the threads' largest logits, whose keys are in `tops`: one that `many` of them reach, the largest such or nearly. By a
+    // warp; the least of them is reached by all.
+    static __device__ __forceinline__ uint32_t reached(const uint32_t* tops, int many, uint32_t low, uint32_t high) {
+        uint32_t x[kThreads / 32];
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) x[i] = tops[32 * i + (threadIdx.x & 31)];
+        ++high;
+#pragma unroll 1
+        for (int i = 0; i < 12 && high - low > (sizeof(T) == 2 ? 0xffffu : 1u); ++i) {  // low: `many` threads at least, high: fewer
+            const uint32_t mid = low + (high - low) / 2;
+            int n = 0;
+#pragma unroll
+            for (int k = 0; k < kThreads / 32; ++k) n += x[k] >= mid;
+            if (__reduce_add_sync(kAll, n) >= many) low = mid;
+            else high = mid;
+        }
+        return low;
+    }
+    // The CTA's largest, and the least logit that decides anything, with a block barrier at the end. With top-k, k up to the
+    // threads of a CTA: if k threads have a logit of x or more, what is below x is not among the first k of the ranking;
+    // and if in every CTA of the row k / C of them have x or more, neither. With min-p alone: those whose weight is clearly
+    // too small.
     __device__ __forceinline__ void survey() {
         uint32_t flags;
         const uint32_t top = largest(flags);
         flags = __reduce_or_sync(kAll, flags);
         const uint32_t hi = __reduce_max_sync(kAll, top), lo = __reduce_min_sync(kAll, top);
+        sh.tops[threadIdx.x] = top;
         if (lane == 0) {
             sh.warp_max[warp] = hi;
             sh.warp_min[warp] = lo;
             if (flags) atomicOr(&sh.flags, flags);
         }
         __syncthreads();
-        const uint32_t h = __reduce_max_sync(kAll, sh.warp_max[lane % kWarps]), l = __reduce_min_sync(kAll, sh.warp_min[lane % kWarps]);
-        if (threadIdx.x == 0) {
-            sh.max_key = h;
-            sh.min_key = l;
+        const uint32_t high = __reduce_max_sync(kAll, sh.warp_max[lane % kWarps]);
+        uint32_t low = kKeyMinusInf, share = kKeyMinusInf;
+        const RowPar& R = sh.par;
+        if (R.T == 0.f) {
+            low = high;
+        } else if (R.k > 0 && R.k <= kThreads) {
+            low = __reduce_min_sync(kAll, sh.warp_min[lane % kWarps]);
+            if (warp == 0) low = reached(sh.tops, R.k, low, high);
+            if (warp == 1) share = reached(sh.tops, (R.k + team.size - 1) / team.size, low, high);
+        } else if (R.least && !(R.p < 1.f)) {
+            const float x = float_of(high);
+            low = key_of(x + 1.0001f * R.T * __logf(fminf(R.mp, 1.f)) - 1e-5f * (fabsf(x) + R.T));
         }
+        if (threadIdx.x == 0) {
+            sh.max_key = high;
+            sh.low_key = low;
+        }
+        if (threadIdx.x == 32) sh.share_key = share;
         __syncthreads();
     }
-    // Logits below this decide nothing. With top-k, k up to the threads of a CTA: each of them has a logit of at least
-    // min_key, so k have, and what is not among the first k of the ranking does not matter (of 32 K logits a tenth is left).
-    // With min-p alone: those whose weight is clearly too small.
-    __device__ __forceinline__ float lowest() const {
+    // The least logit of the row that decides anything, from all CTAs' surveys.
+    __device__ __forceinline__ float row_low() const {
         const RowPar& R = sh.par;
-        const float top = float_of(sh.max_key);
-        if (R.T == 0.f) return top;
-        if (R.k > 0 && R.k <= kThreads) return float_of(sh.min_key);
-        if (R.least && !(R.p < 1.f)) return top + 1.0001f * R.T * __logf(fminf(R.mp, 1.f)) - 1e-5f * (fabsf(top) + R.T);
-        return -INFINITY;
+        uint32_t low = 0, share = ~0u;
+        if (lane < team.size) {
+            low = *team.of(&sh.low_key, lane);
+            share = *team.of(&sh.share_key, lane);
+        }
+        low = __reduce_max_sync(kAll, low);  // (of top-k any CTA's will do, of the others the largest logit's)
+        share = __reduce_min_sync(kAll, share);
+        if (R.T > 0.f && R.k > 0) low = max(low, share);
+        float f = low <= kKeyMinusInf ? -INFINITY : float_of(low);
+        if (sizeof(T) == 2) f = __bfloat162float(__float2bfloat16_rd(f));
+        return f;
     }
     __device__ __forceinline__ uint32_t cluster_max() const {
         uint32_t k = 0;
@@ -366,48 +429,209 @@ struct Work {
     }
 
     // ------------------------------------------------------------------------------------------------
-    // the quick way (bfloat16)
+    // few candidates
     // ------------------------------------------------------------------------------------------------
-    __device__ __forceinline__ void count_one(uint32_t bits, uint32_t o, uint32_t& flags) {
-        if (o - 1u < kCodes) {
-            const int s = -(int)(bits >> 15 & 1u);
-            atomicAdd(&sh.hist[kMid + (((int)o ^ s) - s)], 1u);
-            return;
-        }
-        const uint32_t a = bits & 0x7fffu;
-        if (a == 0) atomicAdd(&sh.hist[kMid], 1u);
-        else if ((bits & 0xffffu) != 0xff80u) flags |= kOutside;  // -inf is not ranked
-    }
-    __device__ __forceinline__ void count_values(float low) {
-        uint32_t flags = 0;
-        const __nv_bfloat162 low2 = __bfloat162bfloat162(__float2bfloat16_rd(low));
+    __device__ __forceinline__ List& list() const { return reinterpret_cast<List&>(sh.hist); }
+    // The segment's logits from `low` on, into the first CTA's list, in any order.
+    __device__ __forceinline__ void gather() const {
+        const float low = fmaxf(this->low, sizeof(T) == 2 ? -3.3895314e38f : kLowest);  // -inf is not ranked
+        List* to = team.of(&list(), 0);
+        uint32_t* count = team.of(&sh.listed, 0);
 #pragma unroll 2
         for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
             const uint4 q = s.data[c];
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            const uint32_t in = E::from(q, low);
+            if (!in) continue;
+            float x[E::N];
+            E::unpack(q, x);
+            uint32_t at = atomicAdd(count, (uint32_t)__popc(in));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                constexpr uint32_t lo = (kCodeLo - 1) * 0x10001u, hi = (kCodeHi + 1) * 0x10001u;
-                const uint32_t in = __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), low2);
-                const uint32_t o = __vminu2(__vmaxu2(w[i] & 0x7fff7fffu, lo), hi) - lo;
-                if (in & 1u) count_one(w[i], o & 0xffffu, flags);
-                if (in >> 16) count_one(w[i] >> 16, o >> 16, flags);
-            }
+            for (int e = 0; e < E::N; ++e)
+                if (in >> e & 1u) {
+                    if (at < kList) to->order[at] = (u64)key_of(x[e]) << 32 | (uint32_t)~(c * E::N + e - off);
+                    ++at;
+                }
         }
-        flags = __reduce_or_sync(kAll, flags);
-        if (lane == 0 && flags) atomicOr(&sh.flags, flags);
     }
-    // Value of bin kBins - 1 - d, d in the ranking's order.
+    // The CTA's values, one a thread and no two alike (those of threads from n on are 0), sorted: the largest first. Every warp
+    // sorts its own, by a bitonic network of shuffles; a value's place is then its place in its warp and those that it would
+    // have in the others' lists, each found by halving.
+    __device__ __noinline__ u64 sorted(u64 x, int n) const {
+        const int tid = threadIdx.x, lists = (n + 31) / 32;
+        List& L = list();
+        int place = 0;
+        if (warp < lists) {
+#pragma unroll 1
+            for (int k = 2; k <= 32; k *= 2)
+#pragma unroll 1
+                for (int j = k / 2; j > 0; j /= 2) {
+                    const u64 y = __shfl_xor_sync(kAll, x, j);
+                    // the larger one stays where the block of k runs down (the first of two, and the last of all)
+                    const bool larger = ((lane & k) == 0) == ((lane & j) == 0);
+                    if ((y > x) == larger) x = y;
+                }
+            L.trade[0][tid] = x;
+        }
+        __syncthreads();
+        if (warp < lists) {
+            place = lane;
+#pragma unroll 4
+            for (int l = 0; l < lists; ++l) {
+                const u64* v = L.trade[0] + 32 * l;
+                int at = 0;  // values of the list that are larger
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    if (v[at + o - 1] > x) at += o;
+                at += v[31] > x;
+                if (l != warp) place += at;
+            }
+            L.trade[1][x ? place : tid] = x;  // (zeros are the last, wherever)
+        }
+        __syncthreads();
+        return tid < n ? L.trade[1][tid] : 0;
+    }
+    // Sums of the CTA's values up to a thread's.
+    __device__ __noinline__ u64 block_inscan(u64 x) const {
+        const u64 upto = warp_inscan(x, lane);
+        __syncthreads();  // sh.scan is free
+        if (lane == 31) sh.scan[warp] = upto;
+        __syncthreads();
+        const u64 mine = lane < kWarps ? sh.scan[lane] : 0, before = warp_inscan(mine, lane) - mine;
+        return upto + __shfl_sync(kAll, before, warp);
+    }
+    // By the first CTA: the candidates sorted, one a thread, and the sums of their weights; with them what is kept. The draw
+    // is the same once more, with the kept ones by index.
+    template <bool kDraws>
+    __device__ __forceinline__ void rank(int32_t row) {
+        List& L = list();
+        const RowPar& R = sh.par;
+        const int n = (int)sh.listed, tid = threadIdx.x;
+        const uint32_t flags = cluster_flags() & kNonfinite, top = cluster_max();
+        Result res{};
+        res.m = float_of(top);
+        res.listed = 1;
+        res.err = R.err | (flags ? 1u << SV_ERR_NONFINITE : 0u);
+        if (!flags && top <= kKeyMinusInf) res.err |= 1u << SV_ERR_EMPTY_ROW;
+        res.slow = n > kList;
+        if (res.err || res.slow) {
+            if (tid == 0) sh.res = res;
+            return;
+        }
+        const u64 x = sorted(tid < n ? L.order[tid] : 0, n);
+        const u64 w = tid < n ? weight(float_of((uint32_t)(x >> 32)), res.m, R.E, sh.tab) : 0;
+        const u64 upto = block_inscan(w);
+        // the first k, then as many as sum to top_p of their weights
+        const int first = R.T == 0.f ? 1 : R.k > 0 ? min(R.k, n) : n;
+        if (tid == first - 1) sh.total = upto;
+        __syncthreads();
+        u64 enough = ~0ull;
+        if (R.p < 1.f) enough = max(scaled(sh.total, R.p, true), (u64)1);
+        const bool kept = tid < first && upto - w < enough && w >= R.least;
+        res.n = __syncthreads_count(kept);
+        if (tid == res.n - 1) {
+            sh.total = upto;
+            sh.hit_rest = x;
+        }
+        __syncthreads();
+        const u64 total = sh.total, border = sh.hit_rest;  // the last that is kept
+        res.thr = float_of((uint32_t)(border >> 32));
+        res.partial = 1;
+        res.cut = (int32_t)~(uint32_t)border;
+        if (tid == 0) sh.res = res;
+        if (!kDraws) return;
+        if (warp == kWarps - 1 && A.logprob && lane == 0 && R.T > 0.f) sh.log_total = log((double)total) - kBits * 0.6931471805599453;
+        const u64 target = scaled(total, R.u, false);
+        const u64 y = ~sorted(kept ? (u64)(uint32_t)x << 32 | (uint32_t)~(uint32_t)(x >> 32) : 0, res.n);
+        const u64 wy = tid < res.n ? weight(float_of((uint32_t)y), res.m, R.E, sh.tab) : 0;
+        const u64 run = block_inscan(wy);
+        if (run - wy <= target && target < run) {
+            A.tokens[row] = (int32_t)(y >> 32);
+            if (A.logprob) A.logprob[row] = R.T > 0.f ? (float)(((double)float_of((uint32_t)y) - res.m) / R.T - sh.log_total) : 0.f;
+        }
+    }
+
+    // ------------------------------------------------------------------------------------------------
+    // the quick way (bfloat16)
+    // ------------------------------------------------------------------------------------------------
+    // Of a pair of logits, the words of their bins.
+    static __device__ __forceinline__ uint32_t bins_of(uint32_t w) {
+        constexpr uint32_t lo = (kCodeLo - 1) * 0x10001u, hi = (kCodeHi + 1) * 0x10001u;
+        return __vminu2(__vmaxu2(w & 0x7fff7fffu, lo), hi) - lo + (w >> 15 & 0x10001u) * kNegative;
+    }
+    // Whether one of them has no bin: 0 < |x| < 2^-26, or |x| >= 1024 but for -inf.
+    static __device__ __forceinline__ bool outside(uint32_t w, uint32_t in) {
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t b = w >> 16 * i & 0xffffu, a = b & 0x7fffu;
+            any |= (in >> 16 * i & 1u) && (a - 1u < kCodeLo - 1u || (a > kCodeHi && b != 0xff80u));
+        }
+        return any;
+    }
+    // Counts the logits from `low` on.
+    __device__ __forceinline__ void count_values() {
+        bool odd = false;
+        if (low > -INFINITY) {  // few: most chunks have none
+            const __nv_bfloat162 low2 = __float2bfloat162_rn(low);
+#pragma unroll 2
+            for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
+                const uint4 q = s.data[c];
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                uint32_t in[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) in[i] = __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), low2);
+                if (!(in[0] | in[1] | in[2] | in[3])) continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (!in[i]) continue;
+                    const uint32_t at = bins_of(w[i]);
+                    odd |= outside(w[i], in[i]);
+                    if (in[i] & 1u) atomicAdd(&sh.hist[at & 0xffffu], 1u);
+                    if (in[i] >> 16) atomicAdd(&sh.hist[at >> 16], 1u);
+                }
+            }
+        } else {
+            uint32_t least = ~0u, most = 0;  // of |x| - 1, of |x| but for -inf
+#pragma unroll 2
+            for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
+                const uint4 q = s.data[c];
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t at = bins_of(w[i]), a = w[i] & 0x7fff7fffu;
+                    least = __vminu2(least, __vsub2(a, 0x00010001u));
+                    most = __vmaxu2(most, a & ~__vcmpeq2(w[i], 0xff80ff80u));
+                    atomicAdd(&sh.hist[at & 0xffffu], 1u);
+                    atomicAdd(&sh.hist[at >> 16], 1u);
+                }
+            }
+            odd = (least & 0xffffu) < kCodeLo - 1 || least >> 16 < kCodeLo - 1 || (most & 0xffffu) > kCodeHi || most >> 16 > kCodeHi;
+        }
+        if (__any_sync(kAll, odd) && lane == 0) atomicOr(&sh.flags, (uint32_t)kOutside);
+    }
+    // Value of bin d.
     static __device__ __forceinline__ float value_at(int d) {
         const int o = kMid - d;
         const uint32_t a = (uint32_t)(o < 0 ? -o : o);
         return __uint_as_float(a == 0 ? 0u : (o < 0 ? 0x80000000u : 0u) | (kCodeLo - 1 + a) << 16);
     }
+    // Bin of a value.
+    static __device__ __forceinline__ int bin_of(float x) {
+        const uint32_t b = __float_as_uint(x) >> 16;
+        const int a = (int)min(max(b & 0x7fffu, kCodeLo - 1), kCodeHi + 1) - (int)(kCodeLo - 1);
+        return kMid + (b & 0x8000u ? a : -a);
+    }
+    __device__ __forceinline__ uint32_t count_at(int d) const {
+        const int o = kMid - d;
+        if (o >= kMid || o <= -kMid) return 0;
+        if (o > 0) return sh.hist[o];
+        return sh.hist[kNegative - o] + (o == 0 ? sh.hist[0] : 0u);
+    }
     // Of group g of 64 bins, a lane's two: counts and weights. False, for the warp, if there is nothing.
     __device__ __forceinline__ bool pair_at(int g, float m, uint32_t* c, u64* w) const {
         const int d = g * kGroupBins + 2 * lane;
-        c[0] = d < kBins ? sh.hist[kBins - 1 - d] : 0u;
-        c[1] = d + 1 < kBins ? sh.hist[kBins - 2 - d] : 0u;
+        c[0] = count_at(d);
+        c[1] = count_at(d + 1);
         w[0] = w[1] = 0;
         if (!__any_sync(kAll, c[0] | c[1])) return false;
         const Fixed2 f = weights2(value_at(d), value_at(d + 1), m, sh.par.E, sh.tab);
@@ -421,6 +645,7 @@ struct Work {
         const RowPar& R = sh.par;
         const float m = float_of(top);
         const u64 least = R.least;
+        const int g0 = bin_of(m) / kGroupBins, g1 = bin_of(low) / kGroupBins;  // groups that hold something
         uint32_t many = 0;  // of weights of at least `least`, which are the ranking's first
         u64 heavy = 0;
         int last = -1;
@@ -428,7 +653,7 @@ struct Work {
         for (int g = warp; g < kGroups; g += kWarps) {
             uint32_t c[2], cc = 0;
             u64 w[2], mass = 0;
-            if (pair_at(g, m, c, w)) {
+            if (g >= g0 && g <= g1 && pair_at(g, m, c, w)) {
                 mass = c[0] * w[0] + c[1] * w[1];
                 const int d = g * kGroupBins + 2 * lane;
                 if (least && c[0] && w[0] >= least) many += c[0], heavy += c[0] * w[0], last = d;
@@ -531,10 +756,8 @@ struct Work {
             }
         }
         if (R.T == 0.f && top > kKeyMinusInf) {  // the bins hold what equals the largest of a CTA, the first of them that of all
-            const uint32_t a = __float_as_uint(m) >> 16;
-            const int o = max(0, (int)(a & 0x7fffu) - (int)(kCodeLo - 1));
-            res.at = min(max(kMid - (a & 0x8000u ? -o : o), 0), kBins - 1);
-            res.ties = sh.hist[kBins - 1 - res.at];
+            res.at = bin_of(m);
+            res.ties = count_at(res.at);
             res.r = 1;
             res.partial = res.ties > 1;
             res.n = 1;
@@ -549,9 +772,14 @@ struct Work {
     // Histograms of the cluster, summed into the first CTA's, a share of the bins by each.
     __device__ __forceinline__ void merge_counts() {
         if (team.size == 1) return;
-        const int per = (kHist / 4 + team.size - 1) / team.size, v0 = team.rank * per, v1 = min(v0 + per, kHist / 4);
+        // 16 bytes of the words from the least to the largest logit that is counted: of the positive ones, and of the negative
+        const int o1 = kMid - bin_of(float_of(cluster_max())), o0 = kMid - bin_of(low);
+        const int a0 = max(o0, 0) / 4, na = o1 >= 0 ? o1 / 4 - a0 + 1 : 0;
+        const int b0 = (kNegative + max(-o1, 0)) / 4, nb = o0 <= 0 ? (kNegative - o0) / 4 - b0 + 1 : 0;
 #pragma unroll 1
-        for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
+        for (int i = team.rank * kThreads + threadIdx.x; i < na + nb; i += team.size * kThreads) {
+            const int v = i < na ? a0 + i : b0 + i - na;
+            if (i >= na && na > 0 && v < a0 + na) continue;  // the word of both
             uint4 x[kMaxCtas];
 #pragma unroll
             for (int q = 0; q < kMaxCtas; ++q) {
@@ -575,7 +803,7 @@ struct Work {
         u64 mass = 0;
         uint32_t ties = 0, above = 0;
 #pragma unroll 1
-        for (int g = warp; g * kGroupBins <= res.at && team.rank > 0; g += kWarps) {
+        for (int g = bin_of(res.m) / kGroupBins + warp; g * kGroupBins <= res.at && team.rank > 0; g += kWarps) {
             uint32_t c[2];
             u64 w[2];
             if (!pair_at(g, res.m, c, w)) continue;
@@ -1012,55 +1240,42 @@ struct Work {
         const uint32_t before = (uint32_t)__shfl_sync(kAll, warp_inscan(mine, lane) - mine, warp);
         return cut_of(res, s, ties, min(ties, sh.keeps - min(sh.keeps, before)));
     }
-    // The segment with -inf where a token is not kept (copy: as it is).
+    // The segment with -inf where a token is not kept (copy: as it is); of those equal to the threshold, the ones up to index
+    // `cut` are kept.
     __device__ __forceinline__ void write(const Result& res, int32_t row, bool copy, int32_t cut) const {
         typedef typename E::Bits Bits;
         Bits* out = (Bits*)A.out + (int64_t)row * A.out_stride;
         const int32_t o_off = (int32_t)((uintptr_t)out % 16 / sizeof(Bits));
-        if (o_off == off) {
-#pragma unroll 2
-            for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
-                const uint4 q = s.data[c];
-                float x[E::N];
-                E::unpack(q, x);
-                const int32_t i0 = c * E::N - off;
-                const uint32_t k = copy ? ~0u : kept_of(x, i0, res, cut);
-                const uint4 y = E::masked(q, k);
-                if (i0 >= 0 && i0 + E::N <= A.V) {
-                    *reinterpret_cast<uint4*>(out + i0) = y;
-                } else {
-                    const Bits* b = reinterpret_cast<const Bits*>(&y);
-#pragma unroll
-                    for (int e = 0; e < E::N; ++e)
-                        if (i0 + e >= 0 && i0 + e < A.V) out[i0 + e] = b[e];
-                }
-            }
-            return;
-        }
-        // chunks of the output, which begin elsewhere
+        const float at = res.thr, above = E::next(res.thr);
         const Bits* in = reinterpret_cast<const Bits*>(s.data) + off;  // element i at in[i]
         const int32_t e0 = max(0, s.c0 * E::N - off), e1 = min(A.V, s.c1 * E::N - off);
-#pragma unroll 1
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(s.data);
+        const bool same = o_off == off;
+        const uint32_t shift = (uint32_t)((off - o_off) * (int)sizeof(Bits)) % 4 * 8;
+        // by the output's chunks of 16 bytes, which lie as the held ones do, or between two of them
+#pragma unroll 2
         for (int32_t c = (e0 + o_off) / E::N + lane; c * E::N - o_off < e1; c += 32) {
             const int32_t i0 = c * E::N - o_off;
-            Bits b[E::N];
+            if (i0 >= e0 && i0 + E::N <= e1 && (copy || i0 + E::N - 1 <= cut || i0 > cut)) {
+                uint4 q;
+                if (same) {
+                    q = s.data[c];
+                } else {
+                    const uint32_t* w = words + (i0 + off) * (int)sizeof(Bits) / 4;
+                    uint32_t x[5];
 #pragma unroll
-            for (int e = 0; e < E::N; ++e) {
-                const int32_t i = i0 + e;
-                b[e] = E::bits_minus_inf;
-                if (i >= e0 && i < e1) {
-                    const float x = E::value(in[i]);
-                    if (copy || x > res.thr || (x == res.thr && i <= cut)) b[e] = in[i];
+                    for (int i = 0; i < 5; ++i) x[i] = w[i];
+                    q = make_uint4(__funnelshift_r(x[0], x[1], shift), __funnelshift_r(x[1], x[2], shift), __funnelshift_r(x[2], x[3], shift),
+                                   __funnelshift_r(x[3], x[4], shift));
                 }
+                if (!copy) q = E::keep(q, i0 > cut ? above : at);
+                *reinterpret_cast<uint4*>(out + i0) = q;
+                continue;
             }
-            if (i0 >= e0 && i0 + E::N <= e1) {
-                uint4 y;
-                memcpy(&y, b, 16);
-                *reinterpret_cast<uint4*>(out + i0) = y;
-            } else {
-#pragma unroll
-                for (int e = 0; e < E::N; ++e)
-                    if (i0 + e >= e0 && i0 + e < e1) out[i0 + e] = b[e];
+#pragma unroll 1
+            for (int32_t i = max(i0, e0); i < min(i0 + E::N, e1); ++i) {
+                const float x = E::value(in[i]);
+                out[i] = copy || x > res.thr || (x == res.thr && i <= cut) ? in[i] : (Bits)E::bits_minus_inf;
             }
         }
     }
@@ -1132,35 +1347,43 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ Ar
         sh.tab[kExpTab + tid] = A.exp2_tab[tid].y;
     }
     if (tid == kThreads - 1) {
-        sh.flags = 0;
+        sh.flags = sh.listed = 0;
         read_par(A, sh.par, row, kDraws);
     }
-    Work<T> work{A, sh, team, s, off, lane, warp};
+    Work<T> work{A, sh, team, s, off, lane, warp, -INFINITY};
     constexpr bool kQuick = sizeof(T) == 2;
-    if (kQuick) work.zero_hist();
     __syncthreads();
     cp_async_wait<0>();
     __syncwarp();
 
     work.survey();
+    team.sync();
+    work.low = work.row_low();
     Result res{};
     res.slow = 1;
-    if (kQuick) {
-        work.count_values(work.lowest());
+    if (work.low > -INFINITY || A.V <= kList) {
+        work.gather();
+        team.sync();
+        if (team.rank == 0) work.template rank<kDraws>(row);
+        team.sync();
+        res = *team.of(&sh.res, 0);
+    }
+    if (kQuick && res.slow) {
+        work.zero_hist();
+        __syncthreads();
+        work.count_values();
         team.sync();
         work.merge_counts();
         if (team.rank == 0) work.choose();
         team.sync();
         res = *team.of(&sh.res, 0);
-    } else {
-        team.sync();
     }
     const bool known = !res.slow;
     if (res.slow) res = work.choose_slow();
 
     const bool ok = !res.err;
-    int32_t n = ok ? res.n : -1, cut = 0x7fffffff;
-    if (ok && (kDraws || res.partial || !known)) {
+    int32_t n = ok ? res.n : -1, cut = res.listed ? res.cut : 0x7fffffff;
+    if (ok && !res.listed && (kDraws || res.partial || !known)) {
         if (known) {
             work.part_of_counts(res);
         } else {
