@@ -50,7 +50,7 @@ struct Args {
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCtas = 8;
+constexpr int kMostThreads = 1024, kMostWarps = kMostThreads / 32, kMaxCtas = 8;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kBits = 44;  // of a weight's fraction; 2^18 weights of 1 sum to 2^62
 constexpr float kLowest = -3.402823466e38f;
@@ -63,12 +63,11 @@ constexpr uint32_t kCodes = kCodeHi - kCodeLo + 1;
 constexpr int kMid = kCodes + 1, kBins = 2 * kMid + 1, kNegative = kMid + 1;
 constexpr int kGroupBins = 64, kGroups = (kBins + kGroupBins - 1) / kGroupBins;
 constexpr int kHist = kGroups * kGroupBins;  // words
-constexpr int kDigits = 4096;                // bins of the other way: two words each
+constexpr int kDigits = 4608;                // bins of the other way: two words each
 static_assert(2 * kDigits <= kHist, "the histogram's words serve both ways");
 static_assert(kGroups <= 160, "five groups a lane");
 
 typedef unsigned long long u64;
-constexpr int kList = kThreads;  // candidates that the first CTA ranks, a thread each
 
 struct RowPar {
     ExpConst E;
@@ -95,8 +94,8 @@ struct Result {
 
 // A row whose kept tokens lie among few: those candidates, in the first CTA's shared memory (the histogram's place).
 struct List {
-    u64 order[kList];      // key << 32 | ~index: larger is earlier in the ranking
-    u64 trade[2][kList];   // for the sort
+    u64 order[kMostThreads];      // key << 32 | ~index: larger is earlier in the ranking
+    u64 trade[2][kMostThreads];   // for the sort
 };
 
 struct Found {  // a level of the slow way
@@ -117,9 +116,9 @@ struct alignas(16) Shared {
     float tab[2 * kExpTab];
     u64 group_mass[kGroups + 1];
     uint32_t group_count[kGroups + 1];
-    u64 scan[kWarps];
-    Part warp_part[kWarps], part;  // part: the CTA's
-    uint32_t tops[kThreads], warp_max[kWarps], warp_min[kWarps];  // keys of the threads' largest
+    u64 scan[kMostWarps];
+    Part warp_part[kMostWarps], part;  // part: the CTA's
+    uint32_t tops[kMostThreads], warp_max[kMostWarps], warp_min[kMostWarps];  // keys of the threads' largest
     uint32_t max_key, low_key, share_key;  // the CTA's largest logit, the least that it counts, and the least of its share of k
     uint32_t listed;                       // candidates
     uint32_t flags;
@@ -130,7 +129,7 @@ struct alignas(16) Shared {
     int32_t hit;      // the CTA, then the warp of the cluster, that holds the drawn token
     u64 hit_rest, total;
     uint32_t keeps;   // of the ties of the CTA (filter) or of the CTA that holds the draw
-    int32_t warp_keeps[kWarps], n;
+    int32_t warp_keeps[kMostWarps], n;
     int32_t token;
     float logit;
     double log_total;
@@ -208,6 +207,11 @@ struct Elem<float> {
                (uint32_t)(__uint_as_float(q.z) >= least) << 2 | (uint32_t)(__uint_as_float(q.w) >= least) << 3;
     }
     static __device__ __forceinline__ float next(float x) { return float_of(key_of(x) + 1u); }
+    // how many are x
+    static __device__ __forceinline__ uint32_t equal(const uint4& q, float x) {
+        return (uint32_t)(__uint_as_float(q.x) == x) + (uint32_t)(__uint_as_float(q.y) == x) + (uint32_t)(__uint_as_float(q.z) == x) +
+               (uint32_t)(__uint_as_float(q.w) == x);
+    }
     // the largest so far, NaN from the first NaN on
     static __device__ __forceinline__ void larger(uint32_t& top, const uint4& q) {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -254,6 +258,14 @@ struct Elem<__nv_bfloat16> {
         return k;
     }
     static __device__ __forceinline__ float next(float x) { return float_of(key_of(x) + 0x10000u); }
+    static __device__ __forceinline__ uint32_t equal(const uint4& q, float x) {
+        const __nv_bfloat162 v = __float2bfloat162_rn(x);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n += (uint32_t)__popc(__heq2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), v));
+        return n / 16;
+    }
     static __device__ __forceinline__ void larger(uint32_t& top, const uint4& q) {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -325,16 +337,92 @@ __device__ __forceinline__ uint32_t div_up(u64 a, u64 b) {
     return q;
 }
 
-template <typename T>
+// kHeld: the slice lies in shared memory; else it is read where the logits are, again in every pass (from L2, mostly).
+template <typename T, bool kHeld>
 struct Work {
     typedef Elem<T> E;
+    // held rows: two CTAs an SM; others: one, as fewer rows at a time leave more of each in L2 (704 rows of 128256 bf16: 153 us,
+    // with two of 512 threads 163, with four of 256 246)
+    static constexpr int kThreads = kHeld ? 512 : 1024, kWarps = kThreads / 32;
+    static constexpr int kList = kThreads;  // candidates that the first CTA ranks, a thread each
     const Args& A;
     Shared& sh;
     const Team& team;
     Segment s;    // the warp's
     int32_t off;  // elements before the row's first in chunk 0
+    int32_t full0;   // the first chunk that is all the row's, and how many there are
+    uint32_t fulls;
     int lane, warp;
     float low;    // logits below it decide nothing
+
+    // A chunk that is not all the row's.
+    __device__ __noinline__ uint4 edge(const Segment& g, int32_t c) const {
+        typedef typename E::Bits Bits;
+        const Bits* p = reinterpret_cast<const Bits*>(g.data) + off;
+        const int32_t i0 = c * E::N - off;
+        Bits b[E::N];
+#pragma unroll
+        for (int e = 0; e < E::N; ++e) b[e] = i0 + e >= 0 && i0 + e < A.V ? p[i0 + e] : (Bits)E::bits_minus_inf;
+        uint4 q;
+        memcpy(&q, b, 16);
+        return q;
+    }
+    __device__ __forceinline__ uint4 chunk(const Segment& g, int32_t c) const {
+        if (kHeld || (uint32_t)(c - full0) < fulls) return g.data[c];
+        return edge(g, c);
+    }
+    // All chunks of the warp's segment, four reads at a time. back: from the end on, as the pass after one from the beginning
+    // does: what that one read last is still in L2.
+    template <typename F>
+    __device__ __forceinline__ void each(F&& f, bool back = false) const {
+        const int32_t n = (s.c1 - s.c0 + 127) / 128;
+#pragma unroll 1
+        for (int32_t i = 0; i < n; ++i) {
+            const int32_t c0 = s.c0 + lane + 128 * (back ? n - 1 - i : i);
+            uint4 q[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c0 + 32 * k < s.c1) q[k] = chunk(s, c0 + 32 * k);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c0 + 32 * k < s.c1) f(c0 + 32 * k, q[k]);
+        }
+    }
+
+    __device__ __forceinline__ List& list() const { return reinterpret_cast<List&>(sh.hist); }
+    // The logits that f tells (by a bit each) of a chunk, into the first CTA's list, in any order.
+    template <typename F>
+    __device__ __forceinline__ void collect(F&& f) const {
+        typedef typename E::Bits Bits;
+        List* to = team.of(&list(), 0);
+        uint32_t* count = team.of(&sh.listed, 0);
+        const Bits* p = reinterpret_cast<const Bits*>(s.data);
+        const int32_t turns = (s.c1 - s.c0 + 127) / 128;
+#pragma unroll 1
+        for (int32_t t = turns - 1; t >= 0; --t) {
+            const int32_t c0 = s.c0 + 128 * t;
+            uint4 q[4];
+            uint32_t in = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c0 + 32 * k + lane < s.c1) q[k] = chunk(s, c0 + 32 * k + lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c0 + 32 * k + lane < s.c1) in |= f(q[k]) << k * E::N;
+            if (!__any_sync(kAll, in)) continue;
+            // one count for the warp's
+            const uint32_t n = (uint32_t)__popc(in), upto = (uint32_t)warp_inscan(n, lane);
+            uint32_t at = 0;
+            if (lane == 31) at = atomicAdd(count, upto);
+            at = __shfl_sync(kAll, at, 31) + upto - n;
+#pragma unroll 1
+            for (; in; in &= in - 1, ++at) {
+                const int bit = __ffs(in) - 1;
+                const int32_t i = (c0 + 32 * (bit / E::N) + lane) * E::N + bit % E::N;  // from chunk 0 on
+                if (at < kList) to->order[at] = (u64)key_of(E::value(p[i])) << 32 | (uint32_t)~(i - off);
+            }
+        }
+    }
 
     // ------------------------------------------------------------------------------------------------
     // the largest, and what lies too low to matter
@@ -342,8 +430,7 @@ struct Work {
     // The key of a thread's largest, and whether it met a NaN or +inf.
     __device__ __forceinline__ uint32_t largest(uint32_t& flags) const {
         uint32_t top = E::kNone;
-#pragma unroll 4
-        for (int32_t c = s.c0 + lane; c < s.c1; c += 32) E::larger(top, s.data[c]);
+        each([&](int32_t, const uint4& q) { E::larger(top, q); });
         const float x = E::largest(top);
         flags = x < INFINITY ? 0u : (uint32_t)kNonfinite;
         return x < INFINITY ? key_of(x) : kKeyMinusInf;
@@ -431,27 +518,10 @@ struct Work {
     // ------------------------------------------------------------------------------------------------
     // few candidates
     // ------------------------------------------------------------------------------------------------
-    __device__ __forceinline__ List& list() const { return reinterpret_cast<List&>(sh.hist); }
     // The segment's logits from `low` on, into the first CTA's list, in any order.
     __device__ __forceinline__ void gather() const {
         const float low = fmaxf(this->low, sizeof(T) == 2 ? -3.3895314e38f : kLowest);  // -inf is not ranked
-        List* to = team.of(&list(), 0);
-        uint32_t* count = team.of(&sh.listed, 0);
-#pragma unroll 2
-        for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
-            const uint4 q = s.data[c];
-            const uint32_t in = E::from(q, low);
-            if (!in) continue;
-            float x[E::N];
-            E::unpack(q, x);
-            uint32_t at = atomicAdd(count, (uint32_t)__popc(in));
-#pragma unroll
-            for (int e = 0; e < E::N; ++e)
-                if (in >> e & 1u) {
-                    if (at < kList) to->order[at] = (u64)key_of(x[e]) << 32 | (uint32_t)~(c * E::N + e - off);
-                    ++at;
-                }
-        }
+        collect([&](const uint4& q) { return E::from(q, low); });
     }
     // The CTA's values, one a thread and no two alike (those of threads from n on are 0), sorted: the largest first. Every warp
     // sorts its own, by a bitonic network of shuffles; a value's place is then its place in its warp and those that it would
@@ -573,14 +643,12 @@ struct Work {
         bool odd = false;
         if (low > -INFINITY) {  // few: most chunks have none
             const __nv_bfloat162 low2 = __float2bfloat162_rn(low);
-#pragma unroll 2
-            for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
-                const uint4 q = s.data[c];
+            each([&](int32_t, const uint4& q) {
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
                 uint32_t in[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) in[i] = __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), low2);
-                if (!(in[0] | in[1] | in[2] | in[3])) continue;
+                if (!(in[0] | in[1] | in[2] | in[3])) return;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (!in[i]) continue;
@@ -589,12 +657,10 @@ struct Work {
                     if (in[i] & 1u) atomicAdd(&sh.hist[at & 0xffffu], 1u);
                     if (in[i] >> 16) atomicAdd(&sh.hist[at >> 16], 1u);
                 }
-            }
+            }, true);
         } else {
             uint32_t least = ~0u, most = 0;  // of |x| - 1, of |x| but for -inf
-#pragma unroll 2
-            for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
-                const uint4 q = s.data[c];
+            each([&](int32_t, const uint4& q) {
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -604,7 +670,7 @@ struct Work {
                     atomicAdd(&sh.hist[at & 0xffffu], 1u);
                     atomicAdd(&sh.hist[at >> 16], 1u);
                 }
-            }
+            }, true);
             odd = (least & 0xffffu) < kCodeLo - 1 || least >> 16 < kCodeLo - 1 || (most & 0xffffu) > kCodeHi || most >> 16 > kCodeHi;
         }
         if (__any_sync(kAll, odd) && lane == 0) atomicOr(&sh.flags, (uint32_t)kOutside);
@@ -649,7 +715,7 @@ struct Work {
         uint32_t many = 0;  // of weights of at least `least`, which are the ranking's first
         u64 heavy = 0;
         int last = -1;
-#pragma unroll 1
+#pragma unroll 3
         for (int g = warp; g < kGroups; g += kWarps) {
             uint32_t c[2], cc = 0;
             u64 w[2], mass = 0;
@@ -798,7 +864,12 @@ struct Work {
         for (int i = threadIdx.x; i < kHist / 4; i += kThreads) reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0, 0, 0, 0);
     }
     // What a CTA has of the kept, from its histogram. (The first one's is the row's by now: it has what the others have not.)
+    template <bool kMass>
     __device__ __forceinline__ void part_of_counts(const Result& res) {
+        if (!kMass) {
+            if (threadIdx.x == 0) sh.part = Part{0, 0, team.rank > 0 && res.partial ? count_at(res.at) : 0};
+            return;
+        }
         const int end = res.partial ? res.at : res.at + 1;
         u64 mass = 0;
         uint32_t ties = 0, above = 0;
@@ -835,28 +906,22 @@ struct Work {
     // ------------------------------------------------------------------------------------------------
     // the slow way
     // ------------------------------------------------------------------------------------------------
-    // One level: the elements whose keys lie in [lo, lo + (bins << shift)), above `floor` and above -inf's, by digit, and
-    // the digit at which their counts (or weights, in the ranking's order) reach the target. first: the target is top_p
-    // of all weights and `extra`.
-    template <bool kMass>
-    __device__ __noinline__ Found level(uint32_t lo, int shift, int bins, uint32_t floor, float m, u64 target, bool first, u64 extra) {
+    // One level: the logits for which `index` gives a bin below `bins`, the larger ones' higher, and the bin at which their
+    // counts (or weights, in the ranking's order) reach the target. first: the target is top_p of all weights and `extra`.
+    template <bool kMass, typename F>
+    __device__ __forceinline__ Found level(int bins, F&& index, float m, u64 target, bool first, u64 extra) {
         __syncthreads();
         for (int i = threadIdx.x; i < kDigits; i += kThreads) sh.hist[i] = sh.hist[kDigits + i] = 0;
+        if (threadIdx.x == 0) sh.listed = 0;
         __syncthreads();
 #pragma unroll 1
         for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
             float x[E::N];
-            E::unpack(s.data[c], x);
+            E::unpack(chunk(s, c), x);
 #pragma unroll
             for (int e = 0; e < E::N; e += 2) {
-                const uint32_t k[2] = {key_of(x[e]), key_of(x[e + 1])};
-                bool in[2];
-                uint32_t at[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    at[i] = (k[i] - lo) >> shift;
-                    in[i] = k[i] >= lo && at[i] < (uint32_t)bins && k[i] > floor && k[i] > kKeyMinusInf;
-                }
+                const uint32_t at[2] = {index(x[e]), index(x[e + 1])};
+                const bool in[2] = {at[0] < (uint32_t)bins, at[1] < (uint32_t)bins};
                 if (!(in[0] || in[1])) continue;
                 if (!kMass) {
 #pragma unroll
@@ -924,20 +989,73 @@ struct Work {
         team.sync();
         return *team.of(&sh.found, 0);
     }
-    // The key at which the counts or weights of the elements above `floor` reach the target; rest: what is left of the
-    // target there, value: what its elements come to. False: they do not reach it (rest: by how much).
     template <bool kMass>
-    __device__ __forceinline__ bool seek(uint32_t floor, float m, u64 target, u64 extra, uint32_t& key, u64& rest, u64& value) {
-        Found f = level<kMass>(0u, 20, kDigits, floor, m, target, true, extra);
+    __device__ __noinline__ Found digit(uint32_t lo, int shift, int bins, uint32_t floor, float m, u64 target, bool first, u64 extra) {
+        return level<kMass>(
+            bins,
+            [&](float x) {
+                const uint32_t k = key_of(x);
+                return k >= lo && k > floor && k > kKeyMinusInf ? (k - lo) >> shift : ~0u;
+            },
+            m, target, first, extra);
+    }
+    // The key at which the counts or weights of the elements above `floor` reach the target; r: of the elements with that key
+    // so many are needed, of `ties`. False: they do not reach it (rest: by how much).
+    template <bool kMass>
+    __device__ __forceinline__ bool seek(uint32_t floor, float m, u64 target, u64 extra, uint32_t& key, uint32_t& r, uint32_t& ties, u64& rest) {
+        Found f = digit<kMass>(0u, 20, 4096, floor, m, target, true, extra);
         rest = f.rest;
         if (f.bin < 0) return false;
         key = (uint32_t)f.bin << 20;
-        f = level<kMass>(key, 8, kDigits, floor, m, f.rest, false, 0);
+        f = digit<kMass>(key, 8, 4096, floor, m, f.rest, false, 0);
         key += (uint32_t)f.bin << 8;
-        f = level<kMass>(key, 0, 256, floor, m, f.rest, false, 0);
+        f = digit<kMass>(key, 0, 256, floor, m, f.rest, false, 0);
         key += (uint32_t)f.bin;
-        rest = f.rest;
-        value = f.value;
+        const u64 w = kMass ? weight(float_of(key), m, sh.par.E, sh.tab) : 1;
+        r = div_up(f.rest, w);
+        ties = div_up(f.value, w);
+        return true;
+    }
+    // The same for top_p of all weights, in fewer passes: the bins are even in the weights' logarithms, and so narrow that
+    // the one with the crossing has few logits; those are sorted. False, for the cluster, if they are not so few.
+    __device__ __noinline__ bool seek_even(float m, uint32_t& key, uint32_t& r, uint32_t& ties) {
+        const float per = sh.par.E.K_hi * ((float)kDigits / (kBits + 1));
+        auto index = [&](float x) { return (uint32_t)(kDigits - 1) - (uint32_t)fminf((m - x) * per, 1e9f); };  // monotone in x
+        const Found f = level<true>(kDigits, index, m, 0, true, 0);
+        collect([&](const uint4& q) {
+                float x[E::N];
+                E::unpack(q, x);
+                uint32_t in = 0;
+#pragma unroll
+                for (int e = 0; e < E::N; ++e) in |= (uint32_t)(index(x[e]) == (uint32_t)f.bin) << e;
+                return in;
+            });
+        team.sync();
+        if (team.rank == 0) {
+            const int n = (int)sh.listed;
+            Found g{-1, 0, 0};
+            if (n <= kList) {
+                List& L = list();
+                const int tid = threadIdx.x;
+                const u64 x = sorted(tid < n ? L.order[tid] : 0, n);
+                const u64 w = tid < n ? weight(float_of((uint32_t)(x >> 32)), m, sh.par.E, sh.tab) : 0;
+                const u64 upto = block_inscan(w);
+                // the last that is needed, and those like it
+                if (upto - w < f.rest && f.rest <= upto) sh.hit_rest = x;
+                __syncthreads();
+                const uint32_t k = (uint32_t)(sh.hit_rest >> 32);
+                const bool like = tid < n && (uint32_t)(x >> 32) == k;
+                const int need = __syncthreads_count(like && x >= sh.hit_rest), all = __syncthreads_count(like);
+                g = {0, (u64)k << 32 | (uint32_t)need, (u64)all};
+            }
+            if (threadIdx.x == 0) sh.found = g;
+        }
+        team.sync();
+        const Found g = *team.of(&sh.found, 0);
+        if (g.bin < 0) return false;
+        key = (uint32_t)(g.rest >> 32);
+        r = (uint32_t)g.rest;
+        ties = (uint32_t)g.value;
         return true;
     }
     __device__ __forceinline__ Result choose_slow() {
@@ -956,27 +1074,23 @@ struct Work {
             res.partial = 1;
             return res;
         }
-        uint32_t floor = 0;  // keys above it, and r of its own
-        u64 ties = 0, r = 0, rest, value;
-        if (R.k > 0 && R.k < A.V && seek<false>(0u, m, (u64)R.k, 0, floor, rest, value)) {
-            r = rest;
-            ties = value;
-        }
+        uint32_t floor = 0, r = 0, ties = 0, key;  // keys above the floor are kept, and r of its own
+        u64 rest;
+        if (R.k > 0 && R.k < A.V) seek<false>(0u, m, (u64)R.k, 0, floor, r, ties, rest);
         if (R.p < 1.f) {
             const u64 w = r ? weight(float_of(floor), m, R.E, sh.tab) : 0;
-            uint32_t key;
-            if (seek<true>(floor, m, 0, r * w, key, rest, value)) {
-                const u64 wk = weight(float_of(key), m, R.E, sh.tab);
-                floor = key;
-                r = div_up(rest, wk);
-                ties = div_up(value, wk);
+            uint32_t q, all;
+            if (!r && seek_even(m, key, q, all)) {
+                floor = key, r = q, ties = all;
+            } else if (seek<true>(floor, m, 0, r * w, key, q, all, rest)) {
+                floor = key, r = q, ties = all;
             } else {
                 r = div_up(rest, w);
             }
         }
         if (r) {
             res.thr = float_of(floor);
-            res.r = (uint32_t)r;
+            res.r = r;
             res.partial = r < ties;
         }
         if (R.least) {  // the least logit of a weight that is large enough
@@ -1014,7 +1128,7 @@ struct Work {
 #pragma unroll 1
         for (int32_t c = g.c0 + lane; c < g.c1; c += 32) {
             float x[E::N];
-            E::unpack(g.data[c], x);
+            E::unpack(chunk(g, c), x);
 #pragma unroll
             for (int e = 0; e < E::N; e += 2) {
                 const bool in0 = x[e] > res.thr || (whole && x[e] == res.thr), in1 = x[e + 1] > res.thr || (whole && x[e + 1] == res.thr);
@@ -1058,7 +1172,7 @@ struct Work {
             uint32_t eq = 0;
             if (c < g.c1) {
                 float x[E::N];
-                E::unpack(g.data[c], x);
+                E::unpack(chunk(g, c), x);
 #pragma unroll
                 for (int e = 0; e < E::N; ++e) eq |= (uint32_t)(x[e] == thr) << e;
             }
@@ -1115,7 +1229,9 @@ struct Work {
         // the shares
         const int32_t h0 = slices(hit), h1 = slices(hit + 1), n = team.size * kWarps, me = team.rank * kWarps + warp;
         auto share = [&](int i) { return h0 + (int32_t)((int64_t)(h1 - h0) * i / n); };
-        Segment g{team.of(const_cast<uint4*>(reinterpret_cast<const uint4*>(&sh + 1)), hit) - h0, share(me), share(me + 1)};
+        const uint4* data = s.data;
+        if (kHeld) data = team.of(const_cast<uint4*>(reinterpret_cast<const uint4*>(&sh + 1)), hit) - h0;
+        const Segment g{data, share(me), share(me + 1)};
         u64 mass;
         uint32_t above, ties;
         tally<true>(res, g, mass, above, ties);
@@ -1179,7 +1295,7 @@ struct Work {
 #pragma unroll
             for (int e = 0; e < E::N; ++e) w[e] = 0;
             if (c < g.c1) {
-                E::unpack(g.data[c], x);
+                E::unpack(chunk(g, c), x);
                 const uint32_t k = kept_of(x, c * E::N - off, res, cut);
 #pragma unroll
                 for (int e = 0; e < E::N; e += 2)
@@ -1217,8 +1333,7 @@ struct Work {
     // ------------------------------------------------------------------------------------------------
     // The ties that this CTA's warps keep, where they are not all kept; and the row's count where it is not known.
     __device__ __forceinline__ int32_t cut_here(const Result& res, bool known) {
-        u64 none;
-        uint32_t above, ties = 0;
+        uint32_t ties = 0;
         if (warp == 0) {
             uint32_t keeps;
             const Part p = parts(res, known, keeps);
@@ -1226,13 +1341,13 @@ struct Work {
             if (lane == team.rank) {
                 sh.keeps = keeps;
                 sh.total = p.ties;
-                sh.n = (int32_t)n;
+                sh.n = known ? res.n : (int32_t)n;
             }
         }
         __syncthreads();
         if (!res.partial || sh.keeps == (uint32_t)sh.total) return 0x7fffffff;
         if (sh.keeps == 0) return -1;
-        tally<false>(res, s, none, above, ties);
+        each([&](int32_t, const uint4& q) { ties += E::equal(q, res.thr); });
         ties = __reduce_add_sync(kAll, ties);
         if (lane == 0) sh.warp_keeps[warp] = (int32_t)ties;
         __syncthreads();
@@ -1252,30 +1367,43 @@ struct Work {
         const uint32_t* words = reinterpret_cast<const uint32_t*>(s.data);
         const bool same = o_off == off;
         const uint32_t shift = (uint32_t)((off - o_off) * (int)sizeof(Bits)) % 4 * 8;
-        // by the output's chunks of 16 bytes, which lie as the held ones do, or between two of them
-#pragma unroll 2
-        for (int32_t c = (e0 + o_off) / E::N + lane; c * E::N - o_off < e1; c += 32) {
-            const int32_t i0 = c * E::N - o_off;
-            if (i0 >= e0 && i0 + E::N <= e1 && (copy || i0 + E::N - 1 <= cut || i0 > cut)) {
-                uint4 q;
+        // by the output's chunks of 16 bytes, which lie as the logits' do, or between two of them: whole ones, and others, or the
+        // one that the last tie lies in, by element
+        const int32_t w0 = (e0 + o_off + E::N - 1) / E::N, w1 = (min(e1, same ? e1 : A.V - 1) + o_off) / E::N;
+        const int32_t last = copy || cut == 0x7fffffff ? 0x7fffffff : (cut + o_off + E::N) / E::N - 1;  // the chunk of `cut`
+        const int32_t split = copy || cut == 0x7fffffff || (cut + o_off) % E::N == E::N - 1 || cut < 0 ? -1 : last;
+        auto whole = [&](int32_t c) { return c >= w0 && c < w1 && c != split; };
+        constexpr int kAtOnce = 4;
+#pragma unroll 1
+        for (int32_t c0 = (e0 + o_off) / E::N + lane; c0 * E::N - o_off < e1; c0 += 32 * kAtOnce) {
+            uint4 q[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int32_t c = c0 + 32 * k;
+                if (!whole(c)) continue;
                 if (same) {
-                    q = s.data[c];
+                    q[k] = kHeld ? s.data[c] : __ldcs(s.data + c);
                 } else {
-                    const uint32_t* w = words + (i0 + off) * (int)sizeof(Bits) / 4;
+                    const uint32_t* w = words + (c * E::N - o_off + off) * (int)sizeof(Bits) / 4;
                     uint32_t x[5];
 #pragma unroll
                     for (int i = 0; i < 5; ++i) x[i] = w[i];
-                    q = make_uint4(__funnelshift_r(x[0], x[1], shift), __funnelshift_r(x[1], x[2], shift), __funnelshift_r(x[2], x[3], shift),
-                                   __funnelshift_r(x[3], x[4], shift));
+                    q[k] = make_uint4(__funnelshift_r(x[0], x[1], shift), __funnelshift_r(x[1], x[2], shift),
+                                      __funnelshift_r(x[2], x[3], shift), __funnelshift_r(x[3], x[4], shift));
                 }
-                if (!copy) q = E::keep(q, i0 > cut ? above : at);
-                *reinterpret_cast<uint4*>(out + i0) = q;
-                continue;
             }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int32_t c = c0 + 32 * k, i0 = c * E::N - o_off;
+                if (whole(c)) {
+                    __stcs(reinterpret_cast<uint4*>(out + i0), copy ? q[k] : E::keep(q[k], c > last ? above : at));
+                    continue;
+                }
 #pragma unroll 1
-            for (int32_t i = max(i0, e0); i < min(i0 + E::N, e1); ++i) {
-                const float x = E::value(in[i]);
-                out[i] = copy || x > res.thr || (x == res.thr && i <= cut) ? in[i] : (Bits)E::bits_minus_inf;
+                for (int32_t i = max(i0, e0); i < min(i0 + E::N, e1); ++i) {
+                    const float x = E::value(in[i]);
+                    out[i] = copy || x > res.thr || (x == res.thr && i <= cut) ? in[i] : (Bits)E::bits_minus_inf;
+                }
             }
         }
     }
@@ -1309,9 +1437,10 @@ __device__ __forceinline__ void read_par(const Args& A, RowPar& R, int32_t row, 
     if (R.T == 0.f) R.least = 0;  // the first alone, whatever its weight
 }
 
-template <typename T, bool kDraws>
-__global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ Args A, int32_t C) {
+template <typename T, bool kDraws, bool kHeld>
+__global__ void __launch_bounds__(Work<T, kHeld>::kThreads, kHeld ? 2 : 1) k_rows(const __grid_constant__ Args A, int32_t C) {
     typedef Elem<T> E;
+    constexpr int kThreads = Work<T, kHeld>::kThreads, kWarps = kThreads / 32;
     extern __shared__ __align__(16) char raw[];
     Shared& sh = *reinterpret_cast<Shared*>(raw);
     uint4* held = reinterpret_cast<uint4*>(raw + sizeof(Shared));
@@ -1328,20 +1457,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ Ar
     const int parts = C * kWarps, part = team.rank * kWarps + warp;
     auto begin = [&](int i) { return (int32_t)((int64_t)chunks * i / parts); };
     const int32_t first = begin(team.rank * kWarps);
-    const Segment s{held - first, begin(part), begin(part + 1)};
-    for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
-        const int32_t i0 = c * E::N - off;
-        if (i0 >= 0 && i0 + E::N <= A.V) {
-            cp_async16(held + (c - first), base + i0);
-        } else {
-            typename E::Bits b[E::N];
+    const Segment s{kHeld ? held - first : reinterpret_cast<const uint4*>(base - off), begin(part), begin(part + 1)};
+    if (kHeld) {
+        for (int32_t c = s.c0 + lane; c < s.c1; c += 32) {
+            const int32_t i0 = c * E::N - off;
+            if (i0 >= 0 && i0 + E::N <= A.V) {
+                cp_async16(held + (c - first), base + i0);
+            } else {
+                typename E::Bits b[E::N];
 #pragma unroll
-            for (int e = 0; e < E::N; ++e)
-                b[e] = i0 + e >= 0 && i0 + e < A.V ? reinterpret_cast<const typename E::Bits*>(base)[i0 + e] : E::bits_minus_inf;
-            memcpy(held + (c - first), b, 16);
+                for (int e = 0; e < E::N; ++e)
+                    b[e] = i0 + e >= 0 && i0 + e < A.V ? reinterpret_cast<const typename E::Bits*>(base)[i0 + e] : E::bits_minus_inf;
+                memcpy(held + (c - first), b, 16);
+            }
         }
+        cp_async_commit();
     }
-    cp_async_commit();
     if (tid < 128) {
         sh.tab[tid] = A.exp2_tab[tid].x;
         sh.tab[kExpTab + tid] = A.exp2_tab[tid].y;
@@ -1350,18 +1481,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ Ar
         sh.flags = sh.listed = 0;
         read_par(A, sh.par, row, kDraws);
     }
-    Work<T> work{A, sh, team, s, off, lane, warp, -INFINITY};
+    const int32_t full0 = off > 0;
+    Work<T, kHeld> work{A, sh, team, s, off, full0, (uint32_t)max(0, (off + A.V) / E::N - full0), lane, warp, -INFINITY};
     constexpr bool kQuick = sizeof(T) == 2;
     __syncthreads();
-    cp_async_wait<0>();
-    __syncwarp();
+    if (kHeld) {
+        cp_async_wait<0>();
+        __syncwarp();
+    }
 
     work.survey();
     team.sync();
     work.low = work.row_low();
     Result res{};
     res.slow = 1;
-    if (work.low > -INFINITY || A.V <= kList) {
+    if (work.low > -INFINITY || A.V <= Work<T, kHeld>::kList) {
         work.gather();
         team.sync();
         if (team.rank == 0) work.template rank<kDraws>(row);
@@ -1385,7 +1519,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ Ar
     int32_t n = ok ? res.n : -1, cut = res.listed ? res.cut : 0x7fffffff;
     if (ok && !res.listed && (kDraws || res.partial || !known)) {
         if (known) {
-            work.part_of_counts(res);
+            work.template part_of_counts<kDraws>(res);
         } else {
             u64 mass;
             uint32_t above, ties;
@@ -1413,28 +1547,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ Ar
     if (C > 1) team.wait();
 }
 
-// CTAs of a row: as few as hold it, then more while the launch leaves SMs idle and a slice is worth a CTA.
-constexpr int kSmem2 = 113 * 1024, kSmem1 = 227 * 1024;  // of a CTA, two and one an SM
-constexpr int kLeast = 2048;                             // elements of a slice
+constexpr int kSmem = 113 * 1024;  // of a CTA, two an SM
+constexpr int kLeast = 2048;       // logits of a slice that is worth a CTA
+constexpr int kMostShares = 4;     // CTAs of a row that is not held: the draw's shares are 128
 
-template <typename T, bool kDraws>
-cudaError_t launch(const Args& A, cudaStream_t st) {
-    int dev, sms;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    const int64_t chunks = (A.V + Elem<T>::N - 1) / Elem<T>::N + 1;
-    auto bytes = [&](int c) { return (int64_t)sizeof(Shared) + ((chunks + c - 1) / c + 1) * 16; };
-    int C = 1;
-    while (C < kMaxCtas && bytes(C) > kSmem2) C *= 2;
-    while (C < kMaxCtas && (int64_t)A.rows * C <= sms && A.V / (2 * C) >= kLeast) C *= 2;
-    auto kernel = k_rows<T, kDraws>;
-    if (bytes(C) > kSmem1 || (int64_t)A.rows * C > 0x7fffffff) return cudaErrorInvalidValue;
+template <typename T, bool kDraws, bool kHeld>
+cudaError_t launch(const Args& A, int dev, int C, int64_t smem, cudaStream_t st) {
+    auto kernel = k_rows<T, kDraws, kHeld>;
     // the devices on which the kernel may use an SM's shared memory: setting that twice does no harm
     static std::atomic<unsigned long long> allowed{0};
     if (dev >= 64 || !(allowed.load() >> dev & 1u)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem1);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e == cudaSuccess && kHeld) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e != cudaSuccess) return e;
         if (dev < 64) allowed.fetch_or(1ull << dev);
     }
@@ -1446,12 +1570,36 @@ cudaError_t launch(const Args& A, cudaStream_t st) {
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)A.rows * (unsigned)C);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)bytes(C);
+    cfg.blockDim = dim3(Work<T, kHeld>::kThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, A, (int32_t)C);
+}
+
+// CTAs of a row, a power of two: where all rows fit the GPU at once, as few as hold them in shared memory, and more while that
+// leaves SMs idle and a slice is worth a CTA. Else the rows are read where they lie: rows that have to wait for others'
+// shared memory took longer (704 rows of 128256 bf16: 242 us held by clusters of 4).
+template <typename T, bool kDraws>
+cudaError_t launch(const Args& A, cudaStream_t st) {
+    int dev, sms;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int64_t chunks = (A.V + Elem<T>::N - 1) / Elem<T>::N + 1, rows = A.rows;
+    auto bytes = [&](int c) { return (int64_t)sizeof(Shared) + ((chunks + c - 1) / c + 1) * 16; };
+    int C = 1;
+    while (C < kMaxCtas && bytes(C) > kSmem) C *= 2;
+    const bool held = bytes(C) <= kSmem && rows * C <= 2 * sms;
+    if (held) {
+        while (C < kMaxCtas && rows * C <= sms && A.V / (2 * C) >= kLeast) C *= 2;
+    } else {  // measured: 128 rows of 129281 floats 166, 122 and 137 us with 1, 2 and 4; 704 of 128256 bf16 153, 216 and 343
+        C = 1;
+        while (C < kMostShares && 2 * rows * C < 3 * sms && A.V / (2 * C) >= kLeast) C *= 2;
+    }
+    if (rows * C > 0x7fffffff) return cudaErrorInvalidValue;
+    return held ? launch<T, kDraws, true>(A, dev, C, bytes(C), st) : launch<T, kDraws, false>(A, dev, C, sizeof(Shared), st);
 }
 
 struct ExpTable {  // 2^(j / 128) as two floats each
