@@ -435,23 +435,26 @@ struct Work {
         flags = x < INFINITY ? 0u : (uint32_t)kNonfinite;
         return x < INFINITY ? key_of(x) : kKeyMinusInf;
     }
-    // Of the threads' largest logits, whose keys are in `tops`: one that `many` of them reach, the largest such or nearly. By a
-    // warp; the least of them is reached by all.
-    static __device__ __forceinline__ uint32_t reached(const uint32_t* tops, int many, uint32_t low, uint32_t high) {
+    // Of the threads' largest logits, whose keys are in `tops`: a logit that `many` of them reach, the largest such or nearly.
+    // By a warp; the CTA's largest is `high`, the least of the threads' `low`.
+    static __device__ __forceinline__ uint32_t reached(const uint32_t* tops, int many, uint32_t low_key, uint32_t high_key) {
         uint32_t x[kThreads / 32];
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) x[i] = tops[32 * i + (threadIdx.x & 31)];
-        ++high;
+        float low = low_key <= kKeyMinusInf ? -INFINITY : float_of(low_key), high = float_of(high_key), step = 4.f;
 #pragma unroll 1
-        for (int i = 0; i < 12 && high - low > (sizeof(T) == 2 ? 0xffffu : 1u); ++i) {  // low: `many` threads at least, high: fewer
-            const uint32_t mid = low + (high - low) / 2;
+        for (int i = 0; i < 14; ++i) {  // low: `many` threads at least reach it
+            const float mid = low > -INFINITY ? 0.5f * low + 0.5f * high : high - step;
+            if (!(mid > low && mid < high)) break;
+            const uint32_t key = key_of(mid);
             int n = 0;
 #pragma unroll
-            for (int k = 0; k < kThreads / 32; ++k) n += x[k] >= mid;
+            for (int k = 0; k < kThreads / 32; ++k) n += x[k] >= key;
             if (__reduce_add_sync(kAll, n) >= many) low = mid;
             else high = mid;
+            step *= 4.f;
         }
-        return low;
+        return low > -INFINITY ? key_of(low) : kKeyMinusInf;
     }
     // The CTA's largest, and the least logit that decides anything, with a block barrier at the end. With top-k, k up to the
     // threads of a CTA: if k threads have a logit of x or more, what is below x is not among the first k of the ranking;
@@ -1578,22 +1581,25 @@ cudaError_t launch(const Args& A, int dev, int C, int64_t smem, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, kernel, A, (int32_t)C);
 }
 
-// CTAs of a row, a power of two: where all rows fit the GPU at once, as few as hold them in shared memory, and more while that
-// leaves SMs idle and a slice is worth a CTA. Else the rows are read where they lie: rows that have to wait for others'
-// shared memory took longer (704 rows of 128256 bf16: 242 us held by clusters of 4).
+// CTAs of a row, a power of two. Held rows take as few as hold them in shared memory, and more while that leaves SMs idle and a
+// slice is worth a CTA; all CTAs that two an SM allow are hardly ever there at once, as a cluster wants its SMs together, so
+// some are left over. Else the rows are read where they lie. A turn of the GPU's takes held rows about half as long, so they
+// are held if that takes less than twice the turns: measured, held and not, 157 rows of 24559 floats 35 and 53 us (2 turns
+// each), 198 of 59737 bf16 42 and 57 (2 and 2), 121 of 96499 60 and 48 (2 and 1), 704 of 128256 242 and 153 (10 and 5).
 template <typename T, bool kDraws>
 cudaError_t launch(const Args& A, cudaStream_t st) {
     int dev, sms;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const int64_t chunks = (A.V + Elem<T>::N - 1) / Elem<T>::N + 1, rows = A.rows;
+    const int64_t chunks = (A.V + Elem<T>::N - 1) / Elem<T>::N + 1, rows = A.rows, at_once = 15 * (int64_t)sms / 8;
     auto bytes = [&](int c) { return (int64_t)sizeof(Shared) + ((chunks + c - 1) / c + 1) * 16; };
     int C = 1;
     while (C < kMaxCtas && bytes(C) > kSmem) C *= 2;
-    const bool held = bytes(C) <= kSmem && rows * C <= 2 * sms;
+    const int64_t turns = (rows * C + at_once - 1) / at_once;
+    const bool held = bytes(C) <= kSmem && (turns == 1 || turns < 2 * ((rows + sms - 1) / sms));
     if (held) {
-        while (C < kMaxCtas && rows * C <= sms && A.V / (2 * C) >= kLeast) C *= 2;
+        while (C < kMaxCtas && rows * 2 * C <= at_once && A.V / (2 * C) >= kLeast) C *= 2;
     } else {  // measured: 128 rows of 129281 floats 166, 122 and 137 us with 1, 2 and 4; 704 of 128256 bf16 153, 216 and 343
         C = 1;
         while (C < kMostShares && 2 * rows * C < 3 * sms && A.V / (2 * C) >= kLeast) C *= 2;
