@@ -1550,8 +1550,8 @@ __global__ void __launch_bounds__(Work<T, kHeld>::kThreads, kHeld ? 2 : 1) k_row
     if (C > 1) team.wait();
 }
 
-constexpr int kSmem = 113 * 1024;  // of a CTA, two an SM
-constexpr int kLeast = 2048;       // logits of a slice that is worth a CTA
+constexpr int kSmem = 113 * 1024, kSmemAlone = 227 * 1024;  // of a CTA, two an SM and one
+constexpr int kLeast = 4096;       // logits of a slice that is worth a CTA
 constexpr int kMostShares = 4;     // CTAs of a row that is not held: the draw's shares are 128
 
 template <typename T, bool kDraws, bool kHeld>
@@ -1560,7 +1560,7 @@ cudaError_t launch(const Args& A, int dev, int C, int64_t smem, cudaStream_t st)
     // the devices on which the kernel may use an SM's shared memory: setting that twice does no harm
     static std::atomic<unsigned long long> allowed{0};
     if (dev >= 64 || !(allowed.load() >> dev & 1u)) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlone);
         if (e == cudaSuccess && kHeld) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e != cudaSuccess) return e;
         if (dev < 64) allowed.fetch_or(1ull << dev);
@@ -1597,7 +1597,8 @@ cudaError_t launch(const Args& A, cudaStream_t st) {
     int C = 1;
     while (C < kMaxCtas && bytes(C) > kSmem) C *= 2;
     const int64_t turns = (rows * C + at_once - 1) / at_once;
-    const bool held = bytes(C) <= kSmem && (turns == 1 || turns < 2 * ((rows + sms - 1) / sms));
+    const bool alone = bytes(C) > kSmem && bytes(C) <= kSmemAlone && rows * C <= sms * 15 / 16;  // long rows, few
+    const bool held = alone || (bytes(C) <= kSmem && (turns == 1 || turns < 2 * ((rows + sms - 1) / sms)));
     if (held) {
         while (C < kMaxCtas && rows * 2 * C <= at_once && A.V / (2 * C) >= kLeast) C *= 2;
     } else {  // measured: 128 rows of 129281 floats 166, 122 and 137 us with 1, 2 and 4; 704 of 128256 bf16 153, 216 and 343

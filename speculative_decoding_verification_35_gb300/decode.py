@@ -1,14 +1,16 @@
-"""A small decoder that generates with token trees: the cache calls and the verify step as they are used together.
+"""A small decoder that generates with token trees, or samples: the calls as they are used together.
 
-    python -m speculative_decoding_verification_35_gb300.decode [SEQUENCES] [STEPS]
+    python -m speculative_decoding_verification_35_gb300.decode [SEQUENCES] [STEPS] [sample]
 
 The target model is a few layers of attention over a paged cache, with random weights (projections are torch
-products). A step drafts a token tree per sequence, runs the model once over the trees (in every layer
-spec_cache_append and spec_cache_attend), verifies them (spec_verify_tree), moves the accepted paths to the front of
-their slots (spec_cache_compact) and appends the emitted tokens to the histories (spec_verify_commit). The drafts come
-from the model without its layers, a bigram table: the best WIDTH children of the root, and below each of them the
-best continuation, DEPTH tokens deep. No step waits for the host. The prompt is a chunk like any other, a chain whose
-tokens are all kept.
+products) and, if wanted, capped scores. A step makes room for its tokens in the cache (spec_cache_reserve), drafts a
+token tree per sequence, runs the model once over the trees (in every layer spec_cache_append and spec_cache_attend),
+verifies them (spec_verify_tree), moves the accepted paths to the front of their slots (spec_cache_compact) and appends
+the emitted tokens to the histories (spec_verify_commit). The drafts come from the model without its layers, a bigram
+table: the best WIDTH children of the root, and below each of them the best continuation, DEPTH tokens deep. A sampled
+step draws a chain of DEPTH drafts from the bigram's filtered distributions (spec_sample), filters the target's and the
+drafts' logits (spec_filter) and verifies them as they are then (spec_verify_fused). No step waits for the host. The prompt
+is a chunk like any other, a chain whose tokens are all kept.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ import sys
 import torch
 
 from . import speccache as sc
+from . import specsample as ss
 from . import specverify as sv
 
 WIDTH, DEPTH = 3, 3
@@ -30,10 +33,11 @@ def _ok(rc):
 
 
 class Decoder:
-    """Random-weight decoder over a paged cache. dim: of the residual stream; heads: key and value heads."""
+    """Random-weight decoder over a paged cache. dim: of the residual stream; heads: key and value heads; cap: of the
+    attention's scores, 0 for none; pages: of the pool, as many as all sequences can fill by default."""
 
     def __init__(self, sequences, capacity, vocab=512, dim=256, layers=2, q_heads=8, heads=2, head_dim=64, page_size=16,
-                 seed=0, device="cuda"):
+                 seed=0, device="cuda", cap=0.0, pages=None):
         g = torch.Generator(device=device).manual_seed(seed)
 
         def weight(n, m):
@@ -48,10 +52,12 @@ class Decoder:
             -torch.arange(0, head_dim, 2, device=device) / head_dim)
         self.rope = sc.Rope(torch.cat((angles.cos(), angles.sin()), 1).float())
         per = -(-capacity // page_size)
-        pages = torch.randperm(sequences * per, generator=g, device=device).to(torch.int32)
-        shape = (layers, sequences * per, page_size, heads, head_dim)
+        pages = sequences * per if pages is None else pages
+        self.cap = cap
+        self.pool = sc.PagePool.create(sequences, per, pages, page_size, device)
+        shape = (layers, pages, page_size, heads, head_dim)
         self.cache = sc.PagedCache(torch.empty(shape, dtype=torch.bfloat16, device=device),
-                                   torch.empty(shape, dtype=torch.bfloat16, device=device), pages.view(sequences, per))
+                                   torch.empty(shape, dtype=torch.bfloat16, device=device), self.pool.page_table)
         i32 = dict(dtype=torch.int32, device=device)
         self.cached = torch.zeros(sequences, **i32)
         self.history = torch.zeros((sequences, capacity), **i32)
@@ -66,6 +72,11 @@ class Decoder:
         self.path = torch.empty(sequences * n, **i32)
         self.tokens_out = torch.empty(sequences * (n + 1), **i32)
         self.tree = sc.Chunk(self.offs, self.cached, sequences * (n + 1), n, self.parents)
+        # a sampled step's chain, its tokens and the logits of its drafts
+        self.chain_offs = torch.arange(sequences + 1, **i32) * DEPTH
+        self.chain_gammas = torch.full((sequences,), DEPTH, **i32)
+        self.chain = sc.Chunk(self.chain_offs, self.cached, sequences * (DEPTH + 1), DEPTH)
+        self.steps = 0
         self.ws_bytes = sv.spec_verify_workspace_size(sequences, vocab, n)
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=device)
 
@@ -74,7 +85,9 @@ class Decoder:
         return torch.nn.functional.rms_norm(x, x.shape[-1:]).to(torch.bfloat16)
 
     def forward(self, chunk, tokens):
-        """Logits (bfloat16) of a chunk's rows; its keys and values are appended to the cache."""
+        """Logits (bfloat16) of a chunk's rows; its keys and values are appended to the cache, in pages that are taken for
+        them (and of those that the last chunk took, the ones that it left unused go back)."""
+        _ok(self.pool.reserve(chunk))
         x = self.embed[tokens].float()
         D, hq, h = self.head_dim, self.q_heads, self.heads
         q_rot = torch.empty((len(tokens), hq, D), dtype=torch.bfloat16, device=x.device)
@@ -82,7 +95,7 @@ class Decoder:
         for layer in range(self.layers):
             rows = (self._norm(x) @ self.qkv[layer]).view(-1, hq + 2 * h, D)
             _ok(self.cache.append(chunk, rows[:, :hq], rows[:, hq:hq + h], rows[:, hq + h:], q_rot, self.rope, layer))
-            _ok(self.cache.attend(chunk, q_rot, att, layer=layer))
+            _ok(self.cache.attend(chunk, q_rot, att, layer=layer, cap=self.cap))
             x = x + (att.view(len(tokens), -1) @ self.out[layer]).float()
         return self._norm(x) @ self.unembed
 
@@ -128,18 +141,59 @@ class Decoder:
                                   status, stream))
 
 
+    def filters(self, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+        """The filters of a sampled step's draft and target rows; each argument a number, or one a sequence."""
+        def each(x, kind):
+            return torch.as_tensor(x, dtype=kind, device=self.cached.device).expand(self.B).contiguous()
+        asked = (each(temperature, torch.float32), each(top_k, torch.int32), each(top_p, torch.float32),
+                 each(min_p, torch.float32))
+        who = torch.arange(self.B, dtype=torch.int32, device=self.cached.device)
+        return (ss.Filter(*asked), ss.Filter(*asked, request=who.repeat_interleave(DEPTH)),
+                ss.Filter(*asked, request=who.repeat_interleave(DEPTH + 1)))
+
+    def sampled_step(self, filters, temperature, seed=0, generator=None):
+        """Drafts, verifies and keeps up to DEPTH + 1 new tokens a sequence, drawn from the target's filtered
+        distributions. filters: of `filters`, with this temperature."""
+        B, dev = self.B, self.cached.device
+        drafts = torch.empty((B, DEPTH), dtype=torch.int32, device=dev)
+        logits = torch.empty((B, DEPTH, self.vocab), dtype=torch.bfloat16, device=dev)
+        token, drawn = self.next, torch.empty(B, dtype=torch.int32, device=dev)
+        for j in range(DEPTH):
+            logits[:, j] = self._norm(self.embed[token].float()) @ self.unembed
+            _ok(filters[0].sample(logits[:, j], torch.rand(B, generator=generator, device=dev), drawn))
+            drafts[:, j] = drawn
+            token = drawn
+        target = self.forward(self.chain, torch.cat((self.next[:, None], drafts), 1).reshape(-1))
+        draft = logits.view(B * DEPTH, self.vocab)
+        _ok(filters[1].mask(draft, draft))
+        _ok(filters[2].mask(target, target))
+        self.steps += 1
+        _ok(sv.spec_verify_fused(target.data_ptr(), draft.data_ptr(), sv.SV_BF16, drafts.data_ptr(), self.chain_offs.data_ptr(),
+                                 self.chain_gammas.data_ptr(), B, self.vocab, DEPTH, temperature, seed, self.steps,
+                                 self.tokens_out.data_ptr(), self.accepted.data_ptr(), self.status.data_ptr(), self.ws.data_ptr(),
+                                 self.ws_bytes, self.history.data_ptr(), self.capacity, self.lengths.data_ptr(), self.next.data_ptr(),
+                                 torch.cuda.current_stream().cuda_stream))
+        _ok(self.cache.compact(self.chain, self.accepted, None, self.cached))
+
+
 def main(argv=None) -> int:
     argv = sys.argv[1:] if argv is None else argv
     B = int(argv[0]) if argv else 4
     steps = int(argv[1]) if len(argv) > 1 else 32
+    sampled = len(argv) > 2 and argv[2] == "sample"
     n = 20
     d = Decoder(B, n + 1 + steps * (DEPTH + 1) + len(PARENTS))
     d.prompt(torch.randint(d.vocab, (B, n), device="cuda", generator=torch.Generator("cuda").manual_seed(1)))
+    filters = d.filters(0.8, 50, 0.95, 0.01)
     for _ in range(steps):
-        d.step()
+        if sampled:
+            d.sampled_step(filters, 0.8, generator=torch.Generator("cuda").manual_seed(d.steps))
+        else:
+            d.step()
     torch.cuda.synchronize()
-    if int(d.status.item()) or d.cache.status_bits():
-        print("device status", int(d.status.item()), d.cache.status_bits(), file=sys.stderr)
+    found = [int(d.status.item()), d.cache.status_bits(), d.pool.status_bits()] + [f.status_bits() for f in filters]
+    if any(found):
+        print("device status", *found, file=sys.stderr)
         return 1
     got = d.lengths - n - 1
     print(f"{B} sequences, {steps} steps: {got.tolist()} tokens, {got.float().mean().item() / steps:.2f} a step")
