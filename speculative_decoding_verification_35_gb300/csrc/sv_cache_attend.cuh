@@ -611,7 +611,8 @@ __device__ __forceinline__ float row_unit(float unit, float down) { return at_le
 // (5.5e-8; 1.6e-7 with the roundings): nine packed operations for two scores and none of the special-function unit, which
 // the weights keep busy. Past 1, 1 - 2 / (1 + 2^(2 x log2 e)): its error, some 2^-22 of one, is as small a part there.
 struct Cap {
-    F2 c[7];   // times cap log2e, the highest first
+    F2 c[7], d[4];   // times cap log2e, the highest first; d is for x up to kSmall
+    static constexpr float kSmall = 0.55f;
     float by;  // x = s by, for scores of unit 1
     float most;  // cap log2e
     __device__ __forceinline__ explicit Cap(float cap) {
@@ -620,6 +621,17 @@ struct Cap {
         const float q[7] = {0.00105826119f, -0.00625932904f, 0.0203597479f, -0.0534987018f, 0.133264087f, -0.333329868f, 1.f};
 #pragma unroll
         for (int i = 0; i < 7; ++i) c[i] = pack2(q[i] * most, q[i] * most);
+        const float r[4] = {0.0164375687f, -0.0526718062f, 0.133207249f, -0.333329466f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = pack2(r[i] * most, r[i] * most);
+    }
+    // x up to kSmall, degree 4 (4e-8; 1.2e-7 with the roundings)
+    __device__ __forceinline__ F2 small(F2 x) const {
+        const F2 y = mul2(x, x);
+        F2 p = d[0];
+#pragma unroll
+        for (int i = 1; i < 4; ++i) p = fma2(p, y, d[i]);
+        return mul2(fma2(p, y, c[6]), x);
     }
     // x up to 1; and what is added to the score
     __device__ __forceinline__ F2 near(F2 x, F2 o) const {

@@ -199,13 +199,17 @@ struct Scoring {
             tc_wait_ld();
             return;
         }
+        auto each = [&](auto&& g) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            float a, b;
-            unpack2(cap.near(mul2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), f2), 0), a, b);
-            s[i] = __float_as_uint(a);
-            s[i + 1] = __float_as_uint(b);
-        }
+            for (int i = 0; i < 32; i += 2) {
+                float a, b;
+                unpack2(g(mul2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), f2)), a, b);
+                s[i] = __float_as_uint(a);
+                s[i + 1] = __float_as_uint(b);
+            }
+        };
+        if (__any_sync(kAll, big * f > Cap::kSmall)) each([&](F2 x) { return cap.near(x, 0); });
+        else each([&](F2 x) { return cap.small(x); });
     }
 };
 // A tile's scores become logarithms of the weights, in their place: a pass of its own.
