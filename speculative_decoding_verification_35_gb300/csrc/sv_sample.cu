@@ -72,6 +72,7 @@ typedef unsigned long long u64;
 struct RowPar {
     ExpConst E;
     float T, p, u, mp;
+    double per;     // 1 / T
     int32_t k;      // 0: none
     u64 least;      // of a kept weight, 0: none
     uint32_t err;
@@ -443,7 +444,7 @@ struct Work {
         for (int i = 0; i < kThreads / 32; ++i) x[i] = tops[32 * i + (threadIdx.x & 31)];
         float low = low_key <= kKeyMinusInf ? -INFINITY : float_of(low_key), high = float_of(high_key), step = 4.f;
 #pragma unroll 1
-        for (int i = 0; i < 14; ++i) {  // low: `many` threads at least reach it
+        for (int i = 0; i < 9; ++i) {  // low: `many` threads at least reach it
             const float mid = low > -INFINITY ? 0.5f * low + 0.5f * high : high - step;
             if (!(mid > low && mid < high)) break;
             const uint32_t key = key_of(mid);
@@ -619,7 +620,7 @@ struct Work {
         const u64 run = block_inscan(wy);
         if (run - wy <= target && target < run) {
             A.tokens[row] = (int32_t)(y >> 32);
-            if (A.logprob) A.logprob[row] = R.T > 0.f ? (float)(((double)float_of((uint32_t)y) - res.m) / R.T - sh.log_total) : 0.f;
+            if (A.logprob) A.logprob[row] = R.T > 0.f ? (float)(((double)float_of((uint32_t)y) - res.m) * R.per - sh.log_total) : 0.f;
         }
     }
 
@@ -1283,7 +1284,7 @@ struct Work {
             __syncthreads();
             if (threadIdx.x == 0) {
                 A.tokens[row] = sh.token;
-                if (A.logprob) A.logprob[row] = R.T > 0.f ? (float)(((double)sh.logit - res.m) / R.T - sh.log_total) : 0.f;
+                if (A.logprob) A.logprob[row] = R.T > 0.f ? (float)(((double)sh.logit - res.m) * R.per - sh.log_total) : 0.f;
             }
         }
     }
@@ -1430,6 +1431,7 @@ __device__ __forceinline__ void read_par(const Args& A, RowPar& R, int32_t row, 
         if (mp > 0.f) R.least = max((u64)ceil((double)fminf(mp, 1.f) * (double)((u64)1 << kBits)), (u64)1);
     }
     if (ok && R.T > 0.f) {
+        R.per = 1.0 / (double)R.T;
         const double K = 1.4426950408889634074 / (double)R.T;
         R.E.K_hi = (float)K;
         R.E.K_lo = (float)(K - (double)R.E.K_hi);
@@ -1594,13 +1596,19 @@ cudaError_t launch(const Args& A, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int64_t chunks = (A.V + Elem<T>::N - 1) / Elem<T>::N + 1, rows = A.rows, at_once = 15 * (int64_t)sms / 8;
     auto bytes = [&](int c) { return (int64_t)sizeof(Shared) + ((chunks + c - 1) / c + 1) * 16; };
-    int C = 1;
-    while (C < kMaxCtas && bytes(C) > kSmem) C *= 2;
+    auto least = [&](int64_t smem) {
+        int c = 1;
+        while (c < kMaxCtas && bytes(c) > smem) c *= 2;
+        return c;
+    };
+    int C = least(kSmem);
     const int64_t turns = (rows * C + at_once - 1) / at_once;
-    const bool alone = bytes(C) > kSmem && bytes(C) <= kSmemAlone && rows * C <= sms * 15 / 16;  // long rows, few
-    const bool held = alone || (bytes(C) <= kSmem && (turns == 1 || turns < 2 * ((rows + sms - 1) / sms)));
+    // long rows that fit at once by one CTA an SM
+    const bool alone = !(bytes(C) <= kSmem && turns == 1) && bytes(least(kSmemAlone)) <= kSmemAlone && rows * least(kSmemAlone) <= at_once / 2;
+    const bool held = alone || (bytes(C) <= kSmem && turns < 2 * ((rows + sms - 1) / sms));
     if (held) {
-        while (C < kMaxCtas && rows * 2 * C <= at_once && A.V / (2 * C) >= kLeast) C *= 2;
+        if (alone) C = least(kSmemAlone);
+        while (C < kMaxCtas && rows * 2 * C <= (alone ? at_once / 2 : at_once) && A.V / (2 * C) >= kLeast) C *= 2;
     } else {  // measured: 128 rows of 129281 floats 166, 122 and 137 us with 1, 2 and 4; 704 of 128256 bf16 153, 216 and 343
         C = 1;
         while (C < kMostShares && 2 * rows * C < 3 * sms && A.V / (2 * C) >= kLeast) C *= 2;
