@@ -407,7 +407,14 @@ class PagePool:
                 raise ValueError(f"{name} must be contiguous")
         self.struct.out_held, self.struct.out_state = out_held.data_ptr(), out_state.data_ptr()
         return lib.spec_cache_reserve(self._at, None if chunk is None else chunk.at, _ptr(lengths), B, _ptr(slot_map), self._status,
-                                      stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._device))
+                                      self._stream(stream))
+
+    def _stream(self, stream):
+        if self._device < 0:
+            raise ValueError("the pool's tensors must be on a CUDA device")
+        if stream is not None:
+            return stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self._device)
 
     def status_bits(self) -> int:
         return int(self.status.item()) & 0xFFFFFFFF

@@ -122,6 +122,8 @@ class Filter:
         return code
 
     def _stream(self, stream):
+        if self._device < 0:
+            raise ValueError("the filter's tensors must be on a CUDA device")
         if stream is not None:
             return stream.cuda_stream
         return torch._C._cuda_getCurrentRawStream(self._device)  # the current stream's handle alone

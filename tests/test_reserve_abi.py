@@ -74,7 +74,7 @@ def test_binding_checks_tensors(sc, monkeypatch):
     def stop(*args):
         raise Reached
     monkeypatch.setattr(sc.lib, "spec_cache_reserve", stop)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    monkeypatch.setattr(sc.PagePool, "_stream", lambda self, stream: None)
 
     def ints(*shape):
         return torch.zeros(shape, dtype=I32)
@@ -103,3 +103,10 @@ def test_binding_checks_tensors(sc, monkeypatch):
     other.device = 1
     with pytest.raises(ValueError, match="chunk must be on"):
         p.reserve(chunk=other)
+
+
+def test_tensors_of_the_host_are_refused(sc):
+    def ints(*shape):
+        return torch.zeros(shape, dtype=I32)
+    with pytest.raises(ValueError, match="CUDA"):
+        sc.PagePool(ints(3, 4), ints(20), ints(3), ints(2), 16).reserve(lengths=ints(3))

@@ -161,3 +161,11 @@ def test_binding_checks_tensors(ss, monkeypatch):
         shared.mask(x, x)
     with pytest.raises(ValueError):
         shared.mask(x[:3], x[:3])
+
+
+def test_tensors_of_the_host_are_refused(ss):
+    f, x = ss.Filter(temperature=ones(4)), torch.zeros((4, 9))
+    with pytest.raises(ValueError, match="CUDA"):
+        f.mask(x, x.clone())
+    with pytest.raises(ValueError, match="CUDA"):
+        f.sample(x, ones(4), ones(4, torch.int32))
