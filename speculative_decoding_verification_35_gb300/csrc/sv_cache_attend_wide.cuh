@@ -25,6 +25,9 @@
 // bfloat16, D = 128, 3 prompts of 700 to 2048 tokens over 1 to 8192 cached, 32 heads in 8 groups: 233 us (230 to 238),
 // 1.27 PFLOP/s of what the mask leaves (0.67 of a library product's 1.89), 3 us of them the merge. The same prompts on an
 // e4m3 cache take 356 us.
+// Scored: a pass over the scores in tensor memory before the softmax's, 32 columns at a time, is latency and multiply-adds (9 or 7
+// packed operations for two scores) on top of the chain above: the same prompts with a prefix 247 us (more is seen), capped
+// 456, by distance 330. In one pass with the weights it was slower (525: the unrolled code misses the instruction cache; rolled, 519).
 #pragma once
 #include "sv_cache_attend.cuh"
 
