@@ -331,3 +331,62 @@ def test_a_verify_step_on_filtered_rows(ss, drafts):
     assert np.array_equal(got, ref.tokens)
     rows = np.flatnonzero(got >= 0)  # an emitted token is one that the filtered target allows
     assert bool((target[torch.tensor(rows, device="cuda")].gather(1, torch.tensor(got[rows], device="cuda").long()[:, None]) > -INF).all())
+
+
+# Rows too many to be held in shared memory at once are read where they lie, one CTA an SM.
+MANY = {"bf16": (150, 128256), "f32": (60, 129281)}
+
+
+def many(kind, seed, pad=0, shift=0):
+    rows, V = MANY[kind]
+    x = make(rows, V, kind, seed=seed, pad=pad, shift=shift)
+    x[3] = 1.5                                                # all alike
+    x[4, ::2] = -INF                                          # hidden tokens
+    x[5, :] = -INF
+    x[5, V - 1] = 0.0                                         # one is left, the last
+    x[6] = (x[6].float() * 3e4).to(x.dtype)                   # outside the quick bins
+    x[7] = (x[7].float() * 1e-12).to(x.dtype)
+    kw = dict(T=[1.0, 0.7, 1.0, 1.3, 0.9, 1.0, 0.0], k=[0, 50, 0, 5000, 0, 1, 1000, 0, 0], p=[0.9, 1.0, 1.0, 0.95, 0.999],
+              mp=[0.0, 0.0, 0.02, 0.0])
+    return x, {n: np.resize(np.asarray(v), rows) for n, v in kw.items()}
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (3, 1)])
+def test_rows_read_where_they_lie(ss, kind, pad, shift):
+    x, kw = many(kind, 21, pad, shift)
+    check(ss, x, **kw)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (5, 3)])
+def test_rows_read_where_they_lie_are_as_alone(ss, kind, pad, shift):
+    """Tokens, counts and masked rows (elsewhere, and in place) are those of the same rows a few at a time, which are held."""
+    x, kw = many(kind, 22, 1, 2)
+    rows, V = x.shape
+    u = torch.rand(rows, device="cuda", generator=torch.Generator("cuda").manual_seed(8))
+    f = ss.Filter(*requests(rows, **kw), device="cuda")
+    tok, lp, n1, y, n2, bits = run(ss, x, f, u, place(torch.zeros_like(x), pad, shift))
+    assert bits == 0
+    for a in range(0, rows, 10):
+        g = ss.Filter(*requests(len(u[a:a + 10]), **{n: v[a:a + 10] for n, v in kw.items()}), device="cuda")
+        got = run(ss, x[a:a + 10], g, u[a:a + 10])
+        for all_, few in zip((tok, lp, n1, y, n2), got):
+            assert torch.equal(all_[a:a + 10], few), a
+    assert f.mask(x, x, n2) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(x, y) and torch.equal(n1, n2)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_findings_where_rows_are_read_where_they_lie(ss, kind):
+    x, kw = many(kind, 23)
+    want = run(ss, x, ss.Filter(*requests(len(x), **kw), device="cuda"))
+    bad = [0, 11, 40]
+    y = x.clone()
+    y[0, 5], y[11, -1], y[40] = float("nan"), INF, -INF
+    tok, lp, n1, out, n2, bits = run(ss, y, ss.Filter(*requests(len(x), **kw), device="cuda"))
+    assert bits != 0
+    good = [r for r in range(len(x)) if r not in bad]
+    for a, b in zip((tok, lp, n1, out, n2), want):
+        assert torch.equal(a[good], b[good])
