@@ -608,7 +608,7 @@ __device__ __forceinline__ float row_unit(float unit, float down) { return at_le
 
 // Capped scores, cap tanh(z / cap), from scores to log2 of the weights (cap log2e tanh(..)). With x = z / cap up to 1, where a
 // model keeps most of them, tanh x = x q(x^2), q of degree 6 with q(0) = 1 fitted for the least relative error on [0, 1]
-// (5.5e-8; 1.6e-7 with the roundings): nine packed operations for two scores and none of the special-function unit, which
+// (6.1e-8; 1.6e-7 with the roundings): nine packed operations for two scores and none of the special-function unit, which
 // the weights keep busy. Past 1, 1 - 2 / (1 + 2^(2 x log2 e)): its error, some 2^-22 of one, is as small a part there.
 struct Cap {
     F2 c[7], d[4];   // times cap log2e, the highest first; d is for x up to kSmall

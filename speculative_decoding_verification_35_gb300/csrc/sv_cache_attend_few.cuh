@@ -30,9 +30,8 @@
 // rows on the lanes 128), of which some 10 are the launches and the first tiles' way; its 128-byte pieces lie 2 KB apart,
 // and more than half of its items have one tile. e4m3, D = 128, 32 sequences of 4 tokens, 2000 to 16384 cached: 93 us
 // (0.79; rows on the lanes 150). Of the nine kernels the one for e4m3 and 64 rows spills, 76 bytes a thread.
-// Scored, bfloat16, 64 sequences of 6 tokens under a window of 4096: 111 us, capped 113, by distance 125; 16 trees of 32 tokens with 16 heads of
-// 64 (float16) 57, 67 and 65. A lane's row keeps its slope; with the slopes in a shuffle each, and tiles forwards, distance took
-// 168 and 84.
+// Scored, bfloat16, 64 sequences of 6 tokens under a window of 4096: plain 111 to 114 us, capped 113 to 116, by distance 125; 16 trees of 32 tokens with 16 heads of
+// 64 (float16) 57, 67 and 65. Before, with tiles forwards for all, distance took 168 and 84. A lane's row keeps its slope.
 #pragma once
 #include "sv_cache_attend.cuh"
 

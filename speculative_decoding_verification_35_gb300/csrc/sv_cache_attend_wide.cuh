@@ -26,8 +26,9 @@
 // 1.27 PFLOP/s of what the mask leaves (0.67 of a library product's 1.89), 3 us of them the merge. The same prompts on an
 // e4m3 cache take 356 us.
 // Scored: a pass over the scores in tensor memory before the softmax's, 32 columns at a time, is latency and multiply-adds (9 or 7
-// packed operations for two scores) on top of the chain above: the same prompts with a prefix 247 us (more is seen), capped
-// 456, by distance 330. In one pass with the weights it was slower (525: the unrolled code misses the instruction cache; rolled, 519).
+// packed operations for two scores) on top of the chain above: the same prompts, plain 218 us, with a prefix 248 (more is
+// seen), capped 399, both 456, by distance 330. In one pass with the weights it was slower: capped 472 and more unrolled, which
+// waits for instructions, and 454 rolled, where a pass of its own took 418 at the time.
 #pragma once
 #include "sv_cache_attend.cuh"
 

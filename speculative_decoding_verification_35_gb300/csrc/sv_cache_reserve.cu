@@ -9,8 +9,8 @@
 // ones, which they may replace.
 //
 // Bound by the launch and a chain of dependent reads (the offsets and lengths, the queue, the writes): 64 sequences of 6 tokens
-// 5.7 us by one CTA (the call costs the host 6.4). 32 prompts of 700 to 8192 tokens, 93000 slots: 11.3 us by 16 CTAs, 17 by 8, 130 by
-// one; there a slot costs some 60 instructions, where 64-bit sums and a search for each took 200.
+// 5.7 us by one CTA (the call costs the host 6.4 to 6.8). 32 prompts of 700 to 8192 tokens, 93000 slots: 11.3 us by 16 CTAs; by one,
+// with 64-bit sums and a search for each slot, 130.
 #include <cooperative_groups.h>
 
 #include <algorithm>

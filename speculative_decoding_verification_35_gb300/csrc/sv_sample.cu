@@ -23,9 +23,9 @@
 // of 128256: 181 MB read from memory, which is the rows once).
 //
 // What bounds it: small batches a chain of short steps (load, survey, gather, sort, sums: a block or cluster barrier and one to
-// three us each; one row of 32000 14.5 us), many rows the same steps with nothing else on the SM meanwhile, though every byte is
-// moved once (704 rows filtered, a filter for each sequence: 150 us, 0.36 of the copy rate; more rows at a time, 2 or 4 CTAs an SM, cost
-// more in L2 than they hide: 163 and 246 us). 64 rows of 128256, nucleus alone: 33 us, a third of them counting.
+// three us each; one row of 32000 14.5 to 15.5 us), many rows the same steps with nothing else on the SM meanwhile, though a row
+// is read from memory once (704 rows filtered, a filter for each sequence: 150 to 153 us, 0.35 of the copy rate; with 2 and 4 CTAs
+// an SM 163 and 246). 64 rows of 128256, nucleus alone: 33 us, 12 of them counting and finding the threshold, 9 drawing.
 #include <cooperative_groups.h>
 
 #include <algorithm>
