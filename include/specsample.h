@@ -21,8 +21,8 @@
  * calls on several streams may overlap. Bad arguments return SV_ERR_INVALID_ARG before anything is launched. Findings on
  * the device set bit (1u << code) of *device_status (nullable; the caller clears it) and fail their row alone:
  *   SV_ERR_NONFINITE    a NaN or +inf logit          SV_ERR_EMPTY_ROW  all logits -inf
- *   SV_ERR_INVALID_ARG  a temperature that is negative, not finite, or so small that log2(e) / T is not a float; a top_p
- *                       or min_p that is NaN; a uniform outside [0, 1); a request outside [0, requests)
+ *   SV_ERR_INVALID_ARG  a temperature that is negative, above 1e36, not finite, or so small that log2(e) / T is not a
+ *                       float; a top_p or min_p that is NaN; a uniform outside [0, 1); a request outside [0, requests)
  */
 #ifndef SPECSAMPLE_H
 #define SPECSAMPLE_H

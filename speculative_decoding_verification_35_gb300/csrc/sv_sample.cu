@@ -66,6 +66,8 @@ constexpr int kMostThreads = 1024, kMostWarps = kMostThreads / 32, kMaxCtas = 8;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kBits = 44;  // of a weight's fraction; 2^18 weights of 1 sum to 2^62
 constexpr float kLowest = -3.402823466e38f;
+// l - m in float may be minus infinity, which is a weight of 0; up to this temperature it is one (2^-490 and less)
+constexpr float kMostTemperature = 1e36f;
 
 // The bins of the quick way, in the ranking's order: one for each bfloat16 magnitude code in [kCodeLo, kCodeHi] of either sign, one
 // in the middle for zero, and one at either end that counts for nothing (the last has -inf). Their words lie in the order
@@ -1139,7 +1141,7 @@ struct Work {
     template <bool kMass>
     __device__ __forceinline__ void tally(const Result& res, const Segment& g, u64& mass, uint32_t& above, uint32_t& ties) const {
         above = ties = 0;
-        int32_t sa = 0, sb = 0;  // of at most 192 weights
+        int32_t sa = 0, sb = 0;  // of at most 256 weights (2^18 logits by 1024 threads): 2^30
         const bool whole = !res.partial;
 #pragma unroll 1
         for (int32_t c = g.c0 + lane; c < g.c1; c += 32) {
@@ -1439,7 +1441,7 @@ __device__ __forceinline__ void read_par(const Args& A, RowPar& R, int32_t row, 
         if (A.top_p) R.p = A.top_p[q];
         const float mp = R.mp = A.min_p ? A.min_p[q] : 0.f;
         if (draws) R.u = A.uniforms[row];
-        ok = R.T >= 0.f && R.T < INFINITY && R.p == R.p && mp == mp && R.u >= 0.f && R.u < 1.f;
+        ok = R.T >= 0.f && R.T <= kMostTemperature && R.p == R.p && mp == mp && R.u >= 0.f && R.u < 1.f;
         if (mp > 0.f) R.least = max((u64)ceil((double)fminf(mp, 1.f) * (double)((u64)1 << kBits)), (u64)1);
     }
     if (ok && R.T > 0.f) {

@@ -390,3 +390,22 @@ def test_findings_where_rows_are_read_where_they_lie(ss, kind):
     good = [r for r in range(len(x)) if r not in bad]
     for a, b in zip((tok, lp, n1, out, n2), want):
         assert torch.equal(a[good], b[good])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [7, 5003])
+def test_the_largest_temperature(ss, kind, V):
+    """A logit that lies further below the largest than float reaches has no weight up to T = 1e36; above, it would have one
+    (2^-8.7 at 1e38), and the row is refused."""
+    from speculative_decoding_verification_35_gb300 import specverify as sv
+    x = torch.full((4, V), -3e38, device="cuda")
+    x[:, 1::3] = 3e38
+    x = x.to(DT[kind])
+    u = torch.full((4,), 0.999, device="cuda")
+    T = float(np.float32(1e36))
+    check(ss, x, T=T, u=u)
+    check(ss, x, T=T, p=0.9, u=u)
+    for worse in (2e36, 1e38, 3.4e38):
+        tok, lp, n1, y, n2, bits = run(ss, x, ss.Filter(*requests(4, worse), device="cuda"), u)
+        assert bits == 1 << sv.SV_ERR_INVALID_ARG
+        assert tok.tolist() == [-1] * 4 and n1.tolist() == n2.tolist() == [-1] * 4 and torch.equal(y, x)
