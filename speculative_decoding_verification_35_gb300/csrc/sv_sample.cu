@@ -20,12 +20,12 @@
 // Shape. A row is a cluster's of up to 8 CTAs, a warp of which has a contiguous segment of it. Where the rows fit the GPU at
 // once, they are held in shared memory: one read from memory, however many passes follow. Else one CTA of 1024 threads an
 // SM takes a row where it lies, each pass from the end at which the last one stopped, so that L2 has most of it (704 rows
-// of 128256: 181 MB read from memory, which is the rows once).
+// of 128256: 188 MB read from memory, about the rows once), and brings the next one's first bytes there before it writes.
 //
 // What bounds it: small batches a chain of short steps (load, survey, gather, sort, sums: a block or cluster barrier and one to
 // three us each; one row of 32000 14.5 to 15.5 us), many rows the same steps with nothing else on the SM meanwhile, though a row
-// is read from memory once (704 rows filtered, a filter for each sequence: 150 to 153 us, 0.35 of the copy rate; with 2 and 4 CTAs
-// an SM 163 and 246). 64 rows of 128256, nucleus alone: 33 us, 12 of them counting and finding the threshold, 9 drawing.
+// is read from memory once (704 rows filtered, a filter for each sequence: 143 to 148 us, 0.36 of the copy rate; before
+// the next row was brought, 153, and 163 and 246 with 2 and 4 CTAs an SM). 64 rows of 128256, nucleus alone: 33 us, 12 of them counting and finding the threshold, 9 drawing.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -356,7 +356,7 @@ __device__ __forceinline__ uint32_t div_up(u64 a, u64 b) {
 template <typename T, bool kHeld>
 struct Work {
     typedef Elem<T> E;
-    // held rows: two CTAs an SM; others: one, as fewer rows at a time leave more of each in L2 (704 rows of 128256 bf16: 153 us,
+    // held rows: two CTAs an SM; others: one, as fewer rows at a time leave more of each in L2 (704 rows of 128256 bf16, the next not brought yet: 153 us,
     // with two of 512 threads 163, with four of 256 246)
     static constexpr int kThreads = kHeld ? 512 : 1024, kWarps = kThreads / 32;
     static constexpr int kList = kThreads;  // candidates that the first CTA ranks, a thread each
@@ -437,6 +437,20 @@ struct Work {
                 if (at < kList) to->order[at] = (u64)key_of(E::value(p[i])) << 32 | (uint32_t)~(i - off);
             }
         }
+    }
+
+    // The same part of the row `ahead` rows on, which this SM takes next or nearly, into L2: whole chunks, in its bounds. Measured,
+    // in turn: 704 rows filtered 152.6 us without, 147.4 with it once the threshold is known, 148.1 before the candidates are
+    // sorted, 150.3 before they are gathered; 128 float rows 121.8 and 122.2.
+    __device__ __forceinline__ void bring(const T* base, int32_t row, int32_t ahead) const {
+        if (ahead <= 0 || row >= A.rows - ahead || lane > 0) return;
+        const T* next = base + (int64_t)ahead * A.stride;
+        const int32_t o = (int32_t)((uintptr_t)next % 16 / sizeof(T));
+        const int32_t c0 = max(s.c0, (int32_t)(o > 0)), c1 = min(s.c1, (o + A.V) / E::N);
+        if (c0 < c1)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(__cvta_generic_to_global(next - o + (int64_t)c0 * E::N)),
+                         "r"((uint32_t)(c1 - c0) * 16u)
+                         : "memory");
     }
 
     // ------------------------------------------------------------------------------------------------
@@ -1457,7 +1471,7 @@ __device__ __forceinline__ void read_par(const Args& A, RowPar& R, int32_t row, 
 }
 
 template <typename T, bool kDraws, bool kHeld>
-__global__ void __launch_bounds__(Work<T, kHeld>::kThreads, kHeld ? 2 : 1) k_rows(const __grid_constant__ Args A, int32_t C) {
+__global__ void __launch_bounds__(Work<T, kHeld>::kThreads, kHeld ? 2 : 1) k_rows(const __grid_constant__ Args A, int32_t C, int32_t ahead) {
     typedef Elem<T> E;
     constexpr int kThreads = Work<T, kHeld>::kThreads, kWarps = kThreads / 32;
     extern __shared__ __align__(16) char raw[];
@@ -1534,6 +1548,7 @@ __global__ void __launch_bounds__(Work<T, kHeld>::kThreads, kHeld ? 2 : 1) k_row
     const bool known = !res.slow;
     if (res.slow) res = work.choose_slow();
 
+    if (!kHeld) work.bring(base, row, ahead);
     const bool ok = !res.err;
     int32_t n = ok ? res.n : -1, cut = res.listed ? res.cut : 0x7fffffff;
     if (ok && !res.listed && (kDraws || res.partial || !known)) {
@@ -1571,7 +1586,7 @@ constexpr int kLeast = 4096;       // logits of a slice that is worth a CTA
 constexpr int kMostShares = 4;     // CTAs of a row that is not held: the draw's shares are 128
 
 template <typename T, bool kDraws, bool kHeld>
-cudaError_t launch(const Args& A, int dev, int C, int64_t smem, cudaStream_t st) {
+cudaError_t launch(const Args& A, int dev, int C, int32_t ahead, int64_t smem, cudaStream_t st) {
     auto kernel = k_rows<T, kDraws, kHeld>;
     // the devices on which the kernel may use an SM's shared memory: setting that twice does no harm
     static std::atomic<unsigned long long> allowed{0};
@@ -1594,7 +1609,7 @@ cudaError_t launch(const Args& A, int dev, int C, int64_t smem, cudaStream_t st)
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, A, (int32_t)C);
+    return cudaLaunchKernelEx(&cfg, kernel, A, (int32_t)C, ahead);
 }
 
 // CTAs of a row, a power of two. Held rows take as few as hold them in shared memory, and more while that leaves SMs idle and a
@@ -1628,7 +1643,7 @@ cudaError_t launch(const Args& A, cudaStream_t st) {
         while (C < kMostShares && 2 * rows * C < 3 * sms && A.V / (2 * C) >= kLeast) C *= 2;
     }
     if (rows * C > 0x7fffffff) return cudaErrorInvalidValue;
-    return held ? launch<T, kDraws, true>(A, dev, C, bytes(C), st) : launch<T, kDraws, false>(A, dev, C, sizeof(Shared), st);
+    return held ? launch<T, kDraws, true>(A, dev, C, 0, bytes(C), st) : launch<T, kDraws, false>(A, dev, C, sms / C, sizeof(Shared), st);
 }
 
 struct ExpTable {  // 2^(j / 128) as two floats each
