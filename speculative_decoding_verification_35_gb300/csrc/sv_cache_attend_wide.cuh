@@ -233,8 +233,8 @@ __device__ __forceinline__ void score_tile(const Scoring& sc, bool tree, const R
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 float d = far - (float)i;
-                const int32_t t = at + i - it.past;
-                if (rarely(nodes) && t >= 0 && t < it.nt) d = (float)(row.pos - it.past - items.tree().depth[t]);
+                const int32_t t = at + i - it.past;  // (of the tree, whose earlier tokens may be another block's)
+                if (rarely(nodes) && t >= 0 && t < it.t0 + it.nt) d = (float)(row.pos - it.past - items.tree().depth[t]);
                 s[i] = __float_as_uint(fmaf(-row.slope, fabsf(d), __uint_as_float(s[i]) * unit));
             }
         }
