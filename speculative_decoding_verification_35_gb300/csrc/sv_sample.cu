@@ -222,6 +222,8 @@ struct Elem<float> {
                (uint32_t)(__uint_as_float(q.z) >= least) << 2 | (uint32_t)(__uint_as_float(q.w) >= least) << 3;
     }
     static __device__ __forceinline__ float next(float x) { return float_of(key_of(x) + 1u); }
+    // the least value of the type from x on
+    static __device__ __forceinline__ float up(float x) { return x; }
     // how many are x
     static __device__ __forceinline__ uint32_t equal(const uint4& q, float x) {
         return (uint32_t)(__uint_as_float(q.x) == x) + (uint32_t)(__uint_as_float(q.y) == x) + (uint32_t)(__uint_as_float(q.z) == x) +
@@ -273,6 +275,7 @@ struct Elem<__nv_bfloat16> {
         return k;
     }
     static __device__ __forceinline__ float next(float x) { return float_of(key_of(x) + 0x10000u); }
+    static __device__ __forceinline__ float up(float x) { return __bfloat162float(__float2bfloat16_ru(x)); }
     static __device__ __forceinline__ uint32_t equal(const uint4& q, float x) {
         const __nv_bfloat162 v = __float2bfloat162_rn(x);
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -1137,7 +1140,7 @@ struct Work {
                     lo += step * (i < 0 ? 32 : i);
                     hi = at;
                 }
-                if (lane == 0) sh.floor = float_of(hi);
+                if (lane == 0) sh.floor = E::up(float_of(hi));
             }
             __syncthreads();
             if (sh.floor > res.thr) {
