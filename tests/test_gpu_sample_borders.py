@@ -50,3 +50,16 @@ def test_min_p_of_rows_outside_the_quick_bins(ss, rows, V):
     rng = np.random.default_rng(rows)
     check(ss, x, T=rng.choice([0.7, 1.0, 1.4], rows), k=rng.choice([0, 0, 4000], rows), p=rng.choice([0.99, 0.999, 0.99999], rows),
           mp=rng.uniform(0.01, 0.4, rows).astype(np.float32))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V", [(9, 700), (9, 5003), (9, 100000), LYING])
+def test_tiny_temperatures(ss, kind, rows, V):
+    """Down to the least of which log2(e) / T is a float, the largest logit and those like it are all there is."""
+    x = make(rows, V, kind, seed=V, pad=1)
+    x[:, 7] = -1e9  # (no quick bin)
+    x[2] = 0.0
+    x[3, ::2], x[3, 1::2] = 0.0, -1e-45  # (bf16: zeros)
+    T = [1e-37, 5e-39, 1e-38, 3e-38, 4.3e-37, 4.4e-37, 1e-36, 1e-30, 4.3e-39]
+    for kw in (dict(p=0.9), dict(p=0.9, mp=0.3), dict(p=0.5, k=2000), dict()):
+        check(ss, x, T=np.resize(T, rows), **kw)
