@@ -11,7 +11,8 @@
  * the largest first, equal ones by index, those of -inf not at all. The first n of the ranking are kept:
  *   n_k  = top_k, where 1 <= top_k, else all;           S_k = sum of the first n_k weights
  *   n_p  = the least n >= 1 for which the first n weights sum to top_p S_k or more, where top_p < 1, else all
- *   n_m  = the tokens with w_i >= min(min_p, 1), where min_p > 0, else all
+ *   n_m  = the tokens with w_i >= min(min_p, 1), where min_p > 0, else all: those with l_i >= max l + T ln(min(min_p, 1)), a
+ *          sum in double
  *   n    = min(n_k, n_p, n_m)
  * T = 0 keeps the first alone. Weights are held in 64-bit fixed point (steps of 2^-44, each within 2^-31 of itself), so
  * their sums are exact and do not depend on any order: a result is the same on every call and for every batch.

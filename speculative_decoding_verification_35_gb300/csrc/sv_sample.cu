@@ -85,10 +85,11 @@ typedef unsigned long long u64;
 
 struct RowPar {
     ExpConst E;
-    float T, p, u, mp;
+    float T, p, u;
     double per;     // 1 / T
+    double drop;    // T ln min_p: a kept logit is this far below the largest at most
     int32_t k;      // 0: none
-    u64 least;      // of a kept weight, 0: none
+    int32_t drops;  // whether there is such a bound
     uint32_t err;
 };
 
@@ -137,7 +138,6 @@ struct alignas(16) Shared {
     uint32_t max_key, low_key, share_key;  // the CTA's largest logit, the least that it counts, and the least of its share of k
     uint32_t listed;                       // candidates
     uint32_t flags;
-    float floor;
     RowPar par;
     Result res;
     Found found;
@@ -490,8 +490,8 @@ struct Work {
     }
     // The CTA's largest, and the least logit that decides anything, with a block barrier at the end. With top-k, k up to the
     // threads of a CTA: if k threads have a logit of x or more, what is below x is not among the first k of the ranking;
-    // and if in every CTA of the row k / C of them have x or more, neither. With min-p alone: those whose weight is clearly
-    // too small.
+    // and if in every CTA of the row k / C of them have x or more, neither. With min-p alone: those that it does not keep of
+    // the CTA's.
     __device__ __forceinline__ void survey() {
         uint32_t flags;
         const uint32_t top = largest(flags);
@@ -513,9 +513,8 @@ struct Work {
             low = __reduce_min_sync(kAll, sh.warp_min[lane % kWarps]);
             if (warp == 0) low = reached(sh.tops, R.k, low, high);
             if (warp == 1) share = reached(sh.tops, (R.k + team.size - 1) / team.size, low, high);
-        } else if (R.least && !(R.p < 1.f)) {
-            const float x = float_of(high);
-            low = key_of(x + 1.0001f * R.T * __logf(fminf(R.mp, 1.f)) - 1e-5f * (fabsf(x) + R.T));
+        } else if (R.drops && !(R.p < 1.f)) {
+            low = key_of(floor_of(float_of(high)));
         }
         if (threadIdx.x == 0) {
             sh.max_key = high;
@@ -538,6 +537,13 @@ struct Work {
         float f = low <= kKeyMinusInf ? -INFINITY : float_of(low);
         if (sizeof(T) == 2) f = __bfloat162float(__float2bfloat16_rd(f));
         return f;
+    }
+    // The least logit that min-p keeps of a row whose largest is m. By logits and not by their weights: those are within 2^-31 of
+    // themselves only, and of two logits nearer to each other the lesser one's can be the larger one's by a step, but what is
+    // kept has to be the ranking's first, and the same in every way to the threshold.
+    __device__ __forceinline__ float floor_of(float m) const {
+        const RowPar& R = sh.par;
+        return R.drops ? E::up(__double2float_ru((double)m + R.drop)) : -INFINITY;
     }
     __device__ __forceinline__ uint32_t cluster_max() const {
         uint32_t k = 0;
@@ -631,7 +637,7 @@ struct Work {
         __syncthreads();
         u64 enough = ~0ull;
         if (R.p < 1.f) enough = max(scaled(sh.total, R.p, true), (u64)1);
-        const bool kept = tid < first && upto - w < enough && w >= R.least;
+        const bool kept = tid < first && upto - w < enough && float_of((uint32_t)(x >> 32)) >= floor_of(res.m);
         res.n = __syncthreads_count(kept);
         if (tid == res.n - 1) {
             sh.total = upto;
@@ -744,10 +750,9 @@ struct Work {
     __device__ __forceinline__ void choose() {
         const uint32_t flags = cluster_flags(), top = cluster_max();
         const RowPar& R = sh.par;
-        const float m = float_of(top);
-        const u64 least = R.least;
+        const float m = float_of(top), floor = floor_of(m);
         const int g0 = bin_of(m) / kGroupBins, g1 = bin_of(low) / kGroupBins;  // groups that hold something
-        uint32_t many = 0;  // of weights of at least `least`, which are the ranking's first
+        uint32_t many = 0;  // of logits from `floor` on, which are the ranking's first
         u64 heavy = 0;
         int last = -1;
 #pragma unroll 3
@@ -757,8 +762,8 @@ struct Work {
             if (g >= g0 && g <= g1 && pair_at(g, m, c, w)) {
                 mass = c[0] * w[0] + c[1] * w[1];
                 const int d = g * kGroupBins + 2 * lane;
-                if (least && c[0] && w[0] >= least) many += c[0], heavy += c[0] * w[0], last = d;
-                if (least && c[1] && w[1] >= least) many += c[1], heavy += c[1] * w[1], last = d + 1;
+                if (R.drops && c[0] && value_at(d) >= floor) many += c[0], heavy += c[0] * w[0], last = d;
+                if (R.drops && c[1] && value_at(d + 1) >= floor) many += c[1], heavy += c[1] * w[1], last = d + 1;
                 mass = warp_sum(mass);
                 cc = __reduce_add_sync(kAll, c[0] + c[1]);
             }
@@ -844,7 +849,7 @@ struct Work {
                 res.mass = __shfl_sync(kAll, pm + (r < ties ? 0 : r * wt), at);
             }
         }
-        if (least && found) {
+        if (R.drops && found) {
             const Part x = lane < kWarps ? sh.warp_part[lane] : Part{0, 0, 0};
             many = __reduce_add_sync(kAll, x.above);
             last = (int)__reduce_max_sync(kAll, x.ties) - 1;
@@ -1130,25 +1135,10 @@ struct Work {
             res.r = r;
             res.partial = r < ties;
         }
-        if (R.least) {  // the least logit of a weight that is large enough
-            __syncthreads();
-            if (warp == 0) {
-                uint32_t lo = kKeyMinusInf, hi = top;  // lo's weight is too small, hi's is not
-                while (hi - lo > 1) {
-                    const uint32_t step = (hi - lo + 32) / 33, k = lo + step * (lane + 1);
-                    const bool enough = k >= hi || k < lo || weight(float_of(k), m, R.E, sh.tab) >= R.least;
-                    const int i = __ffs(__ballot_sync(kAll, enough)) - 1;  // -1: none
-                    const uint32_t at = i < 0 ? hi : min(hi, lo + step * (i + 1));
-                    lo += step * (i < 0 ? 32 : i);
-                    hi = at;
-                }
-                if (lane == 0) sh.floor = E::up(float_of(hi));
-            }
-            __syncthreads();
-            if (sh.floor > res.thr) {
-                res.thr = sh.floor;
-                res.partial = 0;
-            }
+        const float least = floor_of(m);
+        if (least > res.thr) {
+            res.thr = least;
+            res.partial = 0;
         }
         return res;
     }
@@ -1458,10 +1448,11 @@ __device__ __forceinline__ void read_par(const Args& A, RowPar& R, int32_t row, 
         if (A.temperature) R.T = A.temperature[q];
         if (A.top_k) R.k = max(A.top_k[q], 0);
         if (A.top_p) R.p = A.top_p[q];
-        const float mp = R.mp = A.min_p ? A.min_p[q] : 0.f;
+        const float mp = A.min_p ? A.min_p[q] : 0.f;
         if (draws) R.u = A.uniforms[row];
         ok = R.T >= 0.f && R.T <= kMostTemperature && R.p == R.p && mp == mp && R.u >= 0.f && R.u < 1.f;
-        if (mp > 0.f) R.least = max((u64)ceil((double)fminf(mp, 1.f) * (double)((u64)1 << kBits)), (u64)1);
+        R.drops = mp > 0.f && R.T > 0.f;  // (a temperature of 0 keeps the first alone)
+        if (ok && R.drops) R.drop = (double)R.T * log((double)fminf(mp, 1.f));
     }
     if (ok && R.T > 0.f) {
         R.per = 1.0 / (double)R.T;
@@ -1472,7 +1463,6 @@ __device__ __forceinline__ void read_par(const Args& A, RowPar& R, int32_t row, 
         ok = R.E.K_hi < INFINITY;
     }
     if (!ok) R.err = 1u << SV_ERR_INVALID_ARG;
-    if (R.T == 0.f) R.least = 0;  // the first alone, whatever its weight
 }
 
 template <typename T, bool kDraws, bool kHeld>

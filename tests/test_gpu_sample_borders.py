@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_sample import check, make, place
+from tests.test_gpu_sample import check, make, place, requests, run
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -63,3 +63,41 @@ def test_tiny_temperatures(ss, kind, rows, V):
     T = [1e-37, 5e-39, 1e-38, 3e-38, 4.3e-37, 4.4e-37, 1e-36, 1e-30, 4.3e-39]
     for kw in (dict(p=0.9), dict(p=0.9, mp=0.3), dict(p=0.5, k=2000), dict()):
         check(ss, x, T=np.resize(T, rows), **kw)
+
+
+# (T, largest logit, two neighbouring floats the first below the second, min_p): as the weights are computed, the first's is at least
+# min_p and the second's is not, for they are within 2^-31 of themselves, and the logits are nearer to each other.
+STEPS_BACK = [(t, float.fromhex(m), float.fromhex(a), float.fromhex(b), float.fromhex(mp)) for t, m, a, b, mp in [
+    (float.fromhex("0x1.03bp+0"), "0x1.15814ep-2", "-0x1.deb2p-11", "-0x1.deb1fep-11", "0x1.879caep-1"),
+    (float.fromhex("0x1.044p+0"), "0x1.9cd9f4p-1", "-0x1.37fp-13", "-0x1.37effep-13", "0x1.cf3156p-2"),
+    (float.fromhex("0x1.0f1p+0"), "0x1.adb90ap+1", "0x1.abp-15", "0x1.ab0002p-15", "0x1.57e28p-5"),
+    (float.fromhex("0x1.109p+0"), "0x1.5fdd2cp+2", "0x1.aebffep-12", "0x1.aecp-12", "0x1.770244p-8"),
+    (float.fromhex("0x1.176p+0"), "0x1.93a16ap+2", "-0x1.e35p-10", "-0x1.e34ffep-10", "0x1.948b7cp-9"),
+    (float.fromhex("0x1.1a9p+0"), "0x1.46f14ep-3", "0x1.d96f6p-8", "0x1.d96f62p-8", "0x1.bdf69cp-1")]]
+
+
+@pytest.mark.parametrize("V,p", [(3, 1.0), (400, 1.0), (5003, 1.0), (5003, 0.99999994), (100000, 0.99999994)])
+def test_weights_that_step_back(ss, V, p):
+    """Whichever of the two are kept, they are the ranking's first, the draw is one of them, and every way says the same."""
+    rows = len(STEPS_BACK)
+    x = torch.full((rows, V), -200.0, device="cuda")
+    for r, (_, m, a, b, _) in enumerate(STEPS_BACK):
+        x[r, 0], x[r, 1], x[r, 2] = m, a, b
+    T, mp = [s[0] for s in STEPS_BACK], [s[4] for s in STEPS_BACK]
+    u = torch.full((rows,), 1.0 - 2.0 ** -24, device="cuda")
+    check(ss, x, T=T, mp=mp, p=p, u=u)
+    few, wide = (ss.Filter(*requests(rows, T, None, q, mp)) for q in (None, p))
+    assert torch.equal(run(ss, x[:, :3].contiguous(), few, u)[2], run(ss, x, wide, u)[2])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [50, 5003, 100000])
+def test_min_p_below_the_weights_steps(ss, kind, V):
+    """Logits whose weights are rounded to nothing are kept down to min_p, and not drawn."""
+    x = torch.full((6, V), -90.0, device="cuda")
+    x[:, 3:20], x[:, 20:30], x[:, 30:40], x[:, 1] = -40.0, -50.0, -34.0, 0.0
+    x[5] = place(x[5:6], 0, 0) * 1e4
+    x = place(x.to({"bf16": torch.bfloat16, "f32": torch.float32}[kind]), 1, 1)
+    kw = dict(T=[1.0, 1.0, 2.0, 1.0, 1.0, 1e4], mp=[1e-20, 1e-17, 1e-30, 1e-38, 1e-45, 1e-20], u=torch.full((6,), 1.0 - 2.0 ** -24, device="cuda"))
+    check(ss, x, **kw)
+    check(ss, x, p=0.99999994, **kw)
