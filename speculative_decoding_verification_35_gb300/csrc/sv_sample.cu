@@ -1059,8 +1059,9 @@ struct Work {
     // The same for top_p of all weights, in fewer passes: the bins are even in the weights' logarithms, and so narrow that
     // the one with the crossing has few logits; those are sorted. False, for the cluster, if they are not so few.
     __device__ __noinline__ bool seek_even(float m, uint32_t& key, uint32_t& r, uint32_t& ties) {
-        // (finite, whatever the temperature: the largest logit is 0 bins away)
-        const float per = fminf(sh.par.E.K_hi * ((float)kDigits / (kBits + 1)), -kLowest);
+        // (to 2^-46, past the last weight that is not rounded to nothing; finite, whatever the temperature: the largest logit is
+        // 0 bins away)
+        const float per = fminf(sh.par.E.K_hi * ((float)kDigits / (kBits + 2)), -kLowest);
         auto index = [&](float x) { return (uint32_t)(kDigits - 1) - (uint32_t)fminf((m - x) * per, 1e9f); };  // monotone in x
         const Found f = level<true>(kDigits, index, m, 0, true, 0);
         if (f.bin < 0) return false;

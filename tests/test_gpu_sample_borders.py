@@ -101,3 +101,16 @@ def test_min_p_below_the_weights_steps(ss, kind, V):
     kw = dict(T=[1.0, 1.0, 2.0, 1.0, 1.0, 1e4], mp=[1e-20, 1e-17, 1e-30, 1e-38, 1e-45, 1e-20], u=torch.full((6,), 1.0 - 2.0 ** -24, device="cuda"))
     check(ss, x, **kw)
     check(ss, x, p=0.99999994, **kw)
+
+
+def test_the_last_weights_count(ss):
+    """Weights of one step of 2^-44, at the least logit that has one: of many, rows of either type have the same sums."""
+    V = 240001
+    x = torch.full((2, V), -31.25, device="cuda")
+    x[:, 0], x[:, 1:40001] = 0.0, -21.25
+    f = ss.Filter(*requests(2, float.fromhex("0x1.007aa8p+0"), None, 0.99999994, None))
+    u = torch.tensor([0.3, 0.9999999], device="cuda")
+    got = [run(ss, x.to(t), f, u) for t in (torch.bfloat16, torch.float32)]
+    assert got[0][2].tolist() == [39923] * 2  # the first sums that reach (1 - 2^-24) of the total, by hand
+    for a, b in zip(*(g[:3] for g in got)):
+        assert torch.equal(a, b)
