@@ -214,7 +214,9 @@ typedef struct {
  *   1. A sequence with held[b] > need_b gives back the entries need_b .. held[b] - 1 of its row, to the queue's end, in the
  *      order of the sequences and of their entries (which stay in the table, unused).
  *   2. The sequences with held[b] < need_b take what they lack from the queue's front, in order, into the entries
- *      held[b] .. need_b - 1. The first one for which there are too few pages takes none, and no later one takes any.
+ *      held[b] .. need_b - 1. The first one for which there are too few pages takes none, and no later one takes any. Of a
+ *      sequence that goes without, for want of pages or of entries, those of the entries that the table has become -1, which
+ *      the cache calls refuse: ids that it gave back once may be another sequence's by now.
  * out_held[b] = need_b, or held[b] for a sequence that went without; out_state the queue's new head and count.
  * slot_map (nullable, with a chunk only; int64[rows]): of every chunk token its place page_id * page_size + slot % page_size,
  * or -1 where its sequence has a finding or went without, or the page id lies outside [0, pages). Rows outside every
@@ -222,8 +224,8 @@ typedef struct {
  * Findings: SV_ERR_CAPACITY: too few pages, n_b < 0 or need_b above table_stride; SV_ERR_BAD_OFFSETS: rows as for the other
  * calls, held[b] outside [0, table_stride], a page id outside [0, pages) taken or given back, head outside [0, pages), count
  * below 0, or more free pages than `pages` after step 1. A sequence with a finding keeps its pages; with a bad state nothing is
- * moved, every sequence keeps its pages and the slot map is -1. A bad page id is moved like any other (the cache calls
- * refuse it in turn).
+ * moved, every sequence keeps its pages (those that need more go without) and the slot map is -1. A bad page id is moved
+ * like any other (the cache calls refuse it in turn).
  * At most 65536 sequences.
  */
 int spec_cache_reserve(const sv_pages* pages, const sv_chunk* chunk, const int32_t* lengths, int32_t B, int64_t* slot_map,

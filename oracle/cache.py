@@ -135,16 +135,23 @@ def compact(pages_kv, table, seq_offsets, cached, accepted, path):
 
 def reserve(table, queue, held, state, want, page_size):
     """Pages for sequences that are to hold `want` slots each (None: a sequence with a finding): (table, queue, held,
-    state, sequences that went without). Plain lists, one page after the other."""
+    state, sequences that went without). Plain lists, one page after the other. Entries that a sequence wants and does
+    not get are -1 in the table."""
     table, queue = np.array(table), np.array(queue)
     pages, width = len(queue), table.shape[1]
     head, count = int(state[0]), int(state[1])
     need = []
+
+    def none(b):
+        if want[b] is not None and want[b] >= 0 and held[b] >= 0:
+            table[b, int(held[b]):-(-want[b] // page_size)] = -1
     for b, n in enumerate(want):
         ok = n is not None and n >= 0 and 0 <= held[b] <= width and -(-n // page_size) <= width
         need.append(-(-n // page_size) if ok else None)
     give = sum(int(held[b]) - n for b, n in enumerate(need) if n is not None and n < held[b])
     if not 0 <= head < pages or count < 0 or count + give > pages:
+        for b in range(len(want)):
+            none(b)
         return table, queue, np.array(held), np.array(state), set(range(len(want)))
     for b, n in enumerate(need):
         for i in range(n if n is not None else width, int(held[b]) if n is not None else 0):
@@ -154,12 +161,14 @@ def reserve(table, queue, held, state, want, page_size):
     for b, n in enumerate(need):
         if n is None:
             without.add(b)
+            none(b)
             continue
         lack = n - int(held[b])
         if lack > 0:
             dry = dry or lack > count
             if dry:
                 without.add(b)
+                none(b)
                 continue
             for i in range(int(held[b]), n):
                 table[b, i] = queue[head]

@@ -33,6 +33,7 @@ typedef unsigned long long u64;
 // only sums that are refused exceed, and rows that several sequences claim.
 struct Block {
     int32_t held[kThreads], need[kThreads], past[kThreads], row0[kThreads];
+    int32_t lacks[kThreads];  // its entries from held up to this one it wants and does not get
     bool fine[kThreads];  // has no finding and got what it needs
     uint32_t give[kThreads + 1], take[kThreads + 1], rows[kThreads + 1];
     u64 scan[3][kWarps];
@@ -80,7 +81,7 @@ __device__ __forceinline__ int32_t page_of(const ReserveArgs& A, int32_t n) {
 
 // A thread's sequence, and what it gives back, takes and has of rows, by itself and with those before it.
 struct Mine {
-    int32_t b, held, need;
+    int32_t b, held, need, want;  // want: entries of its row, whether it gets them or not
     uint32_t err;
     u64 gives, takes, takes_upto;
 };
@@ -106,6 +107,7 @@ __device__ __forceinline__ u64 read_block(const ReserveArgs& A, Block& s, int32_
         }
         if (me.held < 0 || me.held > A.table_stride) me.err |= 1u << SV_ERR_BAD_OFFSETS;
         const int64_t pages = (n + A.page_size - 1) / A.page_size;
+        if (!me.err && n >= 0) me.want = (int32_t)min(pages, (int64_t)A.table_stride);
         if (n < 0 || pages > A.table_stride) me.err |= 1u << SV_ERR_CAPACITY;
         me.need = me.err ? me.held : (int32_t)pages;
         if (!me.err) {
@@ -143,7 +145,8 @@ __device__ __forceinline__ u64 read_block(const ReserveArgs& A, Block& s, int32_
     return all[0];
 }
 // Who gets what it lacks, of `free` pages, after the blocks before took (or would have) `before`. All threads; ends with a barrier.
-__device__ __forceinline__ void serve(Block& s, Mine& me, u64 before, u64 free, bool bad, int32_t B) {
+// Whether some go without.
+__device__ __forceinline__ bool serve(Block& s, Mine& me, u64 before, u64 free, bool bad, int32_t B) {
     const int tid = threadIdx.x;
     const bool served = !bad && before + me.takes_upto <= free;
     if (bad || (!served && me.takes)) me.need = me.held;
@@ -152,7 +155,8 @@ __device__ __forceinline__ void serve(Block& s, Mine& me, u64 before, u64 free, 
     if (who && (tid & 31) == 31 - __clz(who)) atomicMax(&s.served, me.takes_upto);
     s.need[tid] = me.need;
     s.fine[tid] = me.b < B && !me.err && !bad;
-    __syncthreads();
+    s.lacks[tid] = me.want > me.need ? me.want : 0;
+    return __syncthreads_or(me.want > me.need);
 }
 
 __global__ void __launch_bounds__(kThreads) k_cache_reserve(const __grid_constant__ ReserveArgs A) {
@@ -204,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_reserve(const __grid_constan
             __syncthreads();
             read_block(A, s, b0, me, takes);
         }
-        serve(s, me, base, free, bad, A.B);
+        const bool lacking = serve(s, me, base, free, bad, A.B);
         err |= me.err;
         if (tid == 0) block_base[b0 / kThreads] = base;
         const uint32_t served = (uint32_t)s.served, from = (uint32_t)base;  // both below `pages` where pages are taken
@@ -214,6 +218,12 @@ __global__ void __launch_bounds__(kThreads) k_cache_reserve(const __grid_constan
             if (id < 0 || id >= A.pages) report(A.status, 1u << SV_ERR_BAD_OFFSETS);
             A.table[(int64_t)(b0 + t) * A.table_stride + (s.held[t] + (int32_t)(i - s.take[t]))] = id;
         }
+        // What lies past a sequence's pages is what it gave back once, and may be another's by now: entries that it wanted and
+        // did not get must not pass for its own.
+        if (lacking)
+#pragma unroll 1
+            for (int t = (int)first / 32; t < kThreads; t += (int)step / 32)
+                for (int32_t i = s.held[t] + (tid & 31); i < s.lacks[t]; i += 32) A.table[(int64_t)(b0 + t) * A.table_stride + i] = -1;
         if (A.slots) {
             // a warp takes a run of slots, several a lane at once where there are many: the sequence of the run's first is
             // searched for once, and is that of most others in a prompt
