@@ -5,7 +5,9 @@
  * A verify step is exact for whatever distributions its logits stand for ("6-1편. Speculative Decoding", section 2-2: the
  * emitted tokens are distributed as the target's p, lines 859-885): filtering the target's rows and the draft's rows and
  * drawing the drafts from the filtered draft rows gives tokens of the filtered target distribution. Logits of -inf have
- * p = 0 in every verify call.
+ * p = 0 in every verify call. The kept logits are written as they are, and a verify call divides by its own temperature: that
+ * has to be the requests'. So requests that are verified in one call have one temperature, or 0, which keeps a single token
+ * (any temperature of the verify call will do for those); others are verified in calls of their own.
  *
  * A row l of V logits with temperature T has weights w_i = exp((l_i - max l) / T). Its tokens are ranked by their logits,
  * the largest first, equal ones by index, those of -inf not at all. The first n of the ranking are kept:

@@ -14,6 +14,7 @@ is a chunk like any other, a chain whose tokens are all kept.
 """
 from __future__ import annotations
 
+import ctypes
 import sys
 
 import torch
@@ -30,6 +31,16 @@ PARENTS = [0] * WIDTH + [j - WIDTH for j in range(WIDTH + 1, WIDTH * DEPTH + 1)]
 def _ok(rc):
     if rc != sv.SV_OK:
         raise RuntimeError(sv.spec_verify_status_string(rc))
+
+
+class Filters(tuple):
+    """A sampled step's filters of the batch, its draft rows and its target rows; temperature: what their rows are verified
+    with, None if any will do."""
+
+    def __new__(cls, filters, temperature):
+        self = super().__new__(cls, filters)
+        self.temperature = temperature
+        return self
 
 
 class Decoder:
@@ -142,18 +153,24 @@ class Decoder:
 
 
     def filters(self, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
-        """The filters of a sampled step's draft and target rows; each argument a number, or one a sequence."""
+        """The filters of a sampled step's draft and target rows; each argument a number, or one a sequence. The sequences
+        are verified by one call, which has one temperature: theirs are the same, or 0."""
         def each(x, kind):
             return torch.as_tensor(x, dtype=kind, device=self.cached.device).expand(self.B).contiguous()
+        given = sorted(set(each(temperature, torch.float32).tolist()) - {0.0})
+        if len(given) > 1:
+            raise ValueError(f"one verify call has one temperature (or 0 for some sequences), got {given}")
         asked = (each(temperature, torch.float32), each(top_k, torch.int32), each(top_p, torch.float32),
                  each(min_p, torch.float32))
         who = torch.arange(self.B, dtype=torch.int32, device=self.cached.device)
-        return (ss.Filter(*asked), ss.Filter(*asked, request=who.repeat_interleave(DEPTH)),
-                ss.Filter(*asked, request=who.repeat_interleave(DEPTH + 1)))
+        return Filters((ss.Filter(*asked), ss.Filter(*asked, request=who.repeat_interleave(DEPTH)),
+                        ss.Filter(*asked, request=who.repeat_interleave(DEPTH + 1))), given[0] if given else None)
 
     def sampled_step(self, filters, temperature, seed=0, generator=None):
         """Drafts, verifies and keeps up to DEPTH + 1 new tokens a sequence, drawn from the target's filtered
         distributions. filters: of `filters`, with this temperature."""
+        if filters.temperature not in (None, ctypes.c_float(temperature).value):
+            raise ValueError(f"the filters' temperature is {filters.temperature}, got {temperature}")
         B, dev = self.B, self.cached.device
         drafts = torch.empty((B, DEPTH), dtype=torch.int32, device=dev)
         logits = torch.empty((B, DEPTH, self.vocab), dtype=torch.bfloat16, device=dev)

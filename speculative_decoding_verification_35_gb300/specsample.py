@@ -7,7 +7,8 @@ filtered alike:
     f.sample(draft_logits, uniforms, tokens)               # one token a row
     f.mask(target_logits, out)                             # -inf where a token is not kept
 
-Rows that share requests (a sequence's gamma + 1 rows) name them with ``request``. Every call enqueues on the given
+Rows that share requests (a sequence's gamma + 1 rows) name them with ``request``. Masked rows keep their logits as they
+are: a verify call has to be given the requests' temperature, which is one, or 0, for all that it verifies. Every call enqueues on the given
 stream (default: torch's current one) and returns the library's host status code. The library reads tensors by
 address: a Filter keeps references to its own, and a caller using another stream than the one its tensors were made
 on orders the two itself.
