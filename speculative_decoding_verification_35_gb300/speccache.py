@@ -361,8 +361,8 @@ class PagePool:
                 raise ValueError(f"{name} must be contiguous")
         self.page_table, self.queue, self.held, self.state = page_table, queue, held, state
         self.sequences, self.page_size, self._device = page_table.shape[0], page_size, at
-        self.struct = SvPages(_ptr(page_table), _ptr(queue), _ptr(held), _ptr(state), 0, 0, page_table.shape[1],
-                              _int32(page_size, "page_size"), queue.shape[0], 0)
+        self.struct = SvPages(_ptr(page_table), _ptr(queue), _ptr(held), _ptr(state), _ptr(held), _ptr(state),
+                              page_table.shape[1], _int32(page_size, "page_size"), queue.shape[0], 0)
         self.status = torch.zeros(1, dtype=torch.int32, device=page_table.device)
         self._at, self._status = ctypes.addressof(self.struct), _ptr(self.status)
 
@@ -396,17 +396,24 @@ class PagePool:
             _check(slot_map, "slot_map", (torch.int64,), (None,), self._device)
             if slot_map.shape[0] < rows:
                 raise ValueError(f"slot_map must have {rows} rows, got {slot_map.shape[0]}")
-        out_held = self.held if out_held is None else out_held
-        out_state = self.state if out_state is None else out_state
-        _check(out_held, "out_held", (torch.int32,), (None,), self._device)
-        _check(out_state, "out_state", (torch.int32,), (2,), self._device)
-        if out_held.shape[0] < B:
-            raise ValueError(f"out_held must have {B} entries, got {out_held.shape[0]}")
+        if out_held is not None:
+            _check(out_held, "out_held", (torch.int32,), (None,), self._device)
+            if out_held.shape[0] < B:
+                raise ValueError(f"out_held must have {B} entries, got {out_held.shape[0]}")
+        if out_state is not None:
+            _check(out_state, "out_state", (torch.int32,), (2,), self._device)
         for t, name in ((lengths, "lengths"), (slot_map, "slot_map"), (out_held, "out_held"), (out_state, "out_state")):
             if t is not None and not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-        self.struct.out_held, self.struct.out_state = out_held.data_ptr(), out_state.data_ptr()
-        return lib.spec_cache_reserve(self._at, None if chunk is None else chunk.at, _ptr(lengths), B, _ptr(slot_map), self._status,
+        at = self._at
+        if out_held is not None or out_state is not None:  # a structure of the call's own: other threads may be in theirs
+            own = SvPages.from_buffer_copy(self.struct)
+            if out_held is not None:
+                own.out_held = out_held.data_ptr()
+            if out_state is not None:
+                own.out_state = out_state.data_ptr()
+            at = ctypes.addressof(own)
+        return lib.spec_cache_reserve(at, None if chunk is None else chunk.at, _ptr(lengths), B, _ptr(slot_map), self._status,
                                       self._stream(stream))
 
     def _stream(self, stream):

@@ -1,0 +1,38 @@
+"""What PagePool.reserve hands to the library (CPU)."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def sc():
+    from speculative_decoding_verification_35_gb300 import _build
+    _build.build()
+    from speculative_decoding_verification_35_gb300 import speccache
+    return speccache
+
+
+def ints(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def test_calls_do_not_write_what_they_share(sc, monkeypatch):
+    """Two threads may use a pool at once, each with outputs of its own: a call inside another changes nothing of it."""
+    p = sc.PagePool(ints(3, 4), ints(20), ints(3), ints(2), 16)
+    monkeypatch.setattr(sc.PagePool, "_stream", lambda self, stream: None)
+    before = bytes(p.struct)
+    mine, theirs, got = (ints(3), ints(2)), (ints(3), ints(2)), []
+
+    def record(at, *rest):
+        if not got:
+            got.append(None)
+            assert p.reserve(lengths=ints(3), out_held=theirs[0], out_state=theirs[1]) == 0
+            assert p.reserve(lengths=ints(3)) == 0
+            assert p.reserve(lengths=ints(3), out_state=theirs[1]) == 0
+        s = sc.SvPages.from_address(at)
+        got.append((s.out_held, s.out_state))
+        return 0
+    monkeypatch.setattr(sc.lib, "spec_cache_reserve", record)
+    assert p.reserve(lengths=ints(3), out_held=mine[0], out_state=mine[1]) == 0
+    a, b, h, s = (t.data_ptr() for t in (*theirs, p.held, p.state))
+    assert got[1:] == [(a, b), (h, s), (h, b), (mine[0].data_ptr(), mine[1].data_ptr())]
+    assert bytes(p.struct) == before
