@@ -35,6 +35,7 @@
 
 #include "../../include/specsample.h"
 #include "sv_device.cuh"
+#include "sv_sample_words.h"
 
 namespace cg = cooperative_groups;
 
@@ -1394,10 +1395,11 @@ struct Work {
         const int32_t e0 = max(0, s.c0 * E::N - off), e1 = min(A.V, s.c1 * E::N - off);
         const uint32_t* words = reinterpret_cast<const uint32_t*>(s.data);
         const bool same = o_off == off;
-        const uint32_t shift = (uint32_t)((off - o_off) * (int)sizeof(Bits)) % 4 * 8;
+        const Apart apart{off, o_off, (int32_t)sizeof(Bits), E::N};
+        const uint32_t shift = apart.shift();
         // by the output's chunks of 16 bytes, which lie as the logits' do, or between two of them: whole ones, and others, or the
         // one that the last tie lies in, by element
-        const int32_t w0 = (e0 + o_off + E::N - 1) / E::N, w1 = (min(e1, same ? e1 : A.V - 1) + o_off) / E::N;
+        const int32_t w0 = apart.c0(e0), w1 = apart.c1(e1, A.V);
         const int32_t last = copy || cut == 0x7fffffff ? 0x7fffffff : (cut + o_off + E::N) / E::N - 1;  // the chunk of `cut`
         const int32_t split = copy || cut == 0x7fffffff || (cut + o_off) % E::N == E::N - 1 || cut < 0 ? -1 : last;
         auto whole = [&](int32_t c) { return c >= w0 && c < w1 && c != split; };
@@ -1412,10 +1414,11 @@ struct Work {
                 if (same) {
                     q[k] = kHeld ? s.data[c] : __ldcs(s.data + c);
                 } else {
-                    const uint32_t* w = words + (c * E::N - o_off + off) * (int)sizeof(Bits) / 4;
+                    const uint32_t* w = words + apart.word(c);
                     uint32_t x[5];
 #pragma unroll
-                    for (int i = 0; i < 5; ++i) x[i] = w[i];
+                    for (int i = 0; i < 4; ++i) x[i] = w[i];
+                    x[4] = apart.words() > 4 ? w[4] : 0u;
                     q[k] = make_uint4(__funnelshift_r(x[0], x[1], shift), __funnelshift_r(x[1], x[2], shift),
                                       __funnelshift_r(x[2], x[3], shift), __funnelshift_r(x[3], x[4], shift));
                 }
