@@ -1,6 +1,6 @@
 """A small decoder that generates with token trees, or samples: the calls as they are used together.
 
-    python -m speculative_decoding_verification_35_gb300.decode [SEQUENCES] [STEPS] [sample]
+    python -m speculative_decoding_verification_35_gb300.decode [SEQUENCES] [STEPS] [sample [CAP]]
 
 The target model is a few layers of attention over a paged cache, with random weights (projections are torch
 products) and, if wanted, capped scores. A step makes room for its tokens in the cache (spec_cache_reserve), drafts a
@@ -198,8 +198,9 @@ def main(argv=None) -> int:
     B = int(argv[0]) if argv else 4
     steps = int(argv[1]) if len(argv) > 1 else 32
     sampled = len(argv) > 2 and argv[2] == "sample"
+    cap = float(argv[3]) if len(argv) > 3 else 0.0
     n = 20
-    d = Decoder(B, n + 1 + steps * (DEPTH + 1) + len(PARENTS))
+    d = Decoder(B, n + 1 + steps * (DEPTH + 1) + len(PARENTS), cap=cap)
     d.prompt(torch.randint(d.vocab, (B, n), device="cuda", generator=torch.Generator("cuda").manual_seed(1)))
     filters = d.filters(0.8, 50, 0.95, 0.01)
     for _ in range(steps):
