@@ -18,6 +18,7 @@ caller using another stream than the one its tensors were made on orders the two
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -342,6 +343,9 @@ class PagedCache:
         return int(self.status.item()) & 0xFFFFFFFF
 
 
+_two_addresses = struct.Struct("=QQ").pack
+
+
 class PagePool:
     """The pages of a pool, dealt out to sequences on the device (see sv_pages).
 
@@ -365,6 +369,8 @@ class PagePool:
                               page_table.shape[1], _int32(page_size, "page_size"), queue.shape[0], 0)
         self.status = torch.zeros(1, dtype=torch.int32, device=page_table.device)
         self._at, self._status = ctypes.addressof(self.struct), _ptr(self.status)
+        at = SvPages.out_held.offset  # what lies before and behind the outputs' addresses
+        self._before, self._behind = bytes(self.struct)[:at], bytes(self.struct)[at + 16:]
 
     @classmethod
     def create(cls, sequences: int, width: int, pages: int, page_size: int, device="cuda"):
@@ -407,12 +413,8 @@ class PagePool:
                 raise ValueError(f"{name} must be contiguous")
         at = self._at
         if out_held is not None or out_state is not None:  # a structure of the call's own: other threads may be in theirs
-            own = SvPages.from_buffer_copy(self.struct)
-            if out_held is not None:
-                own.out_held = out_held.data_ptr()
-            if out_state is not None:
-                own.out_state = out_state.data_ptr()
-            at = ctypes.addressof(own)
+            outs = (self.held if out_held is None else out_held), (self.state if out_state is None else out_state)
+            at = b"%b%b%b" % (self._before, _two_addresses(outs[0].data_ptr(), outs[1].data_ptr()), self._behind)
         return lib.spec_cache_reserve(at, None if chunk is None else chunk.at, _ptr(lengths), B, _ptr(slot_map), self._status,
                                       self._stream(stream))
 
