@@ -21,7 +21,8 @@ def counts(l, T=1.0, k=0, p=1.0, mp=0.0, slack=0.0):
     rank = ranking(l)
     if T == 0:
         return 1, 1
-    w = np.exp((l[rank] - l[rank[0]]) / T)
+    z = (l[rank] - l[rank[0]]) / T
+    w = np.exp(z)
     most = len(rank)
     if k >= 1:
         most = min(most, k)
@@ -32,7 +33,8 @@ def counts(l, T=1.0, k=0, p=1.0, mp=0.0, slack=0.0):
             c = np.cumsum(w[:most])
             n = min(n, int(np.searchsorted(c, p * c[-1] * (1 + sign * slack), side="left")) + 1)
         if mp > 0:
-            n = min(n, int(np.count_nonzero(w >= min(mp, 1.0) * (1 - sign * slack if mp < 1 else 1))))
+            # by logarithms: a weight just below 1 is 1 in fp64
+            n = min(n, int(np.count_nonzero(z >= (np.log(mp) + np.log1p(-sign * slack) if mp < 1 else 0.0))))
         out.append(max(n, 1))
     return out[0], out[1]
 

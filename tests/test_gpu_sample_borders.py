@@ -114,3 +114,13 @@ def test_the_last_weights_count(ss):
     assert got[0][2].tolist() == [39923] * 2  # the first sums that reach (1 - 2^-24) of the total, by hand
     for a, b in zip(*(g[:3] for g in got)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V,p", [(300, 1.0), (5003, 1.0), (5003, 0.999)])
+def test_min_p_of_one_keeps_the_largest_alone(ss, kind, V, p):
+    """And those equal to it, though the others' weights are 1 in any arithmetic: at high temperatures, and among tiny logits."""
+    x = make(5, V, kind, seed=V)
+    x[2:] = (x[2:].float() * 1e-20).to(x.dtype)
+    x[4, 5::7] = x[4].max()
+    check(ss, x, T=[1e12, 1e35, 1.0, 0.3, 1.0], mp=[1.0, 7.0, 1.0, 1.0, 1.0], p=p)

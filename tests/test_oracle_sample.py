@@ -54,3 +54,11 @@ def test_edges():
     assert os_.counts(l, 1.0, 0, 0.0) == (1, 1)
     assert os_.counts(l, 1.0, 0, 1.0, 5.0) == (2, 2)  # both of the largest
     assert os_.draws(l, 0.0, os_.kept(l, 1), 0.99)[:2] == (1, 1)
+
+
+def test_min_p_near_one_counts_logits_and_not_rounded_weights():
+    l = np.array([3e-25, 1e-25, 3e-25, -2.0])
+    assert os_.counts(l, 1.0, mp=1.0) == (2, 2)
+    assert os_.counts(l, 1e30, mp=1.0) == (2, 2)
+    assert os_.counts(l, 1.0, mp=0.5) == (3, 3)
+    assert os_.counts(np.array([0.0, np.log(0.25), np.log(0.25) - 1e-9]), 1.0, mp=0.25, slack=1e-6) == (1, 3)
