@@ -346,13 +346,15 @@ __device__ __forceinline__ u64 scaled(u64 x, float f, bool up) {
     }
     return q + (up && rest);
 }
-// ceil(a / b) where it is at most 2^18 (or so): the quotient in float is off by less than one.
+// ceil(a / b) where it is at most 2^18 (or so): the quotient in float is off by less than one, and one is taken off it, so that
+// four steps are enough. (And no more are made, for a row that someone writes to while it is read where it lies may say
+// anything.)
 __device__ __forceinline__ uint32_t div_up(u64 a, u64 b) {
     if (b == 0) return 1;
     uint32_t q = (uint32_t)__fdividef((float)a, (float)b);
     if (q > 0) --q;
 #pragma unroll 1
-    while (q * b < a) ++q;
+    for (int i = 0; i < 4 && q * b < a; ++i) ++q;
     return q;
 }
 
@@ -1511,6 +1513,8 @@ __global__ void __launch_bounds__(Work<T, kHeld>::kThreads, kHeld ? 2 : 1) k_row
     }
     if (tid == kThreads - 1) {
         sh.flags = sh.listed = 0;
+        sh.hit = 0;  // of a CTA and a warp that there are, whatever the row's passes see
+        sh.token = -1;
         read_par(A, sh.par, row, kDraws);
     }
     const int32_t full0 = off > 0;
