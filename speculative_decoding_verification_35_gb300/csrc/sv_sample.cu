@@ -4,7 +4,7 @@
 // it are kept, and of those equal to it the first r by index. A weight is w = 2^((l - m) K), K = log2(e) / T, held as an
 // integer W = round(2^44 w); sums of them are exact, and so is every comparison of sums (top-p's crossing, the inverse
 // CDF's): the order in which threads add does not matter, and a draw differs from one in real numbers only where its
-// target lies within the weights' own errors, some 2^-31 of each, of a border.
+// target lies within the weights' own errors, some 2^-31 of each, of a border. min-p compares logits.
 //
 // Three ways to the threshold.
 // - Few candidates. With top-k (up to a CTA's threads), with min-p alone and for T = 0 most logits are known to be too low
@@ -24,7 +24,7 @@
 //
 // What bounds it: small batches a chain of short steps (load, survey, gather, sort, sums: a block or cluster barrier and one to
 // three us each; one row of 32000 14.5 to 15.5 us), many rows the same steps with nothing else on the SM meanwhile, though a row
-// is read from memory once (704 rows filtered, a filter for each sequence: 143 to 148 us, 0.36 of the copy rate; before
+// is read from memory once (704 rows filtered, a filter for each sequence: 141 to 146 us, 0.37 of the copy rate; before
 // the next row was brought, 153, and 163 and 246 with 2 and 4 CTAs an SM). 64 rows of 128256, nucleus alone: 33 us, 12 of them counting and finding the threshold, 9 drawing.
 #include <cooperative_groups.h>
 

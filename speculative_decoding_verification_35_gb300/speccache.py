@@ -381,7 +381,8 @@ class PagePool:
 
     def reserve(self, chunk: Chunk | None = None, lengths=None, slot_map=None, out_held=None, out_state=None,
                 stream=None) -> int:
-        """Enqueue spec_cache_reserve: pages for the chunk's tokens, or for `lengths` (int32 [sequences]) to hold.
+        """Enqueue spec_cache_reserve: pages for the chunk's tokens, or for `lengths` (int32 [sequences]) to hold. A
+        sequence that there are too few for keeps its own; the table has -1 where it wanted more, which the cache refuses.
         slot_map: int64 [rows], the chunk's places. out_held, out_state: held and state themselves by default."""
         if (chunk is None) == (lengths is None):
             raise ValueError("one of chunk and lengths is wanted")
